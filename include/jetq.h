@@ -558,6 +558,60 @@ JETQ_API jetq_status jetq_gemm_nvfp4(const uint8_t *qa, const uint8_t *sfa, cons
                                      int64_t m, int64_t n, int64_t k,
                                      void *out, jetq_out_dtype out_dtype, int64_t ldo, void *stream);
 
+/* ======================================================================== */
+/* The head: softmax cross entropy over the vocabulary                      */
+/* ======================================================================== */
+/*
+ * Token losses of a linear head without keeping the logits (the log-
+ * probabilities that on-policy RL scores its rollouts with, and the loss of
+ * supervised training).  BF16 hidden states and head, FP32 arithmetic:
+ *   z[i, j] = scale * sum_k x[i, k] * w[j, k]
+ *   lse[i]  = log sum_j exp(z[i, j])
+ *   loss[i] = lse[i] - z[i, target[i]]      (minus the token's log-probability)
+ * A target outside [0, v) marks a row without a loss: loss[i] = 0, lse[i] as
+ * for any row, and no gradient.  `scale` is 1 / temperature.
+ *
+ *   x, n, c, ldx   BF16 [n x c], row stride ldx (multiple of 8); c a multiple of 8
+ *   w, v, ldw      BF16 [v x c], row stride ldw (multiple of 8); any v >= 1
+ *   target         device int64 [n]
+ *   scale          > 0, finite
+ *   loss, lse      float [n]
+ *   workspace      device memory, 16-byte aligned, at least
+ *                  jetq_linear_ce_workspace_bytes(n, v) bytes; calls that
+ *                  share one must not overlap on the GPU
+ * n == 0 is a no-op.  Results are bitwise repeatable.  Two launches.
+ */
+JETQ_API size_t jetq_linear_ce_workspace_bytes(int64_t n, int64_t v);
+JETQ_API jetq_status jetq_linear_ce_fwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx,
+                                        const uint16_t *w, int64_t v, int64_t ldw,
+                                        const int64_t *target, float scale, float *loss, float *lse,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradient, from the forward call's lse (the logits are computed again, a
+ * piece of the vocabulary at a time):
+ *   d[i, j] = (exp(z[i, j] - lse[i]) - [j = target[i]]) * dloss[i]
+ *   dx = scale * d w   (BF16 [n x c], stride lddx),   dw = scale * d^T x   ([v x c], stride lddw)
+ * d is rounded to BF16 (relative to the largest |dloss|) for the tensor cores;
+ * every sum is FP32, rounded once.  dw: BF16, or FP32 with accumulate = 1 to
+ * add into it.  Rows without a loss give zero rows of dx and add nothing to dw
+ * (their x must be finite: the products run over every row).
+ *
+ *   dloss      float [n]
+ *   workspace  device memory, 16-byte aligned.  Its size decides how much of
+ *              the vocabulary a piece covers: jetq_linear_ce_bwd_workspace_bytes
+ *              gives the preferred size (smallest = 0; more is not used) and
+ *              the smallest one that is accepted (smallest = 1)
+ * n == 0: dw is set to zero (accumulate = 0) or left unchanged.
+ */
+JETQ_API size_t jetq_linear_ce_bwd_workspace_bytes(int64_t n, int64_t v, int64_t c, int smallest);
+JETQ_API jetq_status jetq_linear_ce_bwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx,
+                                        const uint16_t *w, int64_t v, int64_t ldw,
+                                        const int64_t *target, float scale, const float *lse, const float *dloss,
+                                        uint16_t *dx, int64_t lddx,
+                                        void *dw, jetq_out_dtype dw_dtype, int64_t lddw, int accumulate,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -46,7 +46,7 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"jetq CUDA library missing ({LIB_PATH}); build it with __graft_entry__.build()")
         L = ctypes.CDLL(LIB_PATH)
-        P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+        P, I64, I32, F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
         sig = {
             "jetq_status_string": (ctypes.c_char_p, [I32]),
             "jetq_version": (I32, []),
@@ -77,6 +77,11 @@ def lib() -> ctypes.CDLL:
             "jetq_nvfp4_atom_bytes": (I64, [I64, I64]),
             "jetq_nvfp4_scale_atoms": (I32, [P, I64, I64, P, P]),
             "jetq_gemm_nvfp4": (I32, [P, P, P, I32, P, P, P, I64, I64, I64, P, I32, I64, P]),
+            "jetq_linear_ce_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
+            "jetq_linear_ce_fwd": (I32, [P, I64, I64, I64, P, I64, I64, P, F32, P, P, P, ctypes.c_size_t, P]),
+            "jetq_linear_ce_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I32]),
+            "jetq_linear_ce_bwd": (I32, [P, I64, I64, I64, P, I64, I64, P, F32, P, P, P, I64, P, I32, I64, I32, P,
+                                         ctypes.c_size_t, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -285,6 +290,47 @@ def jetq_gemm_grouped(kind, recipe, a, sa, b, sb, m, n, k, ldk, seg_offsets, num
                                    _s(stream)), "jetq_gemm_grouped")
 
 
+def jetq_linear_ce_workspace_bytes(n: int, v: int) -> int:
+    return int(lib().jetq_linear_ce_workspace_bytes(n, v))
+
+
+def jetq_linear_ce_fwd(x, w, target, scale, loss, lse, ws, stream=None):
+    n, c = x.shape
+    _check(lib().jetq_linear_ce_fwd(_p(x), n, c, x.stride(0), _p(w), w.shape[0], w.stride(0), _p(target), scale,
+                                    _p(loss), _p(lse), _p(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                    _s(stream)), "jetq_linear_ce_fwd")
+
+
+def jetq_linear_ce_bwd_workspace_bytes(n: int, v: int, c: int, smallest: bool = False) -> int:
+    return int(lib().jetq_linear_ce_bwd_workspace_bytes(n, v, c, 1 if smallest else 0))
+
+
+def jetq_linear_ce_bwd(x, w, target, scale, lse, dloss, dx, dw, accumulate, ws, stream=None):
+    n, c = x.shape
+    _check(lib().jetq_linear_ce_bwd(_p(x), n, c, x.stride(0), _p(w), w.shape[0], w.stride(0), _p(target), scale,
+                                    _p(lse), _p(dloss), _p(dx), dx.stride(0), _p(dw), _out_dtype(dw), dw.stride(0),
+                                    1 if accumulate else 0, _p(ws),
+                                    0 if ws is None else ws.numel() * ws.element_size(), _s(stream)),
+           "jetq_linear_ce_bwd")
+
+
+# ------------------------------------------------------------------ argument checks of the tensor helpers
+
+def _want(t, name, dtype, shape=None, rows=False):
+    """A CUDA tensor of `dtype` (and shape); rows: unit stride along the last axis, else dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is wanted")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name}: {dtype} is wanted, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
+    if rows:
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name}: rows of consecutive elements are wanted, got strides {t.stride()}")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is wanted")
+
+
 # ------------------------------------------------------------------ allocating helpers
 
 def quant_act(x, row=True, col=True, seg_offsets=None, stream=None):
@@ -490,3 +536,44 @@ def grouped(kind, a, sa, b, sb, seg_offsets, n, k, out_dtype=torch.float32, reci
             out = torch.empty((m, n), dtype=out_dtype, device=a.device)
     jetq_gemm_grouped(kind, recipe, a, sa, b, sb, m, n, k, ldk, seg_offsets, E, out, accumulate, stream)
     return out
+
+
+def _check_head(x, w, target):
+    _want(x, "x", torch.bfloat16, rows=True)
+    _want(w, "w", torch.bfloat16, rows=True)
+    _want(target, "target", torch.int64, (x.shape[0],))
+    if x.shape[1] != w.shape[1]:
+        raise ValueError(f"x and w: widths {x.shape[1]} and {w.shape[1]}")
+
+
+def linear_ce(x, w, target, scale=1.0, workspace=None, stream=None):
+    """Token losses of a linear head (see jetq_linear_ce_fwd): BF16 x [n x c], w [v x c], int64
+    target [n] (outside [0, v): no loss) -> (loss [n], lse [n])."""
+    _check_head(x, w, target)
+    n, v = x.shape[0], w.shape[0]
+    loss, lse = torch.empty((2, n), dtype=torch.float32, device=x.device).unbind(0)
+    need = jetq_linear_ce_workspace_bytes(n, v)
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    jetq_linear_ce_fwd(x, w, target, scale, loss, lse, workspace, stream)
+    return loss, lse
+
+
+def linear_ce_bwd(x, w, target, lse, dloss, scale=1.0, dw_dtype=torch.float32, dw=None, accumulate=False,
+                  workspace=None, stream=None):
+    """Gradient of linear_ce (see jetq_linear_ce_bwd) -> (dx BF16 [n x c], dw [v x c]).  A workspace
+    that the caller gives is used as it is: its size decides the vocabulary's pieces."""
+    _check_head(x, w, target)
+    (n, c), v = x.shape, w.shape[0]
+    _want(lse, "lse", torch.float32, (n,))
+    _want(dloss, "dloss", torch.float32, (n,))
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dw to add into")
+        dw = torch.empty((v, c), dtype=dw_dtype, device=x.device)
+    _want(dw, "dw", (torch.float32, torch.bfloat16), (v, c), rows=True)
+    dx = torch.empty((n, c), dtype=torch.bfloat16, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(jetq_linear_ce_bwd_workspace_bytes(n, v, c), dtype=torch.uint8, device=x.device)
+    jetq_linear_ce_bwd(x, w, target, scale, lse, dloss, dx, dw, accumulate, workspace, stream)
+    return dx, dw

@@ -163,7 +163,7 @@ jetq_status jetq_check_device_error(void *stream)
     unsigned word = 0;
     if (gemm_read_and_clear_error(st, &word) != cudaSuccess || gemm_mx_read_and_clear_error(st, &word) != cudaSuccess ||
         gemm_decode_read_and_clear_error(st, &word) != cudaSuccess || quant_read_and_clear_error(st, &word) != cudaSuccess ||
-        gemm_nvfp4_read_and_clear_error(st, &word) != cudaSuccess)
+        gemm_nvfp4_read_and_clear_error(st, &word) != cudaSuccess || linear_ce_read_and_clear_error(st, &word) != cudaSuccess)
         return JETQ_ERR_CUDA;
     return word ? JETQ_ERR_TIMEOUT : JETQ_OK;
 }
@@ -635,6 +635,105 @@ jetq_status jetq_gemm_grouped(jetq_gemm_kind kind, jetq_recipe recipe, const uin
     g.seg = seg_offsets;
     g.num_experts = num_experts;
     return from_cuda(launch_gemm_block128(g, GemmShape::Train, cs));
+}
+
+namespace {
+
+// arguments that both directions of the linear cross entropy share
+jetq_status check_linear_ce(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, const uint16_t *w, int64_t v,
+                            int64_t ldw, const int64_t *target, float scale)
+{
+    JQ_REQUIRE(n >= 0 && v > 0 && c > 0, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(scale > 0.0f && scale <= 3.0e38f, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(c % 8 == 0 && ldx >= c && ldw >= c, JETQ_ERR_UNSUPPORTED_SHAPE);
+    JQ_REQUIRE(n <= (1 << 30) && v <= (1 << 30) && c <= (1 << 24) && (n / 128 + 1) * (v / 256 + 1) <= (1 << 30) &&
+                   (v / 128 + 1) * (c / 256 + 1) <= (1 << 30) && ldx <= ((int64_t)1 << 36) &&
+                   ldw <= ((int64_t)1 << 36),
+               JETQ_ERR_UNSUPPORTED_SHAPE);
+    JQ_REQUIRE(w != nullptr && (n == 0 || (x != nullptr && target != nullptr)), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(aligned16(x) && ldx % 8 == 0 && aligned16(w) && ldw % 8 == 0 &&
+                   (reinterpret_cast<uintptr_t>(target) & 7u) == 0,
+               JETQ_ERR_MISALIGNED);
+    return JETQ_OK;
+}
+
+} // namespace
+
+size_t jetq_linear_ce_workspace_bytes(int64_t n, int64_t v)
+{
+    return n <= 0 || v <= 0 ? 0 : linear_ce_fwd_workspace(n, v);
+}
+
+size_t jetq_linear_ce_bwd_workspace_bytes(int64_t n, int64_t v, int64_t c, int smallest)
+{
+    if (n <= 0 || v <= 0 || c <= 0)
+        return 0;
+    return smallest ? linear_ce_bwd_workspace_min(n, v, c) : linear_ce_bwd_workspace(n, v, c);
+}
+
+jetq_status jetq_linear_ce_fwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, const uint16_t *w, int64_t v,
+                               int64_t ldw, const int64_t *target, float scale, float *loss, float *lse,
+                               void *workspace, size_t workspace_bytes, void *stream)
+{
+    const jetq_status s = check_linear_ce(x, n, c, ldx, w, v, ldw, target, scale);
+    if (s != JETQ_OK || n == 0)
+        return s;
+    JQ_REQUIRE(loss != nullptr && lse != nullptr && workspace != nullptr, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(workspace_bytes >= linear_ce_fwd_workspace(n, v), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(aligned16(workspace) && (reinterpret_cast<uintptr_t>(loss) & 3u) == 0 &&
+                   (reinterpret_cast<uintptr_t>(lse) & 3u) == 0,
+               JETQ_ERR_MISALIGNED);
+    const jetq_status a = check_arch();
+    if (a != JETQ_OK)
+        return a;
+    LinearCeArgs g{x, n, c, ldx, w, v, ldw, target, scale, loss, lse};
+    g.ws = workspace;
+    g.ws_bytes = workspace_bytes;
+    return from_cuda(launch_linear_ce_fwd(g, static_cast<cudaStream_t>(stream)));
+}
+
+jetq_status jetq_linear_ce_bwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, const uint16_t *w, int64_t v,
+                               int64_t ldw, const int64_t *target, float scale, const float *lse, const float *dloss,
+                               uint16_t *dx, int64_t lddx, void *dw, jetq_out_dtype dw_dtype, int64_t lddw,
+                               int accumulate, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const jetq_status s = check_linear_ce(x, n, c, ldx, w, v, ldw, target, scale);
+    if (s != JETQ_OK)
+        return s;
+    const jetq_status o = check_out(dw, dw_dtype, lddw, c);
+    if (o != JETQ_OK)
+        return o;
+    JQ_REQUIRE(accumulate == 0 || (accumulate == 1 && dw_dtype == JETQ_OUT_F32), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(lddw <= ((int64_t)1 << 36), JETQ_ERR_UNSUPPORTED_SHAPE);
+    if (n > 0) {
+        JQ_REQUIRE(lse != nullptr && dloss != nullptr && dx != nullptr && workspace != nullptr, JETQ_ERR_INVALID_ARG);
+        JQ_REQUIRE(lddx >= c, JETQ_ERR_UNSUPPORTED_SHAPE);
+        JQ_REQUIRE(aligned16(dx) && lddx % 8 == 0 && aligned16(workspace) &&
+                       (reinterpret_cast<uintptr_t>(lse) & 3u) == 0 && (reinterpret_cast<uintptr_t>(dloss) & 3u) == 0,
+                   JETQ_ERR_MISALIGNED);
+    }
+    const jetq_status a = check_arch();
+    if (a != JETQ_OK)
+        return a;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (n == 0) { // no token: dw is zero, or stays as it is
+        if (accumulate)
+            return JETQ_OK;
+        const size_t es = dw_dtype == JETQ_OUT_F32 ? 4 : 2;
+        return from_cuda(cudaMemset2DAsync(dw, (size_t)lddw * es, 0, (size_t)c * es, (size_t)v, st));
+    }
+    JQ_REQUIRE(workspace_bytes >= linear_ce_bwd_workspace_min(n, v, c), JETQ_ERR_INVALID_ARG);
+    LinearCeArgs g{x, n, c, ldx, w, v, ldw, target, scale, nullptr, const_cast<float *>(lse)};
+    g.dloss = dloss;
+    g.dx = dx;
+    g.lddx = lddx;
+    g.dw = dw;
+    g.dw_dtype = dw_dtype;
+    g.lddw = lddw;
+    g.accumulate = accumulate;
+    g.ws = workspace;
+    g.ws_bytes = workspace_bytes;
+    return from_cuda(launch_linear_ce_bwd(g, st));
 }
 
 } // extern "C"

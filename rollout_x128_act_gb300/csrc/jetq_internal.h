@@ -241,6 +241,40 @@ cudaError_t quant_read_and_clear_error(cudaStream_t st, unsigned *out);
 cudaError_t make_kmajor_map(CUtensorMap *map, const void *base, int64_t k_extent, int64_t rows, int64_t ld,
                             int box_rows, int kb_per_box = 1);
 
+// TMA descriptor for a BF16 or FP32 matrix [rows x cols], row stride ld
+// elements: boxes of 128 bytes x box_rows, 128-byte swizzle, zero fill out of
+// bounds; slabs > 0: a third axis of that many matrices, slab_stride elements apart.
+cudaError_t make_sw128_map(CUtensorMap *map, const void *base, bool f32, int64_t cols, int64_t rows, int64_t ld,
+                           int box_rows, int64_t slabs = 0, int64_t slab_stride = 0);
+
+// Softmax cross entropy of a linear head (BF16 hidden states x [n x c], head w
+// [v x c]) in pieces of the vocabulary.
+struct LinearCeArgs {
+    const uint16_t *x;
+    int64_t n, c, ldx;
+    const uint16_t *w;
+    int64_t v, ldw;
+    const int64_t *target;
+    float scale;
+    float *loss;        // forward
+    float *lse;         // forward: out, backward: in
+    const float *dloss; // backward ...
+    uint16_t *dx;
+    int64_t lddx;
+    void *dw;
+    jetq_out_dtype dw_dtype;
+    int64_t lddw;
+    int accumulate;
+    void *ws;
+    size_t ws_bytes;
+};
+size_t linear_ce_fwd_workspace(int64_t n, int64_t v);
+size_t linear_ce_bwd_workspace(int64_t n, int64_t v, int64_t c);     // preferred
+size_t linear_ce_bwd_workspace_min(int64_t n, int64_t v, int64_t c); // one 256-row piece of the vocabulary
+cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st);
+cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st);
+cudaError_t linear_ce_read_and_clear_error(cudaStream_t st, unsigned *out);
+
 // Number of SMs of the current device (cached per device).
 int sm_count();
 

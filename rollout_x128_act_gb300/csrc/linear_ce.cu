@@ -1,0 +1,770 @@
+// Softmax cross entropy of a linear head on sm_103a tensor cores, in pieces of
+// the vocabulary, without keeping the logits.
+//
+//   z[i, j]  = scale * sum_k x[i, k] * w[j, k]             (BF16 products, FP32 sums)
+//   lse[i]   = log sum_j exp(z[i, j])
+//   loss[i]  = lse[i] - z[i, t_i]                          (0 where t_i is outside [0, v))
+//   d[i, j]  = (exp(z[i, j] - lse[i]) - [j = t_i]) * dloss[i]
+//   dx       = scale * d w,   dw = scale * d^T x
+//
+// One GEMM kernel (k_head_gemm) in four modes carries all of it:
+//   forward    x w^T with an epilogue that reduces each row's 128 logits to a
+//              (maximum, sum of exponentials) pair and picks the target's
+//              logit; a small kernel joins the pairs of a row
+//   backward, per piece of the vocabulary (its d is [n x piece] in BF16)
+//     1. x w^T again with an epilogue that writes d
+//     2. dx += d w: d K-major, w with its N axis (c) contiguous; FP32 slabs
+//        in the workspace, one per K split, added to by TMA add-reductions
+//     3. dw = d^T x: both operands with their M / N axis contiguous
+//   and a last kernel that sums the slabs into BF16 dx.
+//
+// d is rounded to BF16 once (the tensor core's operand type), scaled by the
+// largest |dloss| so that it is O(1) whatever the loss's normalisation, and a
+// uniform dloss adds no rounding of its own; sums, softmax statistics, dx
+// across pieces and dw stay in FP32 until their one final rounding.
+//
+// The target's term is left out of the sum of exponentials and joined at the
+// end: loss = log1p(sum of the others / the target's) where the target leads,
+// so a confident token's loss keeps its relative precision.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "jetq_internal.h"
+#include "ptx.cuh"
+
+namespace jetq {
+
+__device__ unsigned g_linear_ce_error;
+
+namespace {
+
+constexpr unsigned kErrTimeout = 1u;
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+enum HeadMode : int {
+    kStats = 0,   // softmax statistics of the logits
+    kGrad = 1,    // d in BF16
+    kGradX = 2,   // FP32 slabs of dx
+    kGradW16 = 3, // dw in BF16
+    kGradW32 = 4  // dw in FP32
+};
+
+struct HeadParams {
+    int mt, nt, splits, num_kb, group; // tiles of M and N, splits and 64-blocks of K, M tiles per raster group
+    int64_t M, N;                      // valid rows and columns of the output
+    float k2;                          // scale * log2(e): exponents in base 2
+    const int64_t *target;
+    int64_t V, col0;                   // whole vocabulary; first vocabulary row of this piece
+    float2 *part;                      // [2 * nt][M] (maximum, sum), base 2
+    float *zt;                         // [M] raw target logits
+    const float *lse, *dloss, *gmax;
+    float scale;
+    int add;                           // FP32 output: add to what is there
+    unsigned long long limit_ns;
+};
+
+template <int CG, int MODE>
+struct HeadCfg {
+    static constexpr int BN = 256, BK = 64;
+    static constexpr int kABytes = 128 * 128;
+    static constexpr int kBRows = BN / CG; // rows of B in one CTA's shared memory
+    static constexpr int kBBytes = kBRows * 128;
+    static constexpr int kStage = kABytes + kBBytes;
+    static constexpr int kStages = 6 * 32768 / kStage;
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kThreads = 128 + 32 * kEpiWarps;
+    static constexpr bool kStaging = MODE != kStats;
+    static constexpr size_t kStagingBytes = kStaging ? kEpiWarps * 4096 : 0;
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kStagingBytes + 256;
+    static constexpr bool kAMn = MODE == kGradW16 || MODE == kGradW32; // A's M axis contiguous
+    static constexpr bool kBMn = MODE >= kGradX;                       // B's N axis contiguous
+    static constexpr int kBars = 2 * kStages + 5;
+    static_assert(kBars * 8 + 8 <= 256, "barrier area");
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Raster: groups of `group` M tiles; inside a group N tiles in turn, M tiles
+// fastest; K splits slowest, so that concurrent tiles read the same K range.
+__device__ __forceinline__ void head_coords(const HeadParams &p, int t, int &mi, int &ni, int &ks)
+{
+    const int mn = p.mt * p.nt;
+    ks = t / mn;
+    t -= ks * mn;
+    const int g = t / (p.group * p.nt);
+    t -= g * p.group * p.nt;
+    const int gm = min(p.group, p.mt - g * p.group);
+    ni = t / gm;
+    mi = g * p.group + t - ni * gm;
+}
+
+template <int CG, int MODE>
+__global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
+    k_head_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmO, const HeadParams p)
+{
+    using C = HeadCfg<CG, MODE>;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *tiles = ptx::align_smem<1024>(smem_raw);
+    uint8_t *staging = tiles + (size_t)S * C::kStage;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + C::kStagingBytes);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const uint32_t bar0 = ptx::smem_addr(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (2 * S + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
+    const uint32_t done = bar0 + 8u * (2 * S + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
+    const int unit = blockIdx.x / CG, units = gridDim.x / CG;
+    unsigned *err = &g_linear_ce_error;
+    const int num_tiles = p.mt * p.nt * p.splits;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full(s), 1);
+            ptx::mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(acc_full(b), 1);
+            ptx::mbar_init(acc_empty(b), C::kEpiWarps * CG);
+        }
+        ptx::mbar_init(done, 1);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tensormap(&tmA);
+        ptx::prefetch_tensormap(&tmB);
+        if (C::kStaging)
+            ptx::prefetch_tensormap(&tmO);
+    }
+    if (warp == 1)
+        ptx::tmem_alloc_cg<CG>(ptx::smem_addr(tmem_slot), 512);
+    ptx::tc_fence_before();
+    if (CG == 2)
+        ptx::cluster_sync(); // the peer's barriers are initialized too
+    else
+        __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+
+    if (warp < 4) {
+        if (warp == 0 && lane == 0) {
+            // -------------------------------------------------- TMA producer
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = unit; t < num_tiles && ok; t += units) {
+                int mi, ni, ks;
+                head_coords(p, t, mi, ni, ks);
+                const int k0 = (int)((int64_t)p.num_kb * ks / p.splits);
+                const int k1 = (int)((int64_t)p.num_kb * (ks + 1) / p.splits);
+                const int m0 = mi * 128 * CG + (int)rank * 128;
+                const int n0 = ni * C::BN + (int)rank * C::kBRows;
+                for (int kb = k0; kb < k1; ++kb, ++it) {
+                    const int s = (int)(it % S);
+                    const uint32_t ph = (it / S) & 1u;
+                    if (!ptx::mbar_wait(empty(s), ph ^ 1u, abort_flag, err, kErrTimeout, p.limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    // the pair's bytes are counted on the even CTA's barrier, whose thread issues the MMAs
+                    if (rank == 0)
+                        ptx::mbar_arrive_expect_tx(full(s), (uint32_t)(CG * C::kStage));
+                    const uint32_t bar = CG == 2 ? ptx::map_to_cta(full(s), 0) : full(s);
+                    const uint32_t da = ptx::smem_addr(tiles + (size_t)s * C::kStage), db = da + C::kABytes;
+                    if (C::kAMn) {
+                        ptx::tma_load_2d_cg<CG>(da, &tmA, bar, m0, kb * C::BK);
+                        ptx::tma_load_2d_cg<CG>(da + 8192u, &tmA, bar, m0 + 64, kb * C::BK);
+                    } else {
+                        ptx::tma_load_2d_cg<CG>(da, &tmA, bar, kb * C::BK, m0);
+                    }
+                    if (C::kBMn) {
+#pragma unroll
+                        for (int j = 0; j < C::kBRows / 64; ++j)
+                            ptx::tma_load_2d_cg<CG>(db + 8192u * j, &tmB, bar, n0 + 64 * j, kb * C::BK);
+                    } else {
+                        ptx::tma_load_2d_cg<CG>(db, &tmB, bar, kb * C::BK, n0);
+                    }
+                }
+            }
+            // no copy may be in flight when the CTA ends (the even CTA's barriers count the pair's)
+            if (rank == 0)
+                for (int s = 0; s < S; ++s)
+                    if (it > (uint32_t)s) {
+                        const uint32_t last = (uint32_t)s + ((it - 1u - (uint32_t)s) / S) * S;
+                        ptx::mbar_wait(full(s), (last / S) & 1u, abort_flag, err, kErrTimeout, p.limit_ns, false);
+                    }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // -------------------------------------------------- MMA issuer
+            constexpr uint32_t idesc = ptx::idesc_bf16_f32(128 * CG, C::BN, C::kAMn, C::kBMn);
+            constexpr uint32_t a_step = C::kAMn ? 2048u >> 4 : 32u >> 4, b_step = C::kBMn ? 2048u >> 4 : 32u >> 4;
+            uint32_t it = 0, tc = 0;
+            bool ok = true;
+            for (int t = unit; t < num_tiles && ok; t += units) {
+                const int ks = t / (p.mt * p.nt);
+                const int k0 = (int)((int64_t)p.num_kb * ks / p.splits);
+                const int k1 = (int)((int64_t)p.num_kb * (ks + 1) / p.splits);
+                if (k0 == k1)
+                    continue;
+                const uint32_t b = tc & 1u;
+                if (!ptx::mbar_wait<CG == 2>(acc_empty(b), ((tc >> 1) & 1u) ^ 1u, abort_flag, err, kErrTimeout,
+                                             p.limit_ns))
+                    break;
+                ptx::tc_fence_after();
+                for (int kb = k0; kb < k1; ++kb, ++it) {
+                    const int s = (int)(it % S);
+                    const uint32_t ph = (it / S) & 1u;
+                    if (!ptx::mbar_wait<CG == 2>(full(s), ph, abort_flag, err, kErrTimeout, p.limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t a = ptx::smem_addr(tiles + (size_t)s * C::kStage);
+                    const uint64_t ad = C::kAMn ? ptx::desc_mnmajor_sw128(a, 8192u) : ptx::desc_kmajor_sw128(a);
+                    const uint64_t bd = C::kBMn ? ptx::desc_mnmajor_sw128(a + C::kABytes, 8192u)
+                                                : ptx::desc_kmajor_sw128(a + C::kABytes);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_bf16<CG>(tmem_base + 256u * b, ad + a_step * k, bd + b_step * k, idesc,
+                                          (kb > k0 || k > 0) ? 1u : 0u);
+                    ptx::mma_commit_cg<CG>(empty(s));
+                }
+                if (!ok)
+                    break;
+                ptx::mma_commit_cg<CG>(acc_full(b));
+                ++tc;
+            }
+            ptx::mma_commit_cg<CG>(done);
+            ptx::mbar_wait(done, 0u, abort_flag, err, kErrTimeout, p.limit_ns, false);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ epilogue
+        const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
+        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+        uint8_t *stage = staging + ew * 4096;
+        const uint32_t stage_row = ptx::smem_addr(stage) + (uint32_t)lane * 128u;
+        float factor = 1.0f;
+        if (MODE == kGradW16 || MODE == kGradW32)
+            factor = __ldg(p.gmax) * p.scale;
+        uint32_t tc = 0;
+        for (int t = unit; t < num_tiles; t += units) {
+            int mi, ni, ks;
+            head_coords(p, t, mi, ni, ks);
+            if ((int64_t)p.num_kb * ks / p.splits == (int64_t)p.num_kb * (ks + 1) / p.splits)
+                continue;
+            const uint32_t b = tc & 1u;
+            const int row0 = mi * 128 * CG + (int)rank * 128 + quarter * 32;
+            const int64_t row = (int64_t)row0 + lane;
+            const int n0 = ni * C::BN + half * 128;
+            // per-row inputs of the softmax modes, loaded before the accumulator is ready
+            int tcol = -1; // the target's column in this thread's 128, or out of range
+            float lse2 = 0.0f, coef = 0.0f;
+            if (MODE == kStats || MODE == kGrad) {
+                if (row < p.M) {
+                    const int64_t tg = __ldg(p.target + row);
+                    const int64_t rel = tg - p.col0 - n0;
+                    if (tg >= 0 && rel >= 0 && rel < 128)
+                        tcol = (int)rel;
+                    if (MODE == kGrad) {
+                        const float gm = __ldg(p.gmax);
+                        lse2 = __ldg(p.lse + row) * kLog2e;
+                        coef = tg >= 0 && tg < p.V && gm > 0.0f ? __fdiv_rn(__ldg(p.dloss + row), gm) : 0.0f;
+                    }
+                }
+            }
+            const bool got = ptx::mbar_wait(acc_full(b), (tc >> 1) & 1u, abort_flag, err, kErrTimeout, p.limit_ns);
+            if (!__all_sync(0xFFFFFFFFu, got))
+                break;
+            ptx::tc_fence_after();
+            const uint32_t acc = tmem_base + 256u * b + lane_addr + (uint32_t)(half * 128);
+            auto release = [&]() {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2)
+                        ptx::mbar_arrive_remote(ptx::map_to_cta(acc_empty(b), 0));
+                    else
+                        ptx::mbar_arrive(acc_empty(b));
+                }
+            };
+            if constexpr (MODE == kStats) {
+                uint32_t v[128];
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    ptx::tmem_ld_32x32b_x32(acc + 32u * ch, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * ch]));
+                ptx::tmem_ld_wait_tie(v);
+                release();
+                const int valid = (int)min((int64_t)128, p.N - n0); // columns of this thread inside the vocabulary
+                if (valid < 128) {
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j >= valid)
+                            v[j] = 0xff800000u; // -inf
+                }
+                float m = __uint_as_float(v[0]);
+#pragma unroll
+                for (int j = 1; j < 128; ++j)
+                    m = fmaxf(m, __uint_as_float(v[j]));
+                const float mk = m * p.k2;
+                float s0 = 0.0f, s1 = 0.0f, zt = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 128; j += 2) {
+                    const float a0 = __uint_as_float(v[j]), a1 = __uint_as_float(v[j + 1]);
+                    const float e0 = ex2(fmaf(a0, p.k2, -mk)), e1 = ex2(fmaf(a1, p.k2, -mk));
+                    zt = j == tcol ? a0 : (j + 1 == tcol ? a1 : zt);
+                    s0 += j == tcol ? 0.0f : e0; // the target's term is joined exactly by the last kernel
+                    s1 += j + 1 == tcol ? 0.0f : e1;
+                }
+                if (row < p.M) {
+                    // no column, or all of them -inf: an empty sum; only NaN: NaN (fmaxf passes over single ones)
+                    p.part[(int64_t)(2 * ni + half) * p.M + row] = m == -INFINITY ? make_float2(-INFINITY, 0.0f)
+                                                                   : m == m       ? make_float2(mk, s0 + s1)
+                                                                                  : make_float2(0.0f, m);
+                    if (tcol >= 0)
+                        p.zt[row] = zt;
+                }
+            } else if constexpr (MODE == kGrad || MODE == kGradW16) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) { // 64 BF16 columns: 128 bytes a row
+                    uint32_t v[64];
+#pragma unroll
+                    for (int ch = 0; ch < 2; ++ch)
+                        ptx::tmem_ld_32x32b_x32(acc + 64u * g + 32u * ch,
+                                                *reinterpret_cast<uint32_t(*)[32]>(&v[32 * ch]));
+                    ptx::tmem_ld_wait_tie(v);
+                    if (g == 1)
+                        release();
+                    const int x0 = n0 + 64 * g;
+                    if (MODE == kGradW16 && (x0 >= p.N || row0 >= p.M))
+                        continue;
+                    if (MODE == kGrad && row0 >= p.M)
+                        continue;
+                    uint32_t h[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float y[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float z = __uint_as_float(v[2 * j + e]);
+                            if (MODE == kGrad) {
+                                const int col = 64 * g + 2 * j + e;
+                                const float pr = ex2(fmaf(z, p.k2, -lse2));
+                                const float d = (col == tcol ? pr - 1.0f : pr) * coef;
+                                y[e] = coef != 0.0f && n0 + col < p.N ? d : 0.0f;
+                            } else {
+                                y[e] = z * factor;
+                            }
+                        }
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[0], y[1]);
+                        h[j] = *reinterpret_cast<const uint32_t *>(&b2);
+                    }
+                    if (lane == 0)
+                        ptx::bulk_wait_group_read<0>(); // the previous box has left the staging area
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        ptx::st_shared_v4(stage_row + (uint32_t)((j ^ (lane & 7)) << 4), h[4 * j], h[4 * j + 1],
+                                          h[4 * j + 2], h[4 * j + 3]);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::tma_store_3d(&tmO, ptx::smem_addr(stage), x0, row0, 0);
+                        ptx::bulk_commit_group();
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) { // 32 FP32 columns: 128 bytes a row
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(acc + 32u * g, v);
+                    ptx::tmem_ld_wait_tie(v);
+                    if (g == 3)
+                        release();
+                    const int x0 = n0 + 32 * g;
+                    if (x0 >= p.N || row0 >= p.M)
+                        continue;
+                    if (MODE == kGradW32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __float_as_uint(__uint_as_float(v[j]) * factor);
+                    }
+                    if (lane == 0)
+                        ptx::bulk_wait_group_read<0>();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        ptx::st_shared_v4(stage_row + (uint32_t)((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1],
+                                          v[4 * j + 2], v[4 * j + 3]);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (p.add)
+                            ptx::tma_add_3d(&tmO, ptx::smem_addr(stage), x0, row0, ks);
+                        else
+                            ptx::tma_store_3d(&tmO, ptx::smem_addr(stage), x0, row0, ks);
+                        ptx::bulk_commit_group();
+                    }
+                }
+            }
+            ++tc;
+        }
+        if (C::kStaging && lane == 0)
+            ptx::bulk_wait_group0();
+        __syncwarp();
+    }
+
+    ptx::tc_fence_before();
+    if (CG == 2)
+        ptx::cluster_sync(); // the peer's MMAs and loads that name this CTA's memory are done
+    else
+        __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_cg<CG>(tmem_base, 512);
+    }
+}
+
+// Joins the (maximum, sum) pairs of a row and its target's logit.  blockDim =
+// (rows, lanes): threadIdx.x walks rows (contiguous in part), threadIdx.y parts.
+__global__ void k_ce_join(const float2 *part, const float *zt, const int64_t *target, int64_t n, int64_t v, int parts,
+                          float k2, float *loss, float *lse)
+{
+    extern __shared__ float2 red[];
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    float m = -INFINITY, s = 0.0f;
+    if (row < n)
+        for (int q = threadIdx.y; q < parts; q += blockDim.y) {
+            const float2 a = part[(int64_t)q * n + row];
+            const float nm = fmaxf(m, a.x);
+            if (nm > -INFINITY) {
+                s = s * ex2(m - nm) + a.y * ex2(a.x - nm);
+                m = nm;
+            }
+        }
+    red[threadIdx.y * blockDim.x + threadIdx.x] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.y != 0 || row >= n)
+        return;
+    for (int q = 1; q < (int)blockDim.y; ++q) {
+        const float2 a = red[q * blockDim.x + threadIdx.x];
+        const float nm = fmaxf(m, a.x);
+        if (nm > -INFINITY) {
+            s = s * ex2(m - nm) + a.y * ex2(a.x - nm);
+            m = nm;
+        }
+    }
+    const int64_t tg = target[row];
+    if (tg < 0 || tg >= v) {
+        lse[row] = kLn2 * (m + log2f(s));
+        loss[row] = 0.0f;
+        return;
+    }
+    const float t2 = zt[row] * k2;
+    lse[row] = kLn2 * (m + log2f(s + ex2(t2 - m)));
+    loss[row] = t2 >= m ? log1pf(s) : kLn2 * (m - t2) + logf(s + ex2(t2 - m));
+}
+
+// gmax = max |dloss| over the rows with a target (1 where that is not finite).
+__global__ void k_ce_gmax(const float *dloss, const int64_t *target, int64_t n, int64_t v, float *gmax)
+{
+    __shared__ float red[32];
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    float m = 0.0f;
+    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
+        const int64_t tg = target[i];
+        if (tg >= 0 && tg < v)
+            m = fmaxf(m, fabsf(dloss[i]));
+    }
+    for (int o = 16; o; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        m = threadIdx.x < blockDim.x / 32 ? red[threadIdx.x] : 0.0f;
+        for (int o = 16; o; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        if (threadIdx.x == 0)
+            *gmax = m < INFINITY ? m : 1.0f;
+    }
+}
+
+// dx = BF16(scale * gmax * sum of the slabs), four columns a thread.
+__global__ void k_ce_dx(const float *slab, int slabs, int64_t n, int64_t c, const float *gmax, float scale,
+                        uint16_t *dx, int64_t lddx)
+{
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const float f = __ldg(gmax) * scale;
+    const int64_t c4 = c / 4, total = n * c4;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const float4 *s = reinterpret_cast<const float4 *>(slab) + i;
+        float4 a = *s;
+        for (int q = 1; q < slabs; ++q) {
+            const float4 b = s[q * total];
+            a.x += b.x;
+            a.y += b.y;
+            a.z += b.z;
+            a.w += b.w;
+        }
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * f, a.y * f), hi = __floats2bfloat162_rn(a.z * f, a.w * f);
+        const int64_t r = i / c4, col = 4 * (i - r * c4);
+        *reinterpret_cast<uint2 *>(dx + r * lddx + col) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    }
+}
+
+#ifndef JETQ_HEAD_CG
+#define JETQ_HEAD_CG 1
+#endif
+constexpr int kCg = JETQ_HEAD_CG;
+
+template <int MODE>
+cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, HeadParams p, cudaStream_t st)
+{
+    using C = HeadCfg<kCg, MODE>;
+    auto kern = k_head_gemm<kCg, MODE>;
+    static int configured_device = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (configured_device != dev) {
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem)) != cudaSuccess)
+            return e;
+        configured_device = dev;
+    }
+    p.limit_ns = kWaitLimitNs;
+    const int64_t tiles = (int64_t)p.mt * p.nt * p.splits;
+    const int units = (int)(tiles < sm_count() / kCg ? tiles : sm_count() / kCg);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * kCg));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCg;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kCg == 2 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, b, o, p);
+}
+
+constexpr int kTileM = 128 * kCg, kTileN = 256;
+
+int64_t ceil_div(int64_t a, int64_t b)
+{
+    return (a + b - 1) / b;
+}
+
+// K splits of the dx product: enough work units to fill the machine evenly.
+int dx_splits(int64_t n, int64_t c, int64_t piece)
+{
+    const int64_t tiles = ceil_div(n, kTileM) * ceil_div(c, kTileN), units = sm_count() / kCg;
+    const int64_t most = piece / 64 < 16 ? piece / 64 : 16;
+    int best = 1;
+    double cost = 1e30;
+    for (int64_t s = 1; s <= most; ++s) {
+        // waves of units, each 1/s of a tile's K, plus the slabs' traffic
+        const double t = (double)ceil_div(tiles * s, units) / (double)s + 0.02 * (double)s;
+        if (t < cost - 1e-9) {
+            cost = t;
+            best = (int)s;
+        }
+    }
+    return best;
+}
+
+struct BwdPlan {
+    int64_t piece; // vocabulary rows a piece (a multiple of 256)
+    int splits;
+    size_t slab_off, d_off, total;
+};
+
+BwdPlan bwd_plan(int64_t n, int64_t v, int64_t c, int64_t piece)
+{
+    BwdPlan b;
+    const int64_t all = ceil_div(v, 256) * 256;
+    b.piece = piece < 256 ? 256 : (piece > all ? all : piece / 256 * 256);
+    b.splits = dx_splits(n, c, b.piece);
+    b.slab_off = 256; // gmax first
+    const size_t slabs = (size_t)b.splits * (size_t)n * (size_t)c * 4;
+    b.d_off = (b.slab_off + slabs + 1023) / 1024 * 1024;
+    b.total = b.d_off + (size_t)n * (size_t)b.piece * 2;
+    return b;
+}
+
+// A piece's d is about 256 MB: few pieces (each adds to dx once), little memory.
+int64_t preferred_piece(int64_t n)
+{
+    return ((int64_t)1 << 27) / (n > 0 ? n : 1);
+}
+
+} // namespace
+
+size_t linear_ce_fwd_workspace(int64_t n, int64_t v)
+{
+    return (size_t)(2 * ceil_div(v, kTileN)) * (size_t)n * 8 + (size_t)n * 4;
+}
+
+size_t linear_ce_bwd_workspace(int64_t n, int64_t v, int64_t c)
+{
+    return bwd_plan(n, v, c, preferred_piece(n)).total;
+}
+
+size_t linear_ce_bwd_workspace_min(int64_t n, int64_t v, int64_t c)
+{
+    return bwd_plan(n, v, c, 256).total;
+}
+
+cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
+{
+    CUtensorMap ta, tb;
+    cudaError_t e;
+    if ((e = make_sw128_map(&ta, a.x, false, a.c, a.n, a.ldx, 128)) != cudaSuccess ||
+        (e = make_sw128_map(&tb, a.w, false, a.c, a.v, a.ldw, kTileN / kCg)) != cudaSuccess)
+        return e;
+    HeadParams p = {};
+    p.mt = (int)ceil_div(a.n, kTileM);
+    p.nt = (int)ceil_div(a.v, kTileN);
+    p.splits = 1;
+    p.num_kb = (int)ceil_div(a.c, 64);
+    p.group = p.mt < 32 ? p.mt : 32; // the group's x stays in L2 while w streams through once
+    p.M = a.n;
+    p.N = a.v;
+    p.k2 = a.scale * kLog2e;
+    p.target = a.target;
+    p.V = a.v;
+    p.part = static_cast<float2 *>(a.ws);
+    p.zt = reinterpret_cast<float *>(p.part + (size_t)2 * p.nt * a.n);
+    if ((e = run_head<kStats>(ta, tb, ta, p, st)) != cudaSuccess)
+        return e;
+    int rx = 1;
+    while (rx < 32 && rx < a.n)
+        rx *= 2;
+    return launch_pdl(k_ce_join, dim3((unsigned)ceil_div(a.n, rx)), dim3(rx, 256 / rx), 256 * sizeof(float2), st,
+                      (const float2 *)p.part, (const float *)p.zt, a.target, a.n, a.v, 2 * p.nt, p.k2, a.loss, a.lse);
+}
+
+cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
+{
+    // the largest piece that the workspace holds, up to the preferred one
+    int64_t piece = preferred_piece(a.n);
+    BwdPlan plan = bwd_plan(a.n, a.v, a.c, piece);
+    while (plan.total > a.ws_bytes && plan.piece > 256)
+        plan = bwd_plan(a.n, a.v, a.c, plan.piece / 2);
+    if (plan.total > a.ws_bytes)
+        return cudaErrorInvalidValue;
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    float *gmax = reinterpret_cast<float *>(ws), *slab = reinterpret_cast<float *>(ws + plan.slab_off);
+    uint16_t *d = reinterpret_cast<uint16_t *>(ws + plan.d_off);
+    cudaError_t e = launch_pdl(k_ce_gmax, dim3(1), dim3(1024), 0, st, a.dloss, a.target, a.n, a.v, gmax);
+    if (e != cudaSuccess)
+        return e;
+    const int dw_esize = a.dw_dtype == JETQ_OUT_BF16 ? 2 : 4;
+    for (int64_t v0 = 0; v0 < a.v; v0 += plan.piece) {
+        const int64_t rows = a.v - v0 < plan.piece ? a.v - v0 : plan.piece; // vocabulary rows of this piece
+        const int64_t cols = ceil_div(rows, 256) * 256;                     // columns of d, zero past rows
+        const uint16_t *w = a.w + v0 * a.ldw;
+        CUtensorMap xk, wk, dst, dk, wn, slabs, dm, xn, dw;
+        if ((e = make_sw128_map(&xk, a.x, false, a.c, a.n, a.ldx, 128)) != cudaSuccess ||
+            (e = make_sw128_map(&wk, w, false, a.c, rows, a.ldw, kTileN / kCg)) != cudaSuccess ||
+            (e = make_sw128_map(&dst, d, false, cols, a.n, plan.piece, 32, 1, plan.piece * a.n)) != cudaSuccess ||
+            (e = make_sw128_map(&dk, d, false, cols, a.n, plan.piece, 128)) != cudaSuccess ||
+            (e = make_sw128_map(&wn, w, false, a.c, rows, a.ldw, 64)) != cudaSuccess ||
+            (e = make_sw128_map(&slabs, slab, true, a.c, a.n, a.c, 32, plan.splits, a.n * a.c)) != cudaSuccess ||
+            (e = make_sw128_map(&dm, d, false, cols, a.n, plan.piece, 64)) != cudaSuccess ||
+            (e = make_sw128_map(&xn, a.x, false, a.c, a.n, a.ldx, 64)) != cudaSuccess ||
+            (e = make_sw128_map(&dw, static_cast<uint8_t *>(a.dw) + v0 * a.lddw * dw_esize, dw_esize == 4, a.c, rows,
+                                a.lddw, 32, 1, rows * a.lddw)) != cudaSuccess)
+            return e;
+        HeadParams p = {};
+        p.gmax = gmax;
+        p.scale = a.scale;
+        // d of the piece
+        p.mt = (int)ceil_div(a.n, kTileM);
+        p.nt = (int)ceil_div(rows, kTileN);
+        p.splits = 1;
+        p.num_kb = (int)ceil_div(a.c, 64);
+        p.group = p.mt < 32 ? p.mt : 32;
+        p.M = a.n;
+        p.N = rows;
+        p.k2 = a.scale * kLog2e;
+        p.target = a.target;
+        p.V = a.v;
+        p.col0 = v0;
+        p.lse = a.lse;
+        p.dloss = a.dloss;
+        if ((e = run_head<kGrad>(xk, wk, dst, p, st)) != cudaSuccess)
+            return e;
+        // dx += d w
+        p.nt = (int)ceil_div(a.c, kTileN);
+        p.splits = plan.splits;
+        p.num_kb = (int)(cols / 64);
+        p.N = a.c;
+        p.add = v0 > 0;
+        if ((e = run_head<kGradX>(dk, wn, slabs, p, st)) != cudaSuccess)
+            return e;
+        // dw = d^T x: few vocabulary tiles at a time against all of x
+        p.mt = (int)ceil_div(rows, kTileM);
+        p.group = 4;
+        p.splits = 1;
+        p.num_kb = (int)ceil_div(a.n, 64);
+        p.M = rows;
+        p.add = a.accumulate;
+        e = dw_esize == 2 ? run_head<kGradW16>(dm, xn, dw, p, st) : run_head<kGradW32>(dm, xn, dw, p, st);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const int64_t blocks = ceil_div(a.n * (a.c / 4), 256), cap = (int64_t)sm_count() * 8;
+    return launch_pdl(k_ce_dx, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, st, (const float *)slab,
+                      plan.splits, a.n, a.c, (const float *)gmax, a.scale, a.dx, a.lddx);
+}
+
+cudaError_t linear_ce_read_and_clear_error(cudaStream_t st, unsigned *out)
+{
+    unsigned v = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_linear_ce_error, sizeof v, 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess)
+        return e;
+    *out |= v;
+    if (v) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbolAsync(g_linear_ce_error, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
+        if (e == cudaSuccess)
+            e = cudaStreamSynchronize(st);
+    }
+    return e;
+}
+
+} // namespace jetq

@@ -1,0 +1,217 @@
+"""Softmax cross entropy of a linear head against its definition in binary64.
+
+Bounds.  A logit's FP32 sum is within SUM * sum |x w| of the exact one (SUM =
+1e-5, the bound every GEMM test of this library uses); the loss and lse follow
+from two logits, plus FP32 rounding of values of lse's size.  d is rounded to
+BF16 (2^-8 of its value), its sums again within SUM of the sum of magnitudes,
+an exponential moves by the error of its exponent, and a BF16 result is
+rounded once more (2^-8 of its value).
+"""
+import pytest
+import torch
+
+import rollout_x128_act_gb300 as jq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+SUM = 1e-5
+HALF_BF16, HALF_F32 = 2.0 ** -8, 2.0 ** -24
+
+SIZES = [(1, 1, 8), (1, 1000, 64), (2, 255, 8), (5, 257, 72), (127, 256, 64), (129, 511, 264), (256, 513, 128),
+         (300, 1000, 520), (257, 4097, 1032), (513, 300, 2048)]
+
+
+def _inputs(n, v, c, seed, pad=0, ignored=True):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn((n, c + pad), generator=g, device=DEV).to(torch.bfloat16)[:, :c]
+    w = (torch.randn((v, c + pad), generator=g, device=DEV) * 0.3).to(torch.bfloat16)[:, :c]
+    target = torch.randint(0, v, (n,), generator=g, device=DEV)
+    if ignored and n > 2:
+        target[1::4] = -100
+        target[2::8] = v  # outside the vocabulary on the other side
+    dloss = torch.randn(n, generator=g, device=DEV)
+    return x, w, target, dloss
+
+
+def _define(x, w, target, scale):
+    """(z, lse, loss, bound of a logit's error) in binary64."""
+    z = scale * (x.double() @ w.double().T)
+    lse = torch.logsumexp(z, 1)
+    ok = (target >= 0) & (target < w.shape[0])
+    zt = z.gather(1, target.clamp(0, w.shape[0] - 1)[:, None])[:, 0]
+    loss = torch.where(ok, lse - zt, torch.zeros_like(lse))
+    ez = scale * SUM * (x.double().abs() @ w.double().abs().T).amax(1)
+    return z, lse, loss, ok, ez
+
+
+def _d(z, lse, target, ok, dloss):
+    p = torch.exp(z - lse[:, None])
+    coef = torch.where(ok, dloss.double(), torch.zeros_like(lse))
+    d = p * coef[:, None]
+    row = torch.arange(z.shape[0], device=z.device)[ok]
+    d[row, target[ok]] -= coef[ok]
+    return p * coef.abs()[:, None], d
+
+
+def _check_fwd(x, w, target, scale):
+    loss, lse = jq.linear_ce(x, w, target, scale=scale)
+    assert jq.jetq_check_device_error() == jq.OK
+    _, rlse, rloss, ok, ez = _define(x, w, target, scale)
+    tol = 2 * ez + 8 * HALF_F32 * (rlse.abs() + rloss.abs() + 1)
+    assert bool(((lse.double() - rlse).abs() <= tol).all())
+    assert bool(((loss.double() - rloss).abs() <= tol).all())
+    assert bool((loss[~ok] == 0).all())
+    return lse
+
+
+def _bounds(x, w, target, scale, dloss, lse):
+    """dx, dw in binary64 and what the kernels may be off by before their last rounding."""
+    z, _, _, ok, ez = _define(x, w, target, scale)
+    pg, d = _d(z, lse.double(), target, ok, dloss)
+    moved = ez[:, None] + 8 * HALF_F32 * (1 + lse.double().abs()[:, None])  # of the exponent
+    off = d.abs() * (HALF_BF16 + SUM) + pg * 2 * moved
+    X, W = x.double(), w.double()
+    return (scale * (d @ W), scale * (off @ W.abs())), (scale * (d.T @ X), scale * (off.T @ X.abs()))
+
+
+def _check_bwd(x, w, target, scale, dloss, lse, dw_dtype, workspace=None):
+    dx, dw = jq.linear_ce_bwd(x, w, target, lse, dloss, scale=scale, dw_dtype=dw_dtype, workspace=workspace)
+    assert jq.jetq_check_device_error() == jq.OK
+    assert dx.dtype == torch.bfloat16 and dw.dtype == dw_dtype
+    (rx, tx), (rw, tw) = _bounds(x, w, target, scale, dloss, lse)
+    last = HALF_BF16 if dw_dtype == torch.bfloat16 else HALF_F32
+    assert bool(((dx.double() - rx).abs() <= tx * 1.01 + HALF_BF16 * rx.abs() + 1e-30).all())
+    assert bool(((dw.double() - rw).abs() <= tw * 1.01 + last * rw.abs() + 1e-30).all())
+    return dx, dw
+
+
+@pytest.mark.parametrize("n,v,c", SIZES)
+@pytest.mark.parametrize("scale", [1.0, 1.7])
+def test_forward(n, v, c, scale):
+    x, w, target, _ = _inputs(n, v, c, seed=n + v + c, pad=8 * (n % 3))
+    _check_fwd(x, w, target, scale)
+
+
+@pytest.mark.parametrize("n,v,c", SIZES)
+@pytest.mark.parametrize("dw_dtype", [torch.float32, torch.bfloat16])
+def test_backward(n, v, c, dw_dtype):
+    x, w, target, dloss = _inputs(n, v, c, seed=n + v + c + 1, pad=8 * (n % 3))
+    lse = _check_fwd(x, w, target, 0.8)
+    _check_bwd(x, w, target, 0.8, dloss, lse, dw_dtype)
+
+
+def test_backward_in_small_pieces():
+    """The smallest workspace (256 vocabulary rows a piece) and one in between give the same gradient."""
+    x, w, target, dloss = _inputs(200, 3000, 136, seed=5)
+    _, lse = jq.linear_ce(x, w, target)
+    small = jq.jetq_linear_ce_bwd_workspace_bytes(200, 3000, 136, True)
+    large = jq.jetq_linear_ce_bwd_workspace_bytes(200, 3000, 136)
+    assert small < large
+    for size in (small, (small + large) // 2, large):
+        _check_bwd(x, w, target, 1.0, dloss, lse, torch.float32, torch.empty(size, dtype=torch.uint8, device=DEV))
+
+
+def test_rows_without_a_loss():
+    x, w, target, dloss = _inputs(70, 300, 64, seed=6, ignored=False)
+    target[:] = -100
+    loss, lse = jq.linear_ce(x, w, target)
+    assert bool((loss == 0).all()) and bool(torch.isfinite(lse).all())
+    dx, dw = jq.linear_ce_bwd(x, w, target, lse, dloss)
+    assert bool((dx == 0).all()) and bool((dw == 0).all())
+    target[3] = 7  # an infinite or NaN weight of an ignored row is not looked at
+    bad = dloss.clone()
+    bad[5], bad[6] = float("inf"), float("nan")
+    dx, dw = jq.linear_ce_bwd(x, w, target, lse, bad)
+    dx1, dw1 = jq.linear_ce_bwd(x, w, target, lse, dloss)
+    assert torch.equal(dx, dx1) and torch.equal(dw, dw1)
+    assert bool((dx[[i for i in range(70) if i != 3]] == 0).all()) and bool((dx[3] != 0).any())
+
+
+def test_confident_token_keeps_its_relative_precision():
+    """One logit far above the others: loss = sum of the others over it, far below FP32's step at lse."""
+    v, c = 512, 8
+    w = torch.zeros((v, c), dtype=torch.bfloat16, device=DEV)
+    w[5, 0] = 1.0
+    x = torch.zeros((1, c), dtype=torch.bfloat16, device=DEV)
+    x[0, 0] = 30.0
+    loss, lse = jq.linear_ce(x, w, torch.tensor([5], device=DEV))
+    want = torch.log1p((v - 1) * torch.exp(torch.tensor(-30.0, dtype=torch.float64))).item()
+    assert abs(loss.item() - want) <= 16 * 30 * HALF_F32 * want
+    assert abs(lse.item() - 30.0) <= 8 * 30 * HALF_F32
+
+
+def test_large_logits_and_nan():
+    x, w, target, _ = _inputs(64, 700, 64, seed=8, ignored=False)
+    _check_fwd((x.float() * 64).to(torch.bfloat16), w, target, 4.0)  # exponents far outside FP32's range
+    x[9, 3] = float("nan")
+    loss, lse = jq.linear_ce(x, w, target)
+    bad = torch.isnan(loss)
+    assert bool(bad[9]) and int(bad.sum()) == 1 and bool(torch.isnan(lse[9]))
+
+
+def test_accumulate_into_dw():
+    x, w, target, dloss = _inputs(150, 400, 72, seed=9)
+    _, lse = jq.linear_ce(x, w, target)
+    _, dw = jq.linear_ce_bwd(x, w, target, lse, dloss)
+    base = torch.randn((400, 76), device=DEV)
+    acc = base.clone()[:, :72]
+    jq.linear_ce_bwd(x, w, target, lse, dloss, dw=acc, accumulate=True)
+    want = base[:, :72].double() + dw.double()
+    assert bool(((acc.double() - want).abs() <= HALF_F32 * want.abs() + 1e-30).all())
+
+
+def test_gradient_against_differences():
+    """The kernels' gradient along a direction is the loss's central difference in binary64."""
+    x, w, target, dloss = _inputs(40, 600, 64, seed=10)
+    scale = 0.9
+    _, lse = jq.linear_ce(x, w, target, scale=scale)
+    dx, dw = jq.linear_ce_bwd(x, w, target, lse, dloss, scale=scale)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    ux = torch.randn(x.shape, generator=g, device=DEV, dtype=torch.float64)
+    uw = torch.randn(w.shape, generator=g, device=DEV, dtype=torch.float64)
+    ok = (target >= 0) & (target < 600)
+
+    def total(h):
+        z = scale * ((x.double() + h * ux) @ (w.double() + h * uw).T)
+        loss = torch.logsumexp(z, 1) - z.gather(1, target.clamp(0, 599)[:, None])[:, 0]
+        return (loss * dloss.double())[ok].sum()
+
+    h = 1e-5
+    slope = (total(h) - total(-h)) / (2 * h)
+    (rx, tx), (rw, tw) = _bounds(x, w, target, scale, dloss, lse)
+    got = (dx.double() * ux).sum() + (dw.double() * uw).sum()
+    tol = ((tx * 1.01 + HALF_BF16 * rx.abs()) * ux.abs()).sum() + ((tw * 1.01 + HALF_F32 * rw.abs()) * uw.abs()).sum()
+    third = 1e-6 * (1 + slope.abs())  # the difference's own error
+    assert abs(got - slope) <= tol + third
+
+
+def test_repeatable_streams_and_graph():
+    x, w, target, dloss = _inputs(333, 2000, 264, seed=11)
+    loss, lse = jq.linear_ce(x, w, target)
+    dx, dw = jq.linear_ce_bwd(x, w, target, lse, dloss)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        loss1, lse1 = jq.linear_ce(x, w, target)
+        dx1, dw1 = jq.linear_ce_bwd(x, w, target, lse1, dloss)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(loss, loss1) and torch.equal(lse, lse1) and torch.equal(dx, dx1) and torch.equal(dw, dw1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss2, lse2 = jq.linear_ce(x, w, target)
+        dx2, dw2 = jq.linear_ce_bwd(x, w, target, lse2, dloss)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(loss, loss2) and torch.equal(lse, lse2) and torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+def test_no_tokens():
+    w = torch.randn((300, 64), device=DEV).to(torch.bfloat16)
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
+    target = torch.empty(0, dtype=torch.int64, device=DEV)
+    loss, lse = jq.linear_ce(x, w, target)
+    assert loss.shape == lse.shape == (0,)
+    dw = torch.ones((300, 64), device=DEV)
+    dx, dw = jq.linear_ce_bwd(x, w, target, lse, loss, dw=dw)
+    assert dx.shape == (0, 64) and bool((dw == 0).all())
