@@ -559,6 +559,48 @@ JETQ_API jetq_status jetq_gemm_nvfp4(const uint8_t *qa, const uint8_t *sfa, cons
                                      void *out, jetq_out_dtype out_dtype, int64_t ldo, void *stream);
 
 /* ======================================================================== */
+/* Layer norm and RMS norm                                                  */
+/* ======================================================================== */
+/*
+ * Rows of BF16 or FP32 (the dtype of x, w, b, y and the gradients dx, dy),
+ * FP32 arithmetic, each output rounded once:
+ *   mean = sum(x) / c (LAYER; 0 for RMS), rstd = 1 / sqrt(sum (x - mean)^2 / c + eps)
+ *   y = (x - mean) * rstd * w + b
+ *
+ *   x, n, c, ldx   [n x c], row stride ldx (16-byte aligned rows); any c from 1 to 2^20
+ *   w, b           [c], NULL for 1 and 0; b only with LAYER
+ *   eps            in [0, 1]
+ *   y, ldy         [n x c], 16-byte aligned rows; may be x itself (same stride)
+ *   mean, rstd     float [n], kept for the backward pass (mean: LAYER only)
+ * n == 0 is a no-op.
+ */
+typedef enum {
+    JETQ_NORM_LAYER = 0,
+    JETQ_NORM_RMS = 1
+} jetq_norm_kind;
+JETQ_API jetq_status jetq_norm_fwd(jetq_norm_kind kind, jetq_out_dtype dtype, const void *x, int64_t n, int64_t c,
+                                   int64_t ldx, const void *w, const void *b, float eps, void *y, int64_t ldy,
+                                   float *mean, float *rstd, void *stream);
+
+/*
+ * Backward pass, also of jetq_quant_act_1x128_rmsnorm's norm (its rstd):
+ *   h = (x - mean) * rstd,  t = dy * w
+ *   dx = rstd * (t - sum(t) / c - h * sum(t * h) / c)    (RMS: without sum(t))
+ *   dw = sum over rows of dy * h,  db = sum over rows of dy   (FP32 [c]; db nullable, LAYER only)
+ *
+ *   dy, lddy, dx, lddx   [n x c], 16-byte aligned rows; dx may be dy or x (same stride)
+ *   workspace            device memory, 16-byte aligned, at least
+ *                        jetq_norm_bwd_workspace_bytes(dtype, n, c) bytes (partial sums of dw and
+ *                        db); calls that share one must not overlap on the GPU
+ * Bitwise repeatable (no atomics).  n == 0: dw and db are set to zero.
+ */
+JETQ_API size_t jetq_norm_bwd_workspace_bytes(jetq_out_dtype dtype, int64_t n, int64_t c);
+JETQ_API jetq_status jetq_norm_bwd(jetq_norm_kind kind, jetq_out_dtype dtype, const void *dy, int64_t lddy,
+                                   const void *x, int64_t n, int64_t c, int64_t ldx, const void *w,
+                                   const float *mean, const float *rstd, void *dx, int64_t lddx,
+                                   float *dw, float *db, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ======================================================================== */
 /* The head: softmax cross entropy over the vocabulary                      */
 /* ======================================================================== */
 /*

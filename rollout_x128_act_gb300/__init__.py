@@ -26,6 +26,7 @@ RECIPE_BLOCK128, RECIPE_MXFP8, RECIPE_BLOCK128_POW2 = 0, 1, 2
 PATH_AUTO, PATH_TRAIN, PATH_DECODE = 0, 1, 2
 GEMM_FPROP, GEMM_DGRAD, GEMM_WGRAD = 0, 1, 2
 OUT_F32, OUT_BF16 = 0, 1
+NORM_LAYER, NORM_RMS = 0, 1
 
 _lock = threading.Lock()
 _lib = None
@@ -77,6 +78,10 @@ def lib() -> ctypes.CDLL:
             "jetq_nvfp4_atom_bytes": (I64, [I64, I64]),
             "jetq_nvfp4_scale_atoms": (I32, [P, I64, I64, P, P]),
             "jetq_gemm_nvfp4": (I32, [P, P, P, I32, P, P, P, I64, I64, I64, P, I32, I64, P]),
+            "jetq_norm_fwd": (I32, [I32, I32, P, I64, I64, I64, P, P, F32, P, I64, P, P, P]),
+            "jetq_norm_bwd_workspace_bytes": (ctypes.c_size_t, [I32, I64, I64]),
+            "jetq_norm_bwd": (I32, [I32, I32, P, I64, P, I64, I64, I64, P, P, P, P, I64, P, P, P, ctypes.c_size_t,
+                                    P]),
             "jetq_linear_ce_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
             "jetq_linear_ce_fwd": (I32, [P, I64, I64, I64, P, I64, I64, P, F32, P, P, P, ctypes.c_size_t, P]),
             "jetq_linear_ce_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I32]),
@@ -288,6 +293,23 @@ def jetq_gemm_grouped(kind, recipe, a, sa, b, sb, m, n, k, ldk, seg_offsets, num
     _check(lib().jetq_gemm_grouped(kind, recipe, _p(a), _p(sa), _p(b), _p(sb), m, n, k, ldk, _p(seg_offsets),
                                    num_experts, _p(out), _out_dtype(out), out.stride(-2), 1 if accumulate else 0,
                                    _s(stream)), "jetq_gemm_grouped")
+
+
+def jetq_norm_fwd(kind, x, w, b, eps, y, mean, rstd, stream=None):
+    n, c = x.shape
+    _check(lib().jetq_norm_fwd(kind, _out_dtype(x), _p(x), n, c, x.stride(0), _p(w), _p(b), eps, _p(y), y.stride(0),
+                               _p(mean), _p(rstd), _s(stream)), "jetq_norm_fwd")
+
+
+def jetq_norm_bwd_workspace_bytes(dtype: int, n: int, c: int) -> int:
+    return int(lib().jetq_norm_bwd_workspace_bytes(dtype, n, c))
+
+
+def jetq_norm_bwd(kind, dy, x, w, mean, rstd, dx, dw, db, ws, stream=None):
+    n, c = x.shape
+    _check(lib().jetq_norm_bwd(kind, _out_dtype(x), _p(dy), dy.stride(0), _p(x), n, c, x.stride(0), _p(w), _p(mean),
+                               _p(rstd), _p(dx), dx.stride(0), _p(dw), _p(db), _p(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), _s(stream)), "jetq_norm_bwd")
 
 
 def jetq_linear_ce_workspace_bytes(n: int, v: int) -> int:
@@ -536,6 +558,54 @@ def grouped(kind, a, sa, b, sb, seg_offsets, n, k, out_dtype=torch.float32, reci
             out = torch.empty((m, n), dtype=out_dtype, device=a.device)
     jetq_gemm_grouped(kind, recipe, a, sa, b, sb, m, n, k, ldk, seg_offsets, E, out, accumulate, stream)
     return out
+
+
+_NORM_DTYPES = (torch.bfloat16, torch.float32)
+
+
+def _norm_rows(x):
+    """An uninitialized tensor like x whose rows are 16-byte aligned."""
+    n, c = x.shape
+    step = 8 if x.dtype == torch.bfloat16 else 4
+    ld = (c + step - 1) // step * step
+    t = torch.empty((n, ld), dtype=x.dtype, device=x.device)
+    return t if ld == c else t[:, :c]
+
+
+def norm_fwd(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, stream=None):
+    """Layer norm or RMS norm of BF16 or FP32 rows x [n x c] (see jetq_norm_fwd) ->
+    (y, mean [n] (None for RMS), rstd [n])."""
+    _want(x, "x", _NORM_DTYPES, rows=True)
+    n, c = x.shape
+    if w is not None:
+        _want(w, "w", x.dtype, (c,))
+    if b is not None:
+        _want(b, "b", x.dtype, (c,))
+    y = _norm_rows(x)
+    rstd = torch.empty(n, dtype=torch.float32, device=x.device)
+    mean = torch.empty(n, dtype=torch.float32, device=x.device) if kind == NORM_LAYER else None
+    jetq_norm_fwd(kind, x, w, b, eps, y, mean, rstd, stream)
+    return y, mean, rstd
+
+
+def norm_bwd(dy, x, w, mean, rstd, kind=NORM_LAYER, bias=False, workspace=None, stream=None):
+    """Backward pass of norm_fwd (see jetq_norm_bwd) -> (dx, dw FP32 [c], db FP32 [c] or None)."""
+    _want(x, "x", _NORM_DTYPES, rows=True)
+    n, c = x.shape
+    _want(dy, "dy", x.dtype, (n, c), rows=True)
+    if w is not None:
+        _want(w, "w", x.dtype, (c,))
+    _want(rstd, "rstd", torch.float32, (n,))
+    if kind == NORM_LAYER:
+        _want(mean, "mean", torch.float32, (n,))
+    dx = _norm_rows(x)
+    dw = torch.empty(c, dtype=torch.float32, device=x.device)
+    db = torch.empty(c, dtype=torch.float32, device=x.device) if bias else None
+    if workspace is None:
+        workspace = torch.empty(jetq_norm_bwd_workspace_bytes(_out_dtype(x), n, c), dtype=torch.uint8,
+                                device=x.device)
+    jetq_norm_bwd(kind, dy, x, w, mean if kind == NORM_LAYER else None, rstd, dx, dw, db, workspace, stream)
+    return dx, dw, db
 
 
 def _check_head(x, w, target):

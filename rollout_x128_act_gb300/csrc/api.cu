@@ -163,7 +163,8 @@ jetq_status jetq_check_device_error(void *stream)
     unsigned word = 0;
     if (gemm_read_and_clear_error(st, &word) != cudaSuccess || gemm_mx_read_and_clear_error(st, &word) != cudaSuccess ||
         gemm_decode_read_and_clear_error(st, &word) != cudaSuccess || quant_read_and_clear_error(st, &word) != cudaSuccess ||
-        gemm_nvfp4_read_and_clear_error(st, &word) != cudaSuccess || linear_ce_read_and_clear_error(st, &word) != cudaSuccess)
+        gemm_nvfp4_read_and_clear_error(st, &word) != cudaSuccess || linear_ce_read_and_clear_error(st, &word) != cudaSuccess ||
+        norm_read_and_clear_error(st, &word) != cudaSuccess)
         return JETQ_ERR_CUDA;
     return word ? JETQ_ERR_TIMEOUT : JETQ_OK;
 }
@@ -734,6 +735,128 @@ jetq_status jetq_linear_ce_bwd(const uint16_t *x, int64_t n, int64_t c, int64_t 
     g.ws = workspace;
     g.ws_bytes = workspace_bytes;
     return from_cuda(launch_linear_ce_bwd(g, st));
+}
+
+namespace {
+
+// arguments that both directions of the norms share
+jetq_status check_norm(jetq_norm_kind kind, jetq_out_dtype dtype, const void *x, int64_t n, int64_t c, int64_t ldx,
+                       const void *w)
+{
+    JQ_REQUIRE(kind == JETQ_NORM_LAYER || kind == JETQ_NORM_RMS, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(dtype == JETQ_OUT_F32 || dtype == JETQ_OUT_BF16, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(n >= 0 && c > 0, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(c <= (1 << 20) && ldx >= c, JETQ_ERR_UNSUPPORTED_SHAPE);
+    JQ_REQUIRE(n == 0 || x != nullptr, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(aligned16(x) && ldx % (dtype == JETQ_OUT_F32 ? 4 : 8) == 0 &&
+                   (reinterpret_cast<uintptr_t>(w) & (dtype == JETQ_OUT_F32 ? 3u : 1u)) == 0,
+               JETQ_ERR_MISALIGNED);
+    return JETQ_OK;
+}
+
+bool aligned4(const void *p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
+} // namespace
+
+jetq_status jetq_norm_fwd(jetq_norm_kind kind, jetq_out_dtype dtype, const void *x, int64_t n, int64_t c, int64_t ldx,
+                          const void *w, const void *b, float eps, void *y, int64_t ldy, float *mean, float *rstd,
+                          void *stream)
+{
+    const jetq_status s = check_norm(kind, dtype, x, n, c, ldx, w);
+    if (s != JETQ_OK)
+        return s;
+    JQ_REQUIRE(eps >= 0.0f && eps <= 1.0f, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(kind == JETQ_NORM_LAYER || b == nullptr, JETQ_ERR_INVALID_ARG);
+    if (n == 0)
+        return JETQ_OK;
+    const jetq_status o = check_out(y, dtype, ldy, c);
+    if (o != JETQ_OK)
+        return o;
+    JQ_REQUIRE(rstd != nullptr && (kind == JETQ_NORM_RMS || mean != nullptr), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(aligned4(rstd) && aligned4(mean) &&
+                   (reinterpret_cast<uintptr_t>(b) & (dtype == JETQ_OUT_F32 ? 3u : 1u)) == 0,
+               JETQ_ERR_MISALIGNED);
+    const jetq_status a = check_arch();
+    if (a != JETQ_OK)
+        return a;
+    NormArgs g = {};
+    g.kind = kind;
+    g.dtype = dtype;
+    g.x = x;
+    g.n = n;
+    g.c = c;
+    g.ldx = ldx;
+    g.w = w;
+    g.b = b;
+    g.eps = eps;
+    g.out = y;
+    g.ldo = ldy;
+    g.mean = mean;
+    g.rstd = rstd;
+    return from_cuda(launch_norm_fwd(g, static_cast<cudaStream_t>(stream)));
+}
+
+size_t jetq_norm_bwd_workspace_bytes(jetq_out_dtype dtype, int64_t n, int64_t c)
+{
+    if (n <= 0 || c <= 0 || c > (1 << 20))
+        return 0;
+    return (size_t)norm_bwd_partial_rows(n, c, dtype) * (size_t)((c + 7) / 8 * 8) * 8;
+}
+
+jetq_status jetq_norm_bwd(jetq_norm_kind kind, jetq_out_dtype dtype, const void *dy, int64_t lddy, const void *x,
+                          int64_t n, int64_t c, int64_t ldx, const void *w, const float *mean, const float *rstd,
+                          void *dx, int64_t lddx, float *dw, float *db, void *workspace, size_t workspace_bytes,
+                          void *stream)
+{
+    const jetq_status s = check_norm(kind, dtype, x, n, c, ldx, w);
+    if (s != JETQ_OK)
+        return s;
+    JQ_REQUIRE(dw != nullptr && (kind == JETQ_NORM_LAYER || db == nullptr), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(aligned4(dw) && aligned4(db), JETQ_ERR_MISALIGNED);
+    if (n > 0) {
+        const jetq_status o = check_out(dx, dtype, lddx, c);
+        if (o != JETQ_OK)
+            return o;
+        JQ_REQUIRE(dy != nullptr && rstd != nullptr && (kind == JETQ_NORM_RMS || mean != nullptr) &&
+                       workspace != nullptr,
+                   JETQ_ERR_INVALID_ARG);
+        JQ_REQUIRE(lddy >= c, JETQ_ERR_UNSUPPORTED_SHAPE);
+        JQ_REQUIRE(aligned16(dy) && lddy % (dtype == JETQ_OUT_F32 ? 4 : 8) == 0 && aligned4(mean) && aligned4(rstd) &&
+                       aligned16(workspace),
+                   JETQ_ERR_MISALIGNED);
+    }
+    const jetq_status a = check_arch();
+    if (a != JETQ_OK)
+        return a;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (n == 0) { // no row: the sums are zero
+        cudaError_t e = cudaMemsetAsync(dw, 0, (size_t)c * 4, st);
+        if (e == cudaSuccess && db)
+            e = cudaMemsetAsync(db, 0, (size_t)c * 4, st);
+        return from_cuda(e);
+    }
+    JQ_REQUIRE(workspace_bytes >= jetq_norm_bwd_workspace_bytes(dtype, n, c), JETQ_ERR_INVALID_ARG);
+    NormArgs g = {};
+    g.kind = kind;
+    g.dtype = dtype;
+    g.x = x;
+    g.n = n;
+    g.c = c;
+    g.ldx = ldx;
+    g.dy = dy;
+    g.lddy = lddy;
+    g.w = w;
+    g.out = dx;
+    g.ldo = lddx;
+    g.mean = const_cast<float *>(mean);
+    g.rstd = const_cast<float *>(rstd);
+    g.dw = dw;
+    g.db = db;
+    g.ws = workspace;
+    return from_cuda(launch_norm_bwd(g, st));
 }
 
 } // extern "C"

@@ -247,6 +247,28 @@ cudaError_t make_kmajor_map(CUtensorMap *map, const void *base, int64_t k_extent
 cudaError_t make_sw128_map(CUtensorMap *map, const void *base, bool f32, int64_t cols, int64_t rows, int64_t ld,
                            int box_rows, int64_t slabs = 0, int64_t slab_stride = 0);
 
+// Layer norm / RMS norm of rows [n x c], forward (out = y; mean and rstd
+// written) and backward (out = dx; dw, db).
+struct NormArgs {
+    jetq_norm_kind kind;
+    jetq_out_dtype dtype;
+    const void *x;
+    int64_t n, c, ldx;
+    const void *dy; // backward
+    int64_t lddy;
+    const void *w, *b; // nullable: 1 and 0
+    float eps;
+    void *out;
+    int64_t ldo;
+    float *mean, *rstd;
+    float *dw, *db; // backward; db nullable
+    void *ws;       // backward: norm_bwd_partial_rows x round8(c) floats, twice with db
+};
+int64_t norm_bwd_partial_rows(int64_t n, int64_t c, jetq_out_dtype dtype);
+cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t st);
+cudaError_t norm_read_and_clear_error(cudaStream_t st, unsigned *out);
+
 // Softmax cross entropy of a linear head (BF16 hidden states x [n x c], head w
 // [v x c]) in pieces of the vocabulary.
 struct LinearCeArgs {

@@ -431,6 +431,9 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
         }
         if (C::kStaging && lane == 0)
             ptx::bulk_wait_group0();
+        // the odd CTA's barriers get the even one's commits: the last has arrived before the CTA ends
+        if (CG == 2 && rank == 1 && ew == 0 && lane == 0)
+            ptx::mbar_wait(done, 0u, abort_flag, err, kErrTimeout, p.limit_ns, false);
         __syncwarp();
     }
 
