@@ -82,6 +82,8 @@ struct HeadCfg {
     static constexpr bool kStaging = MODE != kStats;
     static constexpr size_t kStagingBytes = kStaging ? kEpiWarps * 4096 : 0;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kStagingBytes + 256;
+    // 64-blocks of K summed inside the tensor core before the epilogue takes the partial tile
+    static constexpr int kFold = MODE == kStats ? 2 : 1 << 30;
     static constexpr bool kAMn = MODE == kGradW16 || MODE == kGradW32; // A's M axis contiguous
     static constexpr bool kBMn = MODE >= kGradX;                       // B's N axis contiguous
     static constexpr int kBars = 2 * kStages + 5;
@@ -226,33 +228,37 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                 const int k1 = (int)((int64_t)p.num_kb * (ks + 1) / p.splits);
                 if (k0 == k1)
                     continue;
-                const uint32_t b = tc & 1u;
-                if (!ptx::mbar_wait<CG == 2>(acc_empty(b), ((tc >> 1) & 1u) ^ 1u, abort_flag, err, kErrTimeout,
-                                             p.limit_ns))
-                    break;
-                ptx::tc_fence_after();
-                for (int kb = k0; kb < k1; ++kb, ++it) {
-                    const int s = (int)(it % S);
-                    const uint32_t ph = (it / S) & 1u;
-                    if (!ptx::mbar_wait<CG == 2>(full(s), ph, abort_flag, err, kErrTimeout, p.limit_ns)) {
+                for (int kb = k0; kb < k1; ++tc) {
+                    const uint32_t b = tc & 1u;
+                    const int stop = k1 - kb > C::kFold ? kb + C::kFold : k1;
+                    if (!ptx::mbar_wait<CG == 2>(acc_empty(b), ((tc >> 1) & 1u) ^ 1u, abort_flag, err, kErrTimeout,
+                                                 p.limit_ns)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t a = ptx::smem_addr(tiles + (size_t)s * C::kStage);
-                    const uint64_t ad = C::kAMn ? ptx::desc_mnmajor_sw128(a, 8192u) : ptx::desc_kmajor_sw128(a);
-                    const uint64_t bd = C::kBMn ? ptx::desc_mnmajor_sw128(a + C::kABytes, 8192u)
-                                                : ptx::desc_kmajor_sw128(a + C::kABytes);
+                    for (const int start = kb; kb < stop; ++kb, ++it) {
+                        const int s = (int)(it % S);
+                        const uint32_t ph = (it / S) & 1u;
+                        if (!ptx::mbar_wait<CG == 2>(full(s), ph, abort_flag, err, kErrTimeout, p.limit_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        const uint32_t a = ptx::smem_addr(tiles + (size_t)s * C::kStage);
+                        const uint64_t ad = C::kAMn ? ptx::desc_mnmajor_sw128(a, 8192u) : ptx::desc_kmajor_sw128(a);
+                        const uint64_t bd = C::kBMn ? ptx::desc_mnmajor_sw128(a + C::kABytes, 8192u)
+                                                    : ptx::desc_kmajor_sw128(a + C::kABytes);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_bf16<CG>(tmem_base + 256u * b, ad + a_step * k, bd + b_step * k, idesc,
-                                          (kb > k0 || k > 0) ? 1u : 0u);
-                    ptx::mma_commit_cg<CG>(empty(s));
+                        for (int k = 0; k < 4; ++k)
+                            ptx::mma_bf16<CG>(tmem_base + 256u * b, ad + a_step * k, bd + b_step * k, idesc,
+                                              (kb > start || k > 0) ? 1u : 0u);
+                        ptx::mma_commit_cg<CG>(empty(s));
+                    }
+                    if (!ok)
+                        break;
+                    ptx::mma_commit_cg<CG>(acc_full(b));
                 }
-                if (!ok)
-                    break;
-                ptx::mma_commit_cg<CG>(acc_full(b));
-                ++tc;
             }
             ptx::mma_commit_cg<CG>(done);
             ptx::mbar_wait(done, 0u, abort_flag, err, kErrTimeout, p.limit_ns, false);
@@ -273,7 +279,6 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
             head_coords(p, t, mi, ni, ks);
             if ((int64_t)p.num_kb * ks / p.splits == (int64_t)p.num_kb * (ks + 1) / p.splits)
                 continue;
-            const uint32_t b = tc & 1u;
             const int row0 = mi * 128 * CG + (int)rank * 128 + quarter * 32;
             const int64_t row = (int64_t)row0 + lane;
             const int n0 = ni * C::BN + half * 128;
@@ -293,44 +298,79 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     }
                 }
             }
-            const bool got = ptx::mbar_wait(acc_full(b), (tc >> 1) & 1u, abort_flag, err, kErrTimeout, p.limit_ns);
-            if (!__all_sync(0xFFFFFFFFu, got))
-                break;
-            ptx::tc_fence_after();
-            const uint32_t acc = tmem_base + 256u * b + lane_addr + (uint32_t)(half * 128);
-            auto release = [&]() {
+            auto wait_acc = [&](uint32_t n) {
+                const bool got =
+                    ptx::mbar_wait(acc_full(n & 1u), (n >> 1) & 1u, abort_flag, err, kErrTimeout, p.limit_ns);
+                const bool all = __all_sync(0xFFFFFFFFu, got);
+                ptx::tc_fence_after();
+                return all;
+            };
+            auto acc_addr = [&](uint32_t n) {
+                return tmem_base + 256u * (n & 1u) + lane_addr + (uint32_t)(half * 128);
+            };
+            auto release = [&](uint32_t n) {
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     if (CG == 2)
-                        ptx::mbar_arrive_remote(ptx::map_to_cta(acc_empty(b), 0));
+                        ptx::mbar_arrive_remote(ptx::map_to_cta(acc_empty(n & 1u), 0));
                     else
-                        ptx::mbar_arrive(acc_empty(b));
+                        ptx::mbar_arrive(acc_empty(n & 1u));
                 }
             };
             if constexpr (MODE == kStats) {
-                uint32_t v[128];
+                // The tensor core's FP32 accumulator truncates at each step: over a whole K of 4096 the
+                // losses are off by 3e-6 of their value (binary64), with 128 columns of K a partial tile,
+                // summed here in round-to-nearest, by a thirtieth of that.
+                float2 z[64];
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    ptx::tmem_ld_32x32b_x32(acc + 32u * ch, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * ch]));
-                ptx::tmem_ld_wait_tie(v);
-                release();
+                for (int j = 0; j < 64; ++j)
+                    z[j] = make_float2(0.0f, 0.0f);
+                const int folds = (p.num_kb + C::kFold - 1) / C::kFold;
+                bool ok = true;
+                for (int f = 0; f < folds && ok; ++f) {
+                    const uint32_t n = tc + (uint32_t)f;
+                    ok = wait_acc(n);
+                    if (!ok)
+                        break;
+#pragma unroll
+                    for (int ch = 0; ch < 8; ++ch) {
+                        uint32_t v[16];
+                        ptx::tmem_ld_32x32b_x16(acc_addr(n) + 16u * ch, v);
+                        ptx::tmem_ld_wait_regs(v);
+                        if (ch == 7)
+                            release(n);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            z[8 * ch + j] = __fadd2_rn(z[8 * ch + j], make_float2(__uint_as_float(v[2 * j]),
+                                                                                  __uint_as_float(v[2 * j + 1])));
+                    }
+                }
+                if (!ok)
+                    break;
+                tc += (uint32_t)folds;
+                float v[128];
+#pragma unroll
+                for (int j = 0; j < 64; ++j) {
+                    v[2 * j] = z[j].x;
+                    v[2 * j + 1] = z[j].y;
+                }
                 const int valid = (int)min((int64_t)128, p.N - n0); // columns of this thread inside the vocabulary
                 if (valid < 128) {
 #pragma unroll
                     for (int j = 0; j < 128; ++j)
                         if (j >= valid)
-                            v[j] = 0xff800000u; // -inf
+                            v[j] = -INFINITY;
                 }
-                float m = __uint_as_float(v[0]);
+                float m = v[0];
 #pragma unroll
                 for (int j = 1; j < 128; ++j)
-                    m = fmaxf(m, __uint_as_float(v[j]));
+                    m = fmaxf(m, v[j]);
                 const float mk = m * p.k2;
                 float s0 = 0.0f, s1 = 0.0f, zt = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 128; j += 2) {
-                    const float a0 = __uint_as_float(v[j]), a1 = __uint_as_float(v[j + 1]);
+                    const float a0 = v[j], a1 = v[j + 1];
                     const float e0 = ex2(fmaf(a0, p.k2, -mk)), e1 = ex2(fmaf(a1, p.k2, -mk));
                     zt = j == tcol ? a0 : (j + 1 == tcol ? a1 : zt);
                     s0 += j == tcol ? 0.0f : e0; // the target's term is joined exactly by the last kernel
@@ -345,6 +385,9 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                         p.zt[row] = zt;
                 }
             } else if constexpr (MODE == kGrad || MODE == kGradW16) {
+                if (!wait_acc(tc))
+                    break;
+                const uint32_t acc = acc_addr(tc);
 #pragma unroll
                 for (int g = 0; g < 2; ++g) { // 64 BF16 columns: 128 bytes a row
                     uint32_t v[64];
@@ -354,7 +397,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                                                 *reinterpret_cast<uint32_t(*)[32]>(&v[32 * ch]));
                     ptx::tmem_ld_wait_tie(v);
                     if (g == 1)
-                        release();
+                        release(tc);
                     const int x0 = n0 + 64 * g;
                     if (MODE == kGradW16 && (x0 >= p.N || row0 >= p.M))
                         continue;
@@ -393,14 +436,18 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                         ptx::bulk_commit_group();
                     }
                 }
+                ++tc;
             } else {
+                if (!wait_acc(tc))
+                    break;
+                const uint32_t acc = acc_addr(tc);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) { // 32 FP32 columns: 128 bytes a row
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(acc + 32u * g, v);
                     ptx::tmem_ld_wait_tie(v);
                     if (g == 3)
-                        release();
+                        release(tc);
                     const int x0 = n0 + 32 * g;
                     if (x0 >= p.N || row0 >= p.M)
                         continue;
@@ -426,8 +473,8 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                         ptx::bulk_commit_group();
                     }
                 }
+                ++tc;
             }
-            ++tc;
         }
         if (C::kStaging && lane == 0)
             ptx::bulk_wait_group0();
