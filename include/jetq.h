@@ -558,6 +558,24 @@ JETQ_API jetq_status jetq_gemm_nvfp4(const uint8_t *qa, const uint8_t *sfa, cons
                                      int64_t m, int64_t n, int64_t k,
                                      void *out, jetq_out_dtype out_dtype, int64_t ldo, void *stream);
 
+/*
+ * Few-token product with NVFP4 weights and BF16 activations (weight-only
+ * quantization: rollout decode of 1 to 16 tokens; larger batches quantize the
+ * activations and use jetq_gemm_nvfp4):
+ *   y[i, r] = sgw[0] * sum_k e2m1(qw[r, k]) * e4m3(sbw[r, k / 16]) * x[i, k]
+ * Products are exact, sums FP32, the result rounded once.
+ *
+ *   qw, sbw, sgw  a weight [n x k] as jetq_quant_nvfp4 writes it with a tensor
+ *                 scope: codes [n x k/2] (16-byte aligned), row-major block
+ *                 scales [n x k/16] (2-byte aligned), sgw [1]
+ *   x, m, ldx     BF16 [m x k], row stride ldx (multiple of 8), 0 <= m <= 16
+ *   y, ldy        F32 or BF16 [m x n], any stride ldy >= n, element-aligned
+ * Limits: any n >= 1; k a multiple of 32.  m == 0 is a no-op.  One launch, no workspace.
+ */
+JETQ_API jetq_status jetq_gemv_nvfp4(const uint8_t *qw, const uint8_t *sbw, const float *sgw, int64_t n, int64_t k,
+                                     const uint16_t *x, int64_t m, int64_t ldx, void *y, jetq_out_dtype y_dtype,
+                                     int64_t ldy, void *stream);
+
 /* ======================================================================== */
 /* Layer norm and RMS norm                                                  */
 /* ======================================================================== */

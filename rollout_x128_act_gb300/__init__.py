@@ -78,6 +78,7 @@ def lib() -> ctypes.CDLL:
             "jetq_nvfp4_atom_bytes": (I64, [I64, I64]),
             "jetq_nvfp4_scale_atoms": (I32, [P, I64, I64, P, P]),
             "jetq_gemm_nvfp4": (I32, [P, P, P, I32, P, P, P, I64, I64, I64, P, I32, I64, P]),
+            "jetq_gemv_nvfp4": (I32, [P, P, P, I64, I64, P, I64, I64, P, I32, I64, P]),
             "jetq_norm_fwd": (I32, [I32, I32, P, I64, I64, I64, P, P, F32, P, I64, P, P, P]),
             "jetq_norm_bwd_workspace_bytes": (ctypes.c_size_t, [I32, I64, I64]),
             "jetq_norm_bwd": (I32, [I32, I32, P, I64, P, I64, I64, I64, P, P, P, P, I64, P, P, P, ctypes.c_size_t,
@@ -293,6 +294,12 @@ def jetq_gemm_grouped(kind, recipe, a, sa, b, sb, m, n, k, ldk, seg_offsets, num
     _check(lib().jetq_gemm_grouped(kind, recipe, _p(a), _p(sa), _p(b), _p(sb), m, n, k, ldk, _p(seg_offsets),
                                    num_experts, _p(out), _out_dtype(out), out.stride(-2), 1 if accumulate else 0,
                                    _s(stream)), "jetq_gemm_grouped")
+
+
+def jetq_gemv_nvfp4(qw, sbw, sgw, x, y, stream=None):
+    m, k = x.shape
+    _check(lib().jetq_gemv_nvfp4(_p(qw), _p(sbw), _p(sgw), qw.shape[0], k, _p(x), m, x.stride(0), _p(y),
+                                 _out_dtype(y), y.stride(0), _s(stream)), "jetq_gemv_nvfp4")
 
 
 def jetq_norm_fwd(kind, x, w, b, eps, y, mean, rstd, stream=None):
@@ -558,6 +565,20 @@ def grouped(kind, a, sa, b, sb, seg_offsets, n, k, out_dtype=torch.float32, reci
             out = torch.empty((m, n), dtype=out_dtype, device=a.device)
     jetq_gemm_grouped(kind, recipe, a, sa, b, sb, m, n, k, ldk, seg_offsets, E, out, accumulate, stream)
     return out
+
+
+def gemv_nvfp4(x, b, out_dtype=torch.float32, stream=None):
+    """Few-token product of BF16 x [m x k], m <= 16, with a quant_nvfp4 dict b of a weight
+    [n x k] (tensor scope; see jetq_gemv_nvfp4) -> [m x n]."""
+    q, sb, sg = b["q"], b["sb"], b["sg"]
+    _want(x, "x", torch.bfloat16, rows=True)
+    (m, k), n = x.shape, q.shape[0]
+    _want(q, "q", torch.uint8, (n, k // 2))
+    _want(sb, "sb", torch.uint8, (n, k // 16))
+    _want(sg, "sg", torch.float32, (1,))
+    y = torch.empty((m, n), dtype=out_dtype, device=x.device)
+    jetq_gemv_nvfp4(q, sb, sg, x, y, stream)
+    return y
 
 
 _NORM_DTYPES = (torch.bfloat16, torch.float32)

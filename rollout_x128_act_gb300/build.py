@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libjetq.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "gemm_mx.cu", "gemm_decode.cu", "gemm_nvfp4.cu",
-           "linear_ce.cu", "norm.cu"]
+           "linear_ce.cu", "norm.cu", "gemv_nvfp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--diag-suppress", "177"]

@@ -859,4 +859,26 @@ jetq_status jetq_norm_bwd(jetq_norm_kind kind, jetq_out_dtype dtype, const void 
     return from_cuda(launch_norm_bwd(g, st));
 }
 
+jetq_status jetq_gemv_nvfp4(const uint8_t *qw, const uint8_t *sbw, const float *sgw, int64_t n, int64_t k,
+                            const uint16_t *x, int64_t m, int64_t ldx, void *y, jetq_out_dtype y_dtype, int64_t ldy,
+                            void *stream)
+{
+    JQ_REQUIRE(n > 0 && k > 0 && m >= 0, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(y_dtype == JETQ_OUT_F32 || y_dtype == JETQ_OUT_BF16, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(m <= 16 && k % 32 == 0 && k <= (1 << 24) && n <= ((int64_t)1 << 32) && ldx >= k && ldy >= n,
+               JETQ_ERR_UNSUPPORTED_SHAPE);
+    if (m == 0)
+        return JETQ_OK;
+    JQ_REQUIRE(qw != nullptr && sbw != nullptr && sgw != nullptr && x != nullptr && y != nullptr,
+               JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(aligned16(qw) && (reinterpret_cast<uintptr_t>(sbw) & 1u) == 0 && aligned4(sgw) && aligned16(x) &&
+                   ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & (y_dtype == JETQ_OUT_F32 ? 3u : 1u)) == 0,
+               JETQ_ERR_MISALIGNED);
+    const jetq_status a = check_arch();
+    if (a != JETQ_OK)
+        return a;
+    GemvNvfp4Args g{qw, sbw, sgw, n, k, x, m, ldx, y, y_dtype, ldy};
+    return from_cuda(launch_gemv_nvfp4(g, static_cast<cudaStream_t>(stream)));
+}
+
 } // extern "C"

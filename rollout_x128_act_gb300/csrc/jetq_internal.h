@@ -247,6 +247,19 @@ cudaError_t make_kmajor_map(CUtensorMap *map, const void *base, int64_t k_extent
 cudaError_t make_sw128_map(CUtensorMap *map, const void *base, bool f32, int64_t cols, int64_t rows, int64_t ld,
                            int box_rows, int64_t slabs = 0, int64_t slab_stride = 0);
 
+// Few-token product y [m x n] = x [m x k] W^T with NVFP4 weights and BF16 x, 1 <= m <= 16.
+struct GemvNvfp4Args {
+    const uint8_t *q, *sb;
+    const float *sg;
+    int64_t n, k;
+    const uint16_t *x;
+    int64_t m, ldx;
+    void *y;
+    jetq_out_dtype out_dtype;
+    int64_t ldy;
+};
+cudaError_t launch_gemv_nvfp4(const GemvNvfp4Args &a, cudaStream_t st);
+
 // Layer norm / RMS norm of rows [n x c], forward (out = y; mean and rstd
 // written) and backward (out = dx; dw, db).
 struct NormArgs {
