@@ -41,6 +41,8 @@ class JetqError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded C library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -105,12 +107,15 @@ def status_string(status: int) -> str:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _s(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+
+
+def _bytes(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
 
 
 def _check(status: int, where: str):
@@ -265,7 +270,7 @@ def jetq_decode_workspace_bytes(n, d, c):
 def jetq_gemm_fprop_ws(recipe, qx, sx, qw, sw, n, d, c, y, ws, path=PATH_AUTO, stream=None):
     _check(lib().jetq_gemm_fprop_ws(recipe, _p(qx), _p(sx), _p(qw), _p(sw), n, d, c, _p(y), _out_dtype(y),
                                     y.stride(0), None if ws is None else _p(ws),
-                                    0 if ws is None else ws.numel() * ws.element_size(), path, _s(stream)),
+                                    _bytes(ws), path, _s(stream)),
            "jetq_gemm_fprop_ws")
 
 
@@ -316,7 +321,7 @@ def jetq_norm_bwd(kind, dy, x, w, mean, rstd, dx, dw, db, ws, stream=None):
     n, c = x.shape
     _check(lib().jetq_norm_bwd(kind, _out_dtype(x), _p(dy), dy.stride(0), _p(x), n, c, x.stride(0), _p(w), _p(mean),
                                _p(rstd), _p(dx), dx.stride(0), _p(dw), _p(db), _p(ws),
-                               0 if ws is None else ws.numel() * ws.element_size(), _s(stream)), "jetq_norm_bwd")
+                               _bytes(ws), _s(stream)), "jetq_norm_bwd")
 
 
 def jetq_linear_ce_workspace_bytes(n: int, v: int) -> int:
@@ -326,7 +331,7 @@ def jetq_linear_ce_workspace_bytes(n: int, v: int) -> int:
 def jetq_linear_ce_fwd(x, w, target, scale, loss, lse, ws, stream=None):
     n, c = x.shape
     _check(lib().jetq_linear_ce_fwd(_p(x), n, c, x.stride(0), _p(w), w.shape[0], w.stride(0), _p(target), scale,
-                                    _p(loss), _p(lse), _p(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                    _p(loss), _p(lse), _p(ws), _bytes(ws),
                                     _s(stream)), "jetq_linear_ce_fwd")
 
 
@@ -339,7 +344,7 @@ def jetq_linear_ce_bwd(x, w, target, scale, lse, dloss, dx, dw, accumulate, ws, 
     _check(lib().jetq_linear_ce_bwd(_p(x), n, c, x.stride(0), _p(w), w.shape[0], w.stride(0), _p(target), scale,
                                     _p(lse), _p(dloss), _p(dx), dx.stride(0), _p(dw), _out_dtype(dw), dw.stride(0),
                                     1 if accumulate else 0, _p(ws),
-                                    0 if ws is None else ws.numel() * ws.element_size(), _s(stream)),
+                                    _bytes(ws), _s(stream)),
            "jetq_linear_ce_bwd")
 
 
@@ -349,15 +354,16 @@ def _want(t, name, dtype, shape=None, rows=False):
     """A CUDA tensor of `dtype` (and shape); rows: unit stride along the last axis, else dense."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name}: a CUDA tensor is wanted")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
         raise ValueError(f"{name}: {dtype} is wanted, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
-    if rows:
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-            raise ValueError(f"{name}: rows of consecutive elements are wanted, got strides {t.stride()}")
-    elif not t.is_contiguous():
+    if t.is_contiguous() and (not rows or t.dim() == 2):
+        return
+    if not rows:
         raise ValueError(f"{name}: a contiguous tensor is wanted")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: rows of consecutive elements are wanted, got strides {t.stride()}")
 
 
 # ------------------------------------------------------------------ allocating helpers
@@ -642,7 +648,8 @@ def linear_ce(x, w, target, scale=1.0, workspace=None, stream=None):
     target [n] (outside [0, v): no loss) -> (loss [n], lse [n])."""
     _check_head(x, w, target)
     n, v = x.shape[0], w.shape[0]
-    loss, lse = torch.empty((2, n), dtype=torch.float32, device=x.device).unbind(0)
+    loss = torch.empty(n, dtype=torch.float32, device=x.device)
+    lse = torch.empty(n, dtype=torch.float32, device=x.device)
     need = jetq_linear_ce_workspace_bytes(n, v)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)

@@ -47,6 +47,9 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+#ifndef JETQ_FOLD
+#define JETQ_FOLD 2
+#endif
 enum HeadMode : int {
     kStats = 0,   // softmax statistics of the logits
     kGrad = 1,    // d in BF16
@@ -83,9 +86,12 @@ struct HeadCfg {
     static constexpr size_t kStagingBytes = kStaging ? kEpiWarps * 4096 : 0;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kStagingBytes + 256;
     // 64-blocks of K summed inside the tensor core before the epilogue takes the partial tile
-    static constexpr int kFold = MODE == kStats ? 2 : 1 << 30;
+    static constexpr int kFold = MODE == kStats ? JETQ_FOLD : 1 << 30;
     static constexpr bool kAMn = MODE == kGradW16 || MODE == kGradW32; // A's M axis contiguous
     static constexpr bool kBMn = MODE >= kGradX;                       // B's N axis contiguous
+    // register split (kStats keeps 128 sums a thread): producer warps, epilogue warps
+    static constexpr int kRegProducer = 72, kRegEpilogue = 216;
+    static constexpr bool kRegSplit = MODE == kStats;
     static constexpr int kBars = 2 * kStages + 5;
     static_assert(kBars * 8 + 8 <= 256, "barrier area");
     static_assert(kSmem <= 232448, "shared memory");
@@ -169,6 +175,12 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
+    if constexpr (C::kRegSplit) {
+        if (warp < 4)
+            ptx::setmaxnreg_dec<C::kRegProducer>();
+        else
+            ptx::setmaxnreg_inc<C::kRegEpilogue>();
+    }
 
     if (warp < 4) {
         if (warp == 0 && lane == 0) {
@@ -334,16 +346,19 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     if (!ok)
                         break;
 #pragma unroll
-                    for (int ch = 0; ch < 8; ++ch) {
-                        uint32_t v[16];
-                        ptx::tmem_ld_32x32b_x16(acc_addr(n) + 16u * ch, v);
-                        ptx::tmem_ld_wait_regs(v);
-                        if (ch == 7)
+                    for (int ch = 0; ch < 2; ++ch) {
+                        uint32_t v[64];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            ptx::tmem_ld_32x32b_x32(acc_addr(n) + 64u * ch + 32u * q,
+                                                    *reinterpret_cast<uint32_t(*)[32]>(&v[32 * q]));
+                        ptx::tmem_ld_wait_tie(v);
+                        if (ch == 1)
                             release(n);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            z[8 * ch + j] = __fadd2_rn(z[8 * ch + j], make_float2(__uint_as_float(v[2 * j]),
-                                                                                  __uint_as_float(v[2 * j + 1])));
+                        for (int j = 0; j < 32; ++j)
+                            z[32 * ch + j] = __fadd2_rn(z[32 * ch + j], make_float2(__uint_as_float(v[2 * j]),
+                                                                                    __uint_as_float(v[2 * j + 1])));
                     }
                 }
                 if (!ok)
@@ -588,16 +603,18 @@ __global__ void k_ce_dx(const float *slab, int slabs, int64_t n, int64_t c, cons
     }
 }
 
-#ifndef JETQ_HEAD_CG
-#define JETQ_HEAD_CG 1
-#endif
-constexpr int kCg = JETQ_HEAD_CG;
+constexpr int kTileN = 256;
 
-template <int MODE>
+int64_t ceil_div(int64_t a, int64_t b)
+{
+    return (a + b - 1) / b;
+}
+
+template <int CG, int MODE>
 cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, HeadParams p, cudaStream_t st)
 {
-    using C = HeadCfg<kCg, MODE>;
-    auto kern = k_head_gemm<kCg, MODE>;
+    using C = HeadCfg<CG, MODE>;
+    auto kern = k_head_gemm<CG, MODE>;
     static int configured_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -606,13 +623,23 @@ cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorM
     if (configured_device != dev) {
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem)) != cudaSuccess)
             return e;
+        if (C::kRegSplit) {
+            // setmaxnreg.inc waits until the CTA's registers can serve it: the launch must
+            // provide both shares, or the kernel would stall
+            cudaFuncAttributes fa;
+            if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess)
+                return e;
+            if (fa.numRegs < C::kRegProducer || fa.numRegs > C::kRegEpilogue ||
+                fa.numRegs * C::kThreads < C::kRegProducer * 128 + C::kRegEpilogue * 32 * C::kEpiWarps)
+                return cudaErrorInvalidConfiguration;
+        }
         configured_device = dev;
     }
     p.limit_ns = kWaitLimitNs;
     const int64_t tiles = (int64_t)p.mt * p.nt * p.splits;
-    const int units = (int)(tiles < sm_count() / kCg ? tiles : sm_count() / kCg);
+    const int units = (int)(tiles < sm_count() / CG ? tiles : sm_count() / CG);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * kCg));
+    cfg.gridDim = dim3((unsigned)(units * CG));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
@@ -620,42 +647,50 @@ cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorM
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kCg;
+    attr[1].val.clusterDim.x = CG;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = kCg == 2 ? 2 : 1;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, a, b, o, p);
 }
 
-constexpr int kTileM = 128 * kCg, kTileN = 256;
-
-int64_t ceil_div(int64_t a, int64_t b)
+// CTA pairs (256 x 256 tiles) or single CTAs (128 x 256)?  A tile takes the
+// same time either way and pairs need half the operand traffic, which measured
+// 1.08x faster a tile (dx, dw and d of 4096 tokens x 131072 x 4096: 7.99 ms
+// against 8.72); single CTAs waste less where the rows do not fill pairs.
+int pick_cg(int64_t rows, int64_t tiles_n)
 {
-    return (a + b - 1) / b;
+    const int64_t w1 = ceil_div(ceil_div(rows, 128) * tiles_n, sm_count());
+    const int64_t w2 = ceil_div(ceil_div(rows, 256) * tiles_n, sm_count() / 2);
+    return 100 * w2 <= 108 * w1 ? 2 : 1;
 }
 
-// K splits of the dx product: enough work units to fill the machine evenly.
-int dx_splits(int64_t n, int64_t c, int64_t piece)
+// CTAs a tile and K splits of the dx product: enough work units to fill the
+// machine evenly.  A split costs a slab's traffic, a tile of the whole piece
+// about 4.7 ns for every vocabulary row.
+void dx_shape(int64_t n, int64_t c, int64_t piece, int &cg, int &splits)
 {
-    const int64_t tiles = ceil_div(n, kTileM) * ceil_div(c, kTileN), units = sm_count() / kCg;
     const int64_t most = piece / 64 < 16 ? piece / 64 : 16;
-    int best = 1;
-    double cost = 1e30;
-    for (int64_t s = 1; s <= most; ++s) {
-        // waves of units, each 1/s of a tile's K, plus the slabs' traffic
-        const double t = (double)ceil_div(tiles * s, units) / (double)s + 0.02 * (double)s;
-        if (t < cost - 1e-9) {
-            cost = t;
-            best = (int)s;
+    const double tile_s = 4.7e-9 * (double)piece, slab_s = 0.3 * 8.0 * (double)n * (double)c / 5e12;
+    double best = 1e30;
+    for (int g = 2; g >= 1; --g) {
+        const int64_t tiles = ceil_div(n, 128 * g) * ceil_div(c, kTileN), units = sm_count() / g;
+        for (int64_t s = 1; s <= most; ++s) {
+            const double t = (double)ceil_div(tiles * s, units) / (double)s * tile_s * (g == 2 ? 1.0 : 1.08) +
+                             (double)s * slab_s;
+            if (t < best * 0.999) {
+                best = t;
+                cg = g;
+                splits = (int)s;
+            }
         }
     }
-    return best;
 }
 
 struct BwdPlan {
     int64_t piece; // vocabulary rows a piece (a multiple of 256)
-    int splits;
+    int dx_cg, splits;
     size_t slab_off, d_off, total;
 };
 
@@ -664,7 +699,7 @@ BwdPlan bwd_plan(int64_t n, int64_t v, int64_t c, int64_t piece)
     BwdPlan b;
     const int64_t all = ceil_div(v, 256) * 256;
     b.piece = piece < 256 ? 256 : (piece > all ? all : piece / 256 * 256);
-    b.splits = dx_splits(n, c, b.piece);
+    dx_shape(n, c, b.piece, b.dx_cg, b.splits);
     b.slab_off = 256; // gmax first
     const size_t slabs = (size_t)b.splits * (size_t)n * (size_t)c * 4;
     b.d_off = (b.slab_off + slabs + 1023) / 1024 * 1024;
@@ -697,17 +732,18 @@ size_t linear_ce_bwd_workspace_min(int64_t n, int64_t v, int64_t c)
 
 cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
 {
+    HeadParams p = {};
+    p.nt = (int)ceil_div(a.v, kTileN);
+    const int cg = pick_cg(a.n, p.nt);
     CUtensorMap ta, tb;
     cudaError_t e;
     if ((e = make_sw128_map(&ta, a.x, false, a.c, a.n, a.ldx, 128)) != cudaSuccess ||
-        (e = make_sw128_map(&tb, a.w, false, a.c, a.v, a.ldw, kTileN / kCg)) != cudaSuccess)
+        (e = make_sw128_map(&tb, a.w, false, a.c, a.v, a.ldw, kTileN / cg)) != cudaSuccess)
         return e;
-    HeadParams p = {};
-    p.mt = (int)ceil_div(a.n, kTileM);
-    p.nt = (int)ceil_div(a.v, kTileN);
+    p.mt = (int)ceil_div(a.n, 128 * cg);
     p.splits = 1;
     p.num_kb = (int)ceil_div(a.c, 64);
-    p.group = p.mt < 32 ? p.mt : 32; // the group's x stays in L2 while w streams through once
+    p.group = p.mt < 64 / cg ? p.mt : 64 / cg; // the group's x stays in L2 while w streams through once
     p.M = a.n;
     p.N = a.v;
     p.k2 = a.scale * kLog2e;
@@ -715,7 +751,8 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
     p.V = a.v;
     p.part = static_cast<float2 *>(a.ws);
     p.zt = reinterpret_cast<float *>(p.part + (size_t)2 * p.nt * a.n);
-    if ((e = run_head<kStats>(ta, tb, ta, p, st)) != cudaSuccess)
+    e = cg == 2 ? run_head<2, kStats>(ta, tb, ta, p, st) : run_head<1, kStats>(ta, tb, ta, p, st);
+    if (e != cudaSuccess)
         return e;
     int rx = 1;
     while (rx < 32 && rx < a.n)
@@ -727,8 +764,7 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
 cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
 {
     // the largest piece that the workspace holds, up to the preferred one
-    int64_t piece = preferred_piece(a.n);
-    BwdPlan plan = bwd_plan(a.n, a.v, a.c, piece);
+    BwdPlan plan = bwd_plan(a.n, a.v, a.c, preferred_piece(a.n));
     while (plan.total > a.ws_bytes && plan.piece > 256)
         plan = bwd_plan(a.n, a.v, a.c, plan.piece / 2);
     if (plan.total > a.ws_bytes)
@@ -739,32 +775,33 @@ cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
     cudaError_t e = launch_pdl(k_ce_gmax, dim3(1), dim3(1024), 0, st, a.dloss, a.target, a.n, a.v, gmax);
     if (e != cudaSuccess)
         return e;
-    const int dw_esize = a.dw_dtype == JETQ_OUT_BF16 ? 2 : 4;
+    const bool dw16 = a.dw_dtype == JETQ_OUT_BF16;
     for (int64_t v0 = 0; v0 < a.v; v0 += plan.piece) {
         const int64_t rows = a.v - v0 < plan.piece ? a.v - v0 : plan.piece; // vocabulary rows of this piece
         const int64_t cols = ceil_div(rows, 256) * 256;                     // columns of d, zero past rows
+        const int cg = pick_cg(a.n, ceil_div(rows, kTileN));
         const uint16_t *w = a.w + v0 * a.ldw;
+        void *dwp = static_cast<uint8_t *>(a.dw) + v0 * a.lddw * (dw16 ? 2 : 4);
         CUtensorMap xk, wk, dst, dk, wn, slabs, dm, xn, dw;
         if ((e = make_sw128_map(&xk, a.x, false, a.c, a.n, a.ldx, 128)) != cudaSuccess ||
-            (e = make_sw128_map(&wk, w, false, a.c, rows, a.ldw, kTileN / kCg)) != cudaSuccess ||
+            (e = make_sw128_map(&wk, w, false, a.c, rows, a.ldw, kTileN / cg)) != cudaSuccess ||
             (e = make_sw128_map(&dst, d, false, cols, a.n, plan.piece, 32, 1, plan.piece * a.n)) != cudaSuccess ||
             (e = make_sw128_map(&dk, d, false, cols, a.n, plan.piece, 128)) != cudaSuccess ||
             (e = make_sw128_map(&wn, w, false, a.c, rows, a.ldw, 64)) != cudaSuccess ||
             (e = make_sw128_map(&slabs, slab, true, a.c, a.n, a.c, 32, plan.splits, a.n * a.c)) != cudaSuccess ||
             (e = make_sw128_map(&dm, d, false, cols, a.n, plan.piece, 64)) != cudaSuccess ||
             (e = make_sw128_map(&xn, a.x, false, a.c, a.n, a.ldx, 64)) != cudaSuccess ||
-            (e = make_sw128_map(&dw, static_cast<uint8_t *>(a.dw) + v0 * a.lddw * dw_esize, dw_esize == 4, a.c, rows,
-                                a.lddw, 32, 1, rows * a.lddw)) != cudaSuccess)
+            (e = make_sw128_map(&dw, dwp, !dw16, a.c, rows, a.lddw, 32, 1, rows * a.lddw)) != cudaSuccess)
             return e;
         HeadParams p = {};
         p.gmax = gmax;
         p.scale = a.scale;
         // d of the piece
-        p.mt = (int)ceil_div(a.n, kTileM);
+        p.mt = (int)ceil_div(a.n, 128 * cg);
         p.nt = (int)ceil_div(rows, kTileN);
         p.splits = 1;
         p.num_kb = (int)ceil_div(a.c, 64);
-        p.group = p.mt < 32 ? p.mt : 32;
+        p.group = p.mt < 64 / cg ? p.mt : 64 / cg;
         p.M = a.n;
         p.N = rows;
         p.k2 = a.scale * kLog2e;
@@ -773,24 +810,28 @@ cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
         p.col0 = v0;
         p.lse = a.lse;
         p.dloss = a.dloss;
-        if ((e = run_head<kGrad>(xk, wk, dst, p, st)) != cudaSuccess)
+        e = cg == 2 ? run_head<2, kGrad>(xk, wk, dst, p, st) : run_head<1, kGrad>(xk, wk, dst, p, st);
+        if (e != cudaSuccess)
             return e;
         // dx += d w
+        p.mt = (int)ceil_div(a.n, 128 * plan.dx_cg);
         p.nt = (int)ceil_div(a.c, kTileN);
         p.splits = plan.splits;
         p.num_kb = (int)(cols / 64);
+        p.group = p.mt < 64 / plan.dx_cg ? p.mt : 64 / plan.dx_cg;
         p.N = a.c;
         p.add = v0 > 0;
-        if ((e = run_head<kGradX>(dk, wn, slabs, p, st)) != cudaSuccess)
+        e = plan.dx_cg == 2 ? run_head<2, kGradX>(dk, wn, slabs, p, st) : run_head<1, kGradX>(dk, wn, slabs, p, st);
+        if (e != cudaSuccess)
             return e;
         // dw = d^T x: few vocabulary tiles at a time against all of x
-        p.mt = (int)ceil_div(rows, kTileM);
-        p.group = 4;
+        p.mt = (int)ceil_div(rows, 256);
+        p.group = p.mt < 4 ? p.mt : 4;
         p.splits = 1;
         p.num_kb = (int)ceil_div(a.n, 64);
         p.M = rows;
         p.add = a.accumulate;
-        e = dw_esize == 2 ? run_head<kGradW16>(dm, xn, dw, p, st) : run_head<kGradW32>(dm, xn, dw, p, st);
+        e = dw16 ? run_head<2, kGradW16>(dm, xn, dw, p, st) : run_head<2, kGradW32>(dm, xn, dw, p, st);
         if (e != cudaSuccess)
             return e;
     }

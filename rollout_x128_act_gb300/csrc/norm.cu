@@ -130,18 +130,43 @@ __device__ __forceinline__ void group_sum2(float &a, float &b, float2 *red, int 
     }
 }
 
-// One parameter vector (w, b) of a lane's columns, zero past c; `fallback` without one.
+template <int G>
+__device__ __forceinline__ float group_sum(float a, float2 *red, int group, int wg, int lane, int &buf)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    if constexpr (G > 1) {
+        float *r = reinterpret_cast<float *>(red + buf * 16) + group * G;
+        if (lane == 0)
+            r[wg] = a;
+        ptx::named_bar_sync(1 + group, 32 * G);
+        a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+            a += r[i];
+        buf ^= 1;
+    } else {
+        __syncwarp();
+    }
+    return a;
+}
+
+// The parameters (w, b) of a lane's columns as they are stored, zero past c; `fallback` without one.
 template <class T, int G>
-__device__ __forceinline__ void load_params(const void *p, int c, int lt, float fallback, float (&f)[kLaneElems])
+__device__ __forceinline__ void load_params(const void *p, int c, int lt, float fallback, uint4 *packed)
 {
     using C = NormCfg<T, G>;
 #pragma unroll
-    for (int k = 0; k < C::V; ++k)
+    for (int k = 0; k < C::V; ++k) {
+        float f[C::E];
 #pragma unroll
         for (int e = 0; e < C::E; ++e) {
             const int col = (k * C::kLanes + lt) * C::E + e;
-            f[k * C::E + e] = col < c ? (p ? Vec<T>::get(static_cast<const T *>(p) + col) : fallback) : 0.0f;
+            f[e] = col < c ? (p ? Vec<T>::get(static_cast<const T *>(p) + col) : fallback) : 0.0f;
         }
+        packed[k] = Vec<T>::pack(f);
+    }
 }
 
 // A row vector of a lane from the ring (whole vectors) or, where the last
@@ -193,8 +218,14 @@ __device__ __forceinline__ void issue_row(uint32_t bar, uint32_t dst, uint32_t s
         ptx::bulk_load(dst + stride, b, bytes, bar);
 }
 
+// CTAs an SM that the registers allow (packed BF16 parameters leave room for one more).
+__host__ __device__ constexpr int norm_ctas(int g, int esize, bool bwd)
+{
+    return g == 16 ? 1 : (bwd ? 2 : (esize == 2 ? 4 : 3));
+}
+
 template <class T, int G, bool RMS, bool BWD>
-__global__ void __launch_bounds__(NormCfg<T, G>::kThreads, (G == 16 ? 1 : (BWD ? 2 : 3)))
+__global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_ctas(G, (int)sizeof(T), BWD))
     k_norm(const NormParams p)
 {
     using C = NormCfg<T, G>;
@@ -238,7 +269,7 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, (G == 16 ? 1 : (BWD ?
             last_issued = row;
         }
 
-    float w[kLaneElems], b[BWD ? 1 : kLaneElems];
+    uint4 w[V], b[BWD ? 1 : V]; // unpacked where they are used: registers for another CTA an SM
     load_params<T, G>(p.w, p.c, lt, 1.0f, w);
     if constexpr (!BWD)
         load_params<T, G>(p.b, p.c, lt, 0.0f, b);
@@ -281,13 +312,12 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, (G == 16 ? 1 : (BWD ?
         for (int k = 0; k < V; ++k)
             load_vec<T>(st, x + row * p.ldx, last_row, (k * C::kLanes + lt) * E, p.c, h + k * E);
         if constexpr (!BWD) {
-            float mean = 0.0f, sq = 0.0f, none = 0.0f;
+            float mean = 0.0f, sq = 0.0f;
             if constexpr (!RMS) {
 #pragma unroll
                 for (int i = 0; i < kLaneElems; ++i)
                     mean += h[i];
-                group_sum2<G>(mean, none, red, group, wg, lane, buf);
-                mean *= inv_c;
+                mean = group_sum<G>(mean, red, group, wg, lane, buf) * inv_c;
             }
 #pragma unroll
             for (int k = 0; k < V; ++k)
@@ -298,8 +328,7 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, (G == 16 ? 1 : (BWD ?
                         h[i] = (k * C::kLanes + lt) * E + e < p.c ? h[i] - mean : 0.0f;
                     sq = fmaf(h[i], h[i], sq);
                 }
-            none = 0.0f;
-            group_sum2<G>(sq, none, red, group, wg, lane, buf);
+            sq = group_sum<G>(sq, red, group, wg, lane, buf);
             // every lane has its row in registers: the stage takes the next row
             refill(row + (int64_t)p.stages * step);
             const float rstd = __frcp_rn(__fsqrt_rn(fmaf(sq, inv_c, p.eps)));
@@ -310,10 +339,12 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, (G == 16 ? 1 : (BWD ?
             }
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                float y[E];
+                float y[E], wf[E], bf[E];
+                Vec<T>::unpack(w[k], wf);
+                Vec<T>::unpack(b[k], bf);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    y[e] = fmaf(h[k * E + e] * rstd, w[k * E + e], b[k * E + e]);
+                    y[e] = fmaf(h[k * E + e] * rstd, wf[e], bf[e]);
                 const int pos = (k * C::kLanes + lt) * E;
                 if (pos < p.c)
                     store_vec<T>(out + row * p.ldo, pos, p.c, y);
@@ -330,16 +361,26 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, (G == 16 ? 1 : (BWD ?
                 load_vec<T>(st + row_bytes, dy + row * p.lddy, last_row, (k * C::kLanes + lt) * E, p.c, t + k * E);
             float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kLaneElems; ++i) {
-                h[i] = (h[i] - mean) * rstd;
-                dw[i] = fmaf(t[i], h[i], dw[i]); // columns past c: t = 0
-                if constexpr (!RMS)
-                    db[i] += t[i];
-                t[i] *= w[i];
-                s1 += t[i];
-                s2 = fmaf(t[i], h[i], s2);
+            for (int k = 0; k < V; ++k) {
+                float wf[E];
+                Vec<T>::unpack(w[k], wf);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int i = k * E + e;
+                    h[i] = (h[i] - mean) * rstd;
+                    dw[i] = fmaf(t[i], h[i], dw[i]); // columns past c: t = 0
+                    if constexpr (!RMS)
+                        db[i] += t[i];
+                    t[i] *= wf[e];
+                    if constexpr (!RMS)
+                        s1 += t[i];
+                    s2 = fmaf(t[i], h[i], s2);
+                }
             }
-            group_sum2<G>(s1, s2, red, group, wg, lane, buf);
+            if constexpr (RMS)
+                s2 = group_sum<G>(s2, red, group, wg, lane, buf);
+            else
+                group_sum2<G>(s1, s2, red, group, wg, lane, buf);
             refill(row + (int64_t)p.stages * step);
             s1 = RMS ? 0.0f : s1 * inv_c;
             s2 *= inv_c;
@@ -527,7 +568,7 @@ NormPlan norm_plan(int64_t n, int64_t c, int esize, bool bwd)
     const int g = warps_of(c), per_cta = g < 8 ? 8 / g : 1;
     const size_t row = (size_t)((c * esize + 15) / 16 * 16) * (bwd ? 2 : 1);
     r.stages = kMaxStages;
-    const int ctas = g == 16 ? 1 : (bwd ? 2 : 3);
+    const int ctas = norm_ctas(g, esize, bwd);
     while (r.stages > 2 && ctas * (r.stages * per_cta * row + 2048) > 227 * 1024)
         --r.stages;
     r.smem = r.stages * per_cta * row + 128;
