@@ -610,6 +610,13 @@ int64_t ceil_div(int64_t a, int64_t b)
     return (a + b - 1) / b;
 }
 
+// Tiles in work at a time (1 where no device answers: the size queries run without one).
+int units_of(int cg)
+{
+    const int u = sm_count() / cg;
+    return u > 0 ? u : 1;
+}
+
 template <int CG, int MODE>
 cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, HeadParams p, cudaStream_t st)
 {
@@ -637,7 +644,7 @@ cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorM
     }
     p.limit_ns = kWaitLimitNs;
     const int64_t tiles = (int64_t)p.mt * p.nt * p.splits;
-    const int units = (int)(tiles < sm_count() / CG ? tiles : sm_count() / CG);
+    const int units = (int)(tiles < units_of(CG) ? tiles : units_of(CG));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * CG));
     cfg.blockDim = dim3(C::kThreads);
@@ -661,8 +668,8 @@ cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorM
 // against 8.72); single CTAs waste less where the rows do not fill pairs.
 int pick_cg(int64_t rows, int64_t tiles_n)
 {
-    const int64_t w1 = ceil_div(ceil_div(rows, 128) * tiles_n, sm_count());
-    const int64_t w2 = ceil_div(ceil_div(rows, 256) * tiles_n, sm_count() / 2);
+    const int64_t w1 = ceil_div(ceil_div(rows, 128) * tiles_n, units_of(1));
+    const int64_t w2 = ceil_div(ceil_div(rows, 256) * tiles_n, units_of(2));
     return 100 * w2 <= 108 * w1 ? 2 : 1;
 }
 
@@ -675,7 +682,7 @@ void dx_shape(int64_t n, int64_t c, int64_t piece, int &cg, int &splits)
     const double tile_s = 4.7e-9 * (double)piece, slab_s = 0.3 * 8.0 * (double)n * (double)c / 5e12;
     double best = 1e30;
     for (int g = 2; g >= 1; --g) {
-        const int64_t tiles = ceil_div(n, 128 * g) * ceil_div(c, kTileN), units = sm_count() / g;
+        const int64_t tiles = ceil_div(n, 128 * g) * ceil_div(c, kTileN), units = units_of(g);
         for (int64_t s = 1; s <= most; ++s) {
             const double t = (double)ceil_div(tiles * s, units) / (double)s * tile_s * (g == 2 ? 1.0 : 1.08) +
                              (double)s * slab_s;
