@@ -47,9 +47,6 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-#ifndef JETQ_FOLD
-#define JETQ_FOLD 2
-#endif
 enum HeadMode : int {
     kStats = 0,   // softmax statistics of the logits
     kGrad = 1,    // d in BF16
@@ -86,7 +83,7 @@ struct HeadCfg {
     static constexpr size_t kStagingBytes = kStaging ? kEpiWarps * 4096 : 0;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kStagingBytes + 256;
     // 64-blocks of K summed inside the tensor core before the epilogue takes the partial tile
-    static constexpr int kFold = MODE == kStats ? JETQ_FOLD : 1 << 30;
+    static constexpr int kFold = MODE == kStats ? (CG == 2 ? 8 : 2) : 1 << 30;
     static constexpr bool kAMn = MODE == kGradW16 || MODE == kGradW32; // A's M axis contiguous
     static constexpr bool kBMn = MODE >= kGradX;                       // B's N axis contiguous
     // register split (kStats keeps 128 sums a thread): producer warps, epilogue warps
@@ -331,9 +328,12 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                 }
             };
             if constexpr (MODE == kStats) {
-                // The tensor core's FP32 accumulator truncates at each step: over a whole K of 4096 the
-                // losses are off by 3e-6 of their value (binary64), with 128 columns of K a partial tile,
-                // summed here in round-to-nearest, by a thirtieth of that.
+                // The tensor core's FP32 accumulator truncates at each step: over a whole K of 4096 the losses
+                // of 4096 tokens are off by 3e-6 (2-norm, against binary64), a single token's by up to 2e-5.
+                // So partial tiles of kFold 64-blocks of K are summed here in round-to-nearest: 8 blocks for
+                // batches (4e-7, less than an FP32 matrix product's 6e-7; 4096 tokens x 131072 x 4096: 2.65 ms
+                // against 2.97 with 4 and 4.03 with 2, whose hand-overs stall the pair), 2 for the small row
+                // counts of single CTAs (1e-7; there the time is the weight's stream either way).
                 float2 z[64];
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
