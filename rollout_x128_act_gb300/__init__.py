@@ -111,7 +111,8 @@ def _p(t):
 
 
 def _s(stream):
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+    # the raw handle of torch.cuda.current_stream(), without building the stream object on every call
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
 def _bytes(ws):
@@ -590,13 +591,12 @@ def gemv_nvfp4(x, b, out_dtype=torch.float32, stream=None):
 _NORM_DTYPES = (torch.bfloat16, torch.float32)
 
 
-def _norm_rows(x):
+def _norm_rows(x, n, c):
     """An uninitialized tensor like x whose rows are 16-byte aligned."""
-    n, c = x.shape
-    step = 8 if x.dtype == torch.bfloat16 else 4
-    ld = (c + step - 1) // step * step
-    t = torch.empty((n, ld), dtype=x.dtype, device=x.device)
-    return t if ld == c else t[:, :c]
+    pad = -c % (8 if x.dtype is torch.bfloat16 else 4)
+    if pad == 0:
+        return torch.empty((n, c), dtype=x.dtype, device=x.device)
+    return torch.empty((n, c + pad), dtype=x.dtype, device=x.device)[:, :c]
 
 
 def norm_fwd(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, stream=None):
@@ -608,7 +608,7 @@ def norm_fwd(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, stream=None):
         _want(w, "w", x.dtype, (c,))
     if b is not None:
         _want(b, "b", x.dtype, (c,))
-    y = _norm_rows(x)
+    y = _norm_rows(x, n, c)
     rstd = torch.empty(n, dtype=torch.float32, device=x.device)
     mean = torch.empty(n, dtype=torch.float32, device=x.device) if kind == NORM_LAYER else None
     jetq_norm_fwd(kind, x, w, b, eps, y, mean, rstd, stream)
@@ -625,7 +625,7 @@ def norm_bwd(dy, x, w, mean, rstd, kind=NORM_LAYER, bias=False, workspace=None, 
     _want(rstd, "rstd", torch.float32, (n,))
     if kind == NORM_LAYER:
         _want(mean, "mean", torch.float32, (n,))
-    dx = _norm_rows(x)
+    dx = _norm_rows(x, n, c)
     dw = torch.empty(c, dtype=torch.float32, device=x.device)
     db = torch.empty(c, dtype=torch.float32, device=x.device) if bias else None
     if workspace is None:

@@ -279,7 +279,9 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
         uint8_t *stage = staging + ew * 4096;
         const uint32_t stage_row = ptx::smem_addr(stage) + (uint32_t)lane * 128u;
-        float factor = 1.0f;
+        float factor = 1.0f, gmax = 0.0f;
+        if (MODE == kGrad)
+            gmax = __ldg(p.gmax);
         if (MODE == kGradW16 || MODE == kGradW32)
             factor = __ldg(p.gmax) * p.scale;
         uint32_t tc = 0;
@@ -293,17 +295,17 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
             const int n0 = ni * C::BN + half * 128;
             // per-row inputs of the softmax modes, loaded before the accumulator is ready
             int tcol = -1; // the target's column in this thread's 128, or out of range
-            float lse2 = 0.0f, coef = 0.0f;
+            float lse2 = 0.0f, coef = 0.0f, k2 = 0.0f;
             if (MODE == kStats || MODE == kGrad) {
                 if (row < p.M) {
                     const int64_t tg = __ldg(p.target + row);
                     const int64_t rel = tg - p.col0 - n0;
-                    if (tg >= 0 && rel >= 0 && rel < 128)
+                    if (tg >= 0 && tg < p.V && rel >= 0 && rel < 128)
                         tcol = (int)rel;
-                    if (MODE == kGrad) {
-                        const float gm = __ldg(p.gmax);
+                    if (MODE == kGrad && tg >= 0 && tg < p.V && gmax > 0.0f) {
+                        k2 = p.k2;
                         lse2 = __ldg(p.lse + row) * kLog2e;
-                        coef = tg >= 0 && tg < p.V && gm > 0.0f ? __fdiv_rn(__ldg(p.dloss + row), gm) : 0.0f;
+                        coef = __fdiv_rn(__ldg(p.dloss + row), gmax);
                     }
                 }
             }
@@ -374,27 +376,31 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                 if (valid < 128) {
 #pragma unroll
                     for (int j = 0; j < 128; ++j)
-                        if (j >= valid)
-                            v[j] = -INFINITY;
+                        v[j] = j < valid ? v[j] : -INFINITY;
                 }
-                float m = v[0];
+                float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                for (int j = 1; j < 128; ++j)
-                    m = fmaxf(m, v[j]);
+                for (int j = 4; j < 128; ++j)
+                    m4[j & 3] = fmaxf(m4[j & 3], v[j]);
+                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 const float mk = m * p.k2;
-                float s0 = 0.0f, s1 = 0.0f, zt = 0.0f;
+                float zt = 0.0f;
+                if (__any_sync(0xFFFFFFFFu, tcol >= 0)) { // the target's term is joined exactly by the last kernel
 #pragma unroll
-                for (int j = 0; j < 128; j += 2) {
-                    const float a0 = v[j], a1 = v[j + 1];
-                    const float e0 = ex2(fmaf(a0, p.k2, -mk)), e1 = ex2(fmaf(a1, p.k2, -mk));
-                    zt = j == tcol ? a0 : (j + 1 == tcol ? a1 : zt);
-                    s0 += j == tcol ? 0.0f : e0; // the target's term is joined exactly by the last kernel
-                    s1 += j + 1 == tcol ? 0.0f : e1;
+                    for (int j = 0; j < 128; ++j) {
+                        zt = j == tcol ? v[j] : zt;
+                        v[j] = j == tcol ? -INFINITY : v[j];
+                    }
                 }
+                float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < 128; ++j)
+                    s4[j & 3] += ex2(fmaf(v[j], p.k2, -mk));
                 if (row < p.M) {
                     // no column, or all of them -inf: an empty sum; only NaN: NaN (fmaxf passes over single ones)
+                    const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
                     p.part[(int64_t)(2 * ni + half) * p.M + row] = m == -INFINITY ? make_float2(-INFINITY, 0.0f)
-                                                                   : m == m       ? make_float2(mk, s0 + s1)
+                                                                   : m == m       ? make_float2(mk, sum)
                                                                                   : make_float2(0.0f, m);
                     if (tcol >= 0)
                         p.zt[row] = zt;
@@ -419,22 +425,26 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     if (MODE == kGrad && row0 >= p.M)
                         continue;
                     uint32_t h[32];
+                    if constexpr (MODE == kGrad) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) // a row without a loss: k2, lse2, coef are 0, d = 0
+                            v[j] = __float_as_uint(ex2(fmaf(__uint_as_float(v[j]), k2, -lse2)));
+                        if (__any_sync(0xFFFFFFFFu, tcol >= 64 * g && tcol < 64 * g + 64)) {
+#pragma unroll
+                            for (int j = 0; j < 64; ++j)
+                                v[j] = 64 * g + j == tcol ? __float_as_uint(__uint_as_float(v[j]) - 1.0f) : v[j];
+                        }
+                        if (x0 + 64 > p.N) { // columns past the piece: zero, they are part of the dx product's K
+#pragma unroll
+                            for (int j = 0; j < 64; ++j)
+                                v[j] = x0 + j < p.N ? v[j] : 0u;
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        float y[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float z = __uint_as_float(v[2 * j + e]);
-                            if (MODE == kGrad) {
-                                const int col = 64 * g + 2 * j + e;
-                                const float pr = ex2(fmaf(z, p.k2, -lse2));
-                                const float d = (col == tcol ? pr - 1.0f : pr) * coef;
-                                y[e] = coef != 0.0f && n0 + col < p.N ? d : 0.0f;
-                            } else {
-                                y[e] = z * factor;
-                            }
-                        }
-                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[0], y[1]);
+                        const float f = MODE == kGrad ? coef : factor;
+                        const __nv_bfloat162 b2 =
+                            __floats2bfloat162_rn(__uint_as_float(v[2 * j]) * f, __uint_as_float(v[2 * j + 1]) * f);
                         h[j] = *reinterpret_cast<const uint32_t *>(&b2);
                     }
                     if (lane == 0)
@@ -510,46 +520,57 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
     }
 }
 
-// Joins the (maximum, sum) pairs of a row and its target's logit.  blockDim =
-// (rows, lanes): threadIdx.x walks rows (contiguous in part), threadIdx.y parts.
-__global__ void k_ce_join(const float2 *part, const float *zt, const int64_t *target, int64_t n, int64_t v, int parts,
-                          float k2, float *loss, float *lse)
+__device__ __forceinline__ void join_pair(float2 &a, const float2 b)
 {
-    extern __shared__ float2 red[];
+    const float m = fmaxf(a.x, b.x);
+    if (m > -INFINITY)
+        a = make_float2(m, a.y * ex2(a.x - m) + b.y * ex2(b.x - m));
+    else
+        a.y += b.y; // both empty (or NaN)
+}
+
+// Joins the (maximum, sum) pairs of a row and its target's logit.  blockDim =
+// (rows, lanes), powers of two: threadIdx.x walks rows (contiguous in part),
+// threadIdx.y parts.
+__global__ void __launch_bounds__(1024)
+    k_ce_join(const float2 *part, const float *zt, const int64_t *target, int64_t n, int64_t v, int parts, float k2,
+              float *loss, float *lse)
+{
+    __shared__ float2 red[1024];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    float m = -INFINITY, s = 0.0f;
+    float2 a = make_float2(-INFINITY, 0.0f);
     if (row < n)
-        for (int q = threadIdx.y; q < parts; q += blockDim.y) {
-            const float2 a = part[(int64_t)q * n + row];
-            const float nm = fmaxf(m, a.x);
-            if (nm > -INFINITY) {
-                s = s * ex2(m - nm) + a.y * ex2(a.x - nm);
-                m = nm;
-            }
+        for (int q = threadIdx.y; q < parts; q += 4 * blockDim.y) { // four loads in flight
+            float2 b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b[i] = q + i * (int)blockDim.y < parts ? __ldg(part + (int64_t)(q + i * blockDim.y) * n + row)
+                                                       : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                join_pair(a, b[i]);
         }
-    red[threadIdx.y * blockDim.x + threadIdx.x] = make_float2(m, s);
-    __syncthreads();
-    if (threadIdx.y != 0 || row >= n)
-        return;
-    for (int q = 1; q < (int)blockDim.y; ++q) {
-        const float2 a = red[q * blockDim.x + threadIdx.x];
-        const float nm = fmaxf(m, a.x);
-        if (nm > -INFINITY) {
-            s = s * ex2(m - nm) + a.y * ex2(a.x - nm);
-            m = nm;
+    red[threadIdx.y * blockDim.x + threadIdx.x] = a;
+    for (int o = blockDim.y / 2; o; o >>= 1) {
+        __syncthreads();
+        if ((int)threadIdx.y < o) {
+            join_pair(a, red[(threadIdx.y + o) * blockDim.x + threadIdx.x]);
+            red[threadIdx.y * blockDim.x + threadIdx.x] = a;
         }
     }
+    if (threadIdx.y != 0 || row >= n)
+        return;
     const int64_t tg = target[row];
     if (tg < 0 || tg >= v) {
-        lse[row] = kLn2 * (m + log2f(s));
+        lse[row] = kLn2 * (a.x + log2f(a.y));
         loss[row] = 0.0f;
         return;
     }
     const float t2 = zt[row] * k2;
-    lse[row] = kLn2 * (m + log2f(s + ex2(t2 - m)));
-    loss[row] = t2 >= m ? log1pf(s) : kLn2 * (m - t2) + logf(s + ex2(t2 - m));
+    lse[row] = kLn2 * (a.x + log2f(a.y + ex2(t2 - a.x)));
+    loss[row] = t2 >= a.x ? log1pf(a.y) : kLn2 * (a.x - t2) + logf(a.y + ex2(t2 - a.x));
 }
 
 // gmax = max |dloss| over the rows with a target (1 where that is not finite).
@@ -761,11 +782,14 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
     e = cg == 2 ? run_head<2, kStats>(ta, tb, ta, p, st) : run_head<1, kStats>(ta, tb, ta, p, st);
     if (e != cudaSuccess)
         return e;
-    int rx = 1;
-    while (rx < 32 && rx < a.n)
+    const int parts = 2 * p.nt;
+    int rx = 1, ry = 1;
+    while (rx < 8 && rx < a.n)
         rx *= 2;
-    return launch_pdl(k_ce_join, dim3((unsigned)ceil_div(a.n, rx)), dim3(rx, 256 / rx), 256 * sizeof(float2), st,
-                      (const float2 *)p.part, (const float *)p.zt, a.target, a.n, a.v, 2 * p.nt, p.k2, a.loss, a.lse);
+    while (rx * ry < 1024 && ry < parts)
+        ry *= 2;
+    return launch_pdl(k_ce_join, dim3((unsigned)ceil_div(a.n, rx)), dim3(rx, ry), 0, st, (const float2 *)p.part,
+                      (const float *)p.zt, a.target, a.n, a.v, parts, p.k2, a.loss, a.lse);
 }
 
 cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)

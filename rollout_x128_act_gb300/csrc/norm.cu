@@ -320,14 +320,22 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_ctas(G, (int)siz
                 mean = group_sum<G>(mean, red, group, wg, lane, buf) * inv_c;
             }
 #pragma unroll
-            for (int k = 0; k < V; ++k)
+            for (int k = 0; k < V; ++k) {
+                const int pos = (k * C::kLanes + lt) * E;
+                if (RMS || pos + E <= p.c) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int i = k * E + e;
-                    if constexpr (!RMS)
-                        h[i] = (k * C::kLanes + lt) * E + e < p.c ? h[i] - mean : 0.0f;
-                    sq = fmaf(h[i], h[i], sq);
+                    for (int e = 0; e < E; ++e) {
+                        h[k * E + e] -= mean;
+                        sq = fmaf(h[k * E + e], h[k * E + e], sq);
+                    }
+                } else { // columns past c do not count
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        h[k * E + e] = pos + e < p.c ? h[k * E + e] - mean : 0.0f;
+                        sq = fmaf(h[k * E + e], h[k * E + e], sq);
+                    }
                 }
+            }
             sq = group_sum<G>(sq, red, group, wg, lane, buf);
             // every lane has its row in registers: the stage takes the next row
             refill(row + (int64_t)p.stages * step);
