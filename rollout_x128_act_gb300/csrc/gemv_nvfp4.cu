@@ -28,8 +28,8 @@ namespace jetq {
 
 namespace {
 
-constexpr int kWarps = 8, kRows = 16, kStep = 128; // columns a warp step
-constexpr int kUnroll = 4;                         // steps whose loads are in flight together
+constexpr int kRows = 16, kStep = 128; // rows a CTA, columns a warp step
+constexpr int kUnroll = 2;             // steps a batch; the next batch's loads are in flight under a batch's arithmetic
 
 struct GemvParams {
     const uint8_t *q, *sb;
@@ -81,8 +81,10 @@ __device__ __forceinline__ void decode_scales(uint32_t s2, uint32_t (&out)[2])
     }
 }
 
-template <int MT> // tokens in eights
-__global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2) k_gemv_nvfp4(const GemvParams p)
+// MT: tokens in eights; kWarps: shares of K a CTA
+template <int MT, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 1 : (MT == 1 ? 24 : 16) / kWarps)
+    k_gemv_nvfp4(const GemvParams p)
 {
     __shared__ float red[kWarps][kRows][8 * MT + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -101,30 +103,35 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2) k_gemv_nvfp4(con
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
 
-    for (int s = s0; s < s1; s += kUnroll) {
-        uint4 ca[kUnroll], cb[kUnroll];
+    struct Batch {
+        uint4 ca[kUnroll], cb[kUnroll]; // codes of rows g and g + 8
         uint32_t fa[kUnroll], fb[kUnroll];
+    };
+    auto load = [&](int s, Batch &b) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int64_t k = (int64_t)(s + u) * kStep + t * 32;
-            ca[u] = cb[u] = make_uint4(0, 0, 0, 0);
-            fa[u] = fb[u] = 0;
+            b.ca[u] = b.cb[u] = make_uint4(0, 0, 0, 0);
+            b.fa[u] = b.fb[u] = 0;
             if (s + u < s1 && k < p.k) {
-                ca[u] = __ldcs(reinterpret_cast<const uint4 *>(qa + k / 2)); // each weight is read once
-                cb[u] = __ldcs(reinterpret_cast<const uint4 *>(qb + k / 2));
-                fa[u] = __ldg(reinterpret_cast<const uint16_t *>(sa + k / 16));
-                fb[u] = __ldg(reinterpret_cast<const uint16_t *>(sbb + k / 16));
+                b.ca[u] = __ldcs(reinterpret_cast<const uint4 *>(qa + k / 2)); // each weight is read once
+                b.cb[u] = __ldcs(reinterpret_cast<const uint4 *>(qb + k / 2));
+                b.fa[u] = __ldg(reinterpret_cast<const uint16_t *>(sa + k / 16));
+                b.fb[u] = __ldg(reinterpret_cast<const uint16_t *>(sbb + k / 16));
             }
         }
+    };
+    auto multiply = [&](int s, const Batch &b) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             if (s + u >= s1)
                 break;
             const int64_t k = (int64_t)(s + u) * kStep + t * 32;
             uint32_t sca[2], scb[2];
-            decode_scales(fa[u], sca);
-            decode_scales(fb[u], scb);
-            const uint32_t wa[4] = {ca[u].x, ca[u].y, ca[u].z, ca[u].w}, wb[4] = {cb[u].x, cb[u].y, cb[u].z, cb[u].w};
+            decode_scales(b.fa[u], sca);
+            decode_scales(b.fb[u], scb);
+            const uint32_t wa[4] = {b.ca[u].x, b.ca[u].y, b.ca[u].z, b.ca[u].w};
+            const uint32_t wb[4] = {b.cb[u].x, b.cb[u].y, b.cb[u].z, b.cb[u].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) { // eight values of each row
                 uint32_t pa[4], pb[4];
@@ -144,6 +151,13 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 3 : 2) k_gemv_nvfp4(con
                 }
             }
         }
+    };
+    Batch now, next;
+    load(s0, now);
+    for (int s = s0; s < s1; s += kUnroll) {
+        load(s + kUnroll, next); // past s1: zeros, no load
+        multiply(s, now);
+        now = next;
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -186,9 +200,18 @@ cudaError_t launch_gemv_nvfp4(const GemvNvfp4Args &a, cudaStream_t st)
     p.m = (int)a.m;
     p.y = a.y;
     p.out_bf16 = a.out_dtype == JETQ_OUT_BF16;
-    const dim3 grid((unsigned)((a.n + kRows - 1) / kRows)), block(32 * kWarps);
-    return a.m <= 8 ? launch_pdl(k_gemv_nvfp4<1>, grid, block, 0, st, p)
-                    : launch_pdl(k_gemv_nvfp4<2>, grid, block, 0, st, p);
+    // Shares of K: four warps a CTA where there are CTAs enough for several an
+    // SM, sixteen (more loads of a row block in flight) where there is one at most.
+    const int64_t blocks = (a.n + kRows - 1) / kRows;
+    const dim3 grid((unsigned)blocks);
+    if (blocks >= 3 * (int64_t)sm_count())
+        return a.m <= 8 ? launch_pdl(k_gemv_nvfp4<1, 4>, grid, dim3(128), 0, st, p)
+                        : launch_pdl(k_gemv_nvfp4<2, 4>, grid, dim3(128), 0, st, p);
+    if (blocks > sm_count())
+        return a.m <= 8 ? launch_pdl(k_gemv_nvfp4<1, 8>, grid, dim3(256), 0, st, p)
+                        : launch_pdl(k_gemv_nvfp4<2, 8>, grid, dim3(256), 0, st, p);
+    return a.m <= 8 ? launch_pdl(k_gemv_nvfp4<1, 16>, grid, dim3(512), 0, st, p)
+                    : launch_pdl(k_gemv_nvfp4<2, 16>, grid, dim3(512), 0, st, p);
 }
 
 } // namespace jetq

@@ -58,6 +58,7 @@ enum HeadMode : int {
 struct HeadParams {
     int mt, nt, splits, num_kb, group; // tiles of M and N, splits and 64-blocks of K, M tiles per raster group
     int64_t M, N;                      // valid rows and columns of the output
+    int bn, box_a;                     // columns a tile (kStats; else 256), rows of A's box
     float k2;                          // scale * log2(e): exponents in base 2
     const int64_t *target;
     int64_t V, col0;                   // whole vocabulary; first vocabulary row of this piece
@@ -76,11 +77,12 @@ struct HeadCfg {
     static constexpr int kBRows = BN / CG; // rows of B in one CTA's shared memory
     static constexpr int kBBytes = kBRows * 128;
     static constexpr int kStage = kABytes + kBBytes;
-    static constexpr int kStages = 6 * 32768 / kStage;
     static constexpr int kEpiWarps = 8;
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
     static constexpr bool kStaging = MODE != kStats;
-    static constexpr size_t kStagingBytes = kStaging ? kEpiWarps * 4096 : 0;
+    // two 4 KB boxes a warp: a store leaves under the next box's arithmetic
+    static constexpr size_t kStagingBytes = kStaging ? kEpiWarps * 2 * 4096 : 0;
+    static constexpr int kStages = (int)((225 * 1024 - kStagingBytes) / kStage);
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kStagingBytes + 256;
     // 64-blocks of K summed inside the tensor core before the epilogue takes the partial tile
     static constexpr int kFold = MODE == kStats ? (CG == 2 ? 8 : 2) : 1 << 30;
@@ -141,6 +143,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
     const int unit = blockIdx.x / CG, units = gridDim.x / CG;
     unsigned *err = &g_linear_ce_error;
     const int num_tiles = p.mt * p.nt * p.splits;
+    const int bn = MODE == kStats ? p.bn : C::BN;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -182,6 +185,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
     if (warp < 4) {
         if (warp == 0 && lane == 0) {
             // -------------------------------------------------- TMA producer
+            const uint32_t tx = MODE == kStats ? (uint32_t)(CG * p.box_a + bn) * 128u : (uint32_t)(CG * C::kStage);
             uint32_t it = 0;
             bool ok = true;
             for (int t = unit; t < num_tiles && ok; t += units) {
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                 const int k0 = (int)((int64_t)p.num_kb * ks / p.splits);
                 const int k1 = (int)((int64_t)p.num_kb * (ks + 1) / p.splits);
                 const int m0 = mi * 128 * CG + (int)rank * 128;
-                const int n0 = ni * C::BN + (int)rank * C::kBRows;
+                const int n0 = ni * bn + (int)rank * (bn / CG);
                 for (int kb = k0; kb < k1; ++kb, ++it) {
                     const int s = (int)(it % S);
                     const uint32_t ph = (it / S) & 1u;
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     }
                     // the pair's bytes are counted on the even CTA's barrier, whose thread issues the MMAs
                     if (rank == 0)
-                        ptx::mbar_arrive_expect_tx(full(s), (uint32_t)(CG * C::kStage));
+                        ptx::mbar_arrive_expect_tx(full(s), tx);
                     const uint32_t bar = CG == 2 ? ptx::map_to_cta(full(s), 0) : full(s);
                     const uint32_t da = ptx::smem_addr(tiles + (size_t)s * C::kStage), db = da + C::kABytes;
                     if (C::kAMn) {
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     }
         } else if (warp == 1 && lane == 0 && rank == 0) {
             // -------------------------------------------------- MMA issuer
-            constexpr uint32_t idesc = ptx::idesc_bf16_f32(128 * CG, C::BN, C::kAMn, C::kBMn);
+            const uint32_t idesc = ptx::idesc_bf16_f32(128 * CG, bn, C::kAMn, C::kBMn);
             constexpr uint32_t a_step = C::kAMn ? 2048u >> 4 : 32u >> 4, b_step = C::kBMn ? 2048u >> 4 : 32u >> 4;
             uint32_t it = 0, tc = 0;
             bool ok = true;
@@ -277,8 +281,8 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
         // ------------------------------------------------------ epilogue
         const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-        uint8_t *stage = staging + ew * 4096;
-        const uint32_t stage_row = ptx::smem_addr(stage) + (uint32_t)lane * 128u;
+        const uint32_t stage = ptx::smem_addr(staging) + (uint32_t)ew * 8192u;
+        uint32_t box = 0; // the staging buffer in turn
         float factor = 1.0f, gmax = 0.0f;
         if (MODE == kGrad)
             gmax = __ldg(p.gmax);
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                 continue;
             const int row0 = mi * 128 * CG + (int)rank * 128 + quarter * 32;
             const int64_t row = (int64_t)row0 + lane;
-            const int n0 = ni * C::BN + half * 128;
+            const int n0 = ni * bn + half * 128;
             // per-row inputs of the softmax modes, loaded before the accumulator is ready
             int tcol = -1; // the target's column in this thread's 128, or out of range
             float lse2 = 0.0f, coef = 0.0f, k2 = 0.0f;
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                 if (row < p.M) {
                     const int64_t tg = __ldg(p.target + row);
                     const int64_t rel = tg - p.col0 - n0;
-                    if (tg >= 0 && tg < p.V && rel >= 0 && rel < 128)
+                    if (tg >= 0 && tg < p.V && rel >= 0 && rel < (MODE == kStats ? min(128, bn - half * 128) : 128))
                         tcol = (int)rel;
                     if (MODE == kGrad && tg >= 0 && tg < p.V && gmax > 0.0f) {
                         k2 = p.k2;
@@ -372,7 +376,8 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     v[2 * j] = z[j].x;
                     v[2 * j + 1] = z[j].y;
                 }
-                const int valid = (int)min((int64_t)128, p.N - n0); // columns of this thread inside the vocabulary
+                // this thread's columns inside the tile and the vocabulary
+                const int valid = (int)min((int64_t)min(128, bn - half * 128), p.N - n0);
                 if (valid < 128) {
 #pragma unroll
                     for (int j = 0; j < 128; ++j)
@@ -447,8 +452,10 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                             __floats2bfloat162_rn(__uint_as_float(v[2 * j]) * f, __uint_as_float(v[2 * j + 1]) * f);
                         h[j] = *reinterpret_cast<const uint32_t *>(&b2);
                     }
+                    const uint32_t sbox = stage + box * 4096u, stage_row = sbox + (uint32_t)lane * 128u;
+                    box ^= 1u;
                     if (lane == 0)
-                        ptx::bulk_wait_group_read<0>(); // the previous box has left the staging area
+                        ptx::bulk_wait_group_read<1>(); // the box before last has left its buffer
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -457,7 +464,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        ptx::tma_store_3d(&tmO, ptx::smem_addr(stage), x0, row0, 0);
+                        ptx::tma_store_3d(&tmO, sbox, x0, row0, 0);
                         ptx::bulk_commit_group();
                     }
                 }
@@ -481,8 +488,10 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                         for (int j = 0; j < 32; ++j)
                             v[j] = __float_as_uint(__uint_as_float(v[j]) * factor);
                     }
+                    const uint32_t sbox = stage + box * 4096u, stage_row = sbox + (uint32_t)lane * 128u;
+                    box ^= 1u;
                     if (lane == 0)
-                        ptx::bulk_wait_group_read<0>();
+                        ptx::bulk_wait_group_read<1>();
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -492,9 +501,9 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) {
                         if (p.add)
-                            ptx::tma_add_3d(&tmO, ptx::smem_addr(stage), x0, row0, ks);
+                            ptx::tma_add_3d(&tmO, sbox, x0, row0, ks);
                         else
-                            ptx::tma_store_3d(&tmO, ptx::smem_addr(stage), x0, row0, ks);
+                            ptx::tma_store_3d(&tmO, sbox, x0, row0, ks);
                         ptx::bulk_commit_group();
                     }
                 }
@@ -689,6 +698,8 @@ cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorM
 // against 8.72); single CTAs waste less where the rows do not fill pairs.
 int pick_cg(int64_t rows, int64_t tiles_n)
 {
+    if (rows <= 128)
+        return 1;
     const int64_t w1 = ceil_div(ceil_div(rows, 128) * tiles_n, units_of(1));
     const int64_t w2 = ceil_div(ceil_div(rows, 256) * tiles_n, units_of(2));
     return 100 * w2 <= 108 * w1 ? 2 : 1;
@@ -743,9 +754,14 @@ int64_t preferred_piece(int64_t n)
 
 } // namespace
 
+// Tiles of the forward product's vocabulary axis: 256 columns each, or, for one
+// row tile, evenly over the SMs.
 size_t linear_ce_fwd_workspace(int64_t n, int64_t v)
 {
-    return (size_t)(2 * ceil_div(v, kTileN)) * (size_t)n * 8 + (size_t)n * 4;
+    int64_t nt = ceil_div(v, kTileN);
+    if (n <= 128) // never more than the waves' whole tiles
+        nt = ceil_div(nt, units_of(1)) * units_of(1);
+    return (size_t)(2 * nt) * (size_t)n * 8 + (size_t)n * 4;
 }
 
 size_t linear_ce_bwd_workspace(int64_t n, int64_t v, int64_t c)
@@ -763,10 +779,21 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
     HeadParams p = {};
     p.nt = (int)ceil_div(a.v, kTileN);
     const int cg = pick_cg(a.n, p.nt);
+    p.bn = kTileN;
+    p.box_a = 128;
+    if (cg == 1 && a.n <= 128) {
+        // One row tile: the weight's stream is what takes time, so its rows are
+        // spread evenly over the SMs (a multiple of 16 a tile), and x's box
+        // holds its rows only (the others' sums are not stored).
+        const int64_t waves = ceil_div(p.nt, units_of(1));
+        p.bn = (int)(ceil_div(ceil_div(a.v, waves * units_of(1)), 16) * 16);
+        p.nt = (int)ceil_div(a.v, p.bn);
+        p.box_a = (int)(ceil_div(a.n, 8) * 8);
+    }
     CUtensorMap ta, tb;
     cudaError_t e;
-    if ((e = make_sw128_map(&ta, a.x, false, a.c, a.n, a.ldx, 128)) != cudaSuccess ||
-        (e = make_sw128_map(&tb, a.w, false, a.c, a.v, a.ldw, kTileN / cg)) != cudaSuccess)
+    if ((e = make_sw128_map(&ta, a.x, false, a.c, a.n, a.ldx, p.box_a)) != cudaSuccess ||
+        (e = make_sw128_map(&tb, a.w, false, a.c, a.v, a.ldw, p.bn / cg)) != cudaSuccess)
         return e;
     p.mt = (int)ceil_div(a.n, 128 * cg);
     p.splits = 1;

@@ -34,7 +34,6 @@ namespace {
 
 constexpr unsigned kErrTimeout = 1u;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
-constexpr int kLaneElems = 16;
 
 struct NormParams {
     const void *x, *dy, *w, *b;
@@ -93,10 +92,10 @@ struct Vec<float> {
     static __device__ __forceinline__ void put(float *p, float f) { *p = f; }
 };
 
-template <class T, int G>
+template <class T, int G, int LE>
 struct NormCfg {
     static constexpr int E = Vec<T>::E;
-    static constexpr int V = kLaneElems / E;   // 16-byte vectors a lane
+    static constexpr int V = LE / E;           // 16-byte vectors a lane
     static constexpr int kWarps = G < 8 ? 8 : G;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kGroups = kWarps / G; // rows in work a CTA
@@ -152,21 +151,18 @@ __device__ __forceinline__ float group_sum(float a, float2 *red, int group, int 
     return a;
 }
 
-// The parameters (w, b) of a lane's columns as they are stored, zero past c; `fallback` without one.
-template <class T, int G>
-__device__ __forceinline__ void load_params(const void *p, int c, int lt, float fallback, uint4 *packed)
+// The parameters (w, b) of a lane's columns, zero past c; `fallback` without one.
+template <class T, int G, int LE>
+__device__ __forceinline__ void load_params(const void *p, int c, int lt, float fallback, float (&f)[LE])
 {
-    using C = NormCfg<T, G>;
+    using C = NormCfg<T, G, LE>;
 #pragma unroll
-    for (int k = 0; k < C::V; ++k) {
-        float f[C::E];
+    for (int k = 0; k < C::V; ++k)
 #pragma unroll
         for (int e = 0; e < C::E; ++e) {
             const int col = (k * C::kLanes + lt) * C::E + e;
-            f[e] = col < c ? (p ? Vec<T>::get(static_cast<const T *>(p) + col) : fallback) : 0.0f;
+            f[k * C::E + e] = col < c ? (p ? Vec<T>::get(static_cast<const T *>(p) + col) : fallback) : 0.0f;
         }
-        packed[k] = Vec<T>::pack(f);
-    }
 }
 
 // A row vector of a lane from the ring (whole vectors) or, where the last
@@ -218,17 +214,17 @@ __device__ __forceinline__ void issue_row(uint32_t bar, uint32_t dst, uint32_t s
         ptx::bulk_load(dst + stride, b, bytes, bar);
 }
 
-// CTAs an SM that the registers allow (packed BF16 parameters leave room for one more).
-__host__ __device__ constexpr int norm_ctas(int g, int esize, bool bwd)
+// CTAs an SM that the registers allow.
+__host__ __device__ constexpr int norm_ctas(int g, int le, bool bwd)
 {
-    return g == 16 ? 1 : (bwd ? 2 : (esize == 2 ? 4 : 3));
+    return g == 16 ? 1 : (bwd || le == 32 ? 2 : 3);
 }
 
-template <class T, int G, bool RMS, bool BWD>
-__global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_ctas(G, (int)sizeof(T), BWD))
+template <class T, int G, int LE, bool RMS, bool BWD>
+__global__ void __launch_bounds__(NormCfg<T, G, LE>::kThreads, norm_ctas(G, LE, BWD))
     k_norm(const NormParams p)
 {
-    using C = NormCfg<T, G>;
+    using C = NormCfg<T, G, LE>;
     constexpr int E = C::E, V = C::V;
     extern __shared__ uint8_t smem_raw[];
     __shared__ float2 red[2 * 16];
@@ -269,14 +265,14 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_ctas(G, (int)siz
             last_issued = row;
         }
 
-    uint4 w[V], b[BWD ? 1 : V]; // unpacked where they are used: registers for another CTA an SM
-    load_params<T, G>(p.w, p.c, lt, 1.0f, w);
+    float w[LE], b[BWD ? 1 : LE];
+    load_params<T, G, LE>(p.w, p.c, lt, 1.0f, w);
     if constexpr (!BWD)
-        load_params<T, G>(p.b, p.c, lt, 0.0f, b);
-    float dw[BWD ? kLaneElems : 1], db[BWD && !RMS ? kLaneElems : 1];
+        load_params<T, G, LE>(p.b, p.c, lt, 0.0f, b);
+    float dw[BWD ? LE : 1], db[BWD && !RMS ? LE : 1];
     if constexpr (BWD) {
 #pragma unroll
-        for (int i = 0; i < kLaneElems; ++i) {
+        for (int i = 0; i < LE; ++i) {
             dw[i] = 0.0f;
             if constexpr (!RMS)
                 db[i] = 0.0f;
@@ -307,35 +303,41 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_ctas(G, (int)siz
             ok = ptx::mbar_wait(bar(s), ph, abort_flag, &g_norm_error, kErrTimeout, p.limit_ns);
         const bool last_row = row == p.n - 1;
         const uint8_t *st = mine + (size_t)s * stage_bytes;
-        float h[kLaneElems];
+        float h[LE];
 #pragma unroll
         for (int k = 0; k < V; ++k)
             load_vec<T>(st, x + row * p.ldx, last_row, (k * C::kLanes + lt) * E, p.c, h + k * E);
         if constexpr (!BWD) {
-            float mean = 0.0f, sq = 0.0f;
+            // pairs: the packed FP32 instructions do two elements an issue slot
+            float mean = 0.0f;
             if constexpr (!RMS) {
+                float2 a = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int i = 0; i < kLaneElems; ++i)
-                    mean += h[i];
-                mean = group_sum<G>(mean, red, group, wg, lane, buf) * inv_c;
-            }
+                for (int i = 0; i < LE; i += 2)
+                    a = __fadd2_rn(a, make_float2(h[i], h[i + 1]));
+                mean = group_sum<G>(a.x + a.y, red, group, wg, lane, buf) * inv_c;
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const int pos = (k * C::kLanes + lt) * E;
-                if (RMS || pos + E <= p.c) {
+                for (int k = 0; k < V; ++k) {
+                    const int pos = (k * C::kLanes + lt) * E;
+                    if (pos + E <= p.c) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        h[k * E + e] -= mean;
-                        sq = fmaf(h[k * E + e], h[k * E + e], sq);
-                    }
-                } else { // columns past c do not count
+                        for (int i = k * E; i < (k + 1) * E; i += 2) {
+                            const float2 d = __fadd2_rn(make_float2(h[i], h[i + 1]), make_float2(-mean, -mean));
+                            h[i] = d.x;
+                            h[i + 1] = d.y;
+                        }
+                    } else { // columns past c do not count
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        h[k * E + e] = pos + e < p.c ? h[k * E + e] - mean : 0.0f;
-                        sq = fmaf(h[k * E + e], h[k * E + e], sq);
+                        for (int e = 0; e < E; ++e)
+                            h[k * E + e] = pos + e < p.c ? h[k * E + e] - mean : 0.0f;
                     }
                 }
             }
+            float2 q = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < LE; i += 2)
+                q = __ffma2_rn(make_float2(h[i], h[i + 1]), make_float2(h[i], h[i + 1]), q);
+            float sq = q.x + q.y;
             sq = group_sum<G>(sq, red, group, wg, lane, buf);
             // every lane has its row in registers: the stage takes the next row
             refill(row + (int64_t)p.stages * step);
@@ -347,12 +349,16 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_ctas(G, (int)siz
             }
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                float y[E], wf[E], bf[E];
-                Vec<T>::unpack(w[k], wf);
-                Vec<T>::unpack(b[k], bf);
+                float y[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    y[e] = fmaf(h[k * E + e] * rstd, wf[e], bf[e]);
+                for (int e = 0; e < E; e += 2) {
+                    const int i = k * E + e;
+                    const float2 v = __ffma2_rn(
+                        __fmul2_rn(make_float2(h[i], h[i + 1]), make_float2(rstd, rstd)),
+                        make_float2(w[i], w[i + 1]), make_float2(b[i], b[i + 1]));
+                    y[e] = v.x;
+                    y[e + 1] = v.y;
+                }
                 const int pos = (k * C::kLanes + lt) * E;
                 if (pos < p.c)
                     store_vec<T>(out + row * p.ldo, pos, p.c, y);
@@ -363,15 +369,13 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_ctas(G, (int)siz
                 next_mean = RMS ? 0.0f : __ldg(p.mean + row + step);
                 next_rstd = __ldg(p.rstd + row + step);
             }
-            float t[kLaneElems];
+            float t[LE];
 #pragma unroll
             for (int k = 0; k < V; ++k)
                 load_vec<T>(st + row_bytes, dy + row * p.lddy, last_row, (k * C::kLanes + lt) * E, p.c, t + k * E);
             float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                float wf[E];
-                Vec<T>::unpack(w[k], wf);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const int i = k * E + e;
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_ctas(G, (int)siz
                     dw[i] = fmaf(t[i], h[i], dw[i]); // columns past c: t = 0
                     if constexpr (!RMS)
                         db[i] += t[i];
-                    t[i] *= wf[e];
+                    t[i] *= w[i];
                     if constexpr (!RMS)
                         s1 += t[i];
                     s2 = fmaf(t[i], h[i], s2);
@@ -554,10 +558,19 @@ __global__ void __launch_bounds__(256) k_norm_wide_params(const NormParams p)
 
 constexpr int kWidest = 8192, kWideSlices = 64, kMaxStages = 4;
 
-int warps_of(int64_t c)
+// Elements a lane holds.  Forward: 32 (half the reductions and waits of 16 for
+// every element; 16384 x 4096 measured in the launcher's comment), 16 where a
+// single warp of them holds the row.  Backward: 16 (x, dy and the sums of dw
+// and db take four registers an element).
+int lane_elems(int64_t c, bool bwd)
+{
+    return bwd || c <= 512 ? 16 : 32;
+}
+
+int warps_of(int64_t c, int le)
 {
     int g = 1;
-    while (g * 32 * kLaneElems < c)
+    while (g * 32 * le < c)
         g *= 2;
     return g;
 }
@@ -573,10 +586,10 @@ struct NormPlan {
 NormPlan norm_plan(int64_t n, int64_t c, int esize, bool bwd)
 {
     NormPlan r;
-    const int g = warps_of(c), per_cta = g < 8 ? 8 / g : 1;
+    const int le = lane_elems(c, bwd), g = warps_of(c, le), per_cta = g < 8 ? 8 / g : 1;
     const size_t row = (size_t)((c * esize + 15) / 16 * 16) * (bwd ? 2 : 1);
     r.stages = kMaxStages;
-    const int ctas = norm_ctas(g, esize, bwd);
+    const int ctas = norm_ctas(g, le, bwd);
     while (r.stages > 2 && ctas * (r.stages * per_cta * row + 2048) > 227 * 1024)
         --r.stages;
     r.smem = r.stages * per_cta * row + 128;
@@ -591,10 +604,10 @@ NormPlan norm_plan(int64_t n, int64_t c, int esize, bool bwd)
     return r;
 }
 
-template <class T, int G, bool RMS, bool BWD>
+template <class T, int G, int LE, bool RMS, bool BWD>
 cudaError_t run_norm(const NormParams &p, const NormPlan &plan, cudaStream_t st)
 {
-    auto kern = k_norm<T, G, RMS, BWD>;
+    auto kern = k_norm<T, G, LE, RMS, BWD>;
     static int configured_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -605,19 +618,27 @@ cudaError_t run_norm(const NormParams &p, const NormPlan &plan, cudaStream_t st)
             return e;
         configured_device = dev;
     }
-    return launch_pdl(kern, dim3((unsigned)plan.grid), dim3(NormCfg<T, G>::kThreads), plan.smem, st, p);
+    return launch_pdl(kern, dim3((unsigned)plan.grid), dim3(NormCfg<T, G, LE>::kThreads), plan.smem, st, p);
 }
 
 template <class T, bool RMS, bool BWD>
 cudaError_t pick_norm(const NormParams &p, const NormPlan &plan, cudaStream_t st)
 {
-    switch (warps_of(p.c)) {
-    case 1: return run_norm<T, 1, RMS, BWD>(p, plan, st);
-    case 2: return run_norm<T, 2, RMS, BWD>(p, plan, st);
-    case 4: return run_norm<T, 4, RMS, BWD>(p, plan, st);
-    case 8: return run_norm<T, 8, RMS, BWD>(p, plan, st);
-    default: return run_norm<T, 16, RMS, BWD>(p, plan, st);
+    constexpr int kFull = BWD ? 16 : 32;
+    const int le = lane_elems(p.c, BWD);
+    if (le != kFull)
+        return run_norm<T, 1, 16, RMS, BWD>(p, plan, st);
+    switch (warps_of(p.c, le)) {
+    case 1: return run_norm<T, 1, kFull, RMS, BWD>(p, plan, st);
+    case 2: return run_norm<T, 2, kFull, RMS, BWD>(p, plan, st);
+    case 4: return run_norm<T, 4, kFull, RMS, BWD>(p, plan, st);
+    case 8: return run_norm<T, 8, kFull, RMS, BWD>(p, plan, st);
+    default: break;
     }
+    if constexpr (BWD)
+        return run_norm<T, 16, 16, RMS, true>(p, plan, st);
+    else
+        return cudaErrorInvalidValue; // 8 warps of 32 hold every row up to kWidest
 }
 
 template <class T, bool RMS>
