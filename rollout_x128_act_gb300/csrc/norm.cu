@@ -10,16 +10,24 @@
 // pass over registers), and each output is rounded once.
 //
 // Bound: HBM (two rows of traffic a row forward, three backward).  A group of
-// G warps owns one row at a time, 16 elements a lane, so a row is read from
-// memory once and stays in registers between the statistics and the output.
-// The group's next rows are in flight meanwhile: one thread keeps a ring of
-// bulk copies into shared memory ahead of the group (loads issued by the
-// threads themselves leave too few bytes in flight between a row's two
-// reductions).  A lane's columns are the same in every row, so the backward
-// pass sums dw and db in registers and writes one partial row a group; a
-// second kernel adds the partial rows in a fixed order (no atomics: results
-// are bitwise repeatable).  Rows wider than 16 warps hold (8192) take the
-// k_norm_*_wide kernels, which read a row more than once.
+// warps owns one row at a time; its next rows are in flight meanwhile: one
+// thread keeps a ring of bulk copies into shared memory ahead of the group
+// (loads issued by the threads themselves leave too few bytes in flight
+// between a row's two reductions).
+//
+// Forward: a warp a row (up to 8 KB; 2 or 4 warps above, 8 where there are
+// fewer rows than SMs), which runs over the row in shared memory for the mean,
+// the spread and the output.  A first version with a row in the registers of 8
+// warps spent half its instructions on the reductions, waits and addresses of
+// each warp's 512 elements: 16384 x 4096 BF16 took 62 us.
+//
+// Backward: 1 to 16 warps a row, 16 elements a lane in registers.  A lane's
+// columns are the same in every row, so dw and db are summed in registers; each
+// group writes one partial row and a second kernel adds the partial rows in a
+// fixed order (no atomics: results are bitwise repeatable).
+//
+// Rows wider than 8192 take the k_norm_*wide* kernels, which read a row from
+// memory more than once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -92,7 +100,9 @@ struct Vec<float> {
     static __device__ __forceinline__ void put(float *p, float f) { *p = f; }
 };
 
-template <class T, int G, int LE>
+constexpr int LE = 16; // elements a lane (backward)
+
+template <class T, int G>
 struct NormCfg {
     static constexpr int E = Vec<T>::E;
     static constexpr int V = LE / E;           // 16-byte vectors a lane
@@ -152,10 +162,10 @@ __device__ __forceinline__ float group_sum(float a, float2 *red, int group, int 
 }
 
 // The parameters (w, b) of a lane's columns, zero past c; `fallback` without one.
-template <class T, int G, int LE>
+template <class T, int G>
 __device__ __forceinline__ void load_params(const void *p, int c, int lt, float fallback, float (&f)[LE])
 {
-    using C = NormCfg<T, G, LE>;
+    using C = NormCfg<T, G>;
 #pragma unroll
     for (int k = 0; k < C::V; ++k)
 #pragma unroll
@@ -215,16 +225,15 @@ __device__ __forceinline__ void issue_row(uint32_t bar, uint32_t dst, uint32_t s
 }
 
 // CTAs an SM that the registers allow.
-__host__ __device__ constexpr int norm_ctas(int g, int le, bool bwd)
+__host__ __device__ constexpr int norm_bwd_ctas(int g)
 {
-    return g == 16 ? 1 : (bwd || le == 32 ? 2 : 3);
+    return g == 16 ? 1 : 2;
 }
 
-template <class T, int G, int LE, bool RMS, bool BWD>
-__global__ void __launch_bounds__(NormCfg<T, G, LE>::kThreads, norm_ctas(G, LE, BWD))
-    k_norm(const NormParams p)
+template <class T, int G, bool RMS>
+__global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_bwd_ctas(G)) k_norm_bwd(const NormParams p)
 {
-    using C = NormCfg<T, G, LE>;
+    using C = NormCfg<T, G>;
     constexpr int E = C::E, V = C::V;
     extern __shared__ uint8_t smem_raw[];
     __shared__ float2 red[2 * 16];
@@ -236,7 +245,7 @@ __global__ void __launch_bounds__(NormCfg<T, G, LE>::kThreads, norm_ctas(G, LE, 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = warp / G, wg = warp - group * G, lt = wg * 32 + lane;
     const uint32_t row_bytes = (uint32_t)(((p.c + E - 1) / E) * 16);
-    const uint32_t stage_bytes = BWD ? 2u * row_bytes : row_bytes;
+    const uint32_t stage_bytes = 2u * row_bytes;
     uint8_t *mine = ring + (size_t)group * p.stages * stage_bytes;
     auto bar = [&](int s) { return ptx::smem_addr(&bars[group * 8 + s]); };
 
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(NormCfg<T, G, LE>::kThreads, norm_ctas(G, LE, 
     const int64_t first = (int64_t)blockIdx.x * C::kGroups + group, step = (int64_t)gridDim.x * C::kGroups;
     auto issue = [&](int64_t row, int s) {
         issue_row<T>(bar(s), ptx::smem_addr(mine + (size_t)s * stage_bytes), row_bytes, x + row * p.ldx,
-                     BWD ? dy + row * p.lddy : nullptr, p.c, row == p.n - 1);
+                     dy + row * p.lddy, p.c, row == p.n - 1);
     };
     int64_t last_issued = -1; // row, in the issuing thread
     if (lt == 0)
@@ -265,18 +274,13 @@ __global__ void __launch_bounds__(NormCfg<T, G, LE>::kThreads, norm_ctas(G, LE, 
             last_issued = row;
         }
 
-    float w[LE], b[BWD ? 1 : LE];
-    load_params<T, G, LE>(p.w, p.c, lt, 1.0f, w);
-    if constexpr (!BWD)
-        load_params<T, G, LE>(p.b, p.c, lt, 0.0f, b);
-    float dw[BWD ? LE : 1], db[BWD && !RMS ? LE : 1];
-    if constexpr (BWD) {
+    float w[LE], dw[LE], db[RMS ? 1 : LE];
+    load_params<T, G>(p.w, p.c, lt, 1.0f, w);
 #pragma unroll
-        for (int i = 0; i < LE; ++i) {
-            dw[i] = 0.0f;
-            if constexpr (!RMS)
-                db[i] = 0.0f;
-        }
+    for (int i = 0; i < LE; ++i) {
+        dw[i] = 0.0f;
+        if constexpr (!RMS)
+            db[i] = 0.0f;
     }
     bool ok = true;
     int s = 0, buf = 0;
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(NormCfg<T, G, LE>::kThreads, norm_ctas(G, LE, 
     };
     const float inv_c = 1.0f / (float)p.c;
     float next_mean = 0.0f, next_rstd = 0.0f;
-    if (BWD && first < p.n) {
+    if (first < p.n) {
         next_mean = RMS ? 0.0f : __ldg(p.mean + first);
         next_rstd = __ldg(p.rstd + first);
     }
@@ -307,128 +311,207 @@ __global__ void __launch_bounds__(NormCfg<T, G, LE>::kThreads, norm_ctas(G, LE, 
 #pragma unroll
         for (int k = 0; k < V; ++k)
             load_vec<T>(st, x + row * p.ldx, last_row, (k * C::kLanes + lt) * E, p.c, h + k * E);
-        if constexpr (!BWD) {
-            // pairs: the packed FP32 instructions do two elements an issue slot
-            float mean = 0.0f;
-            if constexpr (!RMS) {
-                float2 a = make_float2(0.0f, 0.0f);
+        const float mean = next_mean, rstd = next_rstd;
+        if (row + step < p.n) {
+            next_mean = RMS ? 0.0f : __ldg(p.mean + row + step);
+            next_rstd = __ldg(p.rstd + row + step);
+        }
+        float t[LE];
 #pragma unroll
-                for (int i = 0; i < LE; i += 2)
-                    a = __fadd2_rn(a, make_float2(h[i], h[i + 1]));
-                mean = group_sum<G>(a.x + a.y, red, group, wg, lane, buf) * inv_c;
+        for (int k = 0; k < V; ++k)
+            load_vec<T>(st + row_bytes, dy + row * p.lddy, last_row, (k * C::kLanes + lt) * E, p.c, t + k * E);
+        float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int pos = (k * C::kLanes + lt) * E;
-                    if (pos + E <= p.c) {
+        for (int k = 0; k < V; ++k) {
 #pragma unroll
-                        for (int i = k * E; i < (k + 1) * E; i += 2) {
-                            const float2 d = __fadd2_rn(make_float2(h[i], h[i + 1]), make_float2(-mean, -mean));
-                            h[i] = d.x;
-                            h[i + 1] = d.y;
-                        }
-                    } else { // columns past c do not count
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            h[k * E + e] = pos + e < p.c ? h[k * E + e] - mean : 0.0f;
-                    }
-                }
+            for (int e = 0; e < E; ++e) {
+                const int i = k * E + e;
+                h[i] = (h[i] - mean) * rstd;
+                dw[i] = fmaf(t[i], h[i], dw[i]); // columns past c: t = 0
+                if constexpr (!RMS)
+                    db[i] += t[i];
+                t[i] *= w[i];
+                if constexpr (!RMS)
+                    s1 += t[i];
+                s2 = fmaf(t[i], h[i], s2);
             }
-            float2 q = make_float2(0.0f, 0.0f);
+        }
+        if constexpr (RMS)
+            s2 = group_sum<G>(s2, red, group, wg, lane, buf);
+        else
+            group_sum2<G>(s1, s2, red, group, wg, lane, buf);
+        refill(row + (int64_t)p.stages * step);
+        s1 = RMS ? 0.0f : s1 * inv_c;
+        s2 *= inv_c;
 #pragma unroll
-            for (int i = 0; i < LE; i += 2)
-                q = __ffma2_rn(make_float2(h[i], h[i + 1]), make_float2(h[i], h[i + 1]), q);
-            float sq = q.x + q.y;
-            sq = group_sum<G>(sq, red, group, wg, lane, buf);
-            // every lane has its row in registers: the stage takes the next row
-            refill(row + (int64_t)p.stages * step);
-            const float rstd = __frcp_rn(__fsqrt_rn(fmaf(sq, inv_c, p.eps)));
-            if (lt == 0) {
-                if (!RMS)
-                    p.mean[row] = mean;
-                p.rstd[row] = rstd;
-            }
+        for (int k = 0; k < V; ++k) {
+            float d[E];
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                float y[E];
-#pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const int i = k * E + e;
-                    const float2 v = __ffma2_rn(
-                        __fmul2_rn(make_float2(h[i], h[i + 1]), make_float2(rstd, rstd)),
-                        make_float2(w[i], w[i + 1]), make_float2(b[i], b[i + 1]));
-                    y[e] = v.x;
-                    y[e + 1] = v.y;
-                }
-                const int pos = (k * C::kLanes + lt) * E;
-                if (pos < p.c)
-                    store_vec<T>(out + row * p.ldo, pos, p.c, y);
-            }
-        } else {
-            const float mean = next_mean, rstd = next_rstd;
-            if (row + step < p.n) {
-                next_mean = RMS ? 0.0f : __ldg(p.mean + row + step);
-                next_rstd = __ldg(p.rstd + row + step);
-            }
-            float t[LE];
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                load_vec<T>(st + row_bytes, dy + row * p.lddy, last_row, (k * C::kLanes + lt) * E, p.c, t + k * E);
-            float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int i = k * E + e;
-                    h[i] = (h[i] - mean) * rstd;
-                    dw[i] = fmaf(t[i], h[i], dw[i]); // columns past c: t = 0
-                    if constexpr (!RMS)
-                        db[i] += t[i];
-                    t[i] *= w[i];
-                    if constexpr (!RMS)
-                        s1 += t[i];
-                    s2 = fmaf(t[i], h[i], s2);
-                }
-            }
-            if constexpr (RMS)
-                s2 = group_sum<G>(s2, red, group, wg, lane, buf);
-            else
-                group_sum2<G>(s1, s2, red, group, wg, lane, buf);
-            refill(row + (int64_t)p.stages * step);
-            s1 = RMS ? 0.0f : s1 * inv_c;
-            s2 *= inv_c;
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                float d[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    d[e] = rstd * (t[k * E + e] - s1 - h[k * E + e] * s2);
-                const int pos = (k * C::kLanes + lt) * E;
-                if (pos < p.c)
-                    store_vec<T>(out + row * p.ldo, pos, p.c, d);
-            }
+            for (int e = 0; e < E; ++e)
+                d[e] = rstd * (t[k * E + e] - s1 - h[k * E + e] * s2);
+            const int pos = (k * C::kLanes + lt) * E;
+            if (pos < p.c)
+                store_vec<T>(out + row * p.ldo, pos, p.c, d);
         }
         if (++s == p.stages) {
             s = 0;
             ph ^= 1u;
         }
     }
-    if constexpr (BWD) {
-        if (first < p.n) {
+    if (first < p.n) {
 #pragma unroll
-            for (int k = 0; k < V; ++k)
+        for (int k = 0; k < V; ++k)
 #pragma unroll
-                for (int e = 0; e < E; e += 4) {
-                    const int col = (k * C::kLanes + lt) * E + e;
-                    if (col < p.cpad) { // cpad is a multiple of 8
-                        const int i = k * E + e;
-                        *reinterpret_cast<float4 *>(p.pdw + first * p.cpad + col) =
-                            make_float4(dw[i], dw[i + 1], dw[i + 2], dw[i + 3]);
-                        if constexpr (!RMS)
-                            if (p.pdb)
-                                *reinterpret_cast<float4 *>(p.pdb + first * p.cpad + col) =
-                                    make_float4(db[i], db[i + 1], db[i + 2], db[i + 3]);
-                    }
+            for (int e = 0; e < E; e += 4) {
+                const int col = (k * C::kLanes + lt) * E + e;
+                if (col < p.cpad) { // cpad is a multiple of 8
+                    const int i = k * E + e;
+                    *reinterpret_cast<float4 *>(p.pdw + first * p.cpad + col) =
+                        make_float4(dw[i], dw[i + 1], dw[i + 2], dw[i + 3]);
+                    if constexpr (!RMS)
+                        if (p.pdb)
+                            *reinterpret_cast<float4 *>(p.pdb + first * p.cpad + col) =
+                                make_float4(db[i], db[i + 1], db[i + 2], db[i + 3]);
                 }
+            }
+    }
+}
+
+// Forward.  blockDim = 32 * G * groups; dynamic shared memory: the parameters
+// (w, b as they are stored, padded to whole vectors), then a ring a group.
+template <class T, int G, bool RMS>
+__global__ void __launch_bounds__(512, 2) k_norm_fwd(const NormParams p)
+{
+    constexpr int E = Vec<T>::E, L = 32 * G;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ float2 red[2 * 16];
+    __shared__ uint64_t bars[16 * 4];
+    __shared__ int abort_word;
+    uint8_t *params = ptx::align_smem<128>(smem_raw);
+    volatile int *abort_flag = &abort_word;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = blockDim.x / L;
+    const int group = warp / G, wg = warp - group * G, lt = wg * 32 + lane;
+    const uint32_t row_bytes = (uint32_t)(((p.c + E - 1) / E) * 16);
+    uint8_t *mine = params + (p.b ? 2u : 1u) * row_bytes + (size_t)group * p.stages * row_bytes;
+    auto bar = [&](int s) { return ptx::smem_addr(&bars[group * 4 + s]); };
+
+    if (threadIdx.x == 0) {
+        abort_word = 0;
+        for (int g = 0; g < groups; ++g)
+            for (int s = 0; s < p.stages; ++s)
+                ptx::mbar_init(ptx::smem_addr(&bars[g * 4 + s]), 1);
+        ptx::fence_barrier_init();
+    }
+    __syncthreads();
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+
+    const T *x = static_cast<const T *>(p.x);
+    T *out = static_cast<T *>(p.out);
+    const int64_t first = (int64_t)blockIdx.x * groups + group, step = (int64_t)gridDim.x * groups;
+    auto issue = [&](int64_t row, int s) {
+        issue_row<T>(bar(s), ptx::smem_addr(mine + (size_t)s * row_bytes), 0, x + row * p.ldx, (const T *)nullptr, p.c,
+                     row == p.n - 1);
+    };
+    int64_t last_issued = -1; // row, in the issuing thread
+    if (lt == 0)
+        for (int64_t row = first, i = 0; row < p.n && i < p.stages; row += step, ++i) {
+            issue(row, (int)i);
+            last_issued = row;
+        }
+    T *ws = reinterpret_cast<T *>(params), *bs = reinterpret_cast<T *>(params + row_bytes);
+    for (int i = threadIdx.x; i < (int)(row_bytes / sizeof(T)); i += blockDim.x) {
+        Vec<T>::put(ws + i, i < p.c ? (p.w ? Vec<T>::get(static_cast<const T *>(p.w) + i) : 1.0f) : 0.0f);
+        if (p.b)
+            Vec<T>::put(bs + i, i < p.c ? Vec<T>::get(static_cast<const T *>(p.b) + i) : 0.0f);
+    }
+    __syncthreads();
+
+    const float inv_c = 1.0f / (float)p.c;
+    const int whole = p.c / E * E; // columns in whole vectors
+    const int tail = whole + lt;   // and one of the rest, in the first lanes
+    bool ok = true;
+    int s = 0, buf = 0;
+    uint32_t ph = 0;
+    for (int64_t row = first; row < p.n; row += step) {
+        // After a timeout every thread still runs through the rows and meets their barriers, without new
+        // copies; the issuing thread waits (within its limit) for each copy that it has started.
+        if (lt == 0)
+            ok = row <= last_issued &&
+                 ptx::mbar_wait(bar(s), ph, abort_flag, &g_norm_error, kErrTimeout, p.limit_ns, false);
+        else
+            ok = ptx::mbar_wait(bar(s), ph, abort_flag, &g_norm_error, kErrTimeout, p.limit_ns);
+        const T *st = reinterpret_cast<const T *>(mine + (size_t)s * row_bytes);
+        float xt = 0.0f; // the last row's padding was not copied: its tail comes from memory
+        if (tail < p.c)
+            xt = Vec<T>::get(row == p.n - 1 ? x + row * p.ldx + tail : st + tail);
+        float mean = 0.0f;
+        if constexpr (!RMS) {
+            float2 a = make_float2(xt, 0.0f);
+#pragma unroll 4
+            for (int pos = lt * E; pos < whole; pos += L * E) {
+                float f[E];
+                Vec<T>::unpack(*reinterpret_cast<const uint4 *>(st + pos), f);
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    a = __fadd2_rn(a, make_float2(f[e], f[e + 1]));
+            }
+            mean = group_sum<G>(a.x + a.y, red, group, wg, lane, buf) * inv_c;
+        }
+        const float2 neg = make_float2(-mean, -mean);
+        float2 q = make_float2(tail < p.c ? (xt - mean) * (xt - mean) : 0.0f, 0.0f);
+#pragma unroll 4
+        for (int pos = lt * E; pos < whole; pos += L * E) {
+            float f[E];
+            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(st + pos), f);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 v = __fadd2_rn(make_float2(f[e], f[e + 1]), neg);
+                q = __ffma2_rn(v, v, q);
+            }
+        }
+        const float sq = group_sum<G>(q.x + q.y, red, group, wg, lane, buf);
+        const float rstd = __frcp_rn(__fsqrt_rn(fmaf(sq, inv_c, p.eps)));
+        if (lt == 0) {
+            if (!RMS)
+                p.mean[row] = mean;
+            p.rstd[row] = rstd;
+        }
+        T *o = out + row * p.ldo;
+        const float2 r2 = make_float2(rstd, rstd);
+#pragma unroll 2
+        for (int pos = lt * E; pos < whole; pos += L * E) {
+            float f[E], w[E], b[E];
+            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(st + pos), f);
+            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(ws + pos), w);
+            if (!RMS && p.b)
+                Vec<T>::unpack(*reinterpret_cast<const uint4 *>(bs + pos), b);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 h = __fmul2_rn(__fadd2_rn(make_float2(f[e], f[e + 1]), neg), r2);
+                const float2 wv = make_float2(w[e], w[e + 1]);
+                const float2 y = !RMS && p.b ? __ffma2_rn(h, wv, make_float2(b[e], b[e + 1])) : __fmul2_rn(h, wv);
+                f[e] = y.x;
+                f[e + 1] = y.y;
+            }
+            *reinterpret_cast<uint4 *>(o + pos) = Vec<T>::pack(f);
+        }
+        if (tail < p.c)
+            Vec<T>::put(o + tail, fmaf((xt - mean) * rstd, Vec<T>::get(ws + tail),
+                                       !RMS && p.b ? Vec<T>::get(bs + tail) : 0.0f));
+        // every lane is through with the stage: it takes the next row
+        if constexpr (G > 1)
+            ptx::named_bar_sync(1 + group, L);
+        else
+            __syncwarp();
+        const int64_t ahead = row + (int64_t)p.stages * step;
+        if (lt == 0 && ok && !*abort_flag && ahead < p.n) {
+            issue(ahead, s);
+            last_issued = ahead;
+        }
+        if (++s == p.stages) {
+            s = 0;
+            ph ^= 1u;
         }
     }
 }
@@ -556,111 +639,144 @@ __global__ void __launch_bounds__(256) k_norm_wide_params(const NormParams p)
         p.pdb[(int64_t)blockIdx.y * p.cpad + col] = db;
 }
 
-constexpr int kWidest = 8192, kWideSlices = 64, kMaxStages = 4;
+constexpr int kWidest = 8192, kWideSlices = 64;
+constexpr size_t kSmemMost = 224 * 1024; // dynamic shared memory of the CTAs of one SM
 
-// Elements a lane holds.  Forward: 32 (half the reductions and waits of 16 for
-// every element; 16384 x 4096 measured in the launcher's comment), 16 where a
-// single warp of them holds the row.  Backward: 16 (x, dy and the sums of dw
-// and db take four registers an element).
-int lane_elems(int64_t c, bool bwd)
-{
-    return bwd || c <= 512 ? 16 : 32;
-}
-
-int warps_of(int64_t c, int le)
+int bwd_warps(int64_t c)
 {
     int g = 1;
-    while (g * 32 * le < c)
+    while (g * 32 * LE < c)
         g *= 2;
     return g;
 }
 
+size_t row_size(int64_t c, int esize)
+{
+    return (size_t)((c * esize + 15) / 16 * 16);
+}
+
 struct NormPlan {
-    int grid, groups, stages; // groups: partial rows of dw and db
+    int warps, threads, grid, stages; // warps a row
+    int groups;                       // backward: partial rows of dw and db
     size_t smem;
 };
 
-// Grid and ring of the register kernels.  CTAs an SM: what the registers allow
-// (the launch bounds) and the rings' shared memory; a group gets four rows or
-// more in the backward pass, so that its partial rows stay a small part of the traffic.
-NormPlan norm_plan(int64_t n, int64_t c, int esize, bool bwd)
+// Backward: what the registers and the rings allow; a group gets four rows or
+// more, so that its partial rows stay a small part of the traffic.
+NormPlan bwd_plan(int64_t n, int64_t c, int esize)
 {
-    NormPlan r;
-    const int le = lane_elems(c, bwd), g = warps_of(c, le), per_cta = g < 8 ? 8 / g : 1;
-    const size_t row = (size_t)((c * esize + 15) / 16 * 16) * (bwd ? 2 : 1);
-    r.stages = kMaxStages;
-    const int ctas = norm_ctas(g, le, bwd);
-    while (r.stages > 2 && ctas * (r.stages * per_cta * row + 2048) > 227 * 1024)
+    NormPlan r = {};
+    r.warps = bwd_warps(c);
+    const int per_cta = r.warps < 8 ? 8 / r.warps : 1, ctas = norm_bwd_ctas(r.warps);
+    const size_t row = 2 * row_size(c, esize);
+    r.stages = 4;
+    while (r.stages > 2 && ctas * (r.stages * per_cta * row + 2048) > kSmemMost)
         --r.stages;
     r.smem = r.stages * per_cta * row + 128;
-    const int64_t rows_a_group = bwd ? 4 : 1;
-    int64_t groups = (n + rows_a_group - 1) / rows_a_group;
+    r.threads = 32 * r.warps * per_cta;
+    int64_t groups = (n + 3) / 4;
     const int64_t most = (int64_t)sm_count() * ctas * per_cta;
     groups = groups < most ? groups : most;
     r.grid = (int)((groups + per_cta - 1) / per_cta);
-    // every group that exists and has a row writes its partial row
+    // every group that has a row writes its partial row
     const int64_t all = (int64_t)r.grid * per_cta;
     r.groups = (int)(all < n ? all : n);
     return r;
 }
 
-template <class T, int G, int LE, bool RMS, bool BWD>
-cudaError_t run_norm(const NormParams &p, const NormPlan &plan, cudaStream_t st)
+// Forward: a warp a row up to 8 KB, more warps above and for few rows; two
+// CTAs an SM where half its shared memory holds rings for 8 warps of rows.
+NormPlan fwd_plan(int64_t n, int64_t c, int esize, bool bias)
 {
-    auto kern = k_norm<T, G, LE, RMS, BWD>;
-    static int configured_device = -1;
+    NormPlan r = {};
+    const size_t row = row_size(c, esize), params = (bias ? 2 : 1) * row + 128;
+    const int sms = sm_count();
+    r.warps = 1;
+    while (r.warps < 8 && (row > (size_t)8192 * r.warps || (n <= sms && row >= (size_t)1024 * r.warps)))
+        r.warps *= 2;
+    r.stages = row <= 4096 ? 3 : 2;
+    int ctas = 2;
+    int64_t groups = ((kSmemMost / 2 - 2048) - params) / (r.stages * row);
+    if (kSmemMost / 2 - 2048 < params || groups * r.warps < 8) {
+        ctas = 1;
+        groups = (kSmemMost - 2048 - params) / (r.stages * row);
+    }
+    if (groups > 16 / r.warps)
+        groups = 16 / r.warps;
+    const int64_t want = (n + sms - 1) / sms; // rows an SM: no more groups than that
+    if (groups > want)
+        groups = want;
+    r.threads = (int)(32 * r.warps * groups);
+    r.smem = params + (size_t)groups * r.stages * row;
+    const int64_t need = (n + groups - 1) / groups, most = (int64_t)sms * ctas;
+    r.grid = (int)(need < most ? need : most);
+    return r;
+}
+
+template <typename K>
+cudaError_t run_norm(K kern, int &configured_device, const NormParams &p, const NormPlan &plan, cudaStream_t st)
+{
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     if (configured_device != dev) {
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024)) != cudaSuccess)
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost)) !=
+            cudaSuccess)
             return e;
         configured_device = dev;
     }
-    return launch_pdl(kern, dim3((unsigned)plan.grid), dim3(NormCfg<T, G, LE>::kThreads), plan.smem, st, p);
+    return launch_pdl(kern, dim3((unsigned)plan.grid), dim3((unsigned)plan.threads), plan.smem, st, p);
 }
 
-template <class T, bool RMS, bool BWD>
-cudaError_t pick_norm(const NormParams &p, const NormPlan &plan, cudaStream_t st)
+template <class T, int G, bool RMS>
+cudaError_t run_norm_bwd(const NormParams &p, const NormPlan &plan, cudaStream_t st)
 {
-    constexpr int kFull = BWD ? 16 : 32;
-    const int le = lane_elems(p.c, BWD);
-    if (le != kFull)
-        return run_norm<T, 1, 16, RMS, BWD>(p, plan, st);
-    switch (warps_of(p.c, le)) {
-    case 1: return run_norm<T, 1, kFull, RMS, BWD>(p, plan, st);
-    case 2: return run_norm<T, 2, kFull, RMS, BWD>(p, plan, st);
-    case 4: return run_norm<T, 4, kFull, RMS, BWD>(p, plan, st);
-    case 8: return run_norm<T, 8, kFull, RMS, BWD>(p, plan, st);
-    default: break;
+    static int configured = -1;
+    return run_norm(k_norm_bwd<T, G, RMS>, configured, p, plan, st);
+}
+
+template <class T, int G, bool RMS>
+cudaError_t run_norm_fwd(const NormParams &p, const NormPlan &plan, cudaStream_t st)
+{
+    static int configured = -1;
+    return run_norm(k_norm_fwd<T, G, RMS>, configured, p, plan, st);
+}
+
+template <class T, bool RMS>
+cudaError_t pick_norm(const NormParams &p, const NormPlan &plan, bool bwd, cudaStream_t st)
+{
+    switch (plan.warps) {
+    case 1: return bwd ? run_norm_bwd<T, 1, RMS>(p, plan, st) : run_norm_fwd<T, 1, RMS>(p, plan, st);
+    case 2: return bwd ? run_norm_bwd<T, 2, RMS>(p, plan, st) : run_norm_fwd<T, 2, RMS>(p, plan, st);
+    case 4: return bwd ? run_norm_bwd<T, 4, RMS>(p, plan, st) : run_norm_fwd<T, 4, RMS>(p, plan, st);
+    case 8: return bwd ? run_norm_bwd<T, 8, RMS>(p, plan, st) : run_norm_fwd<T, 8, RMS>(p, plan, st);
+    default: return run_norm_bwd<T, 16, RMS>(p, plan, st); // the forward pass uses 8 at most
     }
-    if constexpr (BWD)
-        return run_norm<T, 16, 16, RMS, true>(p, plan, st);
-    else
-        return cudaErrorInvalidValue; // 8 warps of 32 hold every row up to kWidest
 }
 
 template <class T, bool RMS>
 cudaError_t norm_any(const NormArgs &a, NormParams p, bool bwd, cudaStream_t st)
 {
     const bool wide = a.c > kWidest;
-    NormPlan plan = {};
-    if (!wide)
-        plan = norm_plan(a.n, a.c, (int)sizeof(T), bwd);
+    const int64_t cap = (int64_t)sm_count() * 2;
+    const dim3 wide_grid((unsigned)(a.n < cap ? a.n : cap));
     if (!bwd) {
-        if (!wide)
-            return pick_norm<T, RMS, false>(p, plan, st);
-        const int64_t cap = (int64_t)sm_count() * 2;
-        return launch_pdl(k_norm_wide<T, RMS, false>, dim3((unsigned)(a.n < cap ? a.n : cap)), dim3(1024), 0, st, p);
+        if (wide)
+            return launch_pdl(k_norm_wide<T, RMS, false>, wide_grid, dim3(1024), 0, st, p);
+        const NormPlan plan = fwd_plan(a.n, a.c, (int)sizeof(T), a.b != nullptr);
+        p.stages = plan.stages;
+        return pick_norm<T, RMS>(p, plan, false, st);
     }
     cudaError_t e;
+    NormPlan plan = {};
     if (!wide) {
-        e = pick_norm<T, RMS, true>(p, plan, st);
+        plan = bwd_plan(a.n, a.c, (int)sizeof(T));
+        p.stages = plan.stages;
+        e = pick_norm<T, RMS>(p, plan, true, st);
     } else {
-        const int64_t cap = (int64_t)sm_count() * 2;
         plan.groups = (int)(a.n < kWideSlices ? a.n : kWideSlices);
-        e = launch_pdl(k_norm_wide<T, RMS, true>, dim3((unsigned)(a.n < cap ? a.n : cap)), dim3(1024), 0, st, p);
+        e = launch_pdl(k_norm_wide<T, RMS, true>, wide_grid, dim3(1024), 0, st, p);
         if (e == cudaSuccess)
             e = launch_pdl(k_norm_wide_params<T, RMS>, dim3((unsigned)((a.c + 255) / 256), (unsigned)plan.groups),
                            dim3(256), 0, st, p);
@@ -694,8 +810,6 @@ cudaError_t launch_norm(const NormArgs &a, bool bwd, cudaStream_t st)
         p.pdw = static_cast<float *>(a.ws);
         p.pdb = a.db ? p.pdw + rows * p.cpad : nullptr;
     }
-    if (a.c <= kWidest)
-        p.stages = norm_plan(a.n, a.c, a.dtype == JETQ_OUT_BF16 ? 2 : 4, bwd).stages;
     const bool rms = a.kind == JETQ_NORM_RMS;
     if (a.dtype == JETQ_OUT_BF16)
         return rms ? norm_any<__nv_bfloat16, true>(a, p, bwd, st) : norm_any<__nv_bfloat16, false>(a, p, bwd, st);
@@ -708,7 +822,7 @@ int64_t norm_bwd_partial_rows(int64_t n, int64_t c, jetq_out_dtype dtype)
 {
     if (c > kWidest)
         return n < kWideSlices ? n : kWideSlices;
-    return norm_plan(n, c, dtype == JETQ_OUT_BF16 ? 2 : 4, true).groups;
+    return bwd_plan(n, c, dtype == JETQ_OUT_BF16 ? 2 : 4).groups;
 }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t st)
