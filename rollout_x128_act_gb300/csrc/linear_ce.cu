@@ -664,17 +664,18 @@ cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorM
     return cudaLaunchKernelEx(&cfg, kern, a, b, o, p);
 }
 
-// CTA pairs (256 x 256 tiles) or single CTAs (128 x 256)?  A tile takes the
-// same time either way and pairs need half the operand traffic, which measured
-// 1.08x faster a tile (dx, dw and d of 4096 tokens x 131072 x 4096: 7.99 ms
-// against 8.72); single CTAs waste less where the rows do not fill pairs.
+// CTA pairs (256 x 256 tiles) or single CTAs (128 x 256)?  A 64-block of K is
+// 512 tensor cycles for either, but a single CTA loads 48 KB for it and a CTA
+// of a pair 32 KB, against an SM's 64 bytes a cycle from L2: single CTAs take
+// 1.2 times as long a tile (4096 tokens x 131072 x 4096: forward 2.81 ms against
+// 2.36, d + dx + dw 8.72 against 7.8).  They waste less where the rows do not fill pairs.
 int pick_cg(int64_t rows, int64_t tiles_n)
 {
     if (rows <= 128)
         return 1;
     const int64_t w1 = ceil_div(ceil_div(rows, 128) * tiles_n, units_of(1));
     const int64_t w2 = ceil_div(ceil_div(rows, 256) * tiles_n, units_of(2));
-    return 100 * w2 <= 108 * w1 ? 2 : 1;
+    return 5 * w2 <= 6 * w1 ? 2 : 1;
 }
 
 // CTAs a tile and K splits of the dx product: enough work units to fill the
@@ -688,7 +689,7 @@ void dx_shape(int64_t n, int64_t c, int64_t piece, int &cg, int &splits)
     for (int g = 2; g >= 1; --g) {
         const int64_t tiles = ceil_div(n, 128 * g) * ceil_div(c, kTileN), units = units_of(g);
         for (int64_t s = 1; s <= most; ++s) {
-            const double t = (double)ceil_div(tiles * s, units) / (double)s * tile_s * (g == 2 ? 1.0 : 1.08) +
+            const double t = (double)ceil_div(tiles * s, units) / (double)s * tile_s * (g == 2 ? 1.0 : 1.2) +
                              (double)s * slab_s;
             if (t < best * 0.999) {
                 best = t;

@@ -420,16 +420,22 @@ __global__ void __launch_bounds__(512, 2) k_norm_fwd(const NormParams p)
             last_issued = row;
         }
     T *ws = reinterpret_cast<T *>(params), *bs = reinterpret_cast<T *>(params + row_bytes);
-    for (int i = threadIdx.x; i < (int)(row_bytes / sizeof(T)); i += blockDim.x) {
-        Vec<T>::put(ws + i, i < p.c ? (p.w ? Vec<T>::get(static_cast<const T *>(p.w) + i) : 1.0f) : 0.0f);
-        if (p.b)
-            Vec<T>::put(bs + i, i < p.c ? Vec<T>::get(static_cast<const T *>(p.b) + i) : 0.0f);
-    }
+    const int whole = p.c / E * E; // columns in whole vectors
+    auto copy_param = [&](T *dst, const T *src, float fallback) {
+        // whole vectors where the pointer allows them (any element-aligned one is taken)
+        const int vec = src && (reinterpret_cast<uintptr_t>(src) & 15u) == 0 ? whole : 0;
+        for (int i = threadIdx.x * E; i < vec; i += blockDim.x * E)
+            *reinterpret_cast<uint4 *>(dst + i) = __ldg(reinterpret_cast<const uint4 *>(src + i));
+        for (int i = vec + threadIdx.x; i < (int)(row_bytes / sizeof(T)); i += blockDim.x)
+            Vec<T>::put(dst + i, i < p.c ? (src ? Vec<T>::get(src + i) : fallback) : 0.0f);
+    };
+    copy_param(ws, static_cast<const T *>(p.w), 1.0f);
+    if (p.b)
+        copy_param(bs, static_cast<const T *>(p.b), 0.0f);
     __syncthreads();
 
     const float inv_c = 1.0f / (float)p.c;
-    const int whole = p.c / E * E; // columns in whole vectors
-    const int tail = whole + lt;   // and one of the rest, in the first lanes
+    const int tail = whole + lt; // one of the columns past the whole vectors, in the first lanes
     bool ok = true;
     int s = 0, buf = 0;
     uint32_t ph = 0;
