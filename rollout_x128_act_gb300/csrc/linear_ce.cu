@@ -8,7 +8,7 @@
 //   dx       = scale * d w,   dw = scale * d^T x
 //
 // One GEMM kernel (k_head_gemm) in four modes carries all of it:
-//   forward    x w^T with an epilogue that reduces each row's logits, 64 at a time, to a
+//   forward    x w^T with an epilogue that reduces each row's 128 logits to a
 //              (maximum, sum of exponentials) pair and picks the target's
 //              logit; a small kernel joins the pairs of a row
 //   backward, per piece of the vocabulary (its d is [n x piece] in BF16)
@@ -47,7 +47,7 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-constexpr int kParts = 4; // the epilogue's column slices of a tile
+constexpr int kParts = 2; // the statistics epilogue's column slices of a tile
 
 enum HeadMode : int {
     kStats = 0,   // softmax statistics of the logits
@@ -79,7 +79,10 @@ struct HeadCfg {
     static constexpr int kBRows = BN / CG; // rows of B in one CTA's shared memory
     static constexpr int kBBytes = kBRows * 128;
     static constexpr int kStage = kABytes + kBBytes;
-    static constexpr int kEpiWarps = 16;
+    // Epilogue: 16 warps of 64 columns a thread for d and the gradients; 8 warps of 128 for the statistics,
+    // whose threads hold their columns' sums (4 to 10% faster forward than 16 warps of 64, except at c = 256).
+    static constexpr int kEpiWarps = MODE == kStats ? 8 : 16;
+    static constexpr int kCols = MODE == kStats ? 128 : 64;
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
     static constexpr bool kStaging = MODE != kStats;
     static constexpr size_t kStagingBytes = kStaging ? kEpiWarps * 4096 : 0; // a 4 KB box a warp
@@ -89,6 +92,9 @@ struct HeadCfg {
     static constexpr int kFold = MODE == kStats ? (CG == 2 ? 8 : 2) : 1 << 30;
     static constexpr bool kAMn = MODE == kGradW16 || MODE == kGradW32; // A's M axis contiguous
     static constexpr bool kBMn = MODE >= kGradX;                       // B's N axis contiguous
+    // register split of the statistics: producer warps, epilogue warps
+    static constexpr bool kRegSplit = MODE == kStats;
+    static constexpr int kRegProducer = 72, kRegEpilogue = 216;
     static constexpr int kBars = 2 * kStages + 5;
     static_assert(kBars * 8 + 8 <= 256, "barrier area");
     static_assert(kSmem <= 232448, "shared memory");
@@ -173,6 +179,13 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
+    if constexpr (C::kRegSplit) {
+        if (warp < 4)
+            ptx::setmaxnreg_dec<C::kRegProducer>();
+        else
+            ptx::setmaxnreg_inc<C::kRegEpilogue>();
+    }
+
     if (warp < 4) {
         if (warp == 0 && lane == 0) {
             // -------------------------------------------------- TMA producer
@@ -269,227 +282,271 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------------ epilogue: a row and 64 columns a thread
+        // ------------------------------------------------------ epilogue: a row and kCols columns a thread
         const int ew = warp - 4, quarter = warp & 3, part = ew >> 2;
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-        const uint32_t stage = ptx::smem_addr(staging) + (uint32_t)ew * 4096u;
-        const uint32_t stage_row = stage + (uint32_t)lane * 128u;
-        float factor = 1.0f, gmax = 0.0f;
-        if (MODE == kGrad)
-            gmax = __ldg(p.gmax);
-        if (MODE == kGradW16 || MODE == kGradW32)
-            factor = __ldg(p.gmax) * p.scale;
-        // the softmax modes' inputs of a row, loaded a tile ahead
-        struct RowIn {
-            int64_t target = -1;
-            float lse = 0.0f, dloss = 0.0f;
-        };
-        auto tile_row = [&](int mi) { return mi * 128 * CG + (int)rank * 128 + quarter * 32; };
-        auto row_in = [&](int t) {
-            RowIn r;
-            if ((MODE == kStats || MODE == kGrad) && t < num_tiles) {
+        if constexpr (MODE == kStats) {
+            uint32_t tc = 0;
+            for (int t = unit; t < num_tiles; t += units) {
                 int mi, ni, ks;
                 head_coords(p, t, mi, ni, ks);
-                const int64_t row = tile_row(mi) + lane;
+                const int row0 = mi * 128 * CG + (int)rank * 128 + quarter * 32;
+                const int64_t row = (int64_t)row0 + lane;
+                const int n0 = ni * bn + part * 128;
+                int tcol = -1; // the target's column in this thread's 128, or out of range
                 if (row < p.M) {
-                    r.target = __ldg(p.target + row);
-                    if (MODE == kGrad) {
-                        r.lse = __ldg(p.lse + row);
-                        r.dloss = __ldg(p.dloss + row);
-                    }
+                    const int64_t tg = __ldg(p.target + row), rel = tg - n0;
+                    if (tg >= 0 && tg < p.V && rel >= 0 && rel < min(128, bn - part * 128))
+                        tcol = (int)rel;
                 }
-            }
-            return r;
-        };
-        auto wait_acc = [&](uint32_t n) {
-            const bool got = ptx::mbar_wait(acc_full(n & 1u), (n >> 1) & 1u, abort_flag, err, kErrTimeout, p.limit_ns);
-            const bool all = __all_sync(0xFFFFFFFFu, got);
-            ptx::tc_fence_after();
-            return all;
-        };
-        auto acc_addr = [&](uint32_t n) { return tmem_base + 256u * (n & 1u) + lane_addr + (uint32_t)(part * 64); };
-        auto release = [&](uint32_t n) {
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2)
-                    ptx::mbar_arrive_remote(ptx::map_to_cta(acc_empty(n & 1u), 0));
-                else
-                    ptx::mbar_arrive(acc_empty(n & 1u));
-            }
-        };
-        // writes a box (128 bytes a row, 32 rows) to the staging buffer once its last store has left it
-        auto stage_box = [&](const uint32_t *h) {
-            if (lane == 0)
-                ptx::bulk_wait_group_read<0>();
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                ptx::st_shared_v4(stage_row + (uint32_t)((j ^ (lane & 7)) << 4), h[4 * j], h[4 * j + 1], h[4 * j + 2],
-                                  h[4 * j + 3]);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-        };
-        uint32_t tc = 0;
-        RowIn next = row_in(unit);
-        for (int t = unit; t < num_tiles; t += units) {
-            int mi, ni, ks;
-            head_coords(p, t, mi, ni, ks);
-            if (MODE == kGradX &&
-                (int64_t)p.num_kb * ks / p.splits == (int64_t)p.num_kb * (ks + 1) / p.splits)
-                continue;
-            const int row0 = tile_row(mi);
-            const int64_t row = (int64_t)row0 + lane;
-            const int n0 = ni * bn + part * 64;
-            const int width = MODE == kStats ? min(64, bn - part * 64) : 64; // columns of this thread in the tile
-            const RowIn in = next;
-            const int64_t rel = in.target - p.col0 - n0;
-            const bool has = in.target >= 0 && in.target < p.V;
-            const int tcol = has && rel >= 0 && rel < width ? (int)rel : -1; // the target's column, if it is here
-            if constexpr (MODE == kStats) {
+                auto wait_acc = [&](uint32_t n) {
+                    const bool got =
+                        ptx::mbar_wait(acc_full(n & 1u), (n >> 1) & 1u, abort_flag, err, kErrTimeout, p.limit_ns);
+                    const bool all = __all_sync(0xFFFFFFFFu, got);
+                    ptx::tc_fence_after();
+                    return all;
+                };
+                auto acc_addr = [&](uint32_t n) {
+                    return tmem_base + 256u * (n & 1u) + lane_addr + (uint32_t)(part * 128);
+                };
+                auto release = [&](uint32_t n) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 2)
+                            ptx::mbar_arrive_remote(ptx::map_to_cta(acc_empty(n & 1u), 0));
+                        else
+                            ptx::mbar_arrive(acc_empty(n & 1u));
+                    }
+                };
                 // The tensor core's FP32 accumulator truncates at each step: over a whole K of 4096 the losses
                 // of 4096 tokens are off by 3e-6 (2-norm, against binary64), a single token's by up to 2e-5.
-                // So partial tiles of kFold 64-blocks of K are summed here in round-to-nearest.
-                float2 z[32];
+                // So partial tiles of kFold 64-blocks of K are summed here in round-to-nearest: 8 blocks for
+                // batches (4e-7, less than an FP32 matrix product's 6e-7; 4096 tokens x 131072 x 4096: 2.65 ms
+                // against 2.97 with 4 and 4.03 with 2, whose hand-overs stall the pair), 2 for the small row
+                // counts of single CTAs (1e-7; there the time is the weight's stream either way).
+                float2 z[64];
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < 64; ++j)
                     z[j] = make_float2(0.0f, 0.0f);
                 const int folds = (p.num_kb + C::kFold - 1) / C::kFold;
                 bool ok = true;
-                for (int f = 0; f < folds && ok; ++f, ++tc) {
-                    ok = wait_acc(tc);
+                for (int f = 0; f < folds && ok; ++f) {
+                    const uint32_t n = tc + (uint32_t)f;
+                    ok = wait_acc(n);
                     if (!ok)
                         break;
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t v[16];
-                        ptx::tmem_ld_32x32b_x16(acc_addr(tc) + 16u * ch, v);
-                        ptx::tmem_ld_wait_regs(v);
-                        if (ch == 3)
-                            release(tc);
+                    for (int ch = 0; ch < 2; ++ch) {
+                        uint32_t v[64];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            z[8 * ch + j] = __fadd2_rn(z[8 * ch + j], make_float2(__uint_as_float(v[2 * j]),
-                                                                                  __uint_as_float(v[2 * j + 1])));
+                        for (int q = 0; q < 2; ++q)
+                            ptx::tmem_ld_32x32b_x32(acc_addr(n) + 64u * ch + 32u * q,
+                                                    *reinterpret_cast<uint32_t(*)[32]>(&v[32 * q]));
+                        ptx::tmem_ld_wait_tie(v);
+                        if (ch == 1)
+                            release(n);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            z[32 * ch + j] = __fadd2_rn(z[32 * ch + j], make_float2(__uint_as_float(v[2 * j]),
+                                                                                    __uint_as_float(v[2 * j + 1])));
                     }
                 }
                 if (!ok)
                     break;
-                next = row_in(t + units);
-                float v[64];
+                tc += (uint32_t)folds;
+                float v[128];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
+                for (int j = 0; j < 64; ++j) {
                     v[2 * j] = z[j].x;
                     v[2 * j + 1] = z[j].y;
                 }
-                const int valid = (int)min((int64_t)width, p.N - n0); // columns inside tile and vocabulary
-                if (valid < 64) {
+                // this thread's columns inside the tile and the vocabulary
+                const int valid = (int)min((int64_t)min(128, bn - part * 128), p.N - n0);
+                if (valid < 128) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
+                    for (int j = 0; j < 128; ++j)
                         v[j] = j < valid ? v[j] : -INFINITY;
                 }
                 float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                for (int j = 4; j < 64; ++j)
+                for (int j = 4; j < 128; ++j)
                     m4[j & 3] = fmaxf(m4[j & 3], v[j]);
                 const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 const float mk = m * p.k2;
                 float zt = 0.0f;
                 if (__any_sync(0xFFFFFFFFu, tcol >= 0)) { // the target's term is joined exactly by the last kernel
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
+                    for (int j = 0; j < 128; ++j) {
                         zt = j == tcol ? v[j] : zt;
                         v[j] = j == tcol ? -INFINITY : v[j];
                     }
                 }
                 float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
+                for (int j = 0; j < 128; ++j)
                     s4[j & 3] += ex2(fmaf(v[j], p.k2, -mk));
                 if (row < p.M) {
                     // no column, or all of them -inf: an empty sum; only NaN: NaN (fmaxf passes over single ones)
                     const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                    p.part[(int64_t)(kParts * ni + part) * p.M + row] =
-                        m == -INFINITY ? make_float2(-INFINITY, 0.0f)
-                                       : (m == m ? make_float2(mk, sum) : make_float2(0.0f, m));
+                    p.part[(int64_t)(kParts * ni + part) * p.M + row] = m == -INFINITY ? make_float2(-INFINITY, 0.0f)
+                                                                   : m == m       ? make_float2(mk, sum)
+                                                                                  : make_float2(0.0f, m);
                     if (tcol >= 0)
                         p.zt[row] = zt;
                 }
-            } else if constexpr (MODE == kGrad || MODE == kGradW16) { // 64 BF16 columns: one box
-                if (!wait_acc(tc))
-                    break;
-                // a row without a loss: exponent 0 and coefficient 0, so that d = 0 whatever its lse
-                const bool loss = MODE == kGrad && has && gmax > 0.0f;
-                const float k2 = loss ? p.k2 : 0.0f, lse2 = loss ? in.lse * kLog2e : 0.0f;
-                const float f = MODE == kGradW16 ? factor : (loss ? __fdiv_rn(in.dloss, gmax) : 0.0f);
-                next = row_in(t + units);
-                uint32_t h[32];
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                    uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(acc_addr(tc) + 32u * ch, v);
-                    ptx::tmem_ld_wait_tie(v);
-                    if (ch == 1)
-                        release(tc);
-                    if constexpr (MODE == kGrad) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = __float_as_uint(ex2(fmaf(__uint_as_float(v[j]), k2, -lse2)));
-                        if (__any_sync(0xFFFFFFFFu, tcol >> 5 == ch)) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = 32 * ch + j == tcol ? __float_as_uint(__uint_as_float(v[j]) - 1.0f) : v[j];
-                        }
-                        if (n0 + 32 * ch + 32 > p.N) { // columns past the piece: zero, part of the dx product's K
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = n0 + 32 * ch + j < p.N ? v[j] : 0u;
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const __nv_bfloat162 b2 =
-                            __floats2bfloat162_rn(__uint_as_float(v[2 * j]) * f, __uint_as_float(v[2 * j + 1]) * f);
-                        h[16 * ch + j] = *reinterpret_cast<const uint32_t *>(&b2);
+            }
+        } else {
+            const uint32_t stage = ptx::smem_addr(staging) + (uint32_t)ew * 4096u;
+            const uint32_t stage_row = stage + (uint32_t)lane * 128u;
+            float factor = 1.0f, gmax = 0.0f;
+            if (MODE == kGrad)
+                gmax = __ldg(p.gmax);
+            if (MODE == kGradW16 || MODE == kGradW32)
+                factor = __ldg(p.gmax) * p.scale;
+            // d's inputs of a row, loaded a tile ahead
+            struct RowIn {
+                int64_t target = -1;
+                float lse = 0.0f, dloss = 0.0f;
+            };
+            auto tile_row = [&](int mi) { return mi * 128 * CG + (int)rank * 128 + quarter * 32; };
+            auto row_in = [&](int t) {
+                RowIn r;
+                if (MODE == kGrad && t < num_tiles) {
+                    int mi, ni, ks;
+                    head_coords(p, t, mi, ni, ks);
+                    const int64_t row = tile_row(mi) + lane;
+                    if (row < p.M) {
+                        r.target = __ldg(p.target + row);
+                        r.lse = __ldg(p.lse + row);
+                        r.dloss = __ldg(p.dloss + row);
                     }
                 }
-                ++tc;
-                if (row0 >= p.M || (MODE == kGradW16 && n0 >= p.N))
-                    continue;
-                stage_box(h);
+                return r;
+            };
+            auto wait_acc = [&](uint32_t n) {
+                const bool got =
+                    ptx::mbar_wait(acc_full(n & 1u), (n >> 1) & 1u, abort_flag, err, kErrTimeout, p.limit_ns);
+                const bool all = __all_sync(0xFFFFFFFFu, got);
+                ptx::tc_fence_after();
+                return all;
+            };
+            auto acc_addr = [&](uint32_t n) {
+                return tmem_base + 256u * (n & 1u) + lane_addr + (uint32_t)(part * C::kCols);
+            };
+            auto release = [&](uint32_t n) {
+                ptx::tc_fence_before();
+                __syncwarp();
                 if (lane == 0) {
-                    ptx::tma_store_3d(&tmO, stage, n0, row0, 0);
-                    ptx::bulk_commit_group();
+                    if (CG == 2)
+                        ptx::mbar_arrive_remote(ptx::map_to_cta(acc_empty(n & 1u), 0));
+                    else
+                        ptx::mbar_arrive(acc_empty(n & 1u));
                 }
-            } else {
-                if (!wait_acc(tc))
-                    break;
-                const uint32_t acc = acc_addr(tc);
+            };
+            // writes a box (128 bytes a row, 32 rows) to the staging buffer once its last store has left it
+            auto stage_box = [&](const uint32_t *h) {
+                if (lane == 0)
+                    ptx::bulk_wait_group_read<0>();
+                __syncwarp();
 #pragma unroll
-                for (int g = 0; g < 2; ++g) { // 32 FP32 columns a box
-                    uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(acc + 32u * g, v);
-                    ptx::tmem_ld_wait_tie(v);
-                    if (g == 1)
-                        release(tc);
-                    const int x0 = n0 + 32 * g;
-                    if (x0 >= p.N || row0 >= p.M)
-                        continue;
-                    if (MODE == kGradW32) {
+                for (int j = 0; j < 8; ++j)
+                    ptx::st_shared_v4(stage_row + (uint32_t)((j ^ (lane & 7)) << 4), h[4 * j], h[4 * j + 1], h[4 * j + 2],
+                                      h[4 * j + 3]);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            };
+            uint32_t tc = 0;
+            RowIn next = row_in(unit);
+            for (int t = unit; t < num_tiles; t += units) {
+                int mi, ni, ks;
+                head_coords(p, t, mi, ni, ks);
+                if (MODE == kGradX &&
+                    (int64_t)p.num_kb * ks / p.splits == (int64_t)p.num_kb * (ks + 1) / p.splits)
+                    continue;
+                const int row0 = tile_row(mi);
+                const int64_t row = (int64_t)row0 + lane;
+                const int n0 = ni * bn + part * C::kCols;
+                const RowIn in = next;
+                const int64_t rel = in.target - p.col0 - n0;
+                const bool has = in.target >= 0 && in.target < p.V;
+                const int tcol = has && rel >= 0 && rel < C::kCols ? (int)rel : -1; // the target's column, if here
+                if constexpr (MODE == kGrad || MODE == kGradW16) { // 64 BF16 columns: one box
+                    if (!wait_acc(tc))
+                        break;
+                    // a row without a loss: exponent 0 and coefficient 0, so that d = 0 whatever its lse
+                    const bool loss = MODE == kGrad && has && gmax > 0.0f;
+                    const float k2 = loss ? p.k2 : 0.0f, lse2 = loss ? in.lse * kLog2e : 0.0f;
+                    const float f = MODE == kGradW16 ? factor : (loss ? __fdiv_rn(in.dloss, gmax) : 0.0f);
+                    next = row_in(t + units);
+                    uint32_t h[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = __float_as_uint(__uint_as_float(v[j]) * factor);
+                    for (int ch = 0; ch < 2; ++ch) {
+                        uint32_t v[32];
+                        ptx::tmem_ld_32x32b_x32(acc_addr(tc) + 32u * ch, v);
+                        ptx::tmem_ld_wait_tie(v);
+                        if (ch == 1)
+                            release(tc);
+                        if constexpr (MODE == kGrad) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = __float_as_uint(ex2(fmaf(__uint_as_float(v[j]), k2, -lse2)));
+                            if (__any_sync(0xFFFFFFFFu, tcol >> 5 == ch)) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    v[j] = 32 * ch + j == tcol ? __float_as_uint(__uint_as_float(v[j]) - 1.0f) : v[j];
+                            }
+                            if (n0 + 32 * ch + 32 > p.N) { // columns past the piece: zero, part of the dx product's K
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    v[j] = n0 + 32 * ch + j < p.N ? v[j] : 0u;
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const __nv_bfloat162 b2 =
+                                __floats2bfloat162_rn(__uint_as_float(v[2 * j]) * f, __uint_as_float(v[2 * j + 1]) * f);
+                            h[16 * ch + j] = *reinterpret_cast<const uint32_t *>(&b2);
+                        }
                     }
-                    stage_box(v);
+                    ++tc;
+                    if (row0 >= p.M || (MODE == kGradW16 && n0 >= p.N))
+                        continue;
+                    stage_box(h);
                     if (lane == 0) {
-                        if (p.add)
-                            ptx::tma_add_3d(&tmO, stage, x0, row0, ks);
-                        else
-                            ptx::tma_store_3d(&tmO, stage, x0, row0, ks);
+                        ptx::tma_store_3d(&tmO, stage, n0, row0, 0);
                         ptx::bulk_commit_group();
                     }
+                } else {
+                    if (!wait_acc(tc))
+                        break;
+                    const uint32_t acc = acc_addr(tc);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) { // 32 FP32 columns a box
+                        uint32_t v[32];
+                        ptx::tmem_ld_32x32b_x32(acc + 32u * g, v);
+                        ptx::tmem_ld_wait_tie(v);
+                        if (g == 1)
+                            release(tc);
+                        const int x0 = n0 + 32 * g;
+                        if (x0 >= p.N || row0 >= p.M)
+                            continue;
+                        if (MODE == kGradW32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = __float_as_uint(__uint_as_float(v[j]) * factor);
+                        }
+                        stage_box(v);
+                        if (lane == 0) {
+                            if (p.add)
+                                ptx::tma_add_3d(&tmO, stage, x0, row0, ks);
+                            else
+                                ptx::tma_store_3d(&tmO, stage, x0, row0, ks);
+                            ptx::bulk_commit_group();
+                        }
+                    }
+                    ++tc;
                 }
-                ++tc;
             }
         }
         if (C::kStaging && lane == 0)
@@ -642,6 +699,16 @@ cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorM
     if (configured_device != dev) {
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem)) != cudaSuccess)
             return e;
+        if (C::kRegSplit) {
+            // setmaxnreg.inc waits until the CTA's registers can serve it: the launch must
+            // provide both shares, or the kernel would stall
+            cudaFuncAttributes fa;
+            if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess)
+                return e;
+            if (fa.numRegs < C::kRegProducer || fa.numRegs > C::kRegEpilogue ||
+                fa.numRegs * C::kThreads < C::kRegProducer * 128 + C::kRegEpilogue * 32 * C::kEpiWarps)
+                return cudaErrorInvalidConfiguration;
+        }
         configured_device = dev;
     }
     p.limit_ns = kWaitLimitNs;
