@@ -92,8 +92,14 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 1 : (MT == 1 ? 24 
     const int steps = (int)((p.k + kStep - 1) / kStep);
     const int s0 = steps * warp / kWarps, s1 = steps * (warp + 1) / kWarps;
     const int64_t ra = min(row0 + g, p.n - 1), rb = min(row0 + g + 8, p.n - 1); // rows past n: read, not stored
-    const uint8_t *qa = p.q + ra * (p.k / 2), *qb = p.q + rb * (p.k / 2);
-    const uint8_t *sa = p.sb + ra * (p.k / 16), *sbb = p.sb + rb * (p.k / 16);
+    // this lane's 32 columns of step 0; a step is 64 bytes of codes, 8 of scales, 256 of x
+    const uint8_t *qa = p.q + ra * (p.k / 2) + 16 * t, *qb = p.q + rb * (p.k / 2) + 16 * t;
+    const uint8_t *sa = p.sb + ra * (p.k / 16) + 2 * t, *sbb = p.sb + rb * (p.k / 16) + 2 * t;
+    const uint16_t *xr[MT]; // lanes past the last token read it too: their sums are not stored
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        xr[i] = p.x + min(8 * i + g, p.m - 1) * p.ldx + 32 * t;
+    const int left = (int)p.k - 32 * t; // columns from this lane's first one on
     float acc[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -110,14 +116,13 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 1 : (MT == 1 ? 24 
     auto load = [&](int s, Batch &b) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int64_t k = (int64_t)(s + u) * kStep + t * 32;
             b.ca[u] = b.cb[u] = make_uint4(0, 0, 0, 0);
             b.fa[u] = b.fb[u] = 0;
-            if (s + u < s1 && k < p.k) {
-                b.ca[u] = __ldcs(reinterpret_cast<const uint4 *>(qa + k / 2)); // each weight is read once
-                b.cb[u] = __ldcs(reinterpret_cast<const uint4 *>(qb + k / 2));
-                b.fa[u] = __ldg(reinterpret_cast<const uint16_t *>(sa + k / 16));
-                b.fb[u] = __ldg(reinterpret_cast<const uint16_t *>(sbb + k / 16));
+            if (s + u < s1 && (s + u) * kStep < left) {
+                b.ca[u] = __ldcs(reinterpret_cast<const uint4 *>(qa + (s + u) * 64)); // each weight is read once
+                b.cb[u] = __ldcs(reinterpret_cast<const uint4 *>(qb + (s + u) * 64));
+                b.fa[u] = __ldg(reinterpret_cast<const uint16_t *>(sa + (s + u) * 8));
+                b.fb[u] = __ldg(reinterpret_cast<const uint16_t *>(sbb + (s + u) * 8));
             }
         }
     };
@@ -126,7 +131,14 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 1 : (MT == 1 ? 24 
         for (int u = 0; u < kUnroll; ++u) {
             if (s + u >= s1)
                 break;
-            const int64_t k = (int64_t)(s + u) * kStep + t * 32;
+            uint4 x[MT][4];
+            const bool in = (s + u) * kStep < left; // false only in the last, partial step
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[i][j] = in ? __ldg(reinterpret_cast<const uint4 *>(xr[i] + (s + u) * kStep + 8 * j))
+                                 : make_uint4(0, 0, 0, 0);
             uint32_t sca[2], scb[2];
             decode_scales(b.fa[u], sca);
             decode_scales(b.fb[u], scb);
@@ -139,15 +151,12 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 1 : (MT == 1 ? 24 
                 decode8(wb[j], scb[j >> 1], pb);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
-                    const int tok = 8 * i + g;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (tok < p.m && k < p.k)
-                        x = __ldg(reinterpret_cast<const uint4 *>(p.x + tok * p.ldx + k + 8 * j));
                     // pairs (0, 4), (1, 5), (2, 6), (3, 7), as the weights come
-                    mma_16816(acc[i], pa[0], pb[0], pa[1], pb[1], __byte_perm(x.x, x.z, 0x5410),
-                              __byte_perm(x.x, x.z, 0x7632));
-                    mma_16816(acc[i], pa[2], pb[2], pa[3], pb[3], __byte_perm(x.y, x.w, 0x5410),
-                              __byte_perm(x.y, x.w, 0x7632));
+                    const uint4 v = x[i][j];
+                    mma_16816(acc[i], pa[0], pb[0], pa[1], pb[1], __byte_perm(v.x, v.z, 0x5410),
+                              __byte_perm(v.x, v.z, 0x7632));
+                    mma_16816(acc[i], pa[2], pb[2], pa[3], pb[3], __byte_perm(v.y, v.w, 0x5410),
+                              __byte_perm(v.y, v.w, 0x7632));
                 }
             }
         }
