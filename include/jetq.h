@@ -634,7 +634,7 @@ JETQ_API jetq_status jetq_norm_bwd(jetq_norm_kind kind, jetq_out_dtype dtype, co
  *   x, n, c, ldx   BF16 [n x c], row stride ldx (multiple of 8); c a multiple of 8
  *   w, v, ldw      BF16 [v x c], row stride ldw (multiple of 8); any v >= 1
  *   target         device int64 [n]
- *   scale          > 0, finite
+ *   scale          in (0, 1e38]
  *   loss, lse      float [n]
  *   workspace      device memory, 16-byte aligned, at least
  *                  jetq_linear_ce_workspace_bytes(n, v) bytes; calls that

@@ -574,9 +574,16 @@ def grouped(kind, a, sa, b, sb, seg_offsets, n, k, out_dtype=torch.float32, reci
     return out
 
 
+# The helpers below allocate on the stream that they launch on (workspaces are
+# released when they return, and their memory must not be reused on another
+# stream before the kernels are done with it).
+
 def gemv_nvfp4(x, b, out_dtype=torch.float32, stream=None):
     """Few-token product of BF16 x [m x k], m <= 16, with a quant_nvfp4 dict b of a weight
     [n x k] (tensor scope; see jetq_gemv_nvfp4) -> [m x n]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gemv_nvfp4(x, b, out_dtype)
     q, sb, sg = b["q"], b["sb"], b["sg"]
     _want(x, "x", torch.bfloat16, rows=True)
     (m, k), n = x.shape, q.shape[0]
@@ -584,7 +591,7 @@ def gemv_nvfp4(x, b, out_dtype=torch.float32, stream=None):
     _want(sb, "sb", torch.uint8, (n, k // 16))
     _want(sg, "sg", torch.float32, (1,))
     y = torch.empty((m, n), dtype=out_dtype, device=x.device)
-    jetq_gemv_nvfp4(q, sb, sg, x, y, stream)
+    jetq_gemv_nvfp4(q, sb, sg, x, y)
     return y
 
 
@@ -602,6 +609,9 @@ def _norm_rows(x, n, c):
 def norm_fwd(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, stream=None):
     """Layer norm or RMS norm of BF16 or FP32 rows x [n x c] (see jetq_norm_fwd) ->
     (y, mean [n] (None for RMS), rstd [n])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_fwd(x, w, b, eps, kind)
     _want(x, "x", _NORM_DTYPES, rows=True)
     n, c = x.shape
     if w is not None:
@@ -611,12 +621,15 @@ def norm_fwd(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, stream=None):
     y = _norm_rows(x, n, c)
     rstd = torch.empty(n, dtype=torch.float32, device=x.device)
     mean = torch.empty(n, dtype=torch.float32, device=x.device) if kind == NORM_LAYER else None
-    jetq_norm_fwd(kind, x, w, b, eps, y, mean, rstd, stream)
+    jetq_norm_fwd(kind, x, w, b, eps, y, mean, rstd)
     return y, mean, rstd
 
 
 def norm_bwd(dy, x, w, mean, rstd, kind=NORM_LAYER, bias=False, workspace=None, stream=None):
     """Backward pass of norm_fwd (see jetq_norm_bwd) -> (dx, dw FP32 [c], db FP32 [c] or None)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_bwd(dy, x, w, mean, rstd, kind, bias, workspace)
     _want(x, "x", _NORM_DTYPES, rows=True)
     n, c = x.shape
     _want(dy, "dy", x.dtype, (n, c), rows=True)
@@ -631,7 +644,7 @@ def norm_bwd(dy, x, w, mean, rstd, kind=NORM_LAYER, bias=False, workspace=None, 
     if workspace is None:
         workspace = torch.empty(jetq_norm_bwd_workspace_bytes(_out_dtype(x), n, c), dtype=torch.uint8,
                                 device=x.device)
-    jetq_norm_bwd(kind, dy, x, w, mean if kind == NORM_LAYER else None, rstd, dx, dw, db, workspace, stream)
+    jetq_norm_bwd(kind, dy, x, w, mean if kind == NORM_LAYER else None, rstd, dx, dw, db, workspace)
     return dx, dw, db
 
 
@@ -646,6 +659,9 @@ def _check_head(x, w, target):
 def linear_ce(x, w, target, scale=1.0, workspace=None, stream=None):
     """Token losses of a linear head (see jetq_linear_ce_fwd): BF16 x [n x c], w [v x c], int64
     target [n] (outside [0, v): no loss) -> (loss [n], lse [n])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_ce(x, w, target, scale, workspace)
     _check_head(x, w, target)
     n, v = x.shape[0], w.shape[0]
     loss = torch.empty(n, dtype=torch.float32, device=x.device)
@@ -653,7 +669,7 @@ def linear_ce(x, w, target, scale=1.0, workspace=None, stream=None):
     need = jetq_linear_ce_workspace_bytes(n, v)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    jetq_linear_ce_fwd(x, w, target, scale, loss, lse, workspace, stream)
+    jetq_linear_ce_fwd(x, w, target, scale, loss, lse, workspace)
     return loss, lse
 
 
@@ -661,6 +677,9 @@ def linear_ce_bwd(x, w, target, lse, dloss, scale=1.0, dw_dtype=torch.float32, d
                   workspace=None, stream=None):
     """Gradient of linear_ce (see jetq_linear_ce_bwd) -> (dx BF16 [n x c], dw [v x c]).  A workspace
     that the caller gives is used as it is: its size decides the vocabulary's pieces."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_ce_bwd(x, w, target, lse, dloss, scale, dw_dtype, dw, accumulate, workspace)
     _check_head(x, w, target)
     (n, c), v = x.shape, w.shape[0]
     _want(lse, "lse", torch.float32, (n,))
@@ -673,5 +692,5 @@ def linear_ce_bwd(x, w, target, lse, dloss, scale=1.0, dw_dtype=torch.float32, d
     dx = torch.empty((n, c), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = torch.empty(jetq_linear_ce_bwd_workspace_bytes(n, v, c), dtype=torch.uint8, device=x.device)
-    jetq_linear_ce_bwd(x, w, target, scale, lse, dloss, dx, dw, accumulate, workspace, stream)
+    jetq_linear_ce_bwd(x, w, target, scale, lse, dloss, dx, dw, accumulate, workspace)
     return dx, dw

@@ -645,11 +645,11 @@ jetq_status check_linear_ce(const uint16_t *x, int64_t n, int64_t c, int64_t ldx
                             int64_t ldw, const int64_t *target, float scale)
 {
     JQ_REQUIRE(n >= 0 && v > 0 && c > 0, JETQ_ERR_INVALID_ARG);
-    JQ_REQUIRE(scale > 0.0f && scale <= 3.0e38f, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(scale > 0.0f && scale <= 1.0e38f, JETQ_ERR_INVALID_ARG);
     JQ_REQUIRE(c % 8 == 0 && ldx >= c && ldw >= c, JETQ_ERR_UNSUPPORTED_SHAPE);
     JQ_REQUIRE(n <= (1 << 30) && v <= (1 << 30) && c <= (1 << 24) && (n / 128 + 1) * (v / 256 + 1) <= (1 << 30) &&
-                   (v / 128 + 1) * (c / 256 + 1) <= (1 << 30) && ldx <= ((int64_t)1 << 36) &&
-                   ldw <= ((int64_t)1 << 36),
+                   (v / 128 + 1) * (c / 256 + 1) <= (1 << 30) && (n / 128 + 1) * (c / 256 + 1) <= (1 << 26) &&
+                   ldx <= ((int64_t)1 << 36) && ldw <= ((int64_t)1 << 36),
                JETQ_ERR_UNSUPPORTED_SHAPE);
     JQ_REQUIRE(w != nullptr && (n == 0 || (x != nullptr && target != nullptr)), JETQ_ERR_INVALID_ARG);
     JQ_REQUIRE(aligned16(x) && ldx % 8 == 0 && aligned16(w) && ldw % 8 == 0 &&

@@ -217,8 +217,8 @@ cudaError_t launch_gemv_nvfp4(const GemvNvfp4Args &a, cudaStream_t st)
         return a.m <= 8 ? launch_pdl(k_gemv_nvfp4<1, 4>, grid, dim3(128), 0, st, p)
                         : launch_pdl(k_gemv_nvfp4<2, 4>, grid, dim3(128), 0, st, p);
     if (blocks > sm_count())
-        return a.m <= 8 ? launch_pdl(k_gemv_nvfp4<1, 8>, grid, dim3(256), 0, st, p)
-                        : launch_pdl(k_gemv_nvfp4<2, 8>, grid, dim3(256), 0, st, p);
+        return a.m <= 8 ? launch_pdl(k_gemv_nvfp4<1, 12>, grid, dim3(384), 0, st, p)
+                        : launch_pdl(k_gemv_nvfp4<2, 12>, grid, dim3(384), 0, st, p);
     return a.m <= 8 ? launch_pdl(k_gemv_nvfp4<1, 16>, grid, dim3(512), 0, st, p)
                     : launch_pdl(k_gemv_nvfp4<2, 16>, grid, dim3(512), 0, st, p);
 }

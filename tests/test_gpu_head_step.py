@@ -60,3 +60,24 @@ def test_a_few_steps_learn():
     losses, hits = head_step.main(steps=20)
     assert losses[0] > 7 and losses[-1] < 0.2 * losses[0]
     assert hits >= 60
+
+
+def test_helpers_on_another_stream():
+    """The helpers' `stream` argument: same results, workspaces and outputs allocated for that stream."""
+    head = head_step.Head(900, 256, seed=7)
+    x, target, weight = _batch(300, 900, 256, 8)
+    y, _, rstd = jq.norm_fwd(x, head.norm16, eps=1e-6, kind=jq.NORM_RMS)
+    loss, lse = jq.linear_ce(y, head.weight16, target)
+    dy, dw = jq.linear_ce_bwd(y, head.weight16, target, lse, weight)
+    dx, dn, _ = jq.norm_bwd(dy, x, head.norm16, None, rstd, kind=jq.NORM_RMS)
+    z = jq.gemv_nvfp4(y[:4], head.weight4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y1, _, rstd1 = jq.norm_fwd(x, head.norm16, eps=1e-6, kind=jq.NORM_RMS, stream=side)
+    loss1, lse1 = jq.linear_ce(y1, head.weight16, target, stream=side)
+    dy1, dw1 = jq.linear_ce_bwd(y1, head.weight16, target, lse1, weight, stream=side)
+    dx1, dn1, _ = jq.norm_bwd(dy1, x, head.norm16, None, rstd1, kind=jq.NORM_RMS, stream=side)
+    z1 = jq.gemv_nvfp4(y1[:4], head.weight4, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in ((y, y1), (loss, loss1), (dy, dy1), (dw, dw1), (dx, dx1), (dn, dn1), (z, z1)):
+        assert torch.equal(a, b)

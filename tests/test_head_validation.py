@@ -38,6 +38,7 @@ def _ce_fwd(L, **k):
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(c=60), SHAPE), (dict(ldx=56), SHAPE), (dict(ldw=56), SHAPE), (dict(v=1 << 31), SHAPE),
     (dict(n=1 << 31), SHAPE), (dict(n=1 << 29, v=1 << 29), SHAPE),
+    (dict(n=1 << 29, c=1 << 16, ldx=1 << 16, ldw=1 << 16), SHAPE),
     (dict(x=P(4104)), ALIGN), (dict(w=P(4104)), ALIGN), (dict(ldx=68), ALIGN), (dict(ldw=68), ALIGN),
     (dict(target=P(4100)), ALIGN), (dict(loss=P(4098)), ALIGN), (dict(ws=P(4104)), ALIGN),
 ])
