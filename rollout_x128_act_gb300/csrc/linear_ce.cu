@@ -23,6 +23,18 @@
 // uniform dloss adds no rounding of its own; sums, softmax statistics, dx
 // across pieces and dw stay in FP32 until their one final rounding.
 //
+// What bounds it.  Batches: the tensor cores.  Two CTAs of a cluster share a
+// 256 x 256 tile (cta_group::2): per 64 columns of K each loads 32 KB for 512
+// tensor cycles, where a single CTA's 128 x 256 tile needs 48 KB, more than an
+// SM's 64 bytes a cycle from L2.  The tile's FP32 sums are double-buffered in
+// TMEM, so the epilogue works under the next tile's products.  4096 tokens x
+// 131072 x 4096: forward 2.36 ms alone (1.86 PFLOP/s, 0.97 of the measured BF16
+// burst rate), 2.61 ms back to back; backward 7.78 ms back to back (1.70
+// PFLOP/s, 0.97 of the rate cuBLAS sustains under the power cap).  Few tokens:
+// the weight's stream from HBM (one token x 32000 x 4096: 47 us for 262 MB).
+// Rows that are not multiples of 128 bytes cost L2 sectors: 1000 x 50257 x 1032
+// backward takes 287 us, 1.08 PFLOP/s.
+//
 // The target's term is left out of the sum of exponentials and joined at the
 // end: loss = log1p(sum of the others / the target's) where the target leads,
 // so a confident token's loss keeps its relative precision.
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                 // The tensor core's FP32 accumulator truncates at each step: over a whole K of 4096 the losses
                 // of 4096 tokens are off by 3e-6 (2-norm, against binary64), a single token's by up to 2e-5.
                 // So partial tiles of kFold 64-blocks of K are summed here in round-to-nearest: 8 blocks for
-                // batches (4e-7, less than an FP32 matrix product's 6e-7; 4096 tokens x 131072 x 4096: 2.65 ms
+                // batches (3e-7, less than an FP32 matrix product's 6e-7; 4096 tokens x 131072 x 4096: 2.65 ms
                 // against 2.97 with 4 and 4.03 with 2, whose hand-overs stall the pair), 2 for the small row
                 // counts of single CTAs (1e-7; there the time is the weight's stream either way).
                 float2 z[64];
@@ -732,10 +744,11 @@ cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorM
 }
 
 // CTA pairs (256 x 256 tiles) or single CTAs (128 x 256)?  A 64-block of K is
-// 512 tensor cycles for either, but a single CTA loads 48 KB for it and a CTA
-// of a pair 32 KB, against an SM's 64 bytes a cycle from L2: single CTAs take
-// 1.2 times as long a tile (4096 tokens x 131072 x 4096: forward 2.81 ms against
-// 2.36, d + dx + dw 8.72 against 7.8).  They waste less where the rows do not fill pairs.
+// 512 tensor cycles for either, but a single CTA loads 48 KB for it, 750 cycles
+// at an SM's 64 bytes a cycle from L2, and a CTA of a pair 32 KB: single CTAs
+// count 1.2 times as long a tile (back to back at the power cap, where clocks
+// fall, d + dx + dw of 4096 tokens x 131072 x 4096 measured 8.72 ms against
+// 7.99).  They waste less where the rows do not fill pairs.
 int pick_cg(int64_t rows, int64_t tiles_n)
 {
     if (rows <= 128)

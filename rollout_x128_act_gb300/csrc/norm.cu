@@ -17,14 +17,17 @@
 //
 // Forward: a warp a row (up to 8 KB; 2 or 4 warps above, 8 where there are
 // fewer rows than SMs), which runs over the row in shared memory for the mean,
-// the spread and the output.  A first version with a row in the registers of 8
-// warps spent half its instructions on the reductions, waits and addresses of
-// each warp's 512 elements: 16384 x 4096 BF16 took 62 us.
+// the spread and the output, two elements an instruction.  16384 x 4096 BF16:
+// 45.5 us, 5.9 TB/s, 0.87 of the measured copy rate.  A first version with a
+// row in the registers of 8 warps (62 us; 4 warps of 32 elements a lane: 60)
+// spent half its instructions on the reductions, waits and addresses of each
+// warp's 512 or 1024 elements.
 //
 // Backward: 1 to 16 warps a row, 16 elements a lane in registers.  A lane's
 // columns are the same in every row, so dw and db are summed in registers; each
 // group writes one partial row and a second kernel adds the partial rows in a
-// fixed order (no atomics: results are bitwise repeatable).
+// fixed order (no atomics: results are bitwise repeatable).  32768 x 2048 BF16:
+// 70.8 us with that kernel, 5.7 TB/s, 0.84 of the copy rate.
 //
 // Rows wider than 8192 take the k_norm_*wide* kernels, which read a row from
 // memory more than once.
