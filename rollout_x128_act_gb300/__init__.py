@@ -603,7 +603,7 @@ def _norm_rows(x, n, c):
     pad = -c % (8 if x.dtype is torch.bfloat16 else 4)
     if pad == 0:
         return torch.empty((n, c), dtype=x.dtype, device=x.device)
-    return torch.empty((n, c + pad), dtype=x.dtype, device=x.device)[:, :c]
+    return torch.empty_strided((n, c), (c + pad, 1), dtype=x.dtype, device=x.device)
 
 
 def norm_fwd(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, stream=None):

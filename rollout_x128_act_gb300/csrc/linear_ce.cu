@@ -75,6 +75,7 @@ struct HeadParams {
     int bn, box_a;                     // columns a tile (kStats; else 256), rows of A's box
     float k2;                          // scale * log2(e): exponents in base 2
     const int64_t *target;
+    int fold;                          // kStats: 64-blocks of K summed inside the tensor core, see the epilogue
     int64_t V, col0;                   // whole vocabulary; first vocabulary row of this piece
     float2 *part;                      // [kParts * nt][M] (maximum, sum), base 2
     float *zt;                         // [M] raw target logits
@@ -100,8 +101,6 @@ struct HeadCfg {
     static constexpr size_t kStagingBytes = kStaging ? kEpiWarps * 4096 : 0; // a 4 KB box a warp
     static constexpr int kStages = (int)((225 * 1024 - kStagingBytes) / kStage);
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kStagingBytes + 256;
-    // 64-blocks of K summed inside the tensor core before the epilogue takes the partial tile
-    static constexpr int kFold = MODE == kStats ? (CG == 2 ? 8 : 2) : 1 << 30;
     static constexpr bool kAMn = MODE == kGradW16 || MODE == kGradW32; // A's M axis contiguous
     static constexpr bool kBMn = MODE >= kGradX;                       // B's N axis contiguous
     // register split of the statistics: producer warps, epilogue warps
@@ -259,7 +258,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     continue;
                 for (int kb = k0; kb < k1; ++tc) {
                     const uint32_t b = tc & 1u;
-                    const int stop = k1 - kb > C::kFold ? kb + C::kFold : k1;
+                    const int stop = MODE == kStats && k1 - kb > p.fold ? kb + p.fold : k1;
                     if (!ptx::mbar_wait<CG == 2>(acc_empty(b), ((tc >> 1) & 1u) ^ 1u, abort_flag, err, kErrTimeout,
                                                  p.limit_ns)) {
                         ok = false;
@@ -333,15 +332,12 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                 };
                 // The tensor core's FP32 accumulator truncates at each step: over a whole K of 4096 the losses
                 // of 4096 tokens are off by 3e-6 (2-norm, against binary64), a single token's by up to 2e-5.
-                // So partial tiles of kFold 64-blocks of K are summed here in round-to-nearest: 8 blocks for
-                // batches (3e-7, less than an FP32 matrix product's 6e-7; 4096 tokens x 131072 x 4096: 2.65 ms
-                // against 2.97 with 4 and 4.03 with 2, whose hand-overs stall the pair), 2 for the small row
-                // counts of single CTAs (1e-7; there the time is the weight's stream either way).
+                // So partial tiles of `fold` 64-blocks of K are summed here in round-to-nearest.
                 float2 z[64];
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
                     z[j] = make_float2(0.0f, 0.0f);
-                const int folds = (p.num_kb + C::kFold - 1) / C::kFold;
+                const int folds = (p.num_kb + p.fold - 1) / p.fold;
                 bool ok = true;
                 for (int f = 0; f < folds && ok; ++f) {
                     const uint32_t n = tc + (uint32_t)f;
@@ -856,6 +852,12 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
     p.N = a.v;
     p.k2 = a.scale * kLog2e;
     p.target = a.target;
+    // The error of a loss grows with the steps of a partial tile.  Pairs: 8 blocks (3e-7 in the 2-norm over
+    // 4096 tokens, an FP32 matrix product has 6e-7; 4096 x 131072 x 4096 took 2.65 ms with 8, 2.97 with 4 and
+    // 4.03 with 2, whose hand-overs between the CTAs stall the tensor core).  Single CTAs: 4 (2e-7; 333 tokens x
+    // 50257 x 2048: 64 us, 67 with 2).  One row tile: 2, for single tokens' losses have no others to average
+    // with (worst of 12 tokens: 1.6e-6 with 4), and there the weight's stream takes the time.
+    p.fold = cg == 2 ? 8 : (a.n > 128 ? 4 : 2);
     p.V = a.v;
     p.part = static_cast<float2 *>(a.ws);
     p.zt = reinterpret_cast<float *>(p.part + (size_t)kParts * p.nt * a.n);
