@@ -624,9 +624,10 @@ __global__ void __launch_bounds__(1024)
         loss[row] = 0.0f;
         return;
     }
-    const float t2 = zt[row] * k2;
-    lse[row] = kLn2 * (a.x + log2f(a.y + ex2(t2 - a.x)));
-    loss[row] = t2 >= a.x ? log1pf(a.y) : kLn2 * (a.x - t2) + logf(a.y + ex2(t2 - a.x));
+    // the target's exponent against the maximum's, rounded once: both products carry errors of lse's size
+    const float dt = fmaf(zt[row], k2, -a.x);
+    lse[row] = kLn2 * (a.x + log2f(a.y + exp2f(dt)));
+    loss[row] = dt >= -1.0f ? log1pf(a.y * exp2f(-dt)) : logf(a.y + exp2f(dt)) - kLn2 * dt;
 }
 
 // gmax = max |dloss| over the rows with a target (1 where that is not finite).
