@@ -639,8 +639,10 @@ __global__ void k_ce_gmax(const float *dloss, const int64_t *target, int64_t n, 
     float m = 0.0f;
     for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
         const int64_t tg = target[i];
-        if (tg >= 0 && tg < v)
-            m = fmaxf(m, fabsf(dloss[i]));
+        if (tg >= 0 && tg < v) {
+            const float g = fabsf(dloss[i]);
+            m = g < INFINITY ? fmaxf(m, g) : INFINITY; // NaN too: the rows then keep their own values
+        }
     }
     for (int o = 16; o; o >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));

@@ -127,6 +127,24 @@ def test_rows_without_a_loss():
     assert bool((dx[[i for i in range(70) if i != 3]] == 0).all()) and bool((dx[3] != 0).any())
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nonfinite_weight_of_a_row_with_a_loss(bad):
+    """It shows in its own row of dx; the other rows' gradients stay what they are."""
+    x, w, target, dloss = _inputs(12, 300, 64, seed=13, ignored=False)
+    _, lse = jq.linear_ce(x, w, target)
+    dx, _ = jq.linear_ce_bwd(x, w, target, lse, dloss / dloss.abs().max())
+    one = dloss / dloss.abs().max()
+    one[4] = bad
+    dx1, _ = jq.linear_ce_bwd(x, w, target, lse, one)
+    keep = [i for i in range(12) if i != 4]
+    assert not bool(torch.isfinite(dx1[4].float()).any())
+    assert torch.equal(dx1[keep], dx[keep])
+    target[:] = -1
+    target[4] = 0  # the only loss
+    dx1, _ = jq.linear_ce_bwd(x, w, target, lse, one)
+    assert not bool(torch.isfinite(dx1[4].float()).any()) and bool((dx1[keep] == 0).all())
+
+
 def test_confident_token_keeps_its_relative_precision():
     """One logit far above the others: loss = sum of the others over it, far below FP32's step at lse."""
     v, c = 512, 8
