@@ -72,7 +72,8 @@ enum HeadMode : int {
 struct HeadParams {
     int mt, nt, splits, num_kb, group; // tiles of M and N, splits and 64-blocks of K, M tiles per raster group
     int64_t M, N;                      // valid rows and columns of the output
-    int bn, box_a;                     // columns a tile (kStats; else 256), rows of A's box
+    int bn;                            // columns a tile (kStats; else 256)
+    int box_a, stages;                 // FEW: rows of A's box, ring stages of box_a rows of A and B's rows
     float k2;                          // scale * log2(e): exponents in base 2
     const int64_t *target;
     int fold;                          // kStats: 64-blocks of K summed inside the tensor core, see the epilogue
@@ -85,7 +86,11 @@ struct HeadParams {
     unsigned long long limit_ns;
 };
 
-template <int CG, int MODE>
+// FEW: one tile of at most 128 rows by single CTAs.  A's box then holds those
+// rows only (the MMA reads on past them: the rows it makes of that are never
+// stored), and the ring has as many stages as fit: one token streams the weight
+// with 7 stages of 29 KB instead of 4 of 48.
+template <int CG, int MODE, bool FEW>
 struct HeadCfg {
     static constexpr int BN = 256, BK = 64;
     static constexpr int kABytes = 128 * 128;
@@ -99,8 +104,9 @@ struct HeadCfg {
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
     static constexpr bool kStaging = MODE != kStats;
     static constexpr size_t kStagingBytes = kStaging ? kEpiWarps * 4096 : 0; // a 4 KB box a warp
-    static constexpr int kStages = (int)((225 * 1024 - kStagingBytes) / kStage);
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kStagingBytes + 256;
+    static constexpr int kStages = FEW ? 12 : (int)((225 * 1024 - kStagingBytes) / kStage); // FEW: at most
+    static constexpr size_t kTileBytes = FEW ? 225 * 1024 - kStagingBytes : (size_t)kStages * kStage;
+    static constexpr size_t kSmem = 1024 + kTileBytes + kStagingBytes + 256;
     static constexpr bool kAMn = MODE == kGradW16 || MODE == kGradW32; // A's M axis contiguous
     static constexpr bool kBMn = MODE >= kGradX;                       // B's N axis contiguous
     // register split of the statistics: producer warps, epilogue warps
@@ -109,6 +115,7 @@ struct HeadCfg {
     static constexpr int kBars = 2 * kStages + 5;
     static_assert(kBars * 8 + 8 <= 256, "barrier area");
     static_assert(kSmem <= 232448, "shared memory");
+    static_assert(!FEW || (CG == 1 && !kAMn), "one tile of rows, K-major");
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -132,26 +139,26 @@ __device__ __forceinline__ void head_coords(const HeadParams &p, int t, int &mi,
     mi = g * p.group + t - ni * gm;
 }
 
-template <int CG, int MODE>
-__global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
+template <int CG, int MODE, bool FEW>
+__global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
     k_head_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmO, const HeadParams p)
 {
-    using C = HeadCfg<CG, MODE>;
-    constexpr int S = C::kStages;
+    using C = HeadCfg<CG, MODE, FEW>;
+    constexpr int kBarS = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = ptx::align_smem<1024>(smem_raw);
-    uint8_t *staging = tiles + (size_t)S * C::kStage;
+    uint8_t *staging = tiles + C::kTileBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(staging + C::kStagingBytes);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const uint32_t bar0 = ptx::smem_addr(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
-    auto empty = [&](int s) { return bar0 + 8u * (S + s); };
-    auto acc_full = [&](int b) { return bar0 + 8u * (2 * S + b); };
-    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
-    const uint32_t done = bar0 + 8u * (2 * S + 4);
+    auto empty = [&](int s) { return bar0 + 8u * (kBarS + s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (2 * kBarS + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * kBarS + 2 + b); };
+    const uint32_t done = bar0 + 8u * (2 * kBarS + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
@@ -159,6 +166,10 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
     unsigned *err = &g_linear_ce_error;
     const int num_tiles = p.mt * p.nt * p.splits;
     const int bn = MODE == kStats ? p.bn : C::BN;
+    const int S = FEW ? p.stages : C::kStages;
+    const uint32_t a_bytes = FEW ? (uint32_t)p.box_a * 128u : (uint32_t)C::kABytes;
+    const uint32_t stage_bytes =
+        FEW ? a_bytes + (C::kBMn ? (uint32_t)C::kBBytes : (uint32_t)bn * 128u) : (uint32_t)C::kStage;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -200,7 +211,10 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
     if (warp < 4) {
         if (warp == 0 && lane == 0) {
             // -------------------------------------------------- TMA producer
-            const uint32_t tx = MODE == kStats ? (uint32_t)(CG * p.box_a + bn) * 128u : (uint32_t)(CG * C::kStage);
+            const uint32_t tx =
+                FEW ? stage_bytes : (MODE == kStats ? (uint32_t)(CG * 128 + bn) * 128u : (uint32_t)(CG * C::kStage));
+            int s = 0;
+            uint32_t ph = 0; // of the ring's pass
             uint32_t it = 0;
             bool ok = true;
             for (int t = unit; t < num_tiles && ok; t += units) {
@@ -211,8 +225,6 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                 const int m0 = mi * 128 * CG + (int)rank * 128;
                 const int n0 = ni * bn + (int)rank * (bn / CG);
                 for (int kb = k0; kb < k1; ++kb, ++it) {
-                    const int s = (int)(it % S);
-                    const uint32_t ph = (it / S) & 1u;
                     if (!ptx::mbar_wait(empty(s), ph ^ 1u, abort_flag, err, kErrTimeout, p.limit_ns)) {
                         ok = false;
                         break;
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     if (rank == 0)
                         ptx::mbar_arrive_expect_tx(full(s), tx);
                     const uint32_t bar = CG == 2 ? ptx::map_to_cta(full(s), 0) : full(s);
-                    const uint32_t da = ptx::smem_addr(tiles + (size_t)s * C::kStage), db = da + C::kABytes;
+                    const uint32_t da = ptx::smem_addr(tiles) + (uint32_t)s * stage_bytes, db = da + a_bytes;
                     if (C::kAMn) {
                         ptx::tma_load_2d_cg<CG>(da, &tmA, bar, m0, kb * C::BK);
                         ptx::tma_load_2d_cg<CG>(da + 8192u, &tmA, bar, m0 + 64, kb * C::BK);
@@ -235,20 +247,25 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                     } else {
                         ptx::tma_load_2d_cg<CG>(db, &tmB, bar, kb * C::BK, n0);
                     }
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
             // no copy may be in flight when the CTA ends (the even CTA's barriers count the pair's)
             if (rank == 0)
-                for (int s = 0; s < S; ++s)
-                    if (it > (uint32_t)s) {
-                        const uint32_t last = (uint32_t)s + ((it - 1u - (uint32_t)s) / S) * S;
-                        ptx::mbar_wait(full(s), (last / S) & 1u, abort_flag, err, kErrTimeout, p.limit_ns, false);
+                for (int q = 0; q < S; ++q)
+                    if (it > (uint32_t)q) {
+                        const uint32_t pass = (it - 1u - (uint32_t)q) / (uint32_t)S;
+                        ptx::mbar_wait(full(q), pass & 1u, abort_flag, err, kErrTimeout, p.limit_ns, false);
                     }
         } else if (warp == 1 && lane == 0 && rank == 0) {
             // -------------------------------------------------- MMA issuer
             const uint32_t idesc = ptx::idesc_bf16_f32(128 * CG, bn, C::kAMn, C::kBMn);
             constexpr uint32_t a_step = C::kAMn ? 2048u >> 4 : 32u >> 4, b_step = C::kBMn ? 2048u >> 4 : 32u >> 4;
-            uint32_t it = 0, tc = 0;
+            int s = 0;
+            uint32_t ph = 0, tc = 0;
             bool ok = true;
             for (int t = unit; t < num_tiles && ok; t += units) {
                 const int ks = t / (p.mt * p.nt);
@@ -265,23 +282,25 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE>::kThreads, 1)
                         break;
                     }
                     ptx::tc_fence_after();
-                    for (const int start = kb; kb < stop; ++kb, ++it) {
-                        const int s = (int)(it % S);
-                        const uint32_t ph = (it / S) & 1u;
+                    for (const int start = kb; kb < stop; ++kb) {
                         if (!ptx::mbar_wait<CG == 2>(full(s), ph, abort_flag, err, kErrTimeout, p.limit_ns)) {
                             ok = false;
                             break;
                         }
                         ptx::tc_fence_after();
-                        const uint32_t a = ptx::smem_addr(tiles + (size_t)s * C::kStage);
+                        const uint32_t a = ptx::smem_addr(tiles) + (uint32_t)s * stage_bytes;
                         const uint64_t ad = C::kAMn ? ptx::desc_mnmajor_sw128(a, 8192u) : ptx::desc_kmajor_sw128(a);
-                        const uint64_t bd = C::kBMn ? ptx::desc_mnmajor_sw128(a + C::kABytes, 8192u)
-                                                    : ptx::desc_kmajor_sw128(a + C::kABytes);
+                        const uint64_t bd = C::kBMn ? ptx::desc_mnmajor_sw128(a + a_bytes, 8192u)
+                                                    : ptx::desc_kmajor_sw128(a + a_bytes);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             ptx::mma_bf16<CG>(tmem_base + 256u * b, ad + a_step * k, bd + b_step * k, idesc,
                                               (kb > start || k > 0) ? 1u : 0u);
                         ptx::mma_commit_cg<CG>(empty(s));
+                        if (++s == S) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
                     if (!ok)
                         break;
@@ -697,11 +716,11 @@ int units_of(int cg)
     return u > 0 ? u : 1;
 }
 
-template <int CG, int MODE>
-cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, HeadParams p, cudaStream_t st)
+template <int CG, int MODE, bool FEW>
+cudaError_t run_tiles(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, HeadParams p, cudaStream_t st)
 {
-    using C = HeadCfg<CG, MODE>;
-    auto kern = k_head_gemm<CG, MODE>;
+    using C = HeadCfg<CG, MODE, FEW>;
+    auto kern = k_head_gemm<CG, MODE, FEW>;
     static int configured_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -723,6 +742,12 @@ cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorM
         configured_device = dev;
     }
     p.limit_ns = kWaitLimitNs;
+    if (FEW) {
+        // 16 KB stay free: what the MMA reads of the last stage past its box lies inside the allocation
+        const int64_t stage = (int64_t)p.box_a * 128 + (C::kBMn ? C::kBBytes : (int64_t)p.bn * 128);
+        const int64_t fit = ((int64_t)C::kTileBytes - C::kABytes) / stage;
+        p.stages = (int)(fit < C::kStages ? fit : C::kStages);
+    }
     const int64_t tiles = (int64_t)p.mt * p.nt * p.splits;
     const int units = (int)(tiles < units_of(CG) ? tiles : units_of(CG));
     cudaLaunchConfig_t cfg = {};
@@ -740,6 +765,24 @@ cudaError_t run_head(const CUtensorMap &a, const CUtensorMap &b, const CUtensorM
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, a, b, o, p);
+}
+
+// cg CTAs a tile; one tile of rows (cg = 1, box_a of them) takes the FEW form.
+template <int MODE>
+cudaError_t run_head(int cg, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, const HeadParams &p,
+                     cudaStream_t st)
+{
+    if constexpr (!HeadCfg<2, MODE, false>::kAMn) {
+        if (cg == 1)
+            return p.mt == 1 ? run_tiles<1, MODE, true>(a, b, o, p, st) : run_tiles<1, MODE, false>(a, b, o, p, st);
+    }
+    return run_tiles<2, MODE, false>(a, b, o, p, st);
+}
+
+// Rows of A's box by single CTAs: 128, or one tile's rows.
+int box_rows(int64_t n)
+{
+    return n <= 128 ? (int)(ceil_div(n, 8) * 8) : 128;
 }
 
 // CTA pairs (256 x 256 tiles) or single CTAs (128 x 256)?  A 64-block of K is
@@ -832,15 +875,13 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
     p.nt = (int)ceil_div(a.v, kTileN);
     const int cg = pick_cg(a.n, p.nt);
     p.bn = kTileN;
-    p.box_a = 128;
+    p.box_a = box_rows(a.n);
     if (cg == 1 && a.n <= 128) {
         // One row tile: the weight's stream is what takes time, so its rows are
-        // spread evenly over the SMs (a multiple of 16 a tile), and x's box
-        // holds its rows only (the others' sums are not stored).
+        // spread evenly over the SMs (a multiple of 16 a tile).
         const int64_t waves = ceil_div(p.nt, units_of(1));
         p.bn = (int)(ceil_div(ceil_div(a.v, waves * units_of(1)), 16) * 16);
         p.nt = (int)ceil_div(a.v, p.bn);
-        p.box_a = (int)(ceil_div(a.n, 8) * 8);
     }
     CUtensorMap ta, tb;
     cudaError_t e;
@@ -864,8 +905,7 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
     p.V = a.v;
     p.part = static_cast<float2 *>(a.ws);
     p.zt = reinterpret_cast<float *>(p.part + (size_t)kParts * p.nt * a.n);
-    e = cg == 2 ? run_head<2, kStats>(ta, tb, ta, p, st) : run_head<1, kStats>(ta, tb, ta, p, st);
-    if (e != cudaSuccess)
+    if ((e = run_head<kStats>(cg, ta, tb, ta, p, st)) != cudaSuccess)
         return e;
     const int parts = kParts * p.nt;
     int rx = 1, ry = 1;
@@ -898,11 +938,12 @@ cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
         const int cg = pick_cg(a.n, ceil_div(rows, kTileN));
         const uint16_t *w = a.w + v0 * a.ldw;
         void *dwp = static_cast<uint8_t *>(a.dw) + v0 * a.lddw * (dw16 ? 2 : 4);
+        const int box = box_rows(a.n);
         CUtensorMap xk, wk, dst, dk, wn, slabs, dm, xn, dw;
-        if ((e = make_sw128_map(&xk, a.x, false, a.c, a.n, a.ldx, 128)) != cudaSuccess ||
+        if ((e = make_sw128_map(&xk, a.x, false, a.c, a.n, a.ldx, cg == 1 ? box : 128)) != cudaSuccess ||
             (e = make_sw128_map(&wk, w, false, a.c, rows, a.ldw, kTileN / cg)) != cudaSuccess ||
             (e = make_sw128_map(&dst, d, false, cols, a.n, plan.piece, 32, 1, plan.piece * a.n)) != cudaSuccess ||
-            (e = make_sw128_map(&dk, d, false, cols, a.n, plan.piece, 128)) != cudaSuccess ||
+            (e = make_sw128_map(&dk, d, false, cols, a.n, plan.piece, plan.dx_cg == 1 ? box : 128)) != cudaSuccess ||
             (e = make_sw128_map(&wn, w, false, a.c, rows, a.ldw, 64)) != cudaSuccess ||
             (e = make_sw128_map(&slabs, slab, true, a.c, a.n, a.c, 32, plan.splits, a.n * a.c)) != cudaSuccess ||
             (e = make_sw128_map(&dm, d, false, cols, a.n, plan.piece, 64)) != cudaSuccess ||
@@ -910,6 +951,8 @@ cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
             (e = make_sw128_map(&dw, dwp, !dw16, a.c, rows, a.lddw, 32, 1, rows * a.lddw)) != cudaSuccess)
             return e;
         HeadParams p = {};
+        p.bn = kTileN;
+        p.box_a = box;
         p.gmax = gmax;
         p.scale = a.scale;
         // d of the piece
@@ -926,8 +969,7 @@ cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
         p.col0 = v0;
         p.lse = a.lse;
         p.dloss = a.dloss;
-        e = cg == 2 ? run_head<2, kGrad>(xk, wk, dst, p, st) : run_head<1, kGrad>(xk, wk, dst, p, st);
-        if (e != cudaSuccess)
+        if ((e = run_head<kGrad>(cg, xk, wk, dst, p, st)) != cudaSuccess)
             return e;
         // dx += d w
         p.mt = (int)ceil_div(a.n, 128 * plan.dx_cg);
@@ -937,8 +979,7 @@ cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
         p.group = p.mt < 64 / plan.dx_cg ? p.mt : 64 / plan.dx_cg;
         p.N = a.c;
         p.add = v0 > 0;
-        e = plan.dx_cg == 2 ? run_head<2, kGradX>(dk, wn, slabs, p, st) : run_head<1, kGradX>(dk, wn, slabs, p, st);
-        if (e != cudaSuccess)
+        if ((e = run_head<kGradX>(plan.dx_cg, dk, wn, slabs, p, st)) != cudaSuccess)
             return e;
         // dw = d^T x: few vocabulary tiles at a time against all of x
         p.mt = (int)ceil_div(rows, 256);
@@ -947,7 +988,7 @@ cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
         p.num_kb = (int)ceil_div(a.n, 64);
         p.M = rows;
         p.add = a.accumulate;
-        e = dw16 ? run_head<2, kGradW16>(dm, xn, dw, p, st) : run_head<2, kGradW32>(dm, xn, dw, p, st);
+        e = dw16 ? run_head<kGradW16>(2, dm, xn, dw, p, st) : run_head<kGradW32>(2, dm, xn, dw, p, st);
         if (e != cudaSuccess)
             return e;
     }
