@@ -23,14 +23,14 @@
 // spent half its instructions on the reductions, waits and addresses of each
 // warp's 512 or 1024 elements.
 //
-// Backward: 1 to 16 warps a row, 16 elements a lane in registers.  A lane's
+// Backward: 2 to 16 warps a row, 16 elements a lane in registers.  A lane's
 // columns are the same in every row, so dw and db are summed in registers; each
 // group writes one partial row and a second kernel adds the partial rows in a
 // fixed order (no atomics: results are bitwise repeatable).  32768 x 2048 BF16:
 // 70.8 us with that kernel, 5.7 TB/s, 0.84 of the copy rate.
 //
-// Rows wider than 8192 take the k_norm_*wide* kernels, which read a row from
-// memory more than once.
+// Rows of up to 512 columns take k_norm_short.  Rows wider than 8192 take the
+// k_norm_*wide* kernels, which read a row from memory more than once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -323,22 +323,31 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_bwd_ctas(G)) k_n
 #pragma unroll
         for (int k = 0; k < V; ++k)
             load_vec<T>(st + row_bytes, dy + row * p.lddy, last_row, (k * C::kLanes + lt) * E, p.c, t + k * E);
-        float s1 = 0.0f, s2 = 0.0f;
+        // pairs: the packed FP32 instructions do two elements an issue slot
+        const float2 neg = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+        float2 a1 = make_float2(0.0f, 0.0f), a2 = a1;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int i = k * E + e;
-                h[i] = (h[i] - mean) * rstd;
-                dw[i] = fmaf(t[i], h[i], dw[i]); // columns past c: t = 0
-                if constexpr (!RMS)
-                    db[i] += t[i];
-                t[i] *= w[i];
-                if constexpr (!RMS)
-                    s1 += t[i];
-                s2 = fmaf(t[i], h[i], s2);
+        for (int i = 0; i < LE; i += 2) {
+            float2 hv = make_float2(h[i], h[i + 1]), tv = make_float2(t[i], t[i + 1]);
+            hv = RMS ? __fmul2_rn(hv, r2) : __fmul2_rn(__fadd2_rn(hv, neg), r2);
+            const float2 g = __ffma2_rn(tv, hv, make_float2(dw[i], dw[i + 1])); // columns past c: t = 0
+            dw[i] = g.x;
+            dw[i + 1] = g.y;
+            if constexpr (!RMS) {
+                const float2 b = __fadd2_rn(make_float2(db[i], db[i + 1]), tv);
+                db[i] = b.x;
+                db[i + 1] = b.y;
             }
+            tv = __fmul2_rn(tv, make_float2(w[i], w[i + 1]));
+            if constexpr (!RMS)
+                a1 = __fadd2_rn(a1, tv);
+            a2 = __ffma2_rn(tv, hv, a2);
+            h[i] = hv.x;
+            h[i + 1] = hv.y;
+            t[i] = tv.x;
+            t[i + 1] = tv.y;
         }
+        float s1 = a1.x + a1.y, s2 = a2.x + a2.y;
         if constexpr (RMS)
             s2 = group_sum<G>(s2, red, group, wg, lane, buf);
         else
@@ -350,8 +359,15 @@ __global__ void __launch_bounds__(NormCfg<T, G>::kThreads, norm_bwd_ctas(G)) k_n
         for (int k = 0; k < V; ++k) {
             float d[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                d[e] = rstd * (t[k * E + e] - s1 - h[k * E + e] * s2);
+            for (int e = 0; e < E; e += 2) {
+                const int i = k * E + e;
+                float2 v = make_float2(t[i], t[i + 1]);
+                if constexpr (!RMS)
+                    v = __fadd2_rn(v, make_float2(-s1, -s1));
+                v = __fmul2_rn(__ffma2_rn(make_float2(h[i], h[i + 1]), make_float2(-s2, -s2), v), r2);
+                d[e] = v.x;
+                d[e + 1] = v.y;
+            }
             const int pos = (k * C::kLanes + lt) * E;
             if (pos < p.c)
                 store_vec<T>(out + row * p.ldo, pos, p.c, d);
@@ -549,6 +565,179 @@ __global__ void __launch_bounds__(1024) k_norm_params(const float *pdw, const fl
         (blockIdx.y == 0 ? dw : db)[oc] = a;
 }
 
+// ------------------------------------------------------------- short rows
+
+// Rows of up to 512 columns (a head's, for one): L lanes a row, 32 / L rows a
+// warp, V vectors a lane, loaded straight from memory for U rows a lane at a
+// time.  There are warps enough here to keep the loads in flight, and a ring's
+// waits and a warp's reductions would cost a row more than its arithmetic
+// (30000 x 128 BF16 through the kernels above: forward 13.5 us, backward 33).
+__host__ __device__ constexpr int short_ctas(int elems, bool bwd) // CTAs an SM
+{
+    return bwd ? 2 : (elems > 8 ? 3 : 4);
+}
+
+template <class T, int L, int V, bool RMS, bool BWD>
+__global__ void __launch_bounds__(256, short_ctas(Vec<T>::E *V, BWD)) k_norm_short(const NormParams p)
+{
+    constexpr int E = Vec<T>::E, N = E * V, R = 32 / L, U = N > 8 ? 2 : 4;
+    __shared__ float red[BWD ? 8 * L * N : 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L, sub = lane / L;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy);
+    T *out = static_cast<T *>(p.out);
+    auto column = [&](int i) { return ((i / E) * L + l) * E + i % E; };
+    float w[N], b[BWD ? 1 : N], dw[BWD ? N : 1], db[BWD && !RMS ? N : 1];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int col = column(i);
+        w[i] = col < p.c ? (p.w ? Vec<T>::get(static_cast<const T *>(p.w) + col) : 1.0f) : 0.0f;
+        if constexpr (!BWD)
+            b[i] = !RMS && p.b && col < p.c ? Vec<T>::get(static_cast<const T *>(p.b) + col) : 0.0f;
+        if constexpr (BWD)
+            dw[i] = 0.0f;
+        if constexpr (BWD && !RMS)
+            db[i] = 0.0f;
+    }
+    // a row's vectors as they are stored: rows that wait for their turn take half the registers
+    auto load = [&](const T *row, uint4 *raw) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int pos = (v * L + l) * E;
+            if (pos + E <= p.c) {
+                raw[v] = *reinterpret_cast<const uint4 *>(row + pos);
+            } else {
+                float f[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    f[e] = pos + e < p.c ? Vec<T>::get(row + pos + e) : 0.0f;
+                raw[v] = Vec<T>::pack(f);
+            }
+        }
+    };
+    auto sum = [&](float a) {
+#pragma unroll
+        for (int o = L / 2; o; o >>= 1)
+            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        return a;
+    };
+    const float inv_c = 1.0f / (float)p.c;
+    const int64_t step = (int64_t)gridDim.x * 8 * R * U;
+    // rows first .. first + R U of a warp, all of its lanes in every pass (the sums are shuffles)
+    for (int64_t first = ((int64_t)blockIdx.x * 8 + warp) * R * U; first < p.n; first += step) {
+        uint4 rx[U][V], ry[BWD ? U : 1][V];
+        float mean[U], rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = first + u * R + sub;
+            mean[u] = rstd[u] = 0.0f;
+            if (row < p.n) {
+                load(x + row * p.ldx, rx[u]);
+                if constexpr (BWD) {
+                    load(dy + row * p.lddy, ry[u]);
+                    mean[u] = RMS ? 0.0f : __ldg(p.mean + row);
+                    rstd[u] = __ldg(p.rstd + row);
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    rx[u][v] = make_uint4(0, 0, 0, 0);
+                    if constexpr (BWD)
+                        ry[u][v] = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = first + u * R + sub;
+            float f[N];
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                Vec<T>::unpack(rx[u][v], f + v * E);
+            if constexpr (!BWD) {
+                float m = 0.0f;
+                if constexpr (!RMS) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        m += f[i];
+                    m = sum(m) * inv_c;
+                }
+                float sq = 0.0f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    if constexpr (!RMS)
+                        f[i] = column(i) < p.c ? f[i] - m : 0.0f;
+                    sq = fmaf(f[i], f[i], sq);
+                }
+                const float r = __frcp_rn(__fsqrt_rn(fmaf(sum(sq), inv_c, p.eps)));
+                if (l == 0 && row < p.n) {
+                    if (!RMS)
+                        p.mean[row] = m;
+                    p.rstd[row] = r;
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    f[i] = fmaf(f[i] * r, w[i], b[i]);
+            } else {
+                float g[N], s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    Vec<T>::unpack(ry[u][v], g + v * E);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    f[i] = (f[i] - mean[u]) * rstd[u];
+                    dw[i] = fmaf(g[i], f[i], dw[i]); // columns past c, rows past n: dy = 0
+                    if constexpr (!RMS)
+                        db[i] += g[i];
+                    g[i] *= w[i];
+                    s1 += g[i];
+                    s2 = fmaf(g[i], f[i], s2);
+                }
+                s1 = RMS ? 0.0f : sum(s1) * inv_c;
+                s2 = sum(s2) * inv_c;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    f[i] = rstd[u] * (g[i] - s1 - f[i] * s2);
+            }
+            if (row < p.n) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int pos = (v * L + l) * E;
+                    if (pos < p.c)
+                        store_vec<T>(out + row * p.ldo, pos, p.c, f + v * E);
+                }
+            }
+        }
+    }
+    if constexpr (BWD) {
+        // the CTA's partial row: over a warp's rows by shuffles, over the warps in order
+        auto write = [&](float *acc, float *dst) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+#pragma unroll
+                for (int o = L; o < 32; o <<= 1)
+                    acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], o);
+                if (sub == 0)
+                    red[warp * L * N + column(i)] = acc[i];
+            }
+            __syncthreads();
+            for (int col = threadIdx.x; col < p.c; col += 256) {
+                float a = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    a += red[q * L * N + col];
+                dst[(int64_t)blockIdx.x * p.cpad + col] = a;
+            }
+            __syncthreads();
+        };
+        write(dw, p.pdw);
+        if constexpr (!RMS)
+            if (p.pdb)
+                write(db, p.pdb);
+    }
+}
+
 // ------------------------------------------------------------- wide rows
 
 __device__ __forceinline__ float2 block_sum2(float a, float b, float2 *red)
@@ -648,12 +837,12 @@ __global__ void __launch_bounds__(256) k_norm_wide_params(const NormParams p)
         p.pdb[(int64_t)blockIdx.y * p.cpad + col] = db;
 }
 
-constexpr int kWidest = 8192, kWideSlices = 64;
+constexpr int kShortest = 512, kWidest = 8192, kWideSlices = 64;
 constexpr size_t kSmemMost = 224 * 1024; // dynamic shared memory of the CTAs of one SM
 
 int bwd_warps(int64_t c)
 {
-    int g = 1;
+    int g = 2; // up to 512 columns: short rows
     while (g * 32 * LE < c)
         g *= 2;
     return g;
@@ -662,6 +851,24 @@ int bwd_warps(int64_t c)
 size_t row_size(int64_t c, int esize)
 {
     return (size_t)((c * esize + 15) / 16 * 16);
+}
+
+// Short rows: lanes a row, vectors a lane, and the grid (a warp's 32 / lanes
+// rows, four or two at a time).
+struct ShortPlan {
+    int lanes, vecs, grid;
+};
+
+ShortPlan short_plan(int64_t n, int64_t c, int esize, bool bwd)
+{
+    const int64_t vectors = (c * esize + 15) / 16;
+    ShortPlan r;
+    r.vecs = vectors <= 32 ? 1 : (vectors <= 64 ? 2 : 4);
+    r.lanes = vectors <= 8 ? 8 : (vectors <= 16 ? 16 : 32);
+    const int elems = 16 / esize * r.vecs, rows = 8 * (32 / r.lanes) * (elems > 8 ? 2 : 4);
+    const int64_t need = (n + rows - 1) / rows, most = (int64_t)sm_count() * short_ctas(elems, bwd);
+    r.grid = (int)(need < most ? need : most);
+    return r;
 }
 
 struct NormPlan {
@@ -752,11 +959,30 @@ cudaError_t run_norm_fwd(const NormParams &p, const NormPlan &plan, cudaStream_t
     return run_norm(k_norm_fwd<T, G, RMS>, configured, p, plan, st);
 }
 
+template <class T, bool RMS, bool BWD>
+cudaError_t run_short(const NormParams &p, const ShortPlan &plan, cudaStream_t st)
+{
+    const dim3 grid((unsigned)plan.grid), block(256);
+    if (plan.vecs == 1) {
+        if (plan.lanes == 8)
+            return launch_pdl(k_norm_short<T, 8, 1, RMS, BWD>, grid, block, 0, st, p);
+        if (plan.lanes == 16)
+            return launch_pdl(k_norm_short<T, 16, 1, RMS, BWD>, grid, block, 0, st, p);
+        return launch_pdl(k_norm_short<T, 32, 1, RMS, BWD>, grid, block, 0, st, p);
+    }
+    if (plan.vecs == 2)
+        return launch_pdl(k_norm_short<T, 32, 2, RMS, BWD>, grid, block, 0, st, p);
+    if constexpr (sizeof(T) == 4)
+        return launch_pdl(k_norm_short<T, 32, 4, RMS, BWD>, grid, block, 0, st, p);
+    else
+        return cudaErrorInvalidValue; // 512 BF16 columns are two vectors a lane
+}
+
 template <class T, bool RMS>
 cudaError_t pick_norm(const NormParams &p, const NormPlan &plan, bool bwd, cudaStream_t st)
 {
     switch (plan.warps) {
-    case 1: return bwd ? run_norm_bwd<T, 1, RMS>(p, plan, st) : run_norm_fwd<T, 1, RMS>(p, plan, st);
+    case 1: return run_norm_fwd<T, 1, RMS>(p, plan, st); // the backward pass uses two or more
     case 2: return bwd ? run_norm_bwd<T, 2, RMS>(p, plan, st) : run_norm_fwd<T, 2, RMS>(p, plan, st);
     case 4: return bwd ? run_norm_bwd<T, 4, RMS>(p, plan, st) : run_norm_fwd<T, 4, RMS>(p, plan, st);
     case 8: return bwd ? run_norm_bwd<T, 8, RMS>(p, plan, st) : run_norm_fwd<T, 8, RMS>(p, plan, st);
@@ -767,10 +993,13 @@ cudaError_t pick_norm(const NormParams &p, const NormPlan &plan, bool bwd, cudaS
 template <class T, bool RMS>
 cudaError_t norm_any(const NormArgs &a, NormParams p, bool bwd, cudaStream_t st)
 {
-    const bool wide = a.c > kWidest;
+    const bool wide = a.c > kWidest, narrow = a.c <= kShortest;
+    const ShortPlan sp = narrow ? short_plan(a.n, a.c, (int)sizeof(T), bwd) : ShortPlan{};
     const int64_t cap = (int64_t)sm_count() * 2;
     const dim3 wide_grid((unsigned)(a.n < cap ? a.n : cap));
     if (!bwd) {
+        if (narrow)
+            return run_short<T, RMS, false>(p, sp, st);
         if (wide)
             return launch_pdl(k_norm_wide<T, RMS, false>, wide_grid, dim3(1024), 0, st, p);
         const NormPlan plan = fwd_plan(a.n, a.c, (int)sizeof(T), a.b != nullptr);
@@ -779,7 +1008,10 @@ cudaError_t norm_any(const NormArgs &a, NormParams p, bool bwd, cudaStream_t st)
     }
     cudaError_t e;
     NormPlan plan = {};
-    if (!wide) {
+    if (narrow) {
+        plan.groups = sp.grid;
+        e = run_short<T, RMS, true>(p, sp, st);
+    } else if (!wide) {
         plan = bwd_plan(a.n, a.c, (int)sizeof(T));
         p.stages = plan.stages;
         e = pick_norm<T, RMS>(p, plan, true, st);
@@ -831,7 +1063,8 @@ int64_t norm_bwd_partial_rows(int64_t n, int64_t c, jetq_out_dtype dtype)
 {
     if (c > kWidest)
         return n < kWideSlices ? n : kWideSlices;
-    return bwd_plan(n, c, dtype == JETQ_OUT_BF16 ? 2 : 4).groups;
+    const int esize = dtype == JETQ_OUT_BF16 ? 2 : 4;
+    return c <= kShortest ? short_plan(n, c, esize, true).grid : bwd_plan(n, c, esize).groups;
 }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t st)

@@ -101,6 +101,17 @@ def test_without_parameters(kind):
     _check_bwd(dy, x, None, mean, rstd, kind, False)
 
 
+@pytest.mark.parametrize("c", [8, 9, 63, 64, 65, 127, 128, 129, 200, 256, 257, 383, 511, 512])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_short_rows(c, dtype):
+    """Rows of up to 512 columns: every number of lanes and vectors a row, whole and partial ones."""
+    for n, kind in ((1, jq.NORM_LAYER), (37, jq.NORM_RMS), (1003, jq.NORM_LAYER)):
+        x, dy, w, b = _inputs(n, c, dtype, seed=n + c)
+        layer = kind == jq.NORM_LAYER
+        mean, rstd = _check_fwd(x, w, b if layer else None, 1e-5, kind)
+        _check_bwd(dy, x, w, mean, rstd, kind, layer)
+
+
 def test_many_rows():
     x, dy, w, b = _inputs(30011, 264, torch.bfloat16, seed=4)
     mean, rstd = _check_fwd(x, w, b, 1e-5, jq.NORM_LAYER)
