@@ -29,11 +29,11 @@
 // SM's 64 bytes a cycle from L2.  The tile's FP32 sums are double-buffered in
 // TMEM, so the epilogue works under the next tile's products.  4096 tokens x
 // 131072 x 4096: forward 2.36 ms alone (1.86 PFLOP/s, 0.97 of the measured BF16
-// burst rate), 2.61 ms back to back; backward 7.78 ms back to back (1.70
+// burst rate), 2.58 ms back to back; backward 7.79 ms back to back (1.69
 // PFLOP/s, 0.97 of the rate cuBLAS sustains under the power cap).  Few tokens:
-// the weight's stream from HBM (one token x 32000 x 4096: 47 us for 262 MB).
+// the weight's stream from HBM (one token x 32000 x 4096: 48 us for 262 MB).
 // Rows that are not multiples of 128 bytes cost L2 sectors: 1000 x 50257 x 1032
-// backward takes 287 us, 1.08 PFLOP/s.
+// backward takes 289 us, 1.08 PFLOP/s.
 //
 // The target's term is left out of the sum of exponentials and joined at the
 // end: loss = log1p(sum of the others / the target's) where the target leads,
@@ -899,7 +899,7 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
     // The error of a loss grows with the steps of a partial tile.  Pairs: 8 blocks (3e-7 in the 2-norm over
     // 4096 tokens, an FP32 matrix product has 6e-7; 4096 x 131072 x 4096 took 2.65 ms with 8, 2.97 with 4 and
     // 4.03 with 2, whose hand-overs between the CTAs stall the tensor core).  Single CTAs: 4 (2e-7; 333 tokens x
-    // 50257 x 2048: 64 us, 67 with 2).  One row tile: 2, for single tokens' losses have no others to average
+    // 50257 x 2048: 64 us, 66 with 2).  One row tile: 2, for single tokens' losses have no others to average
     // with (worst of 12 tokens: 1.6e-6 with 4), and there the weight's stream takes the time.
     p.fold = cg == 2 ? 8 : (a.n > 128 ? 4 : 2);
     p.V = a.v;
