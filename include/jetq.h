@@ -640,6 +640,7 @@ JETQ_API jetq_status jetq_norm_bwd(jetq_norm_kind kind, jetq_out_dtype dtype, co
  *                  jetq_linear_ce_workspace_bytes(n, v) bytes; calls that
  *                  share one must not overlap on the GPU
  * n == 0 is a no-op.  Results are bitwise repeatable.  Two launches.
+ * Workspace sizes are those of the current device (here and below).
  */
 JETQ_API size_t jetq_linear_ce_workspace_bytes(int64_t n, int64_t v);
 JETQ_API jetq_status jetq_linear_ce_fwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx,

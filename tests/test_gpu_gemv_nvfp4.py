@@ -108,3 +108,17 @@ def test_stream_graph_strided_output_and_no_tokens():
     assert torch.equal(y, y1) and torch.equal(y, y2) and torch.equal(y, out[:, 1:101])
     assert bool((out[:, 0] == 7).all()) and bool((out[:, 101:] == 7).all())
     assert jq.gemv_nvfp4(x[:0], w).shape == (0, 100)
+
+
+def test_offsets_past_32_bits():
+    """A weight of 2.5e9 bytes of codes: its first and its last rows."""
+    n, k = 1_200_003, 4096
+    q = torch.randint(0, 256, (n, k // 2), device=DEV, dtype=torch.uint8)
+    sb = torch.randint(0, 127, (n, k // 16), device=DEV, dtype=torch.uint8)
+    w = dict(q=q, sb=sb, sg=torch.tensor([3.1e-4], device=DEV))
+    x = torch.randn((3, k), device=DEV).to(torch.bfloat16)
+    y = jq.gemv_nvfp4(x, w)
+    for a in (0, 2 ** 31 // (k // 2) - 20, n - 40):
+        W = _dequant(dict(q=q[a:a + 40], sb=sb[a:a + 40], sg=w["sg"]))
+        ref, size = x.double() @ W.T, x.double().abs() @ W.abs().T
+        assert bool(((y[:, a:a + 40].double() - ref).abs() <= SUM * size + 2.0 ** -24 * ref.abs()).all())

@@ -233,3 +233,48 @@ def test_no_tokens():
     dw = torch.ones((300, 64), device=DEV)
     dx, dw = jq.linear_ce_bwd(x, w, target, lse, loss, dw=dw)
     assert dx.shape == (0, 64) and bool((dw == 0).all())
+
+
+def test_offsets_past_32_bits():
+    """A head of 2.5e9 weights: the last rows are where they belong, in the losses and in both gradients."""
+    n, v, c = 24, 600_011, 4096
+    g = torch.Generator(device=DEV).manual_seed(14)
+    x = torch.randn((n, c), generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.empty((v, c), dtype=torch.bfloat16, device=DEV)
+    for a in range(0, v, 50_000):
+        b = min(v, a + 50_000)
+        w[a:b] = torch.randn((b - a, c), generator=g, device=DEV) * 0.05
+    target = torch.randint(0, v, (n,), generator=g, device=DEV)
+    target[:4] = torch.tensor([v - 1, v - 2, 0, 2 ** 31 // c + 1], device=DEV)
+    dloss = torch.randn(n, generator=g, device=DEV)
+    loss, lse = jq.linear_ce(x, w, target)
+    dx, dw = jq.linear_ce_bwd(x, w, target, lse, dloss, dw_dtype=torch.bfloat16)
+    assert jq.jetq_check_device_error() == jq.OK
+    X = x.double()
+    rlse = torch.full((n,), -float("inf"), dtype=torch.float64, device=DEV)
+    size = torch.zeros(n, dtype=torch.float64, device=DEV)
+    rx, tx = torch.zeros_like(X), torch.zeros_like(X)
+    coef = dloss.double()
+    rows = torch.arange(n, device=DEV)
+    pieces = [(a, min(v, a + 50_000)) for a in range(0, v, 50_000)]
+    for a, b in pieces:
+        W = w[a:b].double()
+        rlse = torch.logaddexp(rlse, torch.logsumexp(X @ W.T, 1))
+        size = torch.maximum(size, (X.abs() @ W.abs().T).amax(1))
+    zt = (X * w[target].double()).sum(1)
+    tol = 2 * SUM * size + 8 * HALF_F32 * (rlse.abs() + (rlse - zt).abs() + 1)
+    assert bool(((lse.double() - rlse).abs() <= tol).all())
+    assert bool(((loss.double() - (rlse - zt)).abs() <= tol).all())
+    moved = (SUM * size + 8 * HALF_F32 * (1 + lse.double().abs()))[:, None]
+    for a, b in pieces:
+        W = w[a:b].double()
+        p = torch.exp(X @ W.T - lse.double()[:, None])
+        d = p * coef[:, None]
+        here = rows[(target >= a) & (target < b)]
+        d[here, target[here] - a] -= coef[here]
+        off = d.abs() * (HALF_BF16 + SUM) + p * coef.abs()[:, None] * 2 * moved
+        rx += d @ W
+        tx += off @ W.abs()
+        rw, tw = d.T @ X, off.T @ X.abs()
+        assert bool(((dw[a:b].double() - rw).abs() <= tw * 1.01 + HALF_BF16 * rw.abs() + 1e-30).all())
+    assert bool(((dx.double() - rx).abs() <= tx * 1.01 + HALF_BF16 * rx.abs() + 1e-30).all())

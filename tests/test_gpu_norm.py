@@ -209,3 +209,28 @@ def test_no_rows():
     assert y.shape == (0, 256) and mean.shape == rstd.shape == (0,)
     dx, dw, db = jq.norm_bwd(x, x, None, mean, rstd, bias=True)
     assert dx.shape == (0, 256) and bool((dw == 0).all()) and bool((db == 0).all())
+
+
+@pytest.mark.parametrize("n,c", [(300_007, 8192), (9_000_001, 256), (150_001, 16384)])
+def test_offsets_past_32_bits(n, c):
+    """2.3e9 elements and more: the first and the last rows, and dw as a sum over pieces in binary64."""
+    x, dy = (torch.empty((n, c), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    g = torch.Generator(device=DEV).manual_seed(11)
+    pieces = [(a, min(n, a + (1 << 26) // c)) for a in range(0, n, (1 << 26) // c)]
+    for a, b in pieces:
+        x[a:b] = torch.randn((b - a, c), generator=g, device=DEV)
+        dy[a:b] = torch.randn((b - a, c), generator=g, device=DEV)
+    w = (1 + 0.2 * torch.randn(c, generator=g, device=DEV)).to(torch.bfloat16)
+    y, _, rstd = jq.norm_fwd(x, w, None, eps=1e-5, kind=jq.NORM_RMS)
+    dx, dw, _ = jq.norm_bwd(dy, x, w, None, rstd, kind=jq.NORM_RMS)
+    assert jq.jetq_check_device_error() == jq.OK
+    rw, tw = (torch.zeros(c, dtype=torch.float64, device=DEV) for _ in range(2))
+    for a, b in pieces:
+        X, r = x[a:b].double(), rstd[a:b].double()[:, None]
+        ref = X * r * w.double()
+        assert bool(((y[a:b].double() - ref).abs() <= (2.0 ** -8 + 4 * U) * ref.abs()).all())
+        (rx, tx), (pw, _), _ = _define_bwd(dy[a:b], x[a:b], w, None, rstd[a:b], jq.NORM_RMS)
+        assert bool(((dx[a:b].double() - rx).abs() <= tx + 2.0 ** -8 * rx.abs()).all())
+        rw += pw
+        tw += (dy[a:b].double().abs() * 2 * (X * r).abs()).sum(0)
+    assert bool(((dw.double() - rw).abs() <= (100 + n / 300) * U * tw).all())
