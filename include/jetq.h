@@ -637,12 +637,13 @@ JETQ_API jetq_status jetq_norm_bwd(jetq_norm_kind kind, jetq_out_dtype dtype, co
  *   scale          in (0, 1e38]
  *   loss, lse      float [n]
  *   workspace      device memory, 16-byte aligned, at least
- *                  jetq_linear_ce_workspace_bytes(n, v) bytes; calls that
+ *                  jetq_linear_ce_workspace_bytes(n, v, c) bytes; calls that
  *                  share one must not overlap on the GPU
- * n == 0 is a no-op.  Results are bitwise repeatable.  Two launches.
+ * n == 0 is a no-op.  Results are bitwise repeatable.  Two launches, or
+ * three where rows of x that start off 128-byte lines are copied first.
  * Workspace sizes are those of the current device (here and below).
  */
-JETQ_API size_t jetq_linear_ce_workspace_bytes(int64_t n, int64_t v);
+JETQ_API size_t jetq_linear_ce_workspace_bytes(int64_t n, int64_t v, int64_t c);
 JETQ_API jetq_status jetq_linear_ce_fwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx,
                                         const uint16_t *w, int64_t v, int64_t ldw,
                                         const int64_t *target, float scale, float *loss, float *lse,

@@ -85,7 +85,7 @@ def lib() -> ctypes.CDLL:
             "jetq_norm_bwd_workspace_bytes": (ctypes.c_size_t, [I32, I64, I64]),
             "jetq_norm_bwd": (I32, [I32, I32, P, I64, P, I64, I64, I64, P, P, P, P, I64, P, P, P, ctypes.c_size_t,
                                     P]),
-            "jetq_linear_ce_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
+            "jetq_linear_ce_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64]),
             "jetq_linear_ce_fwd": (I32, [P, I64, I64, I64, P, I64, I64, P, F32, P, P, P, ctypes.c_size_t, P]),
             "jetq_linear_ce_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I32]),
             "jetq_linear_ce_bwd": (I32, [P, I64, I64, I64, P, I64, I64, P, F32, P, P, P, I64, P, I32, I64, I32, P,
@@ -325,8 +325,8 @@ def jetq_norm_bwd(kind, dy, x, w, mean, rstd, dx, dw, db, ws, stream=None):
                                _bytes(ws), _s(stream)), "jetq_norm_bwd")
 
 
-def jetq_linear_ce_workspace_bytes(n: int, v: int) -> int:
-    return int(lib().jetq_linear_ce_workspace_bytes(n, v))
+def jetq_linear_ce_workspace_bytes(n: int, v: int, c: int) -> int:
+    return int(lib().jetq_linear_ce_workspace_bytes(n, v, c))
 
 
 def jetq_linear_ce_fwd(x, w, target, scale, loss, lse, ws, stream=None):
@@ -663,10 +663,10 @@ def linear_ce(x, w, target, scale=1.0, workspace=None, stream=None):
         with torch.cuda.stream(stream):
             return linear_ce(x, w, target, scale, workspace)
     _check_head(x, w, target)
-    n, v = x.shape[0], w.shape[0]
+    (n, c), v = x.shape, w.shape[0]
     loss = torch.empty(n, dtype=torch.float32, device=x.device)
     lse = torch.empty(n, dtype=torch.float32, device=x.device)
-    need = jetq_linear_ce_workspace_bytes(n, v)
+    need = jetq_linear_ce_workspace_bytes(n, v, c)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     jetq_linear_ce_fwd(x, w, target, scale, loss, lse, workspace)

@@ -660,9 +660,9 @@ jetq_status check_linear_ce(const uint16_t *x, int64_t n, int64_t c, int64_t ldx
 
 } // namespace
 
-size_t jetq_linear_ce_workspace_bytes(int64_t n, int64_t v)
+size_t jetq_linear_ce_workspace_bytes(int64_t n, int64_t v, int64_t c)
 {
-    return n <= 0 || v <= 0 ? 0 : linear_ce_fwd_workspace(n, v);
+    return n <= 0 || v <= 0 || c <= 0 ? 0 : linear_ce_fwd_workspace(n, v, c);
 }
 
 size_t jetq_linear_ce_bwd_workspace_bytes(int64_t n, int64_t v, int64_t c, int smallest)
@@ -680,7 +680,7 @@ jetq_status jetq_linear_ce_fwd(const uint16_t *x, int64_t n, int64_t c, int64_t 
     if (s != JETQ_OK || n == 0)
         return s;
     JQ_REQUIRE(loss != nullptr && lse != nullptr && workspace != nullptr, JETQ_ERR_INVALID_ARG);
-    JQ_REQUIRE(workspace_bytes >= linear_ce_fwd_workspace(n, v), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(workspace_bytes >= linear_ce_fwd_workspace(n, v, c), JETQ_ERR_INVALID_ARG);
     JQ_REQUIRE(aligned16(workspace) && (reinterpret_cast<uintptr_t>(loss) & 3u) == 0 &&
                    (reinterpret_cast<uintptr_t>(lse) & 3u) == 0,
                JETQ_ERR_MISALIGNED);

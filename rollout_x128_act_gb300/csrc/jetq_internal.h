@@ -303,11 +303,11 @@ struct LinearCeArgs {
     void *ws;
     size_t ws_bytes;
 };
-size_t linear_ce_fwd_workspace(int64_t n, int64_t v);
+size_t linear_ce_fwd_workspace(int64_t n, int64_t v, int64_t c);
 size_t linear_ce_bwd_workspace(int64_t n, int64_t v, int64_t c);     // preferred
 size_t linear_ce_bwd_workspace_min(int64_t n, int64_t v, int64_t c); // one 256-row piece of the vocabulary
-cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st);
-cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st);
+cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st);
+cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st);
 cudaError_t linear_ce_read_and_clear_error(cudaStream_t st, unsigned *out);
 
 // Number of SMs of the current device (cached per device).

@@ -32,8 +32,8 @@
 // burst rate), 2.58 ms back to back; backward 7.79 ms back to back (1.69
 // PFLOP/s, 0.97 of the rate cuBLAS sustains under the power cap).  Few tokens:
 // the weight's stream from HBM (one token x 32000 x 4096: 48 us for 262 MB).
-// Rows that are not multiples of 128 bytes cost L2 sectors: 1000 x 50257 x 1032
-// backward takes 289 us, 1.08 PFLOP/s.
+// Rows of w that are not multiples of 128 bytes cost L2 sectors: 1000 x 50257 x 1032
+// backward takes 276 us, 1.13 PFLOP/s.
 //
 // The target's term is left out of the sum of exponentials and joined at the
 // end: loss = log1p(sum of the others / the target's) where the target leads,
@@ -649,6 +649,18 @@ __global__ void __launch_bounds__(1024)
     loss[row] = dt >= -1.0f ? log1pf(a.y * exp2f(-dt)) : logf(a.y + exp2f(dt)) - kLn2 * dt;
 }
 
+// Rows of x copied to a stride of whole 128-byte lines, 16 bytes a thread.
+__global__ void k_ce_lines(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, uint16_t *out, int64_t ldo)
+{
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int64_t c8 = c / 8, total = n * c8;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t r = i / c8, col = 8 * (i - r * c8);
+        *reinterpret_cast<uint4 *>(out + r * ldo + col) = __ldg(reinterpret_cast<const uint4 *>(x + r * ldx + col));
+    }
+}
+
 // gmax = max |dloss| over the rows with a target (1 where that is not finite).
 __global__ void k_ce_gmax(const float *dloss, const int64_t *target, int64_t n, int64_t v, float *gmax)
 {
@@ -822,10 +834,39 @@ void dx_shape(int64_t n, int64_t c, int64_t piece, int &cg, int &splits)
     }
 }
 
+// A row that does not start on a 128-byte line costs each box row a second
+// line.  x is read by every tile of the vocabulary, so for more than one tile of
+// rows it is copied to aligned rows first where its width makes them start off
+// the lines (with the copy: 1000 x 50257 x 1032 forward 96 us against 104,
+// backward 275 against 282; 2000 x 50257 x 2056 forward 277 against 331; w, read
+// by a few tiles of rows, would not pay).
+int64_t lines_ld(int64_t c)
+{
+    return ceil_div(c, 64) * 64;
+}
+
+size_t lines_bytes(int64_t n, int64_t c)
+{
+    return n > 128 && c % 64 != 0 ? ((size_t)n * (size_t)lines_ld(c) * 2 + 1023) / 1024 * 1024 : 0;
+}
+
+cudaError_t to_lines(LinearCeArgs &a, void *at, cudaStream_t st)
+{
+    if (lines_bytes(a.n, a.c) == 0 || (a.ldx % 64 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 127u) == 0))
+        return cudaSuccess;
+    const int64_t blocks = ceil_div(a.n * (a.c / 8), 256), cap = (int64_t)sm_count() * 8;
+    uint16_t *out = static_cast<uint16_t *>(at);
+    const cudaError_t e = launch_pdl(k_ce_lines, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, st, a.x,
+                                     a.n, a.c, a.ldx, out, lines_ld(a.c));
+    a.x = out;
+    a.ldx = lines_ld(a.c);
+    return e;
+}
+
 struct BwdPlan {
     int64_t piece; // vocabulary rows a piece (a multiple of 256)
     int dx_cg, splits;
-    size_t slab_off, d_off, total;
+    size_t x_off, slab_off, d_off, total;
 };
 
 BwdPlan bwd_plan(int64_t n, int64_t v, int64_t c, int64_t piece)
@@ -834,7 +875,8 @@ BwdPlan bwd_plan(int64_t n, int64_t v, int64_t c, int64_t piece)
     const int64_t all = ceil_div(v, 256) * 256;
     b.piece = piece < 256 ? 256 : (piece > all ? all : piece / 256 * 256);
     dx_shape(n, c, b.piece, b.dx_cg, b.splits);
-    b.slab_off = 256; // gmax first
+    b.x_off = 1024; // gmax first
+    b.slab_off = b.x_off + lines_bytes(n, c);
     const size_t slabs = (size_t)b.splits * (size_t)n * (size_t)c * 4;
     b.d_off = (b.slab_off + slabs + 1023) / 1024 * 1024;
     b.total = b.d_off + (size_t)n * (size_t)b.piece * 2;
@@ -851,12 +893,12 @@ int64_t preferred_piece(int64_t n)
 
 // Tiles of the forward product's vocabulary axis: 256 columns each, or, for one
 // row tile, evenly over the SMs.
-size_t linear_ce_fwd_workspace(int64_t n, int64_t v)
+size_t linear_ce_fwd_workspace(int64_t n, int64_t v, int64_t c)
 {
     int64_t nt = ceil_div(v, kTileN);
     if (n <= 128) // never more than the waves' whole tiles
         nt = ceil_div(nt, units_of(1)) * units_of(1);
-    return (size_t)(kParts * nt) * (size_t)n * 8 + (size_t)n * 4;
+    return lines_bytes(n, c) + (size_t)(kParts * nt) * (size_t)n * 8 + (size_t)n * 4;
 }
 
 size_t linear_ce_bwd_workspace(int64_t n, int64_t v, int64_t c)
@@ -869,8 +911,11 @@ size_t linear_ce_bwd_workspace_min(int64_t n, int64_t v, int64_t c)
     return bwd_plan(n, v, c, 256).total;
 }
 
-cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
+cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
 {
+    cudaError_t e = to_lines(a, a.ws, st);
+    if (e != cudaSuccess)
+        return e;
     HeadParams p = {};
     p.nt = (int)ceil_div(a.v, kTileN);
     const int cg = pick_cg(a.n, p.nt);
@@ -884,7 +929,6 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
         p.nt = (int)ceil_div(a.v, p.bn);
     }
     CUtensorMap ta, tb;
-    cudaError_t e;
     if ((e = make_sw128_map(&ta, a.x, false, a.c, a.n, a.ldx, p.box_a)) != cudaSuccess ||
         (e = make_sw128_map(&tb, a.w, false, a.c, a.v, a.ldw, p.bn / cg)) != cudaSuccess)
         return e;
@@ -903,7 +947,7 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
     // with (worst of 12 tokens: 1.6e-6 with 4), and there the weight's stream takes the time.
     p.fold = cg == 2 ? 8 : (a.n > 128 ? 4 : 2);
     p.V = a.v;
-    p.part = static_cast<float2 *>(a.ws);
+    p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + lines_bytes(a.n, a.c));
     p.zt = reinterpret_cast<float *>(p.part + (size_t)kParts * p.nt * a.n);
     if ((e = run_head<kStats>(cg, ta, tb, ta, p, st)) != cudaSuccess)
         return e;
@@ -917,7 +961,7 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st)
                       (const float *)p.zt, a.target, a.n, a.v, parts, p.k2, a.loss, a.lse);
 }
 
-cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
+cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st)
 {
     // the largest piece that the workspace holds, up to the preferred one
     BwdPlan plan = bwd_plan(a.n, a.v, a.c, preferred_piece(a.n));
@@ -928,8 +972,10 @@ cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st)
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     float *gmax = reinterpret_cast<float *>(ws), *slab = reinterpret_cast<float *>(ws + plan.slab_off);
     uint16_t *d = reinterpret_cast<uint16_t *>(ws + plan.d_off);
-    cudaError_t e = launch_pdl(k_ce_gmax, dim3(1), dim3(1024), 0, st, a.dloss, a.target, a.n, a.v, gmax);
+    cudaError_t e = to_lines(a, ws + plan.x_off, st);
     if (e != cudaSuccess)
+        return e;
+    if ((e = launch_pdl(k_ce_gmax, dim3(1), dim3(1024), 0, st, a.dloss, a.target, a.n, a.v, gmax)) != cudaSuccess)
         return e;
     const bool dw16 = a.dw_dtype == JETQ_OUT_BF16;
     for (int64_t v0 = 0; v0 < a.v; v0 += plan.piece) {

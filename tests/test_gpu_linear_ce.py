@@ -111,6 +111,20 @@ def test_backward_in_small_pieces():
         _check_bwd(x, w, target, 1.0, dloss, lse, torch.float32, torch.empty(size, dtype=torch.uint8, device=DEV))
 
 
+def test_rows_on_and_off_the_lines():
+    """x in rows of whole 128-byte lines, off them, and in a view that starts off them: the same bits."""
+    x, w, target, dloss = _inputs(200, 600, 136, seed=15)
+    _check_fwd(x, w, target, 1.0)
+    loss, lse = jq.linear_ce(x, w, target)
+    dx, dw = jq.linear_ce_bwd(x, w, target, lse, dloss)
+    wide = torch.full((200, 256), float("nan"), dtype=torch.bfloat16, device=DEV)
+    for at in (0, 8, 64):
+        wide[:, at:at + 136] = x
+        loss1, lse1 = jq.linear_ce(wide[:, at:at + 136], w, target)
+        dx1, dw1 = jq.linear_ce_bwd(wide[:, at:at + 136], w, target, lse, dloss)
+        assert torch.equal(loss, loss1) and torch.equal(lse, lse1) and torch.equal(dx, dx1) and torch.equal(dw, dw1)
+
+
 def test_rows_without_a_loss():
     x, w, target, dloss = _inputs(70, 300, 64, seed=6, ignored=False)
     target[:] = -100

@@ -71,9 +71,9 @@ def test_linear_ce_backward_refuses(L, change, status):
 
 
 def test_linear_ce_workspaces(L):
-    assert L.jetq_linear_ce_workspace_bytes(0, 300) == 0
-    assert L.jetq_linear_ce_workspace_bytes(4, 300) >= 2 * 2 * 4 * 8 + 4 * 4  # a pair every 128 columns, a logit
-    assert L.jetq_linear_ce_workspace_bytes(4096, 131072) == 2 * 512 * 4096 * 8 + 4096 * 4
+    assert L.jetq_linear_ce_workspace_bytes(0, 300, 64) == 0
+    assert L.jetq_linear_ce_workspace_bytes(4, 300, 64) >= 2 * 2 * 4 * 8 + 4 * 4  # a pair every 128 columns, a logit
+    assert L.jetq_linear_ce_workspace_bytes(4096, 131072, 4096) == 2 * 512 * 4096 * 8 + 4096 * 4
     assert L.jetq_linear_ce_bwd_workspace_bytes(0, 300, 64, 0) == 0
     small = L.jetq_linear_ce_bwd_workspace_bytes(4096, 131072, 4096, 1)
     large = L.jetq_linear_ce_bwd_workspace_bytes(4096, 131072, 4096, 0)
