@@ -606,15 +606,39 @@ __device__ __forceinline__ void join_pair(float2 &a, const float2 b)
 
 // Joins the (maximum, sum) pairs of a row and its target's logit.  blockDim =
 // (rows, lanes), powers of two: threadIdx.x walks rows (contiguous in part),
-// threadIdx.y parts.
+// threadIdx.y parts.  DOT (one tile of rows): the target's logit is summed here
+// once more, in round-to-nearest.  It is the largest logit of a confident token
+// and its truncation error is that of the loss, which other tokens' do not
+// average out there (worst single token of many seeds: 2.4e-6 of its loss
+// without, 4e-7 with).
+template <bool DOT>
 __global__ void __launch_bounds__(1024)
-    k_ce_join(const float2 *part, const float *zt, const int64_t *target, int64_t n, int64_t v, int parts, float k2,
-              float *loss, float *lse)
+    k_ce_join(const float2 *part, const float *zt, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw,
+              int64_t c, const int64_t *target, int64_t n, int64_t v, int parts, float k2, float *loss, float *lse)
 {
     __shared__ float2 red[1024];
+    __shared__ float dots[DOT ? 1024 : 1];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t tg = row < n ? target[row] : -1;
+    const bool has = tg >= 0 && tg < v;
+    const int at = threadIdx.y * blockDim.x + threadIdx.x;
+    if constexpr (DOT) {
+        float d = 0.0f;
+        if (has)
+            for (int64_t k = 8 * threadIdx.y; k < c; k += 8 * blockDim.y) { // c and the rows are whole vectors
+                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + row * ldx + k));
+                const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w + tg * ldw + k));
+                const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    d = fmaf(__uint_as_float(p[e] << 16), __uint_as_float(q[e] << 16), d);
+                    d = fmaf(__uint_as_float(p[e] & 0xffff0000u), __uint_as_float(q[e] & 0xffff0000u), d);
+                }
+            }
+        dots[at] = d;
+    }
     float2 a = make_float2(-INFINITY, 0.0f);
     if (row < n)
         for (int q = threadIdx.y; q < parts; q += 4 * blockDim.y) { // four loads in flight
@@ -627,24 +651,25 @@ __global__ void __launch_bounds__(1024)
             for (int i = 0; i < 4; ++i)
                 join_pair(a, b[i]);
         }
-    red[threadIdx.y * blockDim.x + threadIdx.x] = a;
+    red[at] = a;
     for (int o = blockDim.y / 2; o; o >>= 1) {
         __syncthreads();
         if ((int)threadIdx.y < o) {
-            join_pair(a, red[(threadIdx.y + o) * blockDim.x + threadIdx.x]);
-            red[threadIdx.y * blockDim.x + threadIdx.x] = a;
+            join_pair(a, red[at + o * blockDim.x]);
+            red[at] = a;
+            if constexpr (DOT)
+                dots[at] += dots[at + o * blockDim.x];
         }
     }
     if (threadIdx.y != 0 || row >= n)
         return;
-    const int64_t tg = target[row];
-    if (tg < 0 || tg >= v) {
+    if (!has) {
         lse[row] = kLn2 * (a.x + log2f(a.y));
         loss[row] = 0.0f;
         return;
     }
     // the target's exponent against the maximum's, rounded once: both products carry errors of lse's size
-    const float dt = fmaf(zt[row], k2, -a.x);
+    const float dt = fmaf(DOT ? dots[at] : zt[row], k2, -a.x);
     lse[row] = kLn2 * (a.x + log2f(a.y + exp2f(dt)));
     loss[row] = dt >= -1.0f ? log1pf(a.y * exp2f(-dt)) : logf(a.y + exp2f(dt)) - kLn2 * dt;
 }
@@ -957,8 +982,12 @@ cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
         rx *= 2;
     while (rx * ry < 1024 && ry < parts)
         ry *= 2;
-    return launch_pdl(k_ce_join, dim3((unsigned)ceil_div(a.n, rx)), dim3(rx, ry), 0, st, (const float2 *)p.part,
-                      (const float *)p.zt, a.target, a.n, a.v, parts, p.k2, a.loss, a.lse);
+    const dim3 grid((unsigned)ceil_div(a.n, rx)), block(rx, ry);
+    auto join = [&](auto kern) {
+        return launch_pdl(kern, grid, block, 0, st, (const float2 *)p.part, (const float *)p.zt, a.x, a.ldx, a.w, a.ldw,
+                          a.c, a.target, a.n, a.v, parts, p.k2, a.loss, a.lse);
+    };
+    return a.n <= 128 ? join(k_ce_join<true>) : join(k_ce_join<false>);
 }
 
 cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st)
