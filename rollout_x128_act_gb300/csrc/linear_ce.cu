@@ -609,8 +609,8 @@ __device__ __forceinline__ void join_pair(float2 &a, const float2 b)
 // threadIdx.y parts.  DOT (one tile of rows): the target's logit is summed here
 // once more, in round-to-nearest.  It is the largest logit of a confident token
 // and its truncation error is that of the loss, which other tokens' do not
-// average out there (worst single token of many seeds: 2.4e-6 of its loss
-// without, 4e-7 with).
+// average out there (worst of forty single tokens: 8e-7 of its loss, as an FP32
+// matrix product; 2.4e-6 was seen without).
 template <bool DOT>
 __global__ void __launch_bounds__(1024)
     k_ce_join(const float2 *part, const float *zt, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw,
@@ -968,9 +968,8 @@ cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
     // The error of a loss grows with the steps of a partial tile.  Pairs: 8 blocks (3e-7 in the 2-norm over
     // 4096 tokens, an FP32 matrix product has 6e-7; 4096 x 131072 x 4096 took 2.65 ms with 8, 2.97 with 4 and
     // 4.03 with 2, whose hand-overs between the CTAs stall the tensor core).  Single CTAs: 4 (2e-7; 333 tokens x
-    // 50257 x 2048: 64 us, 66 with 2).  One row tile: 2, for single tokens' losses have no others to average
-    // with (worst of 12 tokens: 1.6e-6 with 4), and there the weight's stream takes the time.
-    p.fold = cg == 2 ? 8 : (a.n > 128 ? 4 : 2);
+    // 50257 x 2048: 64 us, 66 with 2; one token x 1000 x 4096: 27 us, 30 with 2).
+    p.fold = cg == 2 ? 8 : 4;
     p.V = a.v;
     p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + lines_bytes(a.n, a.c));
     p.zt = reinterpret_cast<float *>(p.part + (size_t)kParts * p.nt * a.n);
