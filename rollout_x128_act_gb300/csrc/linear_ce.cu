@@ -29,11 +29,11 @@
 // SM's 64 bytes a cycle from L2.  The tile's FP32 sums are double-buffered in
 // TMEM, so the epilogue works under the next tile's products.  4096 tokens x
 // 131072 x 4096: forward 2.36 ms alone (1.86 PFLOP/s, 0.97 of the measured BF16
-// burst rate), 2.58 ms back to back; backward 7.79 ms back to back (1.69
-// PFLOP/s, 0.97 of the rate cuBLAS sustains under the power cap).  Few tokens:
+// burst rate), 2.58 to 2.64 ms back to back; backward 7.8 to 7.9 ms back to back
+// (1.68 PFLOP/s, 0.96 of the rate cuBLAS sustains under the power cap).  Few tokens:
 // the weight's stream from HBM (one token x 32000 x 4096: 48 us for 262 MB).
 // Rows of w that are not multiples of 128 bytes cost L2 sectors: 1000 x 50257 x 1032
-// backward takes 276 us, 1.13 PFLOP/s.
+// backward takes 285 us, 1.09 PFLOP/s.
 //
 // The target's term is left out of the sum of exponentials and joined at the
 // end: loss = log1p(sum of the others / the target's) where the target leads,
