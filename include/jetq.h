@@ -656,8 +656,8 @@ JETQ_API jetq_status jetq_linear_ce_fwd(const uint16_t *x, int64_t n, int64_t c,
  *   dx = scale * d w   (BF16 [n x c], stride lddx),   dw = scale * d^T x   ([v x c], stride lddw)
  * d is rounded to BF16 (relative to the largest |dloss|) for the tensor cores;
  * every sum is FP32, rounded once.  dw: BF16, or FP32 with accumulate = 1 to
- * add into it.  Rows without a loss give zero rows of dx and add nothing to dw
- * (their x must be finite: the products run over every row).
+ * add into it.  Rows without a loss give zero rows of dx and add nothing to dw,
+ * whatever their x, lse and dloss hold.
  *
  *   dloss      float [n]
  *   workspace  device memory, 16-byte aligned.  Its size decides how much of

@@ -11,7 +11,8 @@
 //   forward    x w^T with an epilogue that reduces each row's 128 logits to a
 //              (maximum, sum of exponentials) pair and picks the target's
 //              logit; a small kernel joins the pairs of a row
-//   backward, per piece of the vocabulary (its d is [n x piece] in BF16)
+//   backward, from a copy of x in rows of whole lines (zero without a loss), per
+//   piece of the vocabulary (its d is [n x piece] in BF16)
 //     1. x w^T again with an epilogue that writes d
 //     2. dx += d w: d K-major, w with its N axis (c) contiguous; FP32 slabs
 //        in the workspace, one per K split, added to by TMA add-reductions
@@ -29,11 +30,11 @@
 // SM's 64 bytes a cycle from L2.  The tile's FP32 sums are double-buffered in
 // TMEM, so the epilogue works under the next tile's products.  4096 tokens x
 // 131072 x 4096: forward 2.36 ms alone (1.86 PFLOP/s, 0.97 of the measured BF16
-// burst rate), 2.58 to 2.64 ms back to back; backward 7.8 to 7.9 ms back to back
-// (1.68 PFLOP/s, 0.96 of the rate cuBLAS sustains under the power cap).  Few tokens:
+// burst rate), 2.58 to 2.64 ms back to back; backward 7.7 to 7.9 ms back to back
+// (1.69 PFLOP/s, 0.96 of the rate cuBLAS sustains under the power cap).  Few tokens:
 // the weight's stream from HBM (one token x 32000 x 4096: 48 us for 262 MB).
 // Rows of w that are not multiples of 128 bytes cost L2 sectors: 1000 x 50257 x 1032
-// backward takes 285 us, 1.09 PFLOP/s.
+// backward takes 280 us, 1.11 PFLOP/s.
 //
 // The target's term is left out of the sum of exponentials and joined at the
 // end: loss = log1p(sum of the others / the target's) where the target leads,
@@ -674,24 +675,29 @@ __global__ void __launch_bounds__(1024)
     loss[row] = dt >= -1.0f ? log1pf(a.y * exp2f(-dt)) : logf(a.y + exp2f(dt)) - kLn2 * dt;
 }
 
-// Rows of x copied to a stride of whole 128-byte lines, 16 bytes a thread.
-__global__ void k_ce_lines(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, uint16_t *out, int64_t ldo)
+// Rows of x copied to a stride of whole 128-byte lines, 16 bytes a thread; with
+// `target`, rows without a loss become zero (whatever they hold: the backward
+// products run over every row, and 0 * NaN would reach all of dw).  Block 0
+// has the backward pass's other start: gmax = max |dloss| over the rows with a
+// target (1 where that is not finite).
+__global__ void __launch_bounds__(256)
+    k_ce_start(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, uint16_t *out, int64_t ldo, const float *dloss,
+               const int64_t *target, int64_t v, float *gmax)
 {
+    __shared__ float red[8];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int64_t c8 = c / 8, total = n * c8;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = i / c8, col = 8 * (i - r * c8);
-        *reinterpret_cast<uint4 *>(out + r * ldo + col) = __ldg(reinterpret_cast<const uint4 *>(x + r * ldx + col));
+    if (blockIdx.x > 0) {
+        const int64_t c8 = c / 8, total = n * c8, step = (int64_t)(gridDim.x - 1) * blockDim.x;
+        for (int64_t i = (int64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x; i < total; i += step) {
+            const int64_t r = i / c8, col = 8 * (i - r * c8), tg = target ? __ldg(target + r) : 0;
+            *reinterpret_cast<uint4 *>(out + r * ldo + col) =
+                tg >= 0 && tg < v ? __ldg(reinterpret_cast<const uint4 *>(x + r * ldx + col)) : make_uint4(0, 0, 0, 0);
+        }
+        return;
     }
-}
-
-// gmax = max |dloss| over the rows with a target (1 where that is not finite).
-__global__ void k_ce_gmax(const float *dloss, const int64_t *target, int64_t n, int64_t v, float *gmax)
-{
-    __shared__ float red[32];
-    ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
+    if (!gmax)
+        return;
     float m = 0.0f;
     for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
         const int64_t tg = target[i];
@@ -705,12 +711,10 @@ __global__ void k_ce_gmax(const float *dloss, const int64_t *target, int64_t n, 
     if ((threadIdx.x & 31) == 0)
         red[threadIdx.x >> 5] = m;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        m = threadIdx.x < blockDim.x / 32 ? red[threadIdx.x] : 0.0f;
-        for (int o = 16; o; o >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (threadIdx.x == 0)
-            *gmax = m < INFINITY ? m : 1.0f;
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 8; ++i)
+            m = fmaxf(m, red[i]);
+        *gmax = m < INFINITY ? m : 1.0f;
     }
 }
 
@@ -859,12 +863,7 @@ void dx_shape(int64_t n, int64_t c, int64_t piece, int &cg, int &splits)
     }
 }
 
-// A row that does not start on a 128-byte line costs each box row a second
-// line.  x is read by every tile of the vocabulary, so for more than one tile of
-// rows it is copied to aligned rows first where its width makes them start off
-// the lines (with the copy: 1000 x 50257 x 1032 forward 96 us against 104,
-// backward 275 against 282; 2000 x 50257 x 2056 forward 277 against 331; w, read
-// by a few tiles of rows, would not pay).
+// Row stride of x's copies: whole 128-byte lines.
 int64_t lines_ld(int64_t c)
 {
     return ceil_div(c, 64) * 64;
@@ -872,17 +871,28 @@ int64_t lines_ld(int64_t c)
 
 size_t lines_bytes(int64_t n, int64_t c)
 {
-    return n > 128 && c % 64 != 0 ? ((size_t)n * (size_t)lines_ld(c) * 2 + 1023) / 1024 * 1024 : 0;
+    return ((size_t)n * (size_t)lines_ld(c) * 2 + 1023) / 1024 * 1024;
 }
 
-cudaError_t to_lines(LinearCeArgs &a, void *at, cudaStream_t st)
+// Forward: a row that does not start on a 128-byte line costs each box row a
+// second line.  x is read by every tile of the vocabulary, so for more than one
+// tile of rows it is copied first where its width makes rows start off the
+// lines (with the copy: 1000 x 50257 x 1032 96 us against 104, 2000 x 50257 x
+// 2056 277 against 331; w, read by a few tiles of rows, would not pay).
+size_t fwd_lines(int64_t n, int64_t c)
 {
-    if (lines_bytes(a.n, a.c) == 0 || (a.ldx % 64 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 127u) == 0))
-        return cudaSuccess;
+    return n > 128 && c % 64 != 0 ? lines_bytes(n, c) : 0;
+}
+
+// Copies a.x to `at` and makes it the copy; backward: zeroes its rows without a
+// loss, and computes gmax.
+cudaError_t start(LinearCeArgs &a, void *at, float *gmax, cudaStream_t st)
+{
     const int64_t blocks = ceil_div(a.n * (a.c / 8), 256), cap = (int64_t)sm_count() * 8;
     uint16_t *out = static_cast<uint16_t *>(at);
-    const cudaError_t e = launch_pdl(k_ce_lines, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, st, a.x,
-                                     a.n, a.c, a.ldx, out, lines_ld(a.c));
+    const cudaError_t e =
+        launch_pdl(k_ce_start, dim3((unsigned)(1 + (blocks < cap ? blocks : cap))), dim3(256), 0, st, a.x, a.n, a.c,
+                   a.ldx, out, lines_ld(a.c), a.dloss, gmax ? a.target : (const int64_t *)nullptr, a.v, gmax);
     a.x = out;
     a.ldx = lines_ld(a.c);
     return e;
@@ -923,7 +933,7 @@ size_t linear_ce_fwd_workspace(int64_t n, int64_t v, int64_t c)
     int64_t nt = ceil_div(v, kTileN);
     if (n <= 128) // never more than the waves' whole tiles
         nt = ceil_div(nt, units_of(1)) * units_of(1);
-    return lines_bytes(n, c) + (size_t)(kParts * nt) * (size_t)n * 8 + (size_t)n * 4;
+    return fwd_lines(n, c) + (size_t)(kParts * nt) * (size_t)n * 8 + (size_t)n * 4;
 }
 
 size_t linear_ce_bwd_workspace(int64_t n, int64_t v, int64_t c)
@@ -938,8 +948,9 @@ size_t linear_ce_bwd_workspace_min(int64_t n, int64_t v, int64_t c)
 
 cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
 {
-    cudaError_t e = to_lines(a, a.ws, st);
-    if (e != cudaSuccess)
+    cudaError_t e;
+    if (fwd_lines(a.n, a.c) > 0 && (a.ldx % 64 != 0 || (reinterpret_cast<uintptr_t>(a.x) & 127u) != 0) &&
+        (e = start(a, a.ws, nullptr, st)) != cudaSuccess)
         return e;
     HeadParams p = {};
     p.nt = (int)ceil_div(a.v, kTileN);
@@ -971,7 +982,7 @@ cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
     // 50257 x 2048: 64 us, 66 with 2; one token x 1000 x 4096: 27 us, 30 with 2).
     p.fold = cg == 2 ? 8 : 4;
     p.V = a.v;
-    p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + lines_bytes(a.n, a.c));
+    p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + fwd_lines(a.n, a.c));
     p.zt = reinterpret_cast<float *>(p.part + (size_t)kParts * p.nt * a.n);
     if ((e = run_head<kStats>(cg, ta, tb, ta, p, st)) != cudaSuccess)
         return e;
@@ -1000,10 +1011,8 @@ cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st)
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     float *gmax = reinterpret_cast<float *>(ws), *slab = reinterpret_cast<float *>(ws + plan.slab_off);
     uint16_t *d = reinterpret_cast<uint16_t *>(ws + plan.d_off);
-    cudaError_t e = to_lines(a, ws + plan.x_off, st);
+    cudaError_t e = start(a, ws + plan.x_off, gmax, st);
     if (e != cudaSuccess)
-        return e;
-    if ((e = launch_pdl(k_ce_gmax, dim3(1), dim3(1024), 0, st, a.dloss, a.target, a.n, a.v, gmax)) != cudaSuccess)
         return e;
     const bool dw16 = a.dw_dtype == JETQ_OUT_BF16;
     for (int64_t v0 = 0; v0 < a.v; v0 += plan.piece) {

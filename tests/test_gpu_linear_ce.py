@@ -141,6 +141,24 @@ def test_rows_without_a_loss():
     assert bool((dx[[i for i in range(70) if i != 3]] == 0).all()) and bool((dx[3] != 0).any())
 
 
+@pytest.mark.parametrize("n", [70, 200])
+def test_rows_without_a_loss_may_hold_anything(n):
+    """NaN and infinities in the hidden states, lse and dloss of ignored rows reach no gradient and no other row."""
+    x, w, target, dloss = _inputs(n, 300, 72, seed=16)
+    loss, lse = jq.linear_ce(x, w, target)
+    dx, dw = jq.linear_ce_bwd(x, w, target, lse, dloss)
+    out = (target < 0) | (target >= 300)
+    assert 0 < int(out.sum()) < n
+    bad, blse, bloss = x.clone(), lse.clone(), dloss.clone()
+    bad[out] = float("nan")
+    bad[out.nonzero()[0, 0], 3:] = float("inf")
+    blse[out], bloss[out] = float("-inf"), float("nan")
+    loss1, lse1 = jq.linear_ce(bad, w, target)
+    dx1, dw1 = jq.linear_ce_bwd(bad, w, target, blse, bloss)
+    assert torch.equal(loss, loss1) and torch.equal(lse[~out], lse1[~out])
+    assert torch.equal(dx, dx1) and torch.equal(dw, dw1) and bool((dx1[out] == 0).all())
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_nonfinite_weight_of_a_row_with_a_loss(bad):
     """It shows in its own row of dx; the other rows' gradients stay what they are."""
