@@ -1033,10 +1033,11 @@ cudaError_t norm_any(const NormArgs &a, NormParams p, bool bwd, cudaStream_t st)
         e = pick_norm<T, RMS>(p, plan, true, st);
     } else {
         plan.groups = (int)(a.n < kWideSlices ? a.n : kWideSlices);
-        e = launch_pdl(k_norm_wide<T, RMS, true>, wide_grid, dim3(1024), 0, st, p);
+        // the sums over dy and x come first: dx, which may be either of them, is written by the second kernel
+        e = launch_pdl(k_norm_wide_params<T, RMS>, dim3((unsigned)((a.c + 255) / 256), (unsigned)plan.groups),
+                       dim3(256), 0, st, p);
         if (e == cudaSuccess)
-            e = launch_pdl(k_norm_wide_params<T, RMS>, dim3((unsigned)((a.c + 255) / 256), (unsigned)plan.groups),
-                           dim3(256), 0, st, p);
+            e = launch_pdl(k_norm_wide<T, RMS, true>, wide_grid, dim3(1024), 0, st, p);
     }
     if (e != cudaSuccess)
         return e;

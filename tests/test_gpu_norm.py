@@ -152,6 +152,34 @@ def test_in_place():
     assert torch.equal(dx, d)
 
 
+def _same_layout(t):
+    """A copy in rows of the same stride (Tensor.clone would pack them)."""
+    out = torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
+    return out.copy_(t)
+
+
+@pytest.mark.parametrize("c", [64, 300, 511, 520, 1111, 8192, 8193, 12000, 20001])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_every_alias_gives_the_same_bits(c, kind, dtype):
+    """y = x, dx = dy and dx = x: outputs, statistics and parameter gradients as of separate tensors."""
+    n, layer = 41, kind == jq.NORM_LAYER
+    x, dy, w, b = _inputs(n, c, dtype, seed=c)
+    b = b if layer else None
+    y, mean, rstd = jq.norm_fwd(x, w, b, kind=kind)
+    z, mean1, rstd1 = _same_layout(x), torch.empty_like(rstd) if layer else None, torch.empty_like(rstd)
+    jq.jetq_norm_fwd(kind, z, w, b, 1e-5, z, mean1, rstd1)
+    assert torch.equal(y, z) and torch.equal(rstd, rstd1) and (not layer or torch.equal(mean, mean1))
+    dx, dw, db = jq.norm_bwd(dy, x, w, mean, rstd, kind=kind, bias=layer)
+    ws = torch.empty(jq.jetq_norm_bwd_workspace_bytes(jq._out_dtype(x), n, c), dtype=torch.uint8, device=DEV)
+    for alias in ("dy", "x"):
+        t = dict(dy=_same_layout(dy), x=_same_layout(x))
+        dw1, db1 = torch.empty_like(dw), torch.empty_like(db) if layer else None
+        jq.jetq_norm_bwd(kind, t["dy"], t["x"], w, mean, rstd, t[alias], dw1, db1, ws)
+        assert torch.equal(dx, t[alias]), alias
+        assert torch.equal(dw, dw1) and (not layer or torch.equal(db, db1)), alias
+
+
 def test_gradient_against_differences():
     x, dy, w, b = _inputs(20, 96, torch.float32, seed=7)
     _, mean, rstd = jq.norm_fwd(x, w, b)
