@@ -654,9 +654,12 @@ JETQ_API jetq_status jetq_linear_ce_fwd(const uint16_t *x, int64_t n, int64_t c,
  * piece of the vocabulary at a time):
  *   d[i, j] = (exp(z[i, j] - lse[i]) - [j = target[i]]) * dloss[i]
  *   dx = scale * d w   (BF16 [n x c], stride lddx),   dw = scale * d^T x   ([v x c], stride lddw)
- * d is rounded to BF16 (relative to the largest |dloss|) for the tensor cores;
- * every sum is FP32, rounded once.  dw: BF16, or FP32 with accumulate = 1 to
- * add into it.  Rows without a loss give zero rows of dx and add nothing to dw,
+ * d is rounded to BF16 (relative to the largest |dloss|) for the tensor cores,
+ * which also bounds an FP32 dw; the entry at the target keeps its relative
+ * precision however confident the token is.  dx and dw are summed in the tensor
+ * cores' FP32 accumulators, which truncate (within 1e-5 of the sum of
+ * magnitudes), and rounded once.  dw: BF16, or FP32 with accumulate = 1 to add
+ * into it.  Rows without a loss give zero rows of dx and add nothing to dw,
  * whatever their x, lse and dloss hold.
  *
  *   dloss      float [n]

@@ -11,8 +11,9 @@
 //   forward    x w^T with an epilogue that reduces each row's 128 logits to a
 //              (maximum, sum of exponentials) pair and picks the target's
 //              logit; a small kernel joins the pairs of a row
-//   backward, from a copy of x in rows of whole lines (zero without a loss), per
-//   piece of the vocabulary (its d is [n x piece] in BF16)
+//   backward, from a copy of x in rows of whole lines (zero without a loss) and
+//   each row's d at its target, per piece of the vocabulary (its d is [n x piece]
+//   in BF16)
 //     1. x w^T again with an epilogue that writes d
 //     2. dx += d w: d K-major, w with its N axis (c) contiguous; FP32 slabs
 //        in the workspace, one per K split, added to by TMA add-reductions
@@ -22,7 +23,10 @@
 // d is rounded to BF16 once (the tensor core's operand type), scaled by the
 // largest |dloss| so that it is O(1) whatever the loss's normalisation, and a
 // uniform dloss adds no rounding of its own; sums, softmax statistics, dx
-// across pieces and dw stay in FP32 until their one final rounding.
+// across pieces and dw stay in FP32 until their one final rounding.  The sums of
+// the backward products stay in the tensor core, whose FP32 accumulator
+// truncates: within 1e-5 of the sum of magnitudes, where d's rounding is 4e-3 of
+// each term.
 //
 // What bounds it.  Batches: the tensor cores.  Two CTAs of a cluster share a
 // 256 x 256 tile (cta_group::2): per 64 columns of K each loads 32 KB for 512
@@ -81,10 +85,19 @@ struct HeadParams {
     int64_t V, col0;                   // whole vocabulary; first vocabulary row of this piece
     float2 *part;                      // [kParts * nt][M] (maximum, sum), base 2
     float *zt;                         // [M] raw target logits
-    const float *lse, *dloss, *gmax;
+    const struct GradRow *rows;        // kGrad: [M]
+    const float *gmax;
     float scale;
     int add;                           // FP32 output: add to what is there
     unsigned long long limit_ns;
+};
+
+// What d needs of a row, written by the backward pass's first kernel.
+struct alignas(16) GradRow {
+    int target; // -1: a row without a loss, the rest is zero
+    float lse2; // lse in base 2
+    float dloss;
+    float dt;   // exp(z_t - lse) - 1, from a logit that this row's own sum gives
 };
 
 // FEW: one tile of at most 128 rows by single CTAs.  A's box then holds those
@@ -432,12 +445,11 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                 gmax = __ldg(p.gmax);
             if (MODE == kGradW16 || MODE == kGradW32)
                 factor = __ldg(p.gmax) * p.scale;
-            // d's inputs of a row, loaded a tile ahead
-            struct RowIn {
-                int64_t target = -1;
-                float lse = 0.0f, dloss = 0.0f;
-            };
             auto tile_row = [&](int mi) { return mi * 128 * CG + (int)rank * 128 + quarter * 32; };
+            struct RowIn { // loaded a tile ahead
+                int target = -1;
+                float lse2 = 0.0f, dloss = 0.0f;
+            };
             auto row_in = [&](int t) {
                 RowIn r;
                 if (MODE == kGrad && t < num_tiles) {
@@ -445,9 +457,10 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                     head_coords(p, t, mi, ni, ks);
                     const int64_t row = tile_row(mi) + lane;
                     if (row < p.M) {
-                        r.target = __ldg(p.target + row);
-                        r.lse = __ldg(p.lse + row);
-                        r.dloss = __ldg(p.dloss + row);
+                        const int4 q = __ldg(reinterpret_cast<const int4 *>(p.rows + row));
+                        r.target = q.x;
+                        r.lse2 = __int_as_float(q.y);
+                        r.dloss = __int_as_float(q.z);
                     }
                 }
                 return r;
@@ -496,16 +509,14 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                 const int64_t row = (int64_t)row0 + lane;
                 const int n0 = ni * bn + part * C::kCols;
                 const RowIn in = next;
-                const int64_t rel = in.target - p.col0 - n0;
-                const bool has = in.target >= 0 && in.target < p.V;
-                const int tcol = has && rel >= 0 && rel < C::kCols ? (int)rel : -1; // the target's column, if here
                 if constexpr (MODE == kGrad || MODE == kGradW16) { // 64 BF16 columns: one box
                     if (!wait_acc(tc))
                         break;
-                    // a row without a loss: exponent 0 and coefficient 0, so that d = 0 whatever its lse
-                    const bool loss = MODE == kGrad && has && gmax > 0.0f;
-                    const float k2 = loss ? p.k2 : 0.0f, lse2 = loss ? in.lse * kLog2e : 0.0f;
-                    const float f = MODE == kGradW16 ? factor : (loss ? __fdiv_rn(in.dloss, gmax) : 0.0f);
+                    // a row without a loss: logits, lse2 and dloss are zero, and so is d
+                    const float lse2 = in.lse2;
+                    const float f = MODE == kGradW16 ? factor : (gmax > 0.0f ? __fdiv_rn(in.dloss, gmax) : 0.0f);
+                    const int rel = in.target - (int)p.col0 - n0;
+                    const int tcol = rel >= 0 && rel < C::kCols ? rel : -1; // the target's column, if here
                     next = row_in(t + units);
                     uint32_t h[32];
 #pragma unroll
@@ -518,11 +529,12 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                         if constexpr (MODE == kGrad) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                v[j] = __float_as_uint(ex2(fmaf(__uint_as_float(v[j]), k2, -lse2)));
+                                v[j] = __float_as_uint(ex2(fmaf(__uint_as_float(v[j]), p.k2, -lse2)));
                             if (__any_sync(0xFFFFFFFFu, tcol >> 5 == ch)) {
+                                const float dt = tcol >= 0 ? __ldg(&p.rows[row].dt) : 0.0f;
 #pragma unroll
                                 for (int j = 0; j < 32; ++j)
-                                    v[j] = 32 * ch + j == tcol ? __float_as_uint(__uint_as_float(v[j]) - 1.0f) : v[j];
+                                    v[j] = 32 * ch + j == tcol ? __float_as_uint(dt) : v[j];
                             }
                             if (n0 + 32 * ch + 32 > p.N) { // columns past the piece: zero, part of the dx product's K
 #pragma unroll
@@ -675,24 +687,75 @@ __global__ void __launch_bounds__(1024)
     loss[row] = dt >= -1.0f ? log1pf(a.y * exp2f(-dt)) : logf(a.y + exp2f(dt)) - kLn2 * dt;
 }
 
-// Rows of x copied to a stride of whole 128-byte lines, 16 bytes a thread; with
-// `target`, rows without a loss become zero (whatever they hold: the backward
-// products run over every row, and 0 * NaN would reach all of dw).  Block 0
-// has the backward pass's other start: gmax = max |dloss| over the rows with a
-// target (1 where that is not finite).
+// s + b as s + c, exactly (Knuth's two-sum), c added to the compensation.
+__device__ __forceinline__ void two_sum(float &s, float &c, float b)
+{
+    const float t = __fadd_rn(s, b), u = __fsub_rn(t, s);
+    c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(b, u)));
+    s = t;
+}
+
+// Rows of x copied to a stride of whole 128-byte lines, a warp a row.  Backward
+// (`rows` given): rows without a loss become zero (whatever they hold: the
+// products run over every row, and 0 * NaN would reach all of dw), and each
+// row's GradRow is written.  A confident token's d at its target is -(1 - p),
+// about minus its loss, so the target's logit has to be good to a small part of
+// the loss: with the tensor core's truncating sum over K = 4096 a row of dx was
+// wrong by half where the loss is 1e-4 to 3e-4 (2000 x 4096 head; 2e-3 now, d's
+// rounding).  It is summed here with compensation (BF16 products are exact in
+// FP32) and leaves through one rounding of z_t - lse.  The other entries are p
+// itself, whose relative error stays that of the exponent, far below d's BF16
+// rounding.
+// Block 0 has the backward pass's other start: gmax = max |dloss| over the rows
+// with a target (1 where that is not finite).
 __global__ void __launch_bounds__(256)
-    k_ce_start(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, uint16_t *out, int64_t ldo, const float *dloss,
-               const int64_t *target, int64_t v, float *gmax)
+    k_ce_start(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, uint16_t *out, int64_t ldo, const uint16_t *w,
+               int64_t ldw, const int64_t *target, int64_t v, float scale, const float *lse, const float *dloss,
+               GradRow *rows, float *gmax)
 {
     __shared__ float red[8];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     if (blockIdx.x > 0) {
-        const int64_t c8 = c / 8, total = n * c8, step = (int64_t)(gridDim.x - 1) * blockDim.x;
-        for (int64_t i = (int64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x; i < total; i += step) {
-            const int64_t r = i / c8, col = 8 * (i - r * c8), tg = target ? __ldg(target + r) : 0;
-            *reinterpret_cast<uint4 *>(out + r * ldo + col) =
-                tg >= 0 && tg < v ? __ldg(reinterpret_cast<const uint4 *>(x + r * ldx + col)) : make_uint4(0, 0, 0, 0);
+        const int lane = threadIdx.x & 31;
+        const int64_t step = (int64_t)(gridDim.x - 1) * 8;
+        for (int64_t r = (int64_t)(blockIdx.x - 1) * 8 + (threadIdx.x >> 5); r < n; r += step) {
+            const int64_t tg = rows ? __ldg(target + r) : 0;
+            const bool has = !rows || (tg >= 0 && tg < v);
+            float s = 0.0f, comp = 0.0f;
+#pragma unroll 4
+            for (int64_t k = 8 * lane; k < c; k += 256) { // c and the rows are whole vectors
+                uint4 a = make_uint4(0, 0, 0, 0);
+                if (has) {
+                    a = __ldg(reinterpret_cast<const uint4 *>(x + r * ldx + k));
+                    if (rows) {
+                        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w + tg * ldw + k));
+                        const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            two_sum(s, comp, __fmul_rn(__uint_as_float(p[e] << 16), __uint_as_float(q[e] << 16)));
+                            two_sum(s, comp, __fmul_rn(__uint_as_float(p[e] & 0xffff0000u),
+                                                       __uint_as_float(q[e] & 0xffff0000u)));
+                        }
+                    }
+                }
+                *reinterpret_cast<uint4 *>(out + r * ldo + k) = a;
+            }
+            if (!rows)
+                continue;
+            for (int o = 16; o; o >>= 1) {
+                const float s2 = __shfl_xor_sync(0xFFFFFFFFu, s, o), c2 = __shfl_xor_sync(0xFFFFFFFFu, comp, o);
+                two_sum(s, comp, s2);
+                comp += c2;
+            }
+            if (lane == 0) {
+                GradRow g = {-1, 0.0f, 0.0f, 0.0f};
+                if (has) {
+                    const double z = comp == comp ? (double)s + (double)comp : (double)s; // an infinite sum has no rest
+                    g = {(int)tg, lse[r] * kLog2e, dloss[r], expm1f((float)(z * (double)scale - (double)lse[r]))};
+                }
+                rows[r] = g;
+            }
         }
         return;
     }
@@ -885,14 +948,15 @@ size_t fwd_lines(int64_t n, int64_t c)
 }
 
 // Copies a.x to `at` and makes it the copy; backward: zeroes its rows without a
-// loss, and computes gmax.
-cudaError_t start(LinearCeArgs &a, void *at, float *gmax, cudaStream_t st)
+// loss, and computes their GradRow and gmax.
+cudaError_t start(LinearCeArgs &a, void *at, GradRow *rows, float *gmax, cudaStream_t st)
 {
-    const int64_t blocks = ceil_div(a.n * (a.c / 8), 256), cap = (int64_t)sm_count() * 8;
+    const int64_t blocks = ceil_div(a.n, 8), cap = (int64_t)sm_count() * 8;
     uint16_t *out = static_cast<uint16_t *>(at);
     const cudaError_t e =
         launch_pdl(k_ce_start, dim3((unsigned)(1 + (blocks < cap ? blocks : cap))), dim3(256), 0, st, a.x, a.n, a.c,
-                   a.ldx, out, lines_ld(a.c), a.dloss, gmax ? a.target : (const int64_t *)nullptr, a.v, gmax);
+                   a.ldx, out, lines_ld(a.c), a.w, a.ldw, a.target, a.v, a.scale, (const float *)a.lse, a.dloss, rows,
+                   gmax);
     a.x = out;
     a.ldx = lines_ld(a.c);
     return e;
@@ -901,7 +965,7 @@ cudaError_t start(LinearCeArgs &a, void *at, float *gmax, cudaStream_t st)
 struct BwdPlan {
     int64_t piece; // vocabulary rows a piece (a multiple of 256)
     int dx_cg, splits;
-    size_t x_off, slab_off, d_off, total;
+    size_t rows_off, x_off, slab_off, d_off, total;
 };
 
 BwdPlan bwd_plan(int64_t n, int64_t v, int64_t c, int64_t piece)
@@ -910,7 +974,8 @@ BwdPlan bwd_plan(int64_t n, int64_t v, int64_t c, int64_t piece)
     const int64_t all = ceil_div(v, 256) * 256;
     b.piece = piece < 256 ? 256 : (piece > all ? all : piece / 256 * 256);
     dx_shape(n, c, b.piece, b.dx_cg, b.splits);
-    b.x_off = 1024; // gmax first
+    b.rows_off = 1024; // gmax first
+    b.x_off = b.rows_off + ((size_t)n * sizeof(GradRow) + 1023) / 1024 * 1024;
     b.slab_off = b.x_off + lines_bytes(n, c);
     const size_t slabs = (size_t)b.splits * (size_t)n * (size_t)c * 4;
     b.d_off = (b.slab_off + slabs + 1023) / 1024 * 1024;
@@ -950,7 +1015,7 @@ cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
 {
     cudaError_t e;
     if (fwd_lines(a.n, a.c) > 0 && (a.ldx % 64 != 0 || (reinterpret_cast<uintptr_t>(a.x) & 127u) != 0) &&
-        (e = start(a, a.ws, nullptr, st)) != cudaSuccess)
+        (e = start(a, a.ws, nullptr, nullptr, st)) != cudaSuccess)
         return e;
     HeadParams p = {};
     p.nt = (int)ceil_div(a.v, kTileN);
@@ -1011,7 +1076,8 @@ cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st)
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     float *gmax = reinterpret_cast<float *>(ws), *slab = reinterpret_cast<float *>(ws + plan.slab_off);
     uint16_t *d = reinterpret_cast<uint16_t *>(ws + plan.d_off);
-    cudaError_t e = start(a, ws + plan.x_off, gmax, st);
+    GradRow *grad_rows = reinterpret_cast<GradRow *>(ws + plan.rows_off);
+    cudaError_t e = start(a, ws + plan.x_off, grad_rows, gmax, st);
     if (e != cudaSuccess)
         return e;
     const bool dw16 = a.dw_dtype == JETQ_OUT_BF16;
@@ -1047,11 +1113,8 @@ cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st)
         p.M = a.n;
         p.N = rows;
         p.k2 = a.scale * kLog2e;
-        p.target = a.target;
-        p.V = a.v;
         p.col0 = v0;
-        p.lse = a.lse;
-        p.dloss = a.dloss;
+        p.rows = grad_rows;
         if ((e = run_head<kGrad>(cg, xk, wk, dst, p, st)) != cudaSuccess)
             return e;
         // dx += d w

@@ -199,6 +199,42 @@ def test_large_logits_and_nan():
     assert bool(bad[9]) and int(bad.sum()) == 1 and bool(torch.isnan(lse[9]))
 
 
+@pytest.mark.parametrize("n", [60, 300])
+@pytest.mark.parametrize("dw_dtype", [torch.float32, torch.bfloat16])
+def test_gradient_of_confident_tokens(n, dw_dtype):
+    """Tokens whose loss is 1e-3 to 1e-5, at a hidden size where the logit's sum is long: d at the target is -(1 - p),
+    so its exponent has to be good to a small part of the loss, not of the logit.  The target's exponent counts 2^-40
+    of the logit's magnitudes (a compensated sum and its one rounding, at most 4 * 2^-24 of the exponent); the other
+    columns' are bounded as everywhere."""
+    v, c = 2000, 4096
+    g = torch.Generator(device=DEV).manual_seed(n)
+    w = (torch.randn((v, c), generator=g, device=DEV) * 0.02).to(torch.bfloat16)
+    target = torch.randperm(v, generator=g, device=DEV)[:n]  # a row of dw has one token's target
+    row = w[target].float()
+    lean = torch.linspace(15.3, 20.0, n, device=DEV)[:, None]
+    x = (torch.randn((n, c), generator=g, device=DEV) + lean * row / row.square().sum(1, keepdim=True)).to(torch.bfloat16)
+    dloss = 0.5 + torch.rand(n, generator=g, device=DEV)
+    loss, lse = jq.linear_ce(x, w, target)
+    assert float(loss.max()) > 3e-4 and float(loss.min()) < 3e-5
+    dx, dw = jq.linear_ce_bwd(x, w, target, lse, dloss, dw_dtype=dw_dtype)
+    assert jq.jetq_check_device_error() == jq.OK
+    X, W, rows = x.double(), w.double(), torch.arange(n, device=DEV)
+    e = X @ W.T - lse.double()[:, None]
+    coef = dloss.double()[:, None]
+    d = torch.exp(e) * coef
+    off = d * (HALF_BF16 + SUM + 2 * (SUM * (X.abs() @ W.abs().T) + 8 * HALF_F32 * (1 + lse.double().abs()[:, None])))
+    et = e[rows, target]
+    d[rows, target] = torch.expm1(et) * coef[:, 0]
+    far = 2.0 ** -40 * (X.abs() * W[target].abs()).sum(1) + 4 * HALF_F32 * et.abs()
+    off[rows, target] = d[rows, target].abs() * (HALF_BF16 + SUM) + coef[:, 0] * 2 * far
+    last = HALF_BF16 if dw_dtype == torch.bfloat16 else HALF_F32
+    rx, rw = d @ W, d.T @ X
+    assert bool(((dx.double() - rx).abs() <= off @ W.abs() * 1.01 + HALF_BF16 * rx.abs() + 1e-30).all())
+    assert bool(((dw.double() - rw).abs() <= off.T @ X.abs() * 1.01 + last * rw.abs() + 1e-30).all())
+    # a whole row: each of its two roundings moves it by at most 2^-8 of its terms, which add up to at most twice d
+    assert float(((dx.double() - rx).norm(dim=1) / rx.norm(dim=1)).max()) <= 4 * HALF_BF16
+
+
 def test_accumulate_into_dw():
     x, w, target, dloss = _inputs(150, 400, 72, seed=9)
     _, lse = jq.linear_ce(x, w, target)
