@@ -9,8 +9,8 @@
 //
 // One GEMM kernel (k_head_gemm) in four modes carries all of it:
 //   forward    x w^T with an epilogue that reduces each row's 128 logits to a
-//              (maximum, sum of exponentials) pair and picks the target's
-//              logit; a small kernel joins the pairs of a row
+//              (maximum, sum of exponentials) pair without the target's term; a
+//              small kernel joins the pairs of a row and its target's logit
 //   backward, from a copy of x in rows of whole lines (zero without a loss) and
 //   each row's d at its target, per piece of the vocabulary (its d is [n x piece]
 //   in BF16)
@@ -84,7 +84,6 @@ struct HeadParams {
     int fold;                          // kStats: 64-blocks of K summed inside the tensor core, see the epilogue
     int64_t V, col0;                   // whole vocabulary; first vocabulary row of this piece
     float2 *part;                      // [kParts * nt][M] (maximum, sum), base 2
-    float *zt;                         // [M] raw target logits
     const struct GradRow *rows;        // kGrad: [M]
     const float *gmax;
     float scale;
@@ -415,13 +414,10 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                     m4[j & 3] = fmaxf(m4[j & 3], v[j]);
                 const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 const float mk = m * p.k2;
-                float zt = 0.0f;
                 if (__any_sync(0xFFFFFFFFu, tcol >= 0)) { // the target's term is joined exactly by the last kernel
 #pragma unroll
-                    for (int j = 0; j < 128; ++j) {
-                        zt = j == tcol ? v[j] : zt;
+                    for (int j = 0; j < 128; ++j)
                         v[j] = j == tcol ? -INFINITY : v[j];
-                    }
                 }
                 float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -433,8 +429,6 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                     p.part[(int64_t)(kParts * ni + part) * p.M + row] = m == -INFINITY ? make_float2(-INFINITY, 0.0f)
                                                                    : m == m       ? make_float2(mk, sum)
                                                                                   : make_float2(0.0f, m);
-                    if (tcol >= 0)
-                        p.zt[row] = zt;
                 }
             }
         } else {
@@ -617,41 +611,54 @@ __device__ __forceinline__ void join_pair(float2 &a, const float2 b)
         a.y += b.y; // both empty (or NaN)
 }
 
+// s + b as s + c, exactly (Knuth's two-sum), c added to the compensation.
+__device__ __forceinline__ void two_sum(float &s, float &c, float b)
+{
+    const float t = __fadd_rn(s, b), u = __fsub_rn(t, s);
+    c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(b, u)));
+    s = t;
+}
+
+// Eight products of BF16 pairs (exact in FP32) added to s + c.
+__device__ __forceinline__ void dot8(float &s, float &c, const uint4 &a, const uint4 &b)
+{
+    const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        two_sum(s, c, __fmul_rn(__uint_as_float(p[e] << 16), __uint_as_float(q[e] << 16)));
+        two_sum(s, c, __fmul_rn(__uint_as_float(p[e] & 0xffff0000u), __uint_as_float(q[e] & 0xffff0000u)));
+    }
+}
+
+// The sum s + c; an infinite one has no rest.
+__device__ __forceinline__ double whole_sum(float s, float c)
+{
+    return c == c ? (double)s + (double)c : (double)s;
+}
+
 // Joins the (maximum, sum) pairs of a row and its target's logit.  blockDim =
 // (rows, lanes), powers of two: threadIdx.x walks rows (contiguous in part),
-// threadIdx.y parts.  DOT (one tile of rows): the target's logit is summed here
-// once more, in round-to-nearest.  It is the largest logit of a confident token
-// and its truncation error is that of the loss, which other tokens' do not
-// average out there (worst of forty single tokens: 8e-7 of its loss, as an FP32
-// matrix product; 2.4e-6 was seen without).
-template <bool DOT>
+// threadIdx.y parts.  The target's logit is summed here, with compensation: it
+// is the largest one of a confident token, whose loss is its distance to the
+// others' and whose lse is that logit plus the loss.  With the tensor core's sum
+// a single token's loss was off by 2.4e-6 of its value, and lse by 1.4e-5 at 300
+// tokens x 2000 x 4096, which the backward pass would meet in exp(z_t - lse) - 1.
 __global__ void __launch_bounds__(1024)
-    k_ce_join(const float2 *part, const float *zt, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw,
-              int64_t c, const int64_t *target, int64_t n, int64_t v, int parts, float k2, float *loss, float *lse)
+    k_ce_join(const float2 *part, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw, int64_t c,
+              const int64_t *target, int64_t n, int64_t v, int parts, float scale, float k2, float *loss, float *lse)
 {
-    __shared__ float2 red[1024];
-    __shared__ float dots[DOT ? 1024 : 1];
+    __shared__ float2 red[1024], dots[1024];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t tg = row < n ? target[row] : -1;
     const bool has = tg >= 0 && tg < v;
     const int at = threadIdx.y * blockDim.x + threadIdx.x;
-    if constexpr (DOT) {
-        float d = 0.0f;
-        if (has)
-            for (int64_t k = 8 * threadIdx.y; k < c; k += 8 * blockDim.y) { // c and the rows are whole vectors
-                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + row * ldx + k));
-                const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w + tg * ldw + k));
-                const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    d = fmaf(__uint_as_float(p[e] << 16), __uint_as_float(q[e] << 16), d);
-                    d = fmaf(__uint_as_float(p[e] & 0xffff0000u), __uint_as_float(q[e] & 0xffff0000u), d);
-                }
-            }
-        dots[at] = d;
-    }
+    float s = 0.0f, comp = 0.0f;
+    if (has)
+        for (int64_t k = 8 * threadIdx.y; k < c; k += 8 * blockDim.y) // c and the rows are whole vectors
+            dot8(s, comp, __ldg(reinterpret_cast<const uint4 *>(x + row * ldx + k)),
+                 __ldg(reinterpret_cast<const uint4 *>(w + tg * ldw + k)));
     float2 a = make_float2(-INFINITY, 0.0f);
     if (row < n)
         for (int q = threadIdx.y; q < parts; q += 4 * blockDim.y) { // four loads in flight
@@ -665,13 +672,16 @@ __global__ void __launch_bounds__(1024)
                 join_pair(a, b[i]);
         }
     red[at] = a;
+    dots[at] = make_float2(s, comp);
     for (int o = blockDim.y / 2; o; o >>= 1) {
         __syncthreads();
         if ((int)threadIdx.y < o) {
             join_pair(a, red[at + o * blockDim.x]);
             red[at] = a;
-            if constexpr (DOT)
-                dots[at] += dots[at + o * blockDim.x];
+            const float2 d = dots[at + o * blockDim.x];
+            two_sum(s, comp, d.x);
+            comp += d.y;
+            dots[at] = make_float2(s, comp);
         }
     }
     if (threadIdx.y != 0 || row >= n)
@@ -682,17 +692,17 @@ __global__ void __launch_bounds__(1024)
         return;
     }
     // the target's exponent against the maximum's, rounded once: both products carry errors of lse's size
-    const float dt = fmaf(DOT ? dots[at] : zt[row], k2, -a.x);
-    lse[row] = kLn2 * (a.x + log2f(a.y + exp2f(dt)));
-    loss[row] = dt >= -1.0f ? log1pf(a.y * exp2f(-dt)) : logf(a.y + exp2f(dt)) - kLn2 * dt;
-}
-
-// s + b as s + c, exactly (Knuth's two-sum), c added to the compensation.
-__device__ __forceinline__ void two_sum(float &s, float &c, float b)
-{
-    const float t = __fadd_rn(s, b), u = __fsub_rn(t, s);
-    c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(b, u)));
-    s = t;
+    const double z = whole_sum(s, comp);
+    const float dt = (float)(z * (double)k2 - (double)a.x);
+    if (dt >= -1.0f) { // the target leads, or almost
+        const float l = log1pf(a.y * exp2f(-dt));
+        loss[row] = l;
+        lse[row] = (float)(z * (double)scale + (double)l);
+    } else {
+        const float rest = a.y + exp2f(dt);
+        loss[row] = logf(rest) - kLn2 * dt;
+        lse[row] = kLn2 * (a.x + log2f(rest));
+    }
 }
 
 // Rows of x copied to a stride of whole 128-byte lines, a warp a row.  Backward
@@ -728,16 +738,8 @@ __global__ void __launch_bounds__(256)
                 uint4 a = make_uint4(0, 0, 0, 0);
                 if (has) {
                     a = __ldg(reinterpret_cast<const uint4 *>(x + r * ldx + k));
-                    if (rows) {
-                        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w + tg * ldw + k));
-                        const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            two_sum(s, comp, __fmul_rn(__uint_as_float(p[e] << 16), __uint_as_float(q[e] << 16)));
-                            two_sum(s, comp, __fmul_rn(__uint_as_float(p[e] & 0xffff0000u),
-                                                       __uint_as_float(q[e] & 0xffff0000u)));
-                        }
-                    }
+                    if (rows)
+                        dot8(s, comp, a, __ldg(reinterpret_cast<const uint4 *>(w + tg * ldw + k)));
                 }
                 *reinterpret_cast<uint4 *>(out + r * ldo + k) = a;
             }
@@ -751,8 +753,8 @@ __global__ void __launch_bounds__(256)
             if (lane == 0) {
                 GradRow g = {-1, 0.0f, 0.0f, 0.0f};
                 if (has) {
-                    const double z = comp == comp ? (double)s + (double)comp : (double)s; // an infinite sum has no rest
-                    g = {(int)tg, lse[r] * kLog2e, dloss[r], expm1f((float)(z * (double)scale - (double)lse[r]))};
+                    const double z = whole_sum(s, comp) * (double)scale;
+                    g = {(int)tg, lse[r] * kLog2e, dloss[r], expm1f((float)(z - (double)lse[r]))};
                 }
                 rows[r] = g;
             }
@@ -992,7 +994,8 @@ int64_t preferred_piece(int64_t n)
 } // namespace
 
 // Tiles of the forward product's vocabulary axis: 256 columns each, or, for one
-// row tile, evenly over the SMs.
+// row tile, evenly over the SMs; and a float a row, which the formula has had
+// from the start (buffers planned by it stay large enough) and no kernel uses.
 size_t linear_ce_fwd_workspace(int64_t n, int64_t v, int64_t c)
 {
     int64_t nt = ceil_div(v, kTileN);
@@ -1048,7 +1051,6 @@ cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
     p.fold = cg == 2 ? 8 : 4;
     p.V = a.v;
     p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + fwd_lines(a.n, a.c));
-    p.zt = reinterpret_cast<float *>(p.part + (size_t)kParts * p.nt * a.n);
     if ((e = run_head<kStats>(cg, ta, tb, ta, p, st)) != cudaSuccess)
         return e;
     const int parts = kParts * p.nt;
@@ -1058,11 +1060,8 @@ cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
     while (rx * ry < 1024 && ry < parts)
         ry *= 2;
     const dim3 grid((unsigned)ceil_div(a.n, rx)), block(rx, ry);
-    auto join = [&](auto kern) {
-        return launch_pdl(kern, grid, block, 0, st, (const float2 *)p.part, (const float *)p.zt, a.x, a.ldx, a.w, a.ldw,
-                          a.c, a.target, a.n, a.v, parts, p.k2, a.loss, a.lse);
-    };
-    return a.n <= 128 ? join(k_ce_join<true>) : join(k_ce_join<false>);
+    return launch_pdl(k_ce_join, grid, block, 0, st, (const float2 *)p.part, a.x, a.ldx, a.w, a.ldw, a.c, a.target, a.n,
+                      a.v, parts, a.scale, p.k2, a.loss, a.lse);
 }
 
 cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st)

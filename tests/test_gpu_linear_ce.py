@@ -235,6 +235,27 @@ def test_gradient_of_confident_tokens(n, dw_dtype):
     assert float(((dx.double() - rx).norm(dim=1) / rx.norm(dim=1)).max()) <= 4 * HALF_BF16
 
 
+@pytest.mark.parametrize("n", [1, 60, 300])
+@pytest.mark.parametrize("scale", [1.0, 1.3])
+def test_lse_of_confident_tokens(n, scale):
+    """lse of a token that its target leads is the target's logit plus the loss: FP32's step at lse (2^-24 of it) and
+    the loss's own error, a small part of a small loss.  The backward pass subtracts it from the same logit, so a larger
+    error of lse would be one of 1 - p."""
+    v, c = 2000, 4096
+    g = torch.Generator(device=DEV).manual_seed(n + 7)
+    w = (torch.randn((v, c), generator=g, device=DEV) * 0.02).to(torch.bfloat16)
+    target = torch.randperm(v, generator=g, device=DEV)[:n]
+    row = w[target].float()
+    lean = torch.linspace(15.3, 20.0, n, device=DEV)[:, None]
+    x = (torch.randn((n, c), generator=g, device=DEV) + lean * row / row.square().sum(1, keepdim=True)).to(torch.bfloat16)
+    loss, lse = jq.linear_ce(x, w, target, scale=scale)
+    assert jq.jetq_check_device_error() == jq.OK
+    _, rlse, rloss, _, ez = _define(x, w, target, torch.tensor(scale).item())  # the entry point takes a float
+    part = rloss * (4 * ez + 16 * HALF_F32 * (1 + rlse.abs()))  # both exponents' errors, relative to the loss
+    assert bool(((loss.double() - rloss).abs() <= part).all())
+    assert bool(((lse.double() - rlse).abs() <= HALF_F32 * rlse.abs() + part).all())
+
+
 def test_accumulate_into_dw():
     x, w, target, dloss = _inputs(150, 400, 72, seed=9)
     _, lse = jq.linear_ce(x, w, target)
