@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                 for (int j = 4; j < 128; ++j)
                     m4[j & 3] = fmaxf(m4[j & 3], v[j]);
                 const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                const float mk = m * p.k2;
+                const float mk = m == -INFINITY ? 0.0f : m * p.k2; // without a number: NaN still reaches the sum
                 if (__any_sync(0xFFFFFFFFu, tcol >= 0)) { // the target's term is joined exactly by the last kernel
 #pragma unroll
                     for (int j = 0; j < 128; ++j)
@@ -424,9 +424,10 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                 for (int j = 0; j < 128; ++j)
                     s4[j & 3] += ex2(fmaf(v[j], p.k2, -mk));
                 if (row < p.M) {
-                    // no column, or all of them -inf: an empty sum; only NaN: NaN (fmaxf passes over single ones)
+                    // no column, or all of them -inf: an empty sum.  fmaxf passes over NaN, the sum does not: NaN
+                    // among numbers or past them (the columns outside are -inf), and where all 128 are NaN
                     const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                    p.part[(int64_t)(kParts * ni + part) * p.M + row] = m == -INFINITY ? make_float2(-INFINITY, 0.0f)
+                    p.part[(int64_t)(kParts * ni + part) * p.M + row] = m == -INFINITY ? make_float2(-INFINITY, sum)
                                                                    : m == m       ? make_float2(mk, sum)
                                                                                   : make_float2(0.0f, m);
                 }

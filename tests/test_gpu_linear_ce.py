@@ -256,6 +256,21 @@ def test_lse_of_confident_tokens(n, scale):
     assert bool(((lse.double() - rlse).abs() <= HALF_F32 * rlse.abs() + part).all())
 
 
+@pytest.mark.parametrize("n,v", [(200, 129), (4, 1000), (4, 129), (300, 4097)])
+def test_nan_in_a_partial_slice(n, v):
+    """NaN in the vocabulary's last, partly filled columns reaches every row; NaN in a hidden state reaches its row."""
+    x, w, target, _ = _inputs(n, v, 64, seed=17, ignored=False)
+    target[0] = -100
+    bad = w.clone()
+    bad[v - 1, 5] = float("nan")
+    loss, lse = jq.linear_ce(x, bad, target)
+    assert bool(torch.isnan(lse).all()) and bool(torch.isnan(loss[1:]).all()) and loss[0].item() == 0
+    x[:2, 7] = float("nan")
+    loss, lse = jq.linear_ce(x, w, target)
+    assert bool(torch.isnan(lse[:2]).all()) and bool(torch.isfinite(lse[2:]).all())
+    assert loss[0].item() == 0 and bool(torch.isnan(loss[1])) and bool(torch.isfinite(loss[2:]).all())
+
+
 def test_accumulate_into_dw():
     x, w, target, dloss = _inputs(150, 400, 72, seed=9)
     _, lse = jq.linear_ce(x, w, target)
