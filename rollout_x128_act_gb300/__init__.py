@@ -606,9 +606,20 @@ def _norm_rows(x, n, c):
     return torch.empty_strided((n, c), (c + pad, 1), dtype=x.dtype, device=x.device)
 
 
+def _aligned_rows(x):
+    """x as the norm kernels take it: itself, or a padded copy where its rows are not 16-byte aligned."""
+    n, c = x.shape
+    ld = x.stride(0)
+    if ld >= c and ld % (8 if x.dtype is torch.bfloat16 else 4) == 0 and x.data_ptr() % 16 == 0:
+        return x
+    return _norm_rows(x, n, c).copy_(x)
+
+
 def norm_fwd(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, stream=None):
     """Layer norm or RMS norm of BF16 or FP32 rows x [n x c] (see jetq_norm_fwd) ->
-    (y, mean [n] (None for RMS), rstd [n])."""
+    (y, mean [n] (None for RMS), rstd [n]).  The kernels read rows that start on 16 bytes: x in
+    other rows (a dense one of odd width, a view off the boundary) is copied to padded ones
+    first, and y's rows are padded where the width asks for it."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return norm_fwd(x, w, b, eps, kind)
@@ -618,6 +629,7 @@ def norm_fwd(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, stream=None):
         _want(w, "w", x.dtype, (c,))
     if b is not None:
         _want(b, "b", x.dtype, (c,))
+    x = _aligned_rows(x)
     y = _norm_rows(x, n, c)
     rstd = torch.empty(n, dtype=torch.float32, device=x.device)
     mean = torch.empty(n, dtype=torch.float32, device=x.device) if kind == NORM_LAYER else None
@@ -626,7 +638,8 @@ def norm_fwd(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, stream=None):
 
 
 def norm_bwd(dy, x, w, mean, rstd, kind=NORM_LAYER, bias=False, workspace=None, stream=None):
-    """Backward pass of norm_fwd (see jetq_norm_bwd) -> (dx, dw FP32 [c], db FP32 [c] or None)."""
+    """Backward pass of norm_fwd (see jetq_norm_bwd) -> (dx, dw FP32 [c], db FP32 [c] or None).
+    dy and x are copied, and dx is padded, as norm_fwd does it."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return norm_bwd(dy, x, w, mean, rstd, kind, bias, workspace)
@@ -638,6 +651,7 @@ def norm_bwd(dy, x, w, mean, rstd, kind=NORM_LAYER, bias=False, workspace=None, 
     _want(rstd, "rstd", torch.float32, (n,))
     if kind == NORM_LAYER:
         _want(mean, "mean", torch.float32, (n,))
+    dy, x = _aligned_rows(dy), _aligned_rows(x)
     dx = _norm_rows(x, n, c)
     dw = torch.empty(c, dtype=torch.float32, device=x.device)
     db = torch.empty(c, dtype=torch.float32, device=x.device) if bias else None

@@ -180,6 +180,22 @@ def test_every_alias_gives_the_same_bits(c, kind, dtype):
         assert torch.equal(dw, dw1) and (not layer or torch.equal(db, db1)), alias
 
 
+@pytest.mark.parametrize("n,c", [(50, 1111), (1, 1111), (7, 63), (1, 1), (3, 8195)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_of_any_layout(n, c, dtype):
+    """Dense rows of odd width, as autograd hands them back, and a view off the 16 bytes: the bits of padded rows."""
+    x, dy, w, b = _inputs(n, c, dtype, seed=n * c)
+    want = jq.norm_fwd(x, w, b)
+    want += jq.norm_bwd(dy, x, w, want[1], want[2], bias=True)
+    wide = torch.empty((2, n, c + 3), dtype=dtype, device=DEV)
+    off = [t[:, 1:c + 1].copy_(v) for t, v in zip(wide, (x, dy))]
+    for xs, dys in ((x.contiguous(), dy.contiguous()), off):
+        got = jq.norm_fwd(xs, w, b)
+        got += jq.norm_bwd(dys, xs, w, got[1], got[2], bias=True)
+        assert all(torch.equal(p, q) for p, q in zip(want, got))
+        assert torch.equal(xs, x) and torch.equal(dys, dy)
+
+
 def test_gradient_against_differences():
     x, dy, w, b = _inputs(20, 96, torch.float32, seed=7)
     _, mean, rstd = jq.norm_fwd(x, w, b)

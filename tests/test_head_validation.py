@@ -204,3 +204,17 @@ def test_tensor_checks(monkeypatch, L):
             (_Fake((8,), f32, (2,)), f32, (8,), False, "contiguous")):
         with pytest.raises(ValueError, match=what):
             jq._want(t, "x", dtype, shape, rows)
+
+
+def test_rows_are_padded_where_their_layout_asks_for_it():
+    import rollout_x128_act_gb300 as jq
+
+    for dtype, step in ((torch.bfloat16, 8), (torch.float32, 4)):
+        base = torch.arange(40 * 24, dtype=torch.float32).to(dtype).view(40, 24)
+        assert base.data_ptr() % 16 == 0
+        for x, same in ((base, True), (base[:, :step], True), (base[3:, step:], True), (base[:, :17], True),
+                        (base[:, 1:], False), (base[:, :17].contiguous(), False), (base.view(-1)[:23].view(1, 23), False),
+                        (torch.as_strided(base, (1, 16), (3, 1)), False), (torch.empty((0, 17), dtype=dtype), False)):
+            y = jq._aligned_rows(x)
+            assert (y is x) == same and torch.equal(x, y)
+            assert y.data_ptr() % 16 == 0 and y.stride(0) % step == 0 and y.stride(0) >= y.shape[1]
