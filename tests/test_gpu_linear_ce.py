@@ -100,6 +100,20 @@ def test_backward(n, v, c, dw_dtype):
     _check_bwd(x, w, target, 0.8, dloss, lse, dw_dtype)
 
 
+# several tiles a CTA or pair (152 SMs): single CTAs with three tiles of rows; pairs with one and with three folds of K;
+# pairs in two raster groups, the second one ragged
+BATCHES = [(333, 50257, 136), (1000, 30011, 72), (700, 20011, 1032), (1100, 6000, 520), (8500, 3000, 64)]
+
+
+@pytest.mark.parametrize("n,v,c", BATCHES)
+@pytest.mark.parametrize("dw_dtype", [torch.float32, torch.bfloat16])
+def test_several_tiles_a_worker(n, v, c, dw_dtype):
+    """The ring, the accumulators and a row's inputs are carried from tile to tile."""
+    x, w, target, dloss = _inputs(n, v, c, seed=n + v + c)
+    lse = _check_fwd(x, w, target, 1.1)
+    _check_bwd(x, w, target, 1.1, dloss, lse, dw_dtype)
+
+
 def test_backward_in_small_pieces():
     """The smallest workspace (256 vocabulary rows a piece) and one in between give the same gradient."""
     x, w, target, dloss = _inputs(200, 3000, 136, seed=5)

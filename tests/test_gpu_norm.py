@@ -118,6 +118,33 @@ def test_many_rows():
     _check_bwd(dy, x, w, mean, rstd, jq.NORM_LAYER, True)
 
 
+@pytest.mark.parametrize("n,c", [(4000, 1111), (6001, 2048), (2500, 4096), (1501, 8192)])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_more_rows_than_the_rings_hold(n, c, kind, dtype):
+    """Every group of warps takes many rows: the rings' stages are filled again in both passes."""
+    x, dy, w, b = _inputs(n, c, dtype, seed=n + c)
+    layer = kind == jq.NORM_LAYER
+    mean, rstd = _check_fwd(x, w, b if layer else None, 1e-5, kind)
+    _check_bwd(dy, x, w, mean, rstd, kind, layer)
+
+
+@pytest.mark.parametrize("c", [128, 1111, 2048, 9000])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_parameters_off_the_vectors(c, dtype):
+    """w and b need the alignment of an element only."""
+    x, dy, w, b = _inputs(30, c, dtype, seed=c)
+    both = torch.empty(2 * c + 3, dtype=dtype, device=DEV)
+    w1, b1 = both[1:c + 1].copy_(w), both[c + 2:2 * c + 2].copy_(b)
+    assert w1.data_ptr() % 16 and b1.data_ptr() % 16
+    y, mean, rstd = jq.norm_fwd(x, w1, b1)
+    y2, mean2, rstd2 = jq.norm_fwd(x, w, b)
+    assert torch.equal(y, y2) and torch.equal(mean, mean2) and torch.equal(rstd, rstd2)
+    for p, q in zip(jq.norm_bwd(dy, x, w1, mean, rstd, bias=True), jq.norm_bwd(dy, x, w, mean, rstd, bias=True)):
+        assert torch.equal(p, q)
+    _check_fwd(x, w1, b1, 1e-5, jq.NORM_LAYER)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_mean_far_above_the_spread(dtype):
     """The variance is summed around the mean: an offset of 64 spreads costs no precision beyond its own rounding."""
