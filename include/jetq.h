@@ -655,8 +655,8 @@ JETQ_API jetq_status jetq_linear_ce_fwd(const uint16_t *x, int64_t n, int64_t c,
  *   d[i, j] = (exp(z[i, j] - lse[i]) - [j = target[i]]) * dloss[i]
  *   dx = scale * d w   (BF16 [n x c], stride lddx),   dw = scale * d^T x   ([v x c], stride lddw)
  * d is rounded to BF16 (relative to the largest |dloss|) for the tensor cores,
- * which also bounds an FP32 dw; the entry at the target keeps its relative
- * precision however confident the token is.  dx and dw are summed in the tensor
+ * which also bounds an FP32 dw; the entry at the target, about minus the loss of
+ * a confident token, is good to FP32's step at lse.  dx and dw are summed in the tensor
  * cores' FP32 accumulators, which truncate (within 1e-5 of the sum of
  * magnitudes), and rounded once.  dw: BF16, or FP32 with accumulate = 1 to add
  * into it.  Rows without a loss give zero rows of dx and add nothing to dw,

@@ -4,17 +4,22 @@
 //
 //   y[i, r] = sg * sum_k e2m1(q[r, k]) * e4m3(sb[r, k / 16]) * x[i, k]
 //
-// Floor: HBM (9/16 byte a weight); what bounds it is the decode's instructions
-// on the ALU pipe.  A CTA owns 16 rows of the weight, its warps a contiguous
-// share of K each, the next batch of loads in flight under a batch's arithmetic.
+// Floor: HBM (9/16 byte a weight).  It runs at three times that, with no pipe
+// full at one token: while an SM is active the ALU pipe (masks of the decode,
+// permutes of x) is 58% busy and the L1 58%, warps wait for loads most, and a
+// third of the time goes at the kernel's two ends.  x is read where it is used,
+// again for every 16 rows of the weight: with 8 tokens the L1 is 74% busy, with
+// 16 it is 86% and the bound.  A CTA owns 16 rows of the weight, its warps a
+// contiguous share of K each, the next batch of the weight's loads in flight
+// under a batch's arithmetic.
 // The product runs on the tensor cores (mma.m16n8k16, weight rows as M, tokens as
 // N): one warp step covers 16 rows x 128 columns, a lane holding 32 consecutive
 // values (16 bytes, two scale blocks) of two rows; since both operands permute K
 // alike, every lane feeds its own values to the MMA and no data moves between
 // lanes.  This is a legacy MMA on purpose: tcgen05 would need the decoded weights
 // in shared memory and 128 rows a tile, and the tensor pipe is 13% busy here.
-// 12288 x 4096, one token: 12.7 us a call back to back (4.2 us of HBM time);
-// 4096 x 12288, eight tokens: 12.7 us.
+// 12288 x 4096 in a graph (4.2 us of HBM time): 12.1 us for one token, 13.1 for
+// eight, 20.7 for nine and 24.6 for sixteen; 4096 x 12288: 11.7, 12.8, 17.4, 20.3.
 //
 // Decoding: the bits of an E2M1 code placed at a BF16's sign and at the low
 // exponent and top mantissa bits are that code's value times 2^-126 (the

@@ -33,12 +33,14 @@
 // tensor cycles, where a single CTA's 128 x 256 tile needs 48 KB, more than an
 // SM's 64 bytes a cycle from L2.  The tile's FP32 sums are double-buffered in
 // TMEM, so the epilogue works under the next tile's products.  4096 tokens x
-// 131072 x 4096: forward 2.36 ms alone (1.86 PFLOP/s, 0.97 of the measured BF16
-// burst rate), 2.58 to 2.64 ms back to back; backward 7.7 to 7.9 ms back to back
-// (1.69 PFLOP/s, 0.96 of the rate cuBLAS sustains under the power cap).  Few tokens:
-// the weight's stream from HBM (one token x 32000 x 4096: 48 us for 262 MB).
-// Rows of w that are not multiples of 128 bytes cost L2 sectors: 1000 x 50257 x 1032
-// backward takes 280 us, 1.11 PFLOP/s.
+// 131072 x 4096, back to back: forward 2.58 to 2.67 ms (1.65 to 1.70 PFLOP/s),
+// backward 7.6 to 7.9 ms with dw in BF16 (1.69 to 1.73 PFLOP/s, 0.97 to 1.0 of the
+// rate cuBLAS sustains under the power cap), 2% more in FP32 and 3 to 5% more where
+// it adds into dw.  Few tokens: the weight's stream from HBM (one token x 32000 x
+// 4096: 48.5 us for 262 MB).  Widths just past a tile cost the most: 1000 x 50257 x
+// 1032 backward takes 280 us (1.11 PFLOP/s), 249 at 1024 columns and 292 at 1280,
+// since dx and dw run five tiles of 256 for 4.03; rows of w and dw off the 128-byte
+// lines are 4% of it (271 us with both in lines).
 //
 // The target's term is left out of the sum of exponentials and joined at the
 // end: loss = log1p(sum of the others / the target's) where the target leads,
@@ -944,7 +946,7 @@ size_t lines_bytes(int64_t n, int64_t c)
 // second line.  x is read by every tile of the vocabulary, so for more than one
 // tile of rows it is copied first where its width makes rows start off the
 // lines (with the copy: 1000 x 50257 x 1032 96 us against 104, 2000 x 50257 x
-// 2056 277 against 331; w, read by a few tiles of rows, would not pay).
+// 2056 277 against 331; w is read by a few tiles of rows only).
 size_t fwd_lines(int64_t n, int64_t c)
 {
     return n > 128 && c % 64 != 0 ? lines_bytes(n, c) : 0;
@@ -1045,10 +1047,10 @@ cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
     p.N = a.v;
     p.k2 = a.scale * kLog2e;
     p.target = a.target;
-    // The error of a loss grows with the steps of a partial tile.  Pairs: 8 blocks (3e-7 in the 2-norm over
-    // 4096 tokens, an FP32 matrix product has 6e-7; 4096 x 131072 x 4096 took 2.65 ms with 8, 2.97 with 4 and
-    // 4.03 with 2, whose hand-overs between the CTAs stall the tensor core).  Single CTAs: 4 (2e-7; 333 tokens x
-    // 50257 x 2048: 64 us, 66 with 2; one token x 1000 x 4096: 27 us, 30 with 2).
+    // The error of a loss grows with the steps of a partial tile.  Pairs: 8 blocks (1.2e-7 in the 2-norm over
+    // 4096 tokens, an FP32 matrix product has 6.7e-7; 4096 x 131072 x 4096 took 2.65 ms with 8, 2.97 with 4 and
+    // 4.03 with 2, whose hand-overs between the CTAs stall the tensor core).  Single CTAs: 4 (1e-7; 2 us less than
+    // with 2 at 333 tokens x 50257 x 2048, 66 in all, and 3 us less at one token x 1000 x 4096).
     p.fold = cg == 2 ? 8 : 4;
     p.V = a.v;
     p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + fwd_lines(a.n, a.c));
