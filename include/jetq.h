@@ -677,6 +677,71 @@ JETQ_API jetq_status jetq_linear_ce_bwd(const uint16_t *x, int64_t n, int64_t c,
                                         void *dw, jetq_out_dtype dw_dtype, int64_t lddw, int accumulate,
                                         void *workspace, size_t workspace_bytes, void *stream);
 
+/* ======================================================================== */
+/* The policy's loss                                                        */
+/* ======================================================================== */
+/*
+ * Clipped policy-gradient loss of packed sequences, from token losses (minus
+ * log-probabilities, as jetq_linear_ce_fwd gives them) of the policy, of the
+ * policy that sampled the tokens and, for a KL term, of a reference policy:
+ *   logr = nll_old - nll
+ *   r    = exp(logr) (TOKEN), or exp(mean of logr over the sequence's counted tokens) (SEGMENT)
+ *   L    = -A m;  A >= 0: m = min(r, 1 + clip_high)
+ *                 A <  0: m = max(r, 1 - clip_low), and min(that, clip_dual) where clip_dual > 0
+ *   kl   = exp(d) - 1 - d,  d = nll - nll_ref      (0 without nll_ref)
+ *   loss = sum of weight * (L + kl_coef * kl) over the counted tokens
+ *   weight = scale / N (MEAN_TOKENS), scale / (S n_s) (MEAN_SEGMENTS), scale (SUM)
+ * with N counted tokens in all, n_s in the token's sequence, S sequences that have one.
+ *
+ *   nll, nll_old, nll_ref, n   float [n]; nll_ref nullable
+ *   adv, adv_per_token         the advantages A: float [n] (1) or [nseg] (0)
+ *   mask                       uint8 [n], nonzero for a counted token; NULL: all are.  A token that is
+ *                              not counted may hold anything
+ *   seg_offsets, nseg          device int64 [nseg + 1], rising (equal ones: an empty sequence); NULL: one
+ *                              sequence of n tokens (nseg is not read).  Tokens outside every sequence
+ *                              (a padded batch) are not counted
+ *   clip_low, clip_high        in [0, 1] and [0, 1e6];  clip_dual: 0 (none) or at least 1
+ *   scale, kl                  finite
+ *   out                        float [6]: loss, sum of weight * L, sum of weight * kl, number of clipped tokens
+ *                              (those whose L has no gradient), N, S (rounded to FP32)
+ *   seg                        float [2 nseg] (2 without seg_offsets), 8-byte aligned, for the backward pass
+ *   workspace                  device memory, 16-byte aligned, at least
+ *                              jetq_policy_loss_workspace_bytes(n, nseg) bytes (nseg = 1 without
+ *                              seg_offsets); calls that share one must not overlap on the GPU
+ * Limits: n <= 2^40, 1 <= nseg <= 2^30.  No counted token: out is zero.  Bitwise repeatable.
+ */
+typedef enum {
+    JETQ_POLICY_TOKEN = 0,
+    JETQ_POLICY_SEGMENT = 1
+} jetq_policy_level;
+typedef enum {
+    JETQ_POLICY_MEAN_TOKENS = 0,
+    JETQ_POLICY_MEAN_SEGMENTS = 1,
+    JETQ_POLICY_SUM = 2
+} jetq_policy_mean;
+JETQ_API size_t jetq_policy_loss_workspace_bytes(int64_t n, int64_t nseg);
+JETQ_API jetq_status jetq_policy_loss_fwd(const float *nll, const float *nll_old, const float *nll_ref,
+                                          const float *adv, int adv_per_token, const uint8_t *mask, int64_t n,
+                                          const int64_t *seg_offsets, int64_t nseg, jetq_policy_level level,
+                                          jetq_policy_mean mean, float scale, float clip_low, float clip_high,
+                                          float clip_dual, float kl, float *out, float *seg, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradient with respect to nll, from the forward call's out and seg and the same other arguments:
+ *   dnll = dloss * weight * (A r [r not clipped] + kl_coef * (exp(d) - 1))      (TOKEN)
+ *   SEGMENT: r / n_s * (sum of A over the sequence's tokens that are not clipped) in place of A r
+ * zero for tokens that are not counted.  The loss of linear_ce has this as its dloss.
+ *   dloss   float [1], the loss's own gradient; NULL for 1
+ *   dnll    float [n]
+ */
+JETQ_API jetq_status jetq_policy_loss_bwd(const float *nll, const float *nll_old, const float *nll_ref,
+                                          const float *adv, int adv_per_token, const uint8_t *mask, int64_t n,
+                                          const int64_t *seg_offsets, int64_t nseg, jetq_policy_level level,
+                                          jetq_policy_mean mean, float scale, float clip_low, float clip_high,
+                                          float clip_dual, float kl, const float *out, const float *seg,
+                                          const float *dloss, float *dnll, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,6 +27,8 @@ PATH_AUTO, PATH_TRAIN, PATH_DECODE = 0, 1, 2
 GEMM_FPROP, GEMM_DGRAD, GEMM_WGRAD = 0, 1, 2
 OUT_F32, OUT_BF16 = 0, 1
 NORM_LAYER, NORM_RMS = 0, 1
+POLICY_TOKEN, POLICY_SEGMENT = 0, 1
+POLICY_MEAN_TOKENS, POLICY_MEAN_SEGMENTS, POLICY_SUM = 0, 1, 2
 
 _lock = threading.Lock()
 _lib = None
@@ -90,6 +92,11 @@ def lib() -> ctypes.CDLL:
             "jetq_linear_ce_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I32]),
             "jetq_linear_ce_bwd": (I32, [P, I64, I64, I64, P, I64, I64, P, F32, P, P, P, I64, P, I32, I64, I32, P,
                                          ctypes.c_size_t, P]),
+            "jetq_policy_loss_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
+            "jetq_policy_loss_fwd": (I32, [P, P, P, P, I32, P, I64, P, I64, I32, I32, F32, F32, F32, F32, F32, P, P, P,
+                                           ctypes.c_size_t, P]),
+            "jetq_policy_loss_bwd": (I32, [P, P, P, P, I32, P, I64, P, I64, I32, I32, F32, F32, F32, F32, F32, P, P, P,
+                                           P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -349,6 +356,26 @@ def jetq_linear_ce_bwd(x, w, target, scale, lse, dloss, dx, dw, accumulate, ws, 
            "jetq_linear_ce_bwd")
 
 
+def jetq_policy_loss_workspace_bytes(n: int, nseg: int = 1) -> int:
+    return int(lib().jetq_policy_loss_workspace_bytes(n, nseg))
+
+
+def jetq_policy_loss_fwd(nll, nll_old, nll_ref, adv, adv_per_token, mask, seg_offsets, nseg, level, mean, scale,
+                         clip_low, clip_high, clip_dual, kl, out, seg, ws, stream=None):
+    _check(lib().jetq_policy_loss_fwd(_p(nll), _p(nll_old), _p(nll_ref), _p(adv), int(adv_per_token), _p(mask),
+                                      nll.numel(), _p(seg_offsets), nseg, level, mean, scale, clip_low, clip_high,
+                                      clip_dual, kl, _p(out), _p(seg), _p(ws), _bytes(ws), _s(stream)),
+           "jetq_policy_loss_fwd")
+
+
+def jetq_policy_loss_bwd(nll, nll_old, nll_ref, adv, adv_per_token, mask, seg_offsets, nseg, level, mean, scale,
+                         clip_low, clip_high, clip_dual, kl, out, seg, dloss, dnll, stream=None):
+    _check(lib().jetq_policy_loss_bwd(_p(nll), _p(nll_old), _p(nll_ref), _p(adv), int(adv_per_token), _p(mask),
+                                      nll.numel(), _p(seg_offsets), nseg, level, mean, scale, clip_low, clip_high,
+                                      clip_dual, kl, _p(out), _p(seg), _p(dloss), _p(dnll), _s(stream)),
+           "jetq_policy_loss_bwd")
+
+
 # ------------------------------------------------------------------ argument checks of the tensor helpers
 
 def _want(t, name, dtype, shape=None, rows=False):
@@ -365,6 +392,15 @@ def _want(t, name, dtype, shape=None, rows=False):
         raise ValueError(f"{name}: a contiguous tensor is wanted")
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
         raise ValueError(f"{name}: rows of consecutive elements are wanted, got strides {t.stride()}")
+
+
+def _one_device(x, **tensors):
+    """All tensors (None passes) on x's device, which is the current one: the launch goes to its stream."""
+    if x.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {x.device}: make it the current device for the call")
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != x.get_device():
+            raise ValueError(f"{name}: on {t.device}, the other tensors on {x.device}")
 
 
 # ------------------------------------------------------------------ allocating helpers
@@ -708,3 +744,88 @@ def linear_ce_bwd(x, w, target, lse, dloss, scale=1.0, dw_dtype=torch.float32, d
         workspace = torch.empty(jetq_linear_ce_bwd_workspace_bytes(n, v, c), dtype=torch.uint8, device=x.device)
     jetq_linear_ce_bwd(x, w, target, scale, lse, dloss, dx, dw, accumulate, workspace)
     return dx, dw
+
+
+def _policy_args(nll, nll_old, adv, seg_offsets, nll_ref, mask, workspace=None, out=None, seg=None, dloss=None):
+    """Checks of the policy loss's tensors -> the number of sequences."""
+    _want(nll, "nll", torch.float32)
+    n = nll.shape[0] if nll.dim() == 1 else -1
+    if n < 0:
+        raise ValueError(f"nll: one axis is wanted, got shape {tuple(nll.shape)}")
+    _want(nll_old, "nll_old", torch.float32, (n,))
+    nseg = 1
+    if seg_offsets is not None:
+        _want(seg_offsets, "seg_offsets", torch.int64)
+        nseg = seg_offsets.numel() - 1
+        if seg_offsets.dim() != 1 or nseg < 1:
+            raise ValueError(f"seg_offsets: at least two on one axis, got shape {tuple(seg_offsets.shape)}")
+    _want(adv, "adv", torch.float32)
+    if adv.shape != (n,) and adv.shape != (nseg,):
+        raise ValueError(f"adv: one for each of {n} tokens or of {nseg} sequences, got shape {tuple(adv.shape)}")
+    if nll_ref is not None:
+        _want(nll_ref, "nll_ref", torch.float32, (n,))
+    if mask is not None:
+        _want(mask, "mask", (torch.bool, torch.uint8), (n,))
+    if out is not None:
+        _want(out, "out", torch.float32, (6,))
+        _want(seg, "seg", torch.float32, (nseg, 2))
+    if dloss is not None:
+        _want(dloss, "dloss", torch.float32)
+        if dloss.numel() != 1:
+            raise ValueError(f"dloss: one value is wanted, got shape {tuple(dloss.shape)}")
+    _one_device(nll, nll_old=nll_old, adv=adv, seg_offsets=seg_offsets, nll_ref=nll_ref, mask=mask, out=out, seg=seg,
+                dloss=dloss, workspace=workspace)
+    return nseg
+
+
+def _adv_per_token(adv, n, nseg, adv_per_token):
+    """Where there are as many tokens as sequences the shape does not tell: per sequence unless it is said."""
+    if adv_per_token is None:
+        return adv.shape[0] != nseg
+    if adv.shape[0] != (n if adv_per_token else nseg):
+        raise ValueError(f"adv: {n if adv_per_token else nseg} are wanted, got {adv.shape[0]}")
+    return bool(adv_per_token)
+
+
+def policy_loss(nll, nll_old, adv, seg_offsets=None, nll_ref=None, mask=None, clip_low=0.2, clip_high=0.2,
+                clip_dual=0.0, kl=0.0, level=POLICY_TOKEN, mean=POLICY_MEAN_TOKENS, scale=1.0, adv_per_token=None,
+                workspace=None, stream=None):
+    """Clipped policy-gradient loss of packed sequences (see jetq_policy_loss_fwd): FP32 token losses nll, nll_old
+    and nll_ref [n], advantages adv of the tokens [n] or of the sequences [nseg] (where both have the same number,
+    adv_per_token tells; None: of the sequences), int64 seg_offsets [nseg + 1], mask bool or uint8 [n] ->
+    (out [6]: loss, its policy part, its mean KL, clipped tokens, counted tokens, counted sequences;
+    seg [nseg x 2] for the backward pass)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return policy_loss(nll, nll_old, adv, seg_offsets, nll_ref, mask, clip_low, clip_high, clip_dual, kl,
+                               level, mean, scale, adv_per_token, workspace)
+    nseg = _policy_args(nll, nll_old, adv, seg_offsets, nll_ref, mask, workspace)
+    n = nll.shape[0]
+    per_token = _adv_per_token(adv, n, nseg, adv_per_token)
+    out = torch.empty(6, dtype=torch.float32, device=nll.device)
+    seg = torch.empty((nseg, 2), dtype=torch.float32, device=nll.device)
+    need = jetq_policy_loss_workspace_bytes(n, nseg)
+    if workspace is None or _bytes(workspace) < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=nll.device)
+    jetq_policy_loss_fwd(nll, nll_old, nll_ref, adv, per_token, mask, seg_offsets, nseg, level, mean, scale, clip_low,
+                         clip_high, clip_dual, kl, out, seg, workspace)
+    return out, seg
+
+
+def policy_loss_bwd(nll, nll_old, adv, out, seg, seg_offsets=None, nll_ref=None, mask=None, clip_low=0.2,
+                    clip_high=0.2, clip_dual=0.0, kl=0.0, level=POLICY_TOKEN, mean=POLICY_MEAN_TOKENS, scale=1.0,
+                    adv_per_token=None, dloss=None, stream=None):
+    """Gradient of policy_loss's out[0] (times dloss [1], where given) with respect to nll (see
+    jetq_policy_loss_bwd) -> dnll [n], which linear_ce_bwd takes as its dloss."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return policy_loss_bwd(nll, nll_old, adv, out, seg, seg_offsets, nll_ref, mask, clip_low, clip_high,
+                                   clip_dual, kl, level, mean, scale, adv_per_token, dloss)
+    if out is None or seg is None:
+        raise ValueError("out and seg: those of the forward call are wanted")
+    nseg = _policy_args(nll, nll_old, adv, seg_offsets, nll_ref, mask, None, out, seg, dloss)
+    per_token = _adv_per_token(adv, nll.shape[0], nseg, adv_per_token)
+    dnll = torch.empty_like(nll)
+    jetq_policy_loss_bwd(nll, nll_old, nll_ref, adv, per_token, mask, seg_offsets, nseg, level, mean, scale, clip_low,
+                         clip_high, clip_dual, kl, out, seg, dloss, dnll)
+    return dnll

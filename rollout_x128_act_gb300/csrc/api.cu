@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "jetq_internal.h"
@@ -879,6 +880,86 @@ jetq_status jetq_gemv_nvfp4(const uint8_t *qw, const uint8_t *sbw, const float *
         return a;
     GemvNvfp4Args g{qw, sbw, sgw, n, k, x, m, ldx, y, y_dtype, ldy};
     return from_cuda(launch_gemv_nvfp4(g, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// arguments that both directions of the policy loss share
+jetq_status check_policy(const PolicyArgs &a, int64_t nseg)
+{
+    JQ_REQUIRE(a.n >= 0 && (a.adv_per_token == 0 || a.adv_per_token == 1), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(a.seg == nullptr || nseg >= 1, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(a.level == JETQ_POLICY_TOKEN || a.level == JETQ_POLICY_SEGMENT, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(a.mean >= JETQ_POLICY_MEAN_TOKENS && a.mean <= JETQ_POLICY_SUM, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(std::isfinite(a.scale) && std::isfinite(a.kl), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(a.low >= 0.0f && a.low <= 1.0f && a.high >= 0.0f && a.high <= 1e6f, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(a.dual == 0.0f || (a.dual >= 1.0f && std::isfinite(a.dual)), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(a.n <= ((int64_t)1 << 40) && (a.seg == nullptr || nseg <= (1 << 30)), JETQ_ERR_UNSUPPORTED_SHAPE);
+    JQ_REQUIRE(a.out != nullptr && a.save != nullptr, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(a.n == 0 || (a.nll != nullptr && a.nll_old != nullptr && a.adv != nullptr), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(aligned4(a.nll) && aligned4(a.nll_old) && aligned4(a.nll_ref) && aligned4(a.adv) && aligned4(a.out) &&
+                   (reinterpret_cast<uintptr_t>(a.seg) & 7u) == 0 && (reinterpret_cast<uintptr_t>(a.save) & 7u) == 0,
+               JETQ_ERR_MISALIGNED);
+    return JETQ_OK;
+}
+
+} // namespace
+
+size_t jetq_policy_loss_workspace_bytes(int64_t n, int64_t nseg)
+{
+    if (n <= 0 || nseg <= 0 || n > ((int64_t)1 << 40) || nseg > (1 << 30))
+        return 0;
+    return policy_loss_workspace(n, nseg);
+}
+
+jetq_status jetq_policy_loss_fwd(const float *nll, const float *nll_old, const float *nll_ref, const float *adv,
+                                 int adv_per_token, const uint8_t *mask, int64_t n, const int64_t *seg_offsets,
+                                 int64_t nseg, jetq_policy_level level, jetq_policy_mean mean, float scale,
+                                 float clip_low, float clip_high, float clip_dual, float kl, float *out, float *seg,
+                                 void *workspace, size_t workspace_bytes, void *stream)
+{
+    PolicyArgs g{nll, nll_old, nll_ref, adv, adv_per_token, mask, n, seg_offsets, seg_offsets ? (int)nseg : 1, level,
+                 mean, scale, clip_low, clip_high, clip_dual, kl, out, seg};
+    const jetq_status s = check_policy(g, nseg);
+    if (s != JETQ_OK)
+        return s;
+    if (n > 0) {
+        JQ_REQUIRE(workspace != nullptr && workspace_bytes >= policy_loss_workspace(n, g.nseg), JETQ_ERR_INVALID_ARG);
+        JQ_REQUIRE(aligned16(workspace), JETQ_ERR_MISALIGNED);
+    }
+    const jetq_status a = check_arch();
+    if (a != JETQ_OK)
+        return a;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (n == 0) { // no token
+        cudaError_t e = cudaMemsetAsync(out, 0, 6 * sizeof(float), st);
+        if (e == cudaSuccess)
+            e = cudaMemsetAsync(seg, 0, (size_t)g.nseg * 2 * sizeof(float), st);
+        return from_cuda(e);
+    }
+    g.ws = workspace;
+    return from_cuda(launch_policy_fwd(g, st));
+}
+
+jetq_status jetq_policy_loss_bwd(const float *nll, const float *nll_old, const float *nll_ref, const float *adv,
+                                 int adv_per_token, const uint8_t *mask, int64_t n, const int64_t *seg_offsets,
+                                 int64_t nseg, jetq_policy_level level, jetq_policy_mean mean, float scale,
+                                 float clip_low, float clip_high, float clip_dual, float kl, const float *out,
+                                 const float *seg, const float *dloss, float *dnll, void *stream)
+{
+    PolicyArgs g{nll, nll_old, nll_ref, adv, adv_per_token, mask, n, seg_offsets, seg_offsets ? (int)nseg : 1, level,
+                 mean, scale, clip_low, clip_high, clip_dual, kl, const_cast<float *>(out), const_cast<float *>(seg)};
+    const jetq_status s = check_policy(g, nseg);
+    if (s != JETQ_OK || n == 0)
+        return s;
+    JQ_REQUIRE(dnll != nullptr, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(aligned4(dnll) && aligned4(dloss), JETQ_ERR_MISALIGNED);
+    const jetq_status a = check_arch();
+    if (a != JETQ_OK)
+        return a;
+    g.dloss = dloss;
+    g.dnll = dnll;
+    return from_cuda(launch_policy_bwd(g, static_cast<cudaStream_t>(stream)));
 }
 
 } // extern "C"

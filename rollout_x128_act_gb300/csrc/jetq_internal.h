@@ -310,6 +310,28 @@ cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st);
 cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st);
 cudaError_t linear_ce_read_and_clear_error(cudaStream_t st, unsigned *out);
 
+// Clipped policy-gradient loss of packed sequences, forward (out, save
+// written) and backward (dnll).
+struct PolicyArgs {
+    const float *nll, *nll_old, *nll_ref; // nll_ref nullable
+    const float *adv;
+    int adv_per_token;
+    const uint8_t *mask; // nullable
+    int64_t n;
+    const int64_t *seg; // nullable: one sequence
+    int nseg;
+    jetq_policy_level level;
+    jetq_policy_mean mean;
+    float scale, low, high, dual, kl;
+    float *out, *save;
+    void *ws;           // forward
+    const float *dloss; // backward, nullable
+    float *dnll;
+};
+size_t policy_loss_workspace(int64_t n, int64_t nseg);
+cudaError_t launch_policy_fwd(const PolicyArgs &a, cudaStream_t st);
+cudaError_t launch_policy_bwd(const PolicyArgs &a, cudaStream_t st);
+
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
