@@ -677,6 +677,54 @@ JETQ_API jetq_status jetq_linear_ce_bwd(const uint16_t *x, int64_t n, int64_t c,
                                         void *dw, jetq_out_dtype dw_dtype, int64_t lddw, int accumulate,
                                         void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Distillation of the same head from a teacher that is known by its top
+ * logits: the Kullback-Leibler divergence of the student's softmax from the
+ * teacher's distribution over the listed columns, without keeping the logits.
+ *   z, lse as above
+ *   q[i, j] = exp(teacher[i, j] - log sum over the row's listed exp(teacher))  (renorm = 1)
+ *           = exp(teacher[i, j])                   (renorm = 0: log-probabilities over the whole vocabulary)
+ *   logp[i, j] = z[i, ids[i, j]] - lse[i]          (0 where nothing is listed)
+ *   loss[i] = sum over the row's listed q (log q - logp)
+ * An id outside [0, v) lists nothing (rows of fewer entries; their teacher
+ * values may hold anything); a row that lists nothing has no loss and no
+ * gradient, nor has one whose q are all zero (0 log 0 = 0).  A column listed
+ * twice counts with the sum of its q in the gradient and with each in the loss.
+ * The listed logits are summed in FP32 with compensation, not on the tensor
+ * cores: the loss is a small difference of them.
+ *
+ *   x, w, n, c, v, scale, lse   as for jetq_linear_ce_fwd
+ *   ids, ldi                    device int64 [n x k], row stride ldi
+ *   teacher, ldt                float [n x k], row stride ldt
+ *   k                           1 to 256
+ *   loss, lse, logp             float [n], [n], [n x k]
+ *   workspace                   device memory, 16-byte aligned, at least
+ *                               jetq_linear_distill_workspace_bytes(n, v, c, k) bytes; calls that
+ *                               share one must not overlap on the GPU
+ * n == 0 is a no-op.  Bitwise repeatable.  Three launches.
+ */
+JETQ_API size_t jetq_linear_distill_workspace_bytes(int64_t n, int64_t v, int64_t c, int64_t k);
+JETQ_API jetq_status jetq_linear_distill_fwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx,
+                                             const uint16_t *w, int64_t v, int64_t ldw, const int64_t *ids,
+                                             int64_t ldi, const float *teacher, int64_t ldt, int64_t k, int renorm,
+                                             float scale, float *loss, float *lse, float *logp,
+                                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradient, from the forward call's lse and logp:
+ *   d[i, j] = (Q p[i, j] - q[i, j]) * dloss[i],  p = exp(z - lse), Q = the row's sum of q, q = 0 where not listed
+ *   dx = scale * d w,   dw = scale * d^T x
+ * d, dx, dw, dloss and workspace as for jetq_linear_ce_bwd; the listed entries of d come from logp and are rounded once.
+ */
+JETQ_API size_t jetq_linear_distill_bwd_workspace_bytes(int64_t n, int64_t v, int64_t c, int64_t k, int smallest);
+JETQ_API jetq_status jetq_linear_distill_bwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx,
+                                             const uint16_t *w, int64_t v, int64_t ldw, const int64_t *ids,
+                                             int64_t ldi, const float *teacher, int64_t ldt, int64_t k, int renorm,
+                                             float scale, const float *lse, const float *logp, const float *dloss,
+                                             uint16_t *dx, int64_t lddx, void *dw, jetq_out_dtype dw_dtype,
+                                             int64_t lddw, int accumulate, void *workspace, size_t workspace_bytes,
+                                             void *stream);
+
 /* ======================================================================== */
 /* The policy's loss                                                        */
 /* ======================================================================== */

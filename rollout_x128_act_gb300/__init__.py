@@ -92,6 +92,12 @@ def lib() -> ctypes.CDLL:
             "jetq_linear_ce_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I32]),
             "jetq_linear_ce_bwd": (I32, [P, I64, I64, I64, P, I64, I64, P, F32, P, P, P, I64, P, I32, I64, I32, P,
                                          ctypes.c_size_t, P]),
+            "jetq_linear_distill_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64]),
+            "jetq_linear_distill_fwd": (I32, [P, I64, I64, I64, P, I64, I64, P, I64, P, I64, I64, I32, F32, P, P, P, P,
+                                              ctypes.c_size_t, P]),
+            "jetq_linear_distill_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64, I32]),
+            "jetq_linear_distill_bwd": (I32, [P, I64, I64, I64, P, I64, I64, P, I64, P, I64, I64, I32, F32, P, P, P, P,
+                                              I64, P, I32, I64, I32, P, ctypes.c_size_t, P]),
             "jetq_policy_loss_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
             "jetq_policy_loss_fwd": (I32, [P, P, P, P, I32, P, I64, P, I64, I32, I32, F32, F32, F32, F32, F32, P, P, P,
                                            ctypes.c_size_t, P]),
@@ -354,6 +360,31 @@ def jetq_linear_ce_bwd(x, w, target, scale, lse, dloss, dx, dw, accumulate, ws, 
                                     1 if accumulate else 0, _p(ws),
                                     _bytes(ws), _s(stream)),
            "jetq_linear_ce_bwd")
+
+
+def jetq_linear_distill_workspace_bytes(n: int, v: int, c: int, k: int) -> int:
+    return int(lib().jetq_linear_distill_workspace_bytes(n, v, c, k))
+
+
+def jetq_linear_distill_fwd(x, w, ids, teacher, renorm, scale, loss, lse, logp, ws, stream=None):
+    n, c = x.shape
+    _check(lib().jetq_linear_distill_fwd(_p(x), n, c, x.stride(0), _p(w), w.shape[0], w.stride(0), _p(ids),
+                                         ids.stride(0), _p(teacher), teacher.stride(0), ids.shape[1],
+                                         1 if renorm else 0, scale, _p(loss), _p(lse), _p(logp), _p(ws), _bytes(ws),
+                                         _s(stream)), "jetq_linear_distill_fwd")
+
+
+def jetq_linear_distill_bwd_workspace_bytes(n: int, v: int, c: int, k: int, smallest: bool = False) -> int:
+    return int(lib().jetq_linear_distill_bwd_workspace_bytes(n, v, c, k, 1 if smallest else 0))
+
+
+def jetq_linear_distill_bwd(x, w, ids, teacher, renorm, scale, lse, logp, dloss, dx, dw, accumulate, ws, stream=None):
+    n, c = x.shape
+    _check(lib().jetq_linear_distill_bwd(_p(x), n, c, x.stride(0), _p(w), w.shape[0], w.stride(0), _p(ids),
+                                         ids.stride(0), _p(teacher), teacher.stride(0), ids.shape[1],
+                                         1 if renorm else 0, scale, _p(lse), _p(logp), _p(dloss), _p(dx),
+                                         dx.stride(0), _p(dw), _out_dtype(dw), dw.stride(0), 1 if accumulate else 0,
+                                         _p(ws), _bytes(ws), _s(stream)), "jetq_linear_distill_bwd")
 
 
 def jetq_policy_loss_workspace_bytes(n: int, nseg: int = 1) -> int:
@@ -743,6 +774,72 @@ def linear_ce_bwd(x, w, target, lse, dloss, scale=1.0, dw_dtype=torch.float32, d
     if workspace is None:
         workspace = torch.empty(jetq_linear_ce_bwd_workspace_bytes(n, v, c), dtype=torch.uint8, device=x.device)
     jetq_linear_ce_bwd(x, w, target, scale, lse, dloss, dx, dw, accumulate, workspace)
+    return dx, dw
+
+
+def _check_distill(x, w, ids, teacher):
+    _want(x, "x", torch.bfloat16, rows=True)
+    _want(w, "w", torch.bfloat16, rows=True)
+    n = x.shape[0]
+    _want(ids, "ids", torch.int64, rows=True)
+    _want(teacher, "teacher", torch.float32, ids.shape, rows=True)
+    if ids.shape[0] != n or not 1 <= ids.shape[1] <= 256:
+        raise ValueError(f"ids: {n} rows of 1 to 256 entries are wanted, got shape {tuple(ids.shape)}")
+    if x.shape[1] != w.shape[1]:
+        raise ValueError(f"x and w: widths {x.shape[1]} and {w.shape[1]}")
+    _one_device(x, w=w, ids=ids, teacher=teacher)
+
+
+def _row_stride(t):
+    """t with a row stride that covers its rows (a single row may carry any)."""
+    return t if t.shape[0] > 1 or t.stride(0) >= t.shape[1] else t.reshape(-1).as_strided(t.shape, (t.shape[1], 1))
+
+
+def linear_distill(x, w, ids, teacher, scale=1.0, renorm=True, workspace=None, stream=None):
+    """Distillation losses of a linear head from a teacher's top logits (see jetq_linear_distill_fwd): BF16 x
+    [n x c], w [v x c], int64 ids [n x k] (outside [0, v): nothing listed), FP32 teacher [n x k] (logits with
+    renorm, else log-probabilities) -> (loss [n], lse [n], logp [n x k])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_distill(x, w, ids, teacher, scale, renorm, workspace)
+    _check_distill(x, w, ids, teacher)
+    (n, c), v, k = x.shape, w.shape[0], ids.shape[1]
+    loss = torch.empty(n, dtype=torch.float32, device=x.device)
+    lse = torch.empty(n, dtype=torch.float32, device=x.device)
+    logp = torch.empty((n, k), dtype=torch.float32, device=x.device)
+    need = jetq_linear_distill_workspace_bytes(n, v, c, k)
+    if workspace is None or _bytes(workspace) < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    jetq_linear_distill_fwd(_row_stride(x), _row_stride(w), _row_stride(ids), _row_stride(teacher), renorm, scale,
+                            loss, lse, logp, workspace)
+    return loss, lse, logp
+
+
+def linear_distill_bwd(x, w, ids, teacher, lse, logp, dloss, scale=1.0, renorm=True, dw_dtype=torch.float32, dw=None,
+                       accumulate=False, workspace=None, stream=None):
+    """Gradient of linear_distill (see jetq_linear_distill_bwd) -> (dx BF16 [n x c], dw [v x c]).  A workspace that
+    the caller gives is used as it is: its size decides the vocabulary's pieces."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_distill_bwd(x, w, ids, teacher, lse, logp, dloss, scale, renorm, dw_dtype, dw, accumulate,
+                                      workspace)
+    _check_distill(x, w, ids, teacher)
+    (n, c), v, k = x.shape, w.shape[0], ids.shape[1]
+    _want(lse, "lse", torch.float32, (n,))
+    _want(logp, "logp", torch.float32, (n, k))
+    _want(dloss, "dloss", torch.float32, (n,))
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dw to add into")
+        dw = torch.empty((v, c), dtype=dw_dtype, device=x.device)
+    _want(dw, "dw", (torch.float32, torch.bfloat16), (v, c), rows=True)
+    _one_device(x, lse=lse, logp=logp, dloss=dloss, dw=dw, workspace=workspace)
+    dx = torch.empty((n, c), dtype=torch.bfloat16, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(jetq_linear_distill_bwd_workspace_bytes(n, v, c, k), dtype=torch.uint8,
+                                device=x.device)
+    jetq_linear_distill_bwd(_row_stride(x), _row_stride(w), _row_stride(ids), _row_stride(teacher), renorm, scale,
+                            lse, logp, dloss, dx, dw, accumulate, workspace)
     return dx, dw
 
 

@@ -694,14 +694,14 @@ jetq_status jetq_linear_ce_fwd(const uint16_t *x, int64_t n, int64_t c, int64_t 
     return from_cuda(launch_linear_ce_fwd(g, static_cast<cudaStream_t>(stream)));
 }
 
-jetq_status jetq_linear_ce_bwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, const uint16_t *w, int64_t v,
-                               int64_t ldw, const int64_t *target, float scale, const float *lse, const float *dloss,
-                               uint16_t *dx, int64_t lddx, void *dw, jetq_out_dtype dw_dtype, int64_t lddw,
-                               int accumulate, void *workspace, size_t workspace_bytes, void *stream)
+namespace {
+
+// the backward pass of the cross entropy (t null) and of the distillation, x, w and targets checked
+jetq_status head_backward(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, const uint16_t *w, int64_t v,
+                          int64_t ldw, const int64_t *target, float scale, const float *lse, const float *dloss,
+                          uint16_t *dx, int64_t lddx, void *dw, jetq_out_dtype dw_dtype, int64_t lddw,
+                          int accumulate, void *workspace, size_t workspace_bytes, const DistillArgs *t, void *stream)
 {
-    const jetq_status s = check_linear_ce(x, n, c, ldx, w, v, ldw, target, scale);
-    if (s != JETQ_OK)
-        return s;
     const jetq_status o = check_out(dw, dw_dtype, lddw, c);
     if (o != JETQ_OK)
         return o;
@@ -724,7 +724,7 @@ jetq_status jetq_linear_ce_bwd(const uint16_t *x, int64_t n, int64_t c, int64_t 
         const size_t es = dw_dtype == JETQ_OUT_F32 ? 4 : 2;
         return from_cuda(cudaMemset2DAsync(dw, (size_t)lddw * es, 0, (size_t)c * es, (size_t)v, st));
     }
-    JQ_REQUIRE(workspace_bytes >= linear_ce_bwd_workspace_min(n, v, c), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(workspace_bytes >= linear_distill_bwd_workspace_min(n, v, c, t ? t->k : 0), JETQ_ERR_INVALID_ARG);
     LinearCeArgs g{x, n, c, ldx, w, v, ldw, target, scale, nullptr, const_cast<float *>(lse)};
     g.dloss = dloss;
     g.dx = dx;
@@ -735,7 +735,98 @@ jetq_status jetq_linear_ce_bwd(const uint16_t *x, int64_t n, int64_t c, int64_t 
     g.accumulate = accumulate;
     g.ws = workspace;
     g.ws_bytes = workspace_bytes;
-    return from_cuda(launch_linear_ce_bwd(g, st));
+    return from_cuda(launch_linear_ce_bwd(g, t, st));
+}
+
+} // namespace
+
+jetq_status jetq_linear_ce_bwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, const uint16_t *w, int64_t v,
+                               int64_t ldw, const int64_t *target, float scale, const float *lse, const float *dloss,
+                               uint16_t *dx, int64_t lddx, void *dw, jetq_out_dtype dw_dtype, int64_t lddw,
+                               int accumulate, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const jetq_status s = check_linear_ce(x, n, c, ldx, w, v, ldw, target, scale);
+    if (s != JETQ_OK)
+        return s;
+    return head_backward(x, n, c, ldx, w, v, ldw, target, scale, lse, dloss, dx, lddx, dw, dw_dtype, lddw, accumulate,
+                         workspace, workspace_bytes, nullptr, stream);
+}
+
+namespace {
+
+// what the distillation adds to the linear cross entropy's arguments
+jetq_status check_distill(const int64_t *ids, int64_t ldi, const float *teacher, int64_t ldt, int64_t k, int renorm,
+                          int64_t n)
+{
+    JQ_REQUIRE(renorm == 0 || renorm == 1, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(k >= 1, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(k <= 256 && ldi >= k && ldt >= k && ldi <= ((int64_t)1 << 36) && ldt <= ((int64_t)1 << 36),
+               JETQ_ERR_UNSUPPORTED_SHAPE);
+    JQ_REQUIRE(n == 0 || (ids != nullptr && teacher != nullptr), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE((reinterpret_cast<uintptr_t>(teacher) & 3u) == 0, JETQ_ERR_MISALIGNED);
+    return JETQ_OK;
+}
+
+} // namespace
+
+size_t jetq_linear_distill_workspace_bytes(int64_t n, int64_t v, int64_t c, int64_t k)
+{
+    return n <= 0 || v <= 0 || c <= 0 || k <= 0 || k > 256 ? 0 : linear_distill_fwd_workspace(n, v, c, k);
+}
+
+size_t jetq_linear_distill_bwd_workspace_bytes(int64_t n, int64_t v, int64_t c, int64_t k, int smallest)
+{
+    if (n <= 0 || v <= 0 || c <= 0 || k <= 0 || k > 256)
+        return 0;
+    return smallest ? linear_distill_bwd_workspace_min(n, v, c, k) : linear_distill_bwd_workspace(n, v, c, k);
+}
+
+jetq_status jetq_linear_distill_fwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, const uint16_t *w,
+                                    int64_t v, int64_t ldw, const int64_t *ids, int64_t ldi, const float *teacher,
+                                    int64_t ldt, int64_t k, int renorm, float scale, float *loss, float *lse,
+                                    float *logp, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const jetq_status t = check_distill(ids, ldi, teacher, ldt, k, renorm, n);
+    if (t != JETQ_OK)
+        return t;
+    const jetq_status s = check_linear_ce(x, n, c, ldx, w, v, ldw, ids, scale);
+    if (s != JETQ_OK || n == 0)
+        return s;
+    JQ_REQUIRE(loss != nullptr && lse != nullptr && logp != nullptr && workspace != nullptr, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(workspace_bytes >= linear_distill_fwd_workspace(n, v, c, k), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(aligned16(workspace) && (reinterpret_cast<uintptr_t>(loss) & 3u) == 0 &&
+                   (reinterpret_cast<uintptr_t>(lse) & 3u) == 0 && (reinterpret_cast<uintptr_t>(logp) & 3u) == 0,
+               JETQ_ERR_MISALIGNED);
+    const jetq_status a = check_arch();
+    if (a != JETQ_OK)
+        return a;
+    LinearCeArgs g{x, n, c, ldx, w, v, ldw, nullptr, scale, loss, lse};
+    g.ws = workspace;
+    g.ws_bytes = workspace_bytes;
+    const DistillArgs d{ids, ldi, teacher, ldt, (int)k, renorm, logp};
+    return from_cuda(launch_linear_distill_fwd(g, d, static_cast<cudaStream_t>(stream)));
+}
+
+jetq_status jetq_linear_distill_bwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, const uint16_t *w,
+                                    int64_t v, int64_t ldw, const int64_t *ids, int64_t ldi, const float *teacher,
+                                    int64_t ldt, int64_t k, int renorm, float scale, const float *lse,
+                                    const float *logp, const float *dloss, uint16_t *dx, int64_t lddx, void *dw,
+                                    jetq_out_dtype dw_dtype, int64_t lddw, int accumulate, void *workspace,
+                                    size_t workspace_bytes, void *stream)
+{
+    const jetq_status t = check_distill(ids, ldi, teacher, ldt, k, renorm, n);
+    if (t != JETQ_OK)
+        return t;
+    const jetq_status s = check_linear_ce(x, n, c, ldx, w, v, ldw, ids, scale);
+    if (s != JETQ_OK)
+        return s;
+    if (n > 0) {
+        JQ_REQUIRE(logp != nullptr, JETQ_ERR_INVALID_ARG);
+        JQ_REQUIRE((reinterpret_cast<uintptr_t>(logp) & 3u) == 0, JETQ_ERR_MISALIGNED);
+    }
+    const DistillArgs d{ids, ldi, teacher, ldt, (int)k, renorm, const_cast<float *>(logp)};
+    return head_backward(x, n, c, ldx, w, v, ldw, nullptr, scale, lse, dloss, dx, lddx, dw, dw_dtype, lddw, accumulate,
+                         workspace, workspace_bytes, &d, stream);
 }
 
 namespace {

@@ -307,7 +307,36 @@ size_t linear_ce_fwd_workspace(int64_t n, int64_t v, int64_t c);
 size_t linear_ce_bwd_workspace(int64_t n, int64_t v, int64_t c);     // preferred
 size_t linear_ce_bwd_workspace_min(int64_t n, int64_t v, int64_t c); // one 256-row piece of the vocabulary
 cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st);
-cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st);
+// What the teacher is known by: k ids and logits or log-probabilities a row.
+struct DistillArgs {
+    const int64_t *ids;
+    int64_t ldi;
+    const float *teacher;
+    int64_t ldt;
+    int k, renorm;
+    float *logp; // [n][k], forward: out, backward: in
+};
+// t: null for the cross entropy; else loss of the distillation (a.target is not read)
+cudaError_t launch_linear_ce_bwd(LinearCeArgs a, const DistillArgs *t, cudaStream_t st);
+size_t linear_distill_fwd_workspace(int64_t n, int64_t v, int64_t c, int64_t k);
+size_t linear_distill_bwd_workspace(int64_t n, int64_t v, int64_t c, int64_t k);
+size_t linear_distill_bwd_workspace_min(int64_t n, int64_t v, int64_t c, int64_t k);
+cudaError_t launch_linear_distill_fwd(LinearCeArgs a, const DistillArgs &t, cudaStream_t st);
+
+// The distillation's own steps around the head's products (linear_distill.cu).
+struct GradRow;
+struct Listed { // an entry of d: its column (-1: none) and Q p - q
+    int id;
+    float d;
+};
+cudaError_t launch_distill_rows(const LinearCeArgs &a, const DistillArgs &t, uint16_t *copy, int64_t ldc, int bn,
+                                int parts, uint4 *skip, float2 *dots, cudaStream_t st);
+cudaError_t launch_distill_join(const LinearCeArgs &a, const DistillArgs &t, const float2 *part, int parts,
+                                const float2 *dots, cudaStream_t st);
+cudaError_t launch_distill_start(const LinearCeArgs &a, const DistillArgs &t, uint16_t *copy, int64_t ldc,
+                                 GradRow *rows, Listed *listed, float *gmax, cudaStream_t st);
+cudaError_t launch_distill_patch(const LinearCeArgs &a, const DistillArgs &t, const Listed *listed, const float *gmax,
+                                 uint16_t *d, int64_t ldd, int64_t col0, int64_t cols, cudaStream_t st);
 cudaError_t linear_ce_read_and_clear_error(cudaStream_t st, unsigned *out);
 
 // Clipped policy-gradient loss of packed sequences, forward (out, save

@@ -52,6 +52,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "head_rows.cuh"
 #include "jetq_internal.h"
 #include "ptx.cuh"
 
@@ -63,18 +64,22 @@ namespace {
 
 constexpr unsigned kErrTimeout = 1u;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kParts = 2; // the statistics epilogue's column slices of a tile
 
 enum HeadMode : int {
-    kStats = 0,   // softmax statistics of the logits
-    kGrad = 1,    // d in BF16
-    kGradX = 2,   // FP32 slabs of dx
-    kGradW16 = 3, // dw in BF16
-    kGradW32 = 4  // dw in FP32
+    kStats = 0,    // softmax statistics of the logits
+    kGrad = 1,     // d in BF16
+    kGradX = 2,    // FP32 slabs of dx
+    kGradW16 = 3,  // dw in BF16
+    kGradW32 = 4,  // dw in FP32
+    kStatsSkip = 5 // kStats without the columns that each row marks
 };
+
+__host__ __device__ constexpr bool is_stats(int mode)
+{
+    return mode == kStats || mode == kStatsSkip;
+}
 
 struct HeadParams {
     int mt, nt, splits, num_kb, group; // tiles of M and N, splits and 64-blocks of K, M tiles per raster group
@@ -83,22 +88,15 @@ struct HeadParams {
     int box_a, stages;                 // FEW: rows of A's box, ring stages of box_a rows of A and B's rows
     float k2;                          // scale * log2(e): exponents in base 2
     const int64_t *target;
+    const uint4 *skip;                 // kStatsSkip: a bit a column, [M][kParts * nt] of 128 columns each
     int fold;                          // kStats: 64-blocks of K summed inside the tensor core, see the epilogue
     int64_t V, col0;                   // whole vocabulary; first vocabulary row of this piece
     float2 *part;                      // [kParts * nt][M] (maximum, sum), base 2
-    const struct GradRow *rows;        // kGrad: [M]
+    const GradRow *rows;               // kGrad: [M]
     const float *gmax;
     float scale;
     int add;                           // FP32 output: add to what is there
     unsigned long long limit_ns;
-};
-
-// What d needs of a row, written by the backward pass's first kernel.
-struct alignas(16) GradRow {
-    int target; // -1: a row without a loss, the rest is zero
-    float lse2; // lse in base 2
-    float dloss;
-    float dt;   // exp(z_t - lse) - 1, from a logit that this row's own sum gives
 };
 
 // FEW: one tile of at most 128 rows by single CTAs.  A's box then holds those
@@ -114,31 +112,24 @@ struct HeadCfg {
     static constexpr int kStage = kABytes + kBBytes;
     // Epilogue: 16 warps of 64 columns a thread for d and the gradients; 8 warps of 128 for the statistics,
     // whose threads hold their columns' sums (4 to 10% faster forward than 16 warps of 64, except at c = 256).
-    static constexpr int kEpiWarps = MODE == kStats ? 8 : 16;
-    static constexpr int kCols = MODE == kStats ? 128 : 64;
+    static constexpr int kEpiWarps = is_stats(MODE) ? 8 : 16;
+    static constexpr int kCols = is_stats(MODE) ? 128 : 64;
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
-    static constexpr bool kStaging = MODE != kStats;
+    static constexpr bool kStaging = !is_stats(MODE);
     static constexpr size_t kStagingBytes = kStaging ? kEpiWarps * 4096 : 0; // a 4 KB box a warp
     static constexpr int kStages = FEW ? 12 : (int)((225 * 1024 - kStagingBytes) / kStage); // FEW: at most
     static constexpr size_t kTileBytes = FEW ? 225 * 1024 - kStagingBytes : (size_t)kStages * kStage;
     static constexpr size_t kSmem = 1024 + kTileBytes + kStagingBytes + 256;
     static constexpr bool kAMn = MODE == kGradW16 || MODE == kGradW32; // A's M axis contiguous
-    static constexpr bool kBMn = MODE >= kGradX;                       // B's N axis contiguous
+    static constexpr bool kBMn = kAMn || MODE == kGradX;               // B's N axis contiguous
     // register split of the statistics: producer warps, epilogue warps
-    static constexpr bool kRegSplit = MODE == kStats;
+    static constexpr bool kRegSplit = is_stats(MODE);
     static constexpr int kRegProducer = 72, kRegEpilogue = 216;
     static constexpr int kBars = 2 * kStages + 5;
     static_assert(kBars * 8 + 8 <= 256, "barrier area");
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(!FEW || (CG == 1 && !kAMn), "one tile of rows, K-major");
 };
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Raster: groups of `group` M tiles; inside a group N tiles in turn, M tiles
 // fastest; K splits slowest, so that concurrent tiles read the same K range.
@@ -180,7 +171,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
     const int unit = blockIdx.x / CG, units = gridDim.x / CG;
     unsigned *err = &g_linear_ce_error;
     const int num_tiles = p.mt * p.nt * p.splits;
-    const int bn = MODE == kStats ? p.bn : C::BN;
+    const int bn = is_stats(MODE) ? p.bn : C::BN;
     const int S = FEW ? p.stages : C::kStages;
     const uint32_t a_bytes = FEW ? (uint32_t)p.box_a * 128u : (uint32_t)C::kABytes;
     const uint32_t stage_bytes =
@@ -227,7 +218,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
         if (warp == 0 && lane == 0) {
             // -------------------------------------------------- TMA producer
             const uint32_t tx =
-                FEW ? stage_bytes : (MODE == kStats ? (uint32_t)(CG * 128 + bn) * 128u : (uint32_t)(CG * C::kStage));
+                FEW ? stage_bytes : (is_stats(MODE) ? (uint32_t)(CG * 128 + bn) * 128u : (uint32_t)(CG * C::kStage));
             int s = 0;
             uint32_t ph = 0; // of the ring's pass
             uint32_t it = 0;
@@ -290,7 +281,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                     continue;
                 for (int kb = k0; kb < k1; ++tc) {
                     const uint32_t b = tc & 1u;
-                    const int stop = MODE == kStats && k1 - kb > p.fold ? kb + p.fold : k1;
+                    const int stop = is_stats(MODE) && k1 - kb > p.fold ? kb + p.fold : k1;
                     if (!ptx::mbar_wait<CG == 2>(acc_empty(b), ((tc >> 1) & 1u) ^ 1u, abort_flag, err, kErrTimeout,
                                                  p.limit_ns)) {
                         ok = false;
@@ -330,7 +321,7 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
         // ------------------------------------------------------ epilogue: a row and kCols columns a thread
         const int ew = warp - 4, quarter = warp & 3, part = ew >> 2;
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-        if constexpr (MODE == kStats) {
+        if constexpr (is_stats(MODE)) {
             uint32_t tc = 0;
             for (int t = unit; t < num_tiles; t += units) {
                 int mi, ni, ks;
@@ -339,7 +330,11 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                 const int64_t row = (int64_t)row0 + lane;
                 const int n0 = ni * bn + part * 128;
                 int tcol = -1; // the target's column in this thread's 128, or out of range
-                if (row < p.M) {
+                uint4 skip = make_uint4(0, 0, 0, 0);
+                if (MODE == kStatsSkip) {
+                    if (row < p.M)
+                        skip = __ldg(p.skip + row * (kParts * p.nt) + kParts * ni + part);
+                } else if (row < p.M) {
                     const int64_t tg = __ldg(p.target + row), rel = tg - n0;
                     if (tg >= 0 && tg < p.V && rel >= 0 && rel < min(128, bn - part * 128))
                         tcol = (int)rel;
@@ -416,7 +411,15 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
                     m4[j & 3] = fmaxf(m4[j & 3], v[j]);
                 const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 const float mk = m == -INFINITY ? 0.0f : m * p.k2; // without a number: NaN still reaches the sum
-                if (__any_sync(0xFFFFFFFFu, tcol >= 0)) { // the target's term is joined exactly by the last kernel
+                if constexpr (MODE == kStatsSkip) { // these terms are joined exactly by the last kernel
+                    const uint32_t bits[4] = {skip.x, skip.y, skip.z, skip.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (__any_sync(0xFFFFFFFFu, bits[q] != 0u))
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[32 * q + j] = bits[q] >> j & 1u ? -INFINITY : v[32 * q + j];
+                } else if (__any_sync(0xFFFFFFFFu, tcol >= 0)) { // the target's term is joined exactly by the last kernel
 #pragma unroll
                     for (int j = 0; j < 128; ++j)
                         v[j] = j == tcol ? -INFINITY : v[j];
@@ -603,40 +606,6 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
         ptx::tc_fence_after();
         ptx::tmem_dealloc_cg<CG>(tmem_base, 512);
     }
-}
-
-__device__ __forceinline__ void join_pair(float2 &a, const float2 b)
-{
-    const float m = fmaxf(a.x, b.x);
-    if (m > -INFINITY)
-        a = make_float2(m, a.y * ex2(a.x - m) + b.y * ex2(b.x - m));
-    else
-        a.y += b.y; // both empty (or NaN)
-}
-
-// s + b as s + c, exactly (Knuth's two-sum), c added to the compensation.
-__device__ __forceinline__ void two_sum(float &s, float &c, float b)
-{
-    const float t = __fadd_rn(s, b), u = __fsub_rn(t, s);
-    c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(b, u)));
-    s = t;
-}
-
-// Eight products of BF16 pairs (exact in FP32) added to s + c.
-__device__ __forceinline__ void dot8(float &s, float &c, const uint4 &a, const uint4 &b)
-{
-    const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        two_sum(s, c, __fmul_rn(__uint_as_float(p[e] << 16), __uint_as_float(q[e] << 16)));
-        two_sum(s, c, __fmul_rn(__uint_as_float(p[e] & 0xffff0000u), __uint_as_float(q[e] & 0xffff0000u)));
-    }
-}
-
-// The sum s + c; an infinite one has no rest.
-__device__ __forceinline__ double whole_sum(float s, float c)
-{
-    return c == c ? (double)s + (double)c : (double)s;
 }
 
 // Joins the (maximum, sum) pairs of a row and its target's logit.  blockDim =
@@ -970,10 +939,11 @@ cudaError_t start(LinearCeArgs &a, void *at, GradRow *rows, float *gmax, cudaStr
 struct BwdPlan {
     int64_t piece; // vocabulary rows a piece (a multiple of 256)
     int dx_cg, splits;
-    size_t rows_off, x_off, slab_off, d_off, total;
+    size_t rows_off, x_off, listed_off, slab_off, d_off, total;
 };
 
-BwdPlan bwd_plan(int64_t n, int64_t v, int64_t c, int64_t piece)
+// k: listed entries a row (distillation; else 0)
+BwdPlan bwd_plan(int64_t n, int64_t v, int64_t c, int64_t k, int64_t piece)
 {
     BwdPlan b;
     const int64_t all = ceil_div(v, 256) * 256;
@@ -981,7 +951,8 @@ BwdPlan bwd_plan(int64_t n, int64_t v, int64_t c, int64_t piece)
     dx_shape(n, c, b.piece, b.dx_cg, b.splits);
     b.rows_off = 1024; // gmax first
     b.x_off = b.rows_off + ((size_t)n * sizeof(GradRow) + 1023) / 1024 * 1024;
-    b.slab_off = b.x_off + lines_bytes(n, c);
+    b.listed_off = b.x_off + lines_bytes(n, c);
+    b.slab_off = b.listed_off + ((size_t)n * (size_t)k * sizeof(Listed) + 1023) / 1024 * 1024;
     const size_t slabs = (size_t)b.splits * (size_t)n * (size_t)c * 4;
     b.d_off = (b.slab_off + slabs + 1023) / 1024 * 1024;
     b.total = b.d_off + (size_t)n * (size_t)b.piece * 2;
@@ -1009,32 +980,57 @@ size_t linear_ce_fwd_workspace(int64_t n, int64_t v, int64_t c)
 
 size_t linear_ce_bwd_workspace(int64_t n, int64_t v, int64_t c)
 {
-    return bwd_plan(n, v, c, preferred_piece(n)).total;
+    return linear_distill_bwd_workspace(n, v, c, 0);
 }
 
 size_t linear_ce_bwd_workspace_min(int64_t n, int64_t v, int64_t c)
 {
-    return bwd_plan(n, v, c, 256).total;
+    return linear_distill_bwd_workspace_min(n, v, c, 0);
 }
 
-cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
+size_t linear_distill_bwd_workspace(int64_t n, int64_t v, int64_t c, int64_t k)
 {
-    cudaError_t e;
-    if (fwd_lines(a.n, a.c) > 0 && (a.ldx % 64 != 0 || (reinterpret_cast<uintptr_t>(a.x) & 127u) != 0) &&
-        (e = start(a, a.ws, nullptr, nullptr, st)) != cudaSuccess)
-        return e;
-    HeadParams p = {};
-    p.nt = (int)ceil_div(a.v, kTileN);
-    const int cg = pick_cg(a.n, p.nt);
-    p.bn = kTileN;
-    p.box_a = box_rows(a.n);
-    if (cg == 1 && a.n <= 128) {
+    return bwd_plan(n, v, c, k, preferred_piece(n)).total;
+}
+
+size_t linear_distill_bwd_workspace_min(int64_t n, int64_t v, int64_t c, int64_t k)
+{
+    return bwd_plan(n, v, c, k, 256).total;
+}
+
+namespace {
+
+// The forward product's geometry: CTAs a tile, its columns and their number.
+struct StatsShape {
+    int cg, bn, nt;
+};
+
+StatsShape stats_shape(int64_t n, int64_t v)
+{
+    StatsShape s;
+    s.nt = (int)ceil_div(v, kTileN);
+    s.cg = pick_cg(n, s.nt);
+    s.bn = kTileN;
+    if (s.cg == 1 && n <= 128) {
         // One row tile: the weight's stream is what takes time, so its rows are
         // spread evenly over the SMs (a multiple of 16 a tile).
-        const int64_t waves = ceil_div(p.nt, units_of(1));
-        p.bn = (int)(ceil_div(ceil_div(a.v, waves * units_of(1)), 16) * 16);
-        p.nt = (int)ceil_div(a.v, p.bn);
+        const int64_t waves = ceil_div(s.nt, units_of(1));
+        s.bn = (int)(ceil_div(ceil_div(v, waves * units_of(1)), 16) * 16);
+        s.nt = (int)ceil_div(v, s.bn);
     }
+    return s;
+}
+
+// The statistics of the logits, a.x in the rows that the product reads.
+template <int MODE>
+cudaError_t run_stats(const LinearCeArgs &a, const StatsShape &shape, float2 *part, const uint4 *skip, cudaStream_t st)
+{
+    HeadParams p = {};
+    const int cg = shape.cg;
+    p.nt = shape.nt;
+    p.bn = shape.bn;
+    p.box_a = box_rows(a.n);
+    cudaError_t e;
     CUtensorMap ta, tb;
     if ((e = make_sw128_map(&ta, a.x, false, a.c, a.n, a.ldx, p.box_a)) != cudaSuccess ||
         (e = make_sw128_map(&tb, a.w, false, a.c, a.v, a.ldw, p.bn / cg)) != cudaSuccess)
@@ -1047,39 +1043,97 @@ cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
     p.N = a.v;
     p.k2 = a.scale * kLog2e;
     p.target = a.target;
+    p.skip = skip;
     // The error of a loss grows with the steps of a partial tile.  Pairs: 8 blocks (1.2e-7 in the 2-norm over
     // 4096 tokens, an FP32 matrix product has 6.7e-7; 4096 x 131072 x 4096 took 2.65 ms with 8, 2.97 with 4 and
     // 4.03 with 2, whose hand-overs between the CTAs stall the tensor core).  Single CTAs: 4 (1e-7; 2 us less than
     // with 2 at 333 tokens x 50257 x 2048, 66 in all, and 3 us less at one token x 1000 x 4096).
     p.fold = cg == 2 ? 8 : 4;
     p.V = a.v;
-    p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + fwd_lines(a.n, a.c));
-    if ((e = run_head<kStats>(cg, ta, tb, ta, p, st)) != cudaSuccess)
+    p.part = part;
+    return run_head<MODE>(cg, ta, tb, ta, p, st);
+}
+
+// Whether the forward product reads a copy of x.
+bool copies_x(const LinearCeArgs &a)
+{
+    return fwd_lines(a.n, a.c) > 0 && (a.ldx % 64 != 0 || (reinterpret_cast<uintptr_t>(a.x) & 127u) != 0);
+}
+
+} // namespace
+
+cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
+{
+    cudaError_t e;
+    if (copies_x(a) && (e = start(a, a.ws, nullptr, nullptr, st)) != cudaSuccess)
         return e;
-    const int parts = kParts * p.nt;
+    const StatsShape shape = stats_shape(a.n, a.v);
+    float2 *part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + fwd_lines(a.n, a.c));
+    if ((e = run_stats<kStats>(a, shape, part, nullptr, st)) != cudaSuccess)
+        return e;
+    const int parts = kParts * shape.nt;
     int rx = 1, ry = 1;
     while (rx < 8 && rx < a.n)
         rx *= 2;
     while (rx * ry < 1024 && ry < parts)
         ry *= 2;
     const dim3 grid((unsigned)ceil_div(a.n, rx)), block(rx, ry);
-    return launch_pdl(k_ce_join, grid, block, 0, st, (const float2 *)p.part, a.x, a.ldx, a.w, a.ldw, a.c, a.target, a.n,
-                      a.v, parts, a.scale, p.k2, a.loss, a.lse);
+    return launch_pdl(k_ce_join, grid, block, 0, st, (const float2 *)part, a.x, a.ldx, a.w, a.ldw, a.c, a.target, a.n,
+                      a.v, parts, a.scale, a.scale * kLog2e, a.loss, a.lse);
 }
 
-cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st)
+size_t linear_distill_fwd_workspace(int64_t n, int64_t v, int64_t c, int64_t k)
+{
+    const size_t parts = linear_ce_fwd_workspace(n, v, c) - fwd_lines(n, c); // the pairs, and 4 bytes a row
+    return fwd_lines(n, c) + (parts + 15) / 16 * 16 + 2 * parts + (size_t)n * (size_t)k * sizeof(float2);
+}
+
+// Marks and logits of the listed columns, the statistics of all others, and their join.
+cudaError_t launch_linear_distill_fwd(LinearCeArgs a, const DistillArgs &t, cudaStream_t st)
+{
+    const StatsShape shape = stats_shape(a.n, a.v);
+    const int parts = kParts * shape.nt;
+    uint8_t *ws = static_cast<uint8_t *>(a.ws) + fwd_lines(a.n, a.c);
+    float2 *part = reinterpret_cast<float2 *>(ws);
+    const size_t pairs = (size_t)parts * (size_t)a.n * sizeof(float2);
+    uint4 *skip = reinterpret_cast<uint4 *>(ws + (pairs + 15) / 16 * 16);
+    float2 *dots = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(skip) + 2 * pairs);
+    uint16_t *copy = copies_x(a) ? static_cast<uint16_t *>(a.ws) : nullptr;
+    cudaError_t e = launch_distill_rows(a, t, copy, lines_ld(a.c), shape.bn, parts, skip, dots, st);
+    if (e != cudaSuccess)
+        return e;
+    if (copy) {
+        a.x = copy;
+        a.ldx = lines_ld(a.c);
+    }
+    if ((e = run_stats<kStatsSkip>(a, shape, part, skip, st)) != cudaSuccess)
+        return e;
+    return launch_distill_join(a, t, part, parts, dots, st);
+}
+
+cudaError_t launch_linear_ce_bwd(LinearCeArgs a, const DistillArgs *t, cudaStream_t st)
 {
     // the largest piece that the workspace holds, up to the preferred one
-    BwdPlan plan = bwd_plan(a.n, a.v, a.c, preferred_piece(a.n));
+    const int64_t k = t ? t->k : 0;
+    BwdPlan plan = bwd_plan(a.n, a.v, a.c, k, preferred_piece(a.n));
     while (plan.total > a.ws_bytes && plan.piece > 256)
-        plan = bwd_plan(a.n, a.v, a.c, plan.piece / 2);
+        plan = bwd_plan(a.n, a.v, a.c, k, plan.piece / 2);
     if (plan.total > a.ws_bytes)
         return cudaErrorInvalidValue;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     float *gmax = reinterpret_cast<float *>(ws), *slab = reinterpret_cast<float *>(ws + plan.slab_off);
     uint16_t *d = reinterpret_cast<uint16_t *>(ws + plan.d_off);
     GradRow *grad_rows = reinterpret_cast<GradRow *>(ws + plan.rows_off);
-    cudaError_t e = start(a, ws + plan.x_off, grad_rows, gmax, st);
+    Listed *listed = reinterpret_cast<Listed *>(ws + plan.listed_off);
+    cudaError_t e;
+    if (t) {
+        uint16_t *copy = reinterpret_cast<uint16_t *>(ws + plan.x_off);
+        e = launch_distill_start(a, *t, copy, lines_ld(a.c), grad_rows, listed, gmax, st);
+        a.x = copy;
+        a.ldx = lines_ld(a.c);
+    } else {
+        e = start(a, ws + plan.x_off, grad_rows, gmax, st);
+    }
     if (e != cudaSuccess)
         return e;
     const bool dw16 = a.dw_dtype == JETQ_OUT_BF16;
@@ -1118,6 +1172,9 @@ cudaError_t launch_linear_ce_bwd(LinearCeArgs a, cudaStream_t st)
         p.col0 = v0;
         p.rows = grad_rows;
         if ((e = run_head<kGrad>(cg, xk, wk, dst, p, st)) != cudaSuccess)
+            return e;
+        // the listed columns' entries, where both of d's terms meet
+        if (t && (e = launch_distill_patch(a, *t, listed, gmax, d, plan.piece, v0, rows, st)) != cudaSuccess)
             return e;
         // dx += d w
         p.mt = (int)ceil_div(a.n, 128 * plan.dx_cg);

@@ -84,3 +84,67 @@ def test_policy_loss_helper_checks_its_tensors():
         jq.policy_loss(cpu, cpu, cpu)
     with pytest.raises(ValueError):
         jq.policy_loss_bwd(cpu, cpu, cpu, None, None)
+
+
+# ------------------------------------------------------------------ distillation
+
+def _distill(L, back, **k):
+    a = dict(x=FAKE, n=4, c=64, ldx=64, w=FAKE, v=300, ldw=64, ids=FAKE, ldi=8, t=FAKE, ldt=8, k=8, renorm=1,
+             scale=1.0, loss=FAKE, lse=FAKE, logp=FAKE, dloss=FAKE, dx=FAKE, lddx=64, dw=FAKE, dt=0, lddw=64, acc=0,
+             ws=FAKE, bytes=BIG)
+    a.update(k)
+    common = (a["x"], a["n"], a["c"], a["ldx"], a["w"], a["v"], a["ldw"], a["ids"], a["ldi"], a["t"], a["ldt"], a["k"],
+              a["renorm"], F(a["scale"]))
+    if back:
+        return L.jetq_linear_distill_bwd(*common, a["lse"], a["logp"], a["dloss"], a["dx"], a["lddx"], a["dw"],
+                                         a["dt"], a["lddw"], a["acc"], a["ws"], ctypes.c_size_t(a["bytes"]), None)
+    return L.jetq_linear_distill_fwd(*common, a["loss"], a["lse"], a["logp"], a["ws"], ctypes.c_size_t(a["bytes"]),
+                                     None)
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("change,status", [
+    (dict(n=-1), INVALID), (dict(v=0), INVALID), (dict(c=0), INVALID), (dict(k=0), INVALID), (dict(x=None), INVALID),
+    (dict(w=None), INVALID), (dict(ids=None), INVALID), (dict(t=None), INVALID), (dict(renorm=2), INVALID),
+    (dict(lse=None), INVALID), (dict(logp=None), INVALID), (dict(ws=None), INVALID), (dict(bytes=100), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=NAN), INVALID),
+    (dict(c=60), SHAPE), (dict(ldx=56), SHAPE), (dict(ldw=56), SHAPE), (dict(k=257, ldi=300, ldt=300), SHAPE),
+    (dict(ldi=7), SHAPE), (dict(ldt=7), SHAPE), (dict(v=1 << 31), SHAPE), (dict(n=1 << 31), SHAPE),
+    (dict(x=P(4104)), ALIGN), (dict(w=P(4104)), ALIGN), (dict(ids=P(4100)), ALIGN), (dict(t=P(4098)), ALIGN),
+    (dict(ws=P(4104)), ALIGN), (dict(logp=P(4098)), ALIGN),
+])
+def test_distillation_refuses(L, back, change, status):
+    assert _distill(L, back, **change) == status
+
+
+@pytest.mark.parametrize("change,status", [(dict(dloss=None), INVALID), (dict(dx=None), INVALID),
+                                           (dict(dw=None), INVALID), (dict(acc=1, dt=1), INVALID),
+                                           (dict(lddx=56), SHAPE), (dict(lddw=66), ALIGN), (dict(dx=P(4104)), ALIGN)])
+def test_distillation_backward_refuses(L, change, status):
+    assert _distill(L, True, **change) == status
+
+
+def test_distillation_of_no_rows(L):
+    assert _distill(L, False, n=0, x=None, ids=None, t=None, loss=None, lse=None, logp=None, ws=None, bytes=0) == OK
+
+
+def test_distillation_workspaces(L):
+    size, back = L.jetq_linear_distill_workspace_bytes, L.jetq_linear_distill_bwd_workspace_bytes
+    for f in (size, lambda *a: back(*a, 0), lambda *a: back(*a, 1)):
+        assert f(0, 300, 64, 8) == f(4, 300, 64, 0) == f(4, 300, 64, 257) == 0
+    # the cross entropy's, a bit a logit, 8 bytes an entry
+    more = size(4096, 131072, 4096, 64) - L.jetq_linear_ce_workspace_bytes(4096, 131072, 4096)
+    assert 4096 * 131072 // 8 + 4096 * 64 * 8 <= more <= 4096 * 131072 // 8 + 4096 * 64 * 8 + (1 << 16)
+    assert back(4096, 131072, 4096, 64, 1) < back(4096, 131072, 4096, 64, 0)
+    entries = back(4096, 131072, 4096, 64, 0) - L.jetq_linear_ce_bwd_workspace_bytes(4096, 131072, 4096, 0)
+    assert entries == 4096 * 64 * 8
+
+
+def test_distillation_helper_checks_its_tensors():
+    import rollout_x128_act_gb300 as jq
+
+    x, i, t = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((4, 8), dtype=torch.int64), torch.zeros((4, 8))
+    with pytest.raises(ValueError):
+        jq.linear_distill(x, x, i, t)
+    with pytest.raises(ValueError):
+        jq.linear_distill_bwd(x, x, i, t, t[:, 0], t, t[:, 0])
