@@ -713,6 +713,8 @@ jetq_status head_backward(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, 
         JQ_REQUIRE(aligned16(dx) && lddx % 8 == 0 && aligned16(workspace) &&
                        (reinterpret_cast<uintptr_t>(lse) & 3u) == 0 && (reinterpret_cast<uintptr_t>(dloss) & 3u) == 0,
                    JETQ_ERR_MISALIGNED);
+        JQ_REQUIRE(workspace_bytes >= linear_distill_bwd_workspace_min(n, v, c, t ? t->k : 0),
+                   JETQ_ERR_INVALID_ARG);
     }
     const jetq_status a = check_arch();
     if (a != JETQ_OK)
@@ -724,7 +726,6 @@ jetq_status head_backward(const uint16_t *x, int64_t n, int64_t c, int64_t ldx, 
         const size_t es = dw_dtype == JETQ_OUT_F32 ? 4 : 2;
         return from_cuda(cudaMemset2DAsync(dw, (size_t)lddw * es, 0, (size_t)c * es, (size_t)v, st));
     }
-    JQ_REQUIRE(workspace_bytes >= linear_distill_bwd_workspace_min(n, v, c, t ? t->k : 0), JETQ_ERR_INVALID_ARG);
     LinearCeArgs g{x, n, c, ldx, w, v, ldw, target, scale, nullptr, const_cast<float *>(lse)};
     g.dloss = dloss;
     g.dx = dx;
