@@ -98,6 +98,9 @@ def lib() -> ctypes.CDLL:
             "jetq_linear_distill_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64, I32]),
             "jetq_linear_distill_bwd": (I32, [P, I64, I64, I64, P, I64, I64, P, I64, P, I64, I64, I32, F32, P, P, P, P,
                                               I64, P, I32, I64, I32, P, ctypes.c_size_t, P]),
+            "jetq_moe_nvfp4_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64]),
+            "jetq_moe_nvfp4": (I32, [P, I64, I64, I64, P, I64, I64, I64, I32, P, P, P, I64, P, P, P, P, I32, I64, P, P,
+                                     P, ctypes.c_size_t, P]),
             "jetq_policy_loss_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
             "jetq_policy_loss_fwd": (I32, [P, P, P, P, I32, P, I64, P, I64, I32, I32, F32, F32, F32, F32, F32, P, P, P,
                                            ctypes.c_size_t, P]),
@@ -319,6 +322,18 @@ def jetq_gemv_nvfp4(qw, sbw, sgw, x, y, stream=None):
     m, k = x.shape
     _check(lib().jetq_gemv_nvfp4(_p(qw), _p(sbw), _p(sgw), qw.shape[0], k, _p(x), m, x.stride(0), _p(y),
                                  _out_dtype(y), y.stride(0), _s(stream)), "jetq_gemv_nvfp4")
+
+
+def jetq_moe_nvfp4_workspace_bytes(m: int, num_experts: int, inter: int, topk: int) -> int:
+    return int(lib().jetq_moe_nvfp4_workspace_bytes(m, num_experts, inter, topk))
+
+
+def jetq_moe_nvfp4(x, router, topk, renorm, q13, sb13, sg13, q2, sb2, sg2, y, ids, weights, ws, stream=None):
+    m, h = x.shape
+    _check(lib().jetq_moe_nvfp4(_p(x), m, h, x.stride(0), _p(router), router.stride(0), router.shape[0], topk,
+                                1 if renorm else 0, _p(q13), _p(sb13), _p(sg13), q13.shape[1] // 2, _p(q2), _p(sb2),
+                                _p(sg2), _p(y), _out_dtype(y), y.stride(0), _p(ids), _p(weights), _p(ws), _bytes(ws),
+                                _s(stream)), "jetq_moe_nvfp4")
 
 
 def jetq_norm_fwd(kind, x, w, b, eps, y, mean, rstd, stream=None):
@@ -660,6 +675,55 @@ def gemv_nvfp4(x, b, out_dtype=torch.float32, stream=None):
     y = torch.empty((m, n), dtype=out_dtype, device=x.device)
     jetq_gemv_nvfp4(q, sb, sg, x, y)
     return y
+
+
+def quant_nvfp4_experts(w, stream=None):
+    """NVFP4 copies of stacked expert weights, BF16 w [e x r x c], a tensor scope each:
+    dict(q [e x r x c/2] u8, sb [e x r x c/16] u8, sg [e] f32), as moe_nvfp4 takes them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quant_nvfp4_experts(w)
+    e, r, c = w.shape
+    out = dict(q=torch.empty((e, r, c // 2), dtype=torch.uint8, device=w.device),
+               sb=torch.empty((e, r, c // 16), dtype=torch.uint8, device=w.device),
+               sg=torch.empty(e, dtype=torch.float32, device=w.device))
+    for i in range(e):
+        jetq_quant_nvfp4(w[i], out["q"][i], out["sb"][i], out["sg"][i:i + 1], amax_bf16(w[i]))
+    return out
+
+
+def moe_nvfp4(x, router, w13, w2, topk, renorm=True, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """Mixture-of-experts layer for up to 16 tokens (see jetq_moe_nvfp4): BF16 x [m x h], router [e x h], NVFP4
+    dicts (as quant_nvfp4_experts makes them) w13 of [e x 2i x h], gate rows before up rows, and w2 of [e x h x i]
+    -> (y [m x h], ids int64 [m x topk], p [m x topk])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_nvfp4(x, router, w13, w2, topk, renorm, out_dtype, workspace)
+    _want(x, "x", torch.bfloat16, rows=True)
+    _want(router, "router", torch.bfloat16, rows=True)
+    (m, h), e = x.shape, router.shape[0]
+    if router.shape[1] != h:
+        raise ValueError(f"x and router: widths {h} and {router.shape[1]}")
+    q13, sb13, sg13, q2, sb2, sg2 = w13["q"], w13["sb"], w13["sg"], w2["q"], w2["sb"], w2["sg"]
+    i = q2.shape[-1] * 2
+    _want(q13, "w13['q']", torch.uint8, (e, 2 * i, h // 2))
+    _want(sb13, "w13['sb']", torch.uint8, (e, 2 * i, h // 16))
+    _want(sg13, "w13['sg']", torch.float32, (e,))
+    _want(q2, "w2['q']", torch.uint8, (e, h, i // 2))
+    _want(sb2, "w2['sb']", torch.uint8, (e, h, i // 16))
+    _want(sg2, "w2['sg']", torch.float32, (e,))
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype: {out_dtype} is neither BF16 nor FP32")
+    _one_device(x, router=router, q13=q13, sb13=sb13, sg13=sg13, q2=q2, sb2=sb2, sg2=sg2, workspace=workspace)
+    y = torch.empty((m, h), dtype=out_dtype, device=x.device)
+    ids = torch.empty((m, topk), dtype=torch.int64, device=x.device)
+    p = torch.empty((m, topk), dtype=torch.float32, device=x.device)
+    need = jetq_moe_nvfp4_workspace_bytes(m, e, i, topk)
+    if workspace is None or _bytes(workspace) < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    jetq_moe_nvfp4(_row_stride(x), _row_stride(router), topk, renorm, q13, sb13, sg13, q2, sb2, sg2, y, ids, p,
+                   workspace)
+    return y, ids, p
 
 
 _NORM_DTYPES = (torch.bfloat16, torch.float32)

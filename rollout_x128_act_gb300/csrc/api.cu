@@ -1054,4 +1054,46 @@ jetq_status jetq_policy_loss_bwd(const float *nll, const float *nll_old, const f
     return from_cuda(launch_policy_bwd(g, static_cast<cudaStream_t>(stream)));
 }
 
+size_t jetq_moe_nvfp4_workspace_bytes(int64_t m, int64_t num_experts, int64_t inter, int64_t topk)
+{
+    if (m <= 0 || m > 16 || num_experts <= 0 || num_experts > 256 || inter <= 0 || inter > (1 << 20) || topk <= 0 ||
+        topk > 16)
+        return 0;
+    return moe_nvfp4_workspace(m, num_experts, inter, topk);
+}
+
+jetq_status jetq_moe_nvfp4(const uint16_t *x, int64_t m, int64_t h, int64_t ldx, const uint16_t *router, int64_t ldr,
+                           int64_t num_experts, int64_t topk, int renorm, const uint8_t *q13, const uint8_t *sb13,
+                           const float *sg13, int64_t inter, const uint8_t *q2, const uint8_t *sb2, const float *sg2,
+                           void *y, jetq_out_dtype y_dtype, int64_t ldy, int64_t *ids, float *weights, void *workspace,
+                           size_t workspace_bytes, void *stream)
+{
+    JQ_REQUIRE(m >= 0 && h > 0 && inter > 0 && num_experts > 0 && topk > 0, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(renorm == 0 || renorm == 1, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(y_dtype == JETQ_OUT_F32 || y_dtype == JETQ_OUT_BF16, JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(m <= 16 && num_experts <= 256 && topk <= 16 && topk <= num_experts && h % 32 == 0 && inter % 32 == 0 &&
+                   h <= (1 << 20) && inter <= (1 << 20) && ldx >= h && ldr >= h && ldy >= h,
+               JETQ_ERR_UNSUPPORTED_SHAPE);
+    JQ_REQUIRE(ldx <= ((int64_t)1 << 36) && ldr <= ((int64_t)1 << 36) && ldy <= ((int64_t)1 << 36),
+               JETQ_ERR_UNSUPPORTED_SHAPE);
+    if (m == 0)
+        return JETQ_OK;
+    JQ_REQUIRE(x != nullptr && router != nullptr && q13 != nullptr && sb13 != nullptr && sg13 != nullptr &&
+                   q2 != nullptr && sb2 != nullptr && sg2 != nullptr && y != nullptr && workspace != nullptr,
+               JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(workspace_bytes >= moe_nvfp4_workspace(m, num_experts, inter, topk), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(aligned16(x) && ldx % 8 == 0 && aligned16(router) && ldr % 8 == 0 && aligned16(q13) && aligned16(q2) &&
+                   ((reinterpret_cast<uintptr_t>(sb13) | reinterpret_cast<uintptr_t>(sb2)) & 1u) == 0 &&
+                   aligned4(sg13) && aligned4(sg2) && aligned16(workspace) &&
+                   (reinterpret_cast<uintptr_t>(y) & (y_dtype == JETQ_OUT_F32 ? 3u : 1u)) == 0 &&
+                   (reinterpret_cast<uintptr_t>(ids) & 7u) == 0 && aligned4(weights),
+               JETQ_ERR_MISALIGNED);
+    const jetq_status a = check_arch();
+    if (a != JETQ_OK)
+        return a;
+    const MoeNvfp4Args g{x, m, h, ldx, router, ldr, num_experts, topk, renorm, q13, sb13, sg13, inter, q2, sb2, sg2,
+                         y, y_dtype, ldy, ids, weights, workspace};
+    return from_cuda(launch_moe_nvfp4(g, static_cast<cudaStream_t>(stream)));
+}
+
 } // extern "C"

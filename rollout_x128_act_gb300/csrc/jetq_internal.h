@@ -260,6 +260,28 @@ struct GemvNvfp4Args {
 };
 cudaError_t launch_gemv_nvfp4(const GemvNvfp4Args &a, cudaStream_t st);
 
+// A mixture-of-experts layer for 1 <= m <= 16 tokens: router, NVFP4 gate/up and down.
+struct MoeNvfp4Args {
+    const uint16_t *x;
+    int64_t m, h, ldx;
+    const uint16_t *router;
+    int64_t ldr, experts, topk;
+    int renorm;
+    const uint8_t *q13, *sb13;
+    const float *sg13;
+    int64_t inter;
+    const uint8_t *q2, *sb2;
+    const float *sg2;
+    void *y;
+    jetq_out_dtype out_dtype;
+    int64_t ldy;
+    int64_t *ids;   // nullable
+    float *weights; // nullable
+    void *ws;
+};
+size_t moe_nvfp4_workspace(int64_t m, int64_t experts, int64_t inter, int64_t topk);
+cudaError_t launch_moe_nvfp4(const MoeNvfp4Args &a, cudaStream_t st);
+
 // Layer norm / RMS norm of rows [n x c], forward (out = y; mean and rstd
 // written) and backward (out = dx; dw, db).
 struct NormArgs {

@@ -148,3 +148,51 @@ def test_distillation_helper_checks_its_tensors():
         jq.linear_distill(x, x, i, t)
     with pytest.raises(ValueError):
         jq.linear_distill_bwd(x, x, i, t, t[:, 0], t, t[:, 0])
+
+
+# ------------------------------------------------------------------ mixture of experts
+
+def _moe(L, **k):
+    a = dict(x=FAKE, m=4, h=64, ldx=64, router=FAKE, ldr=64, e=8, topk=2, renorm=1, q13=FAKE, sb13=FAKE, sg13=FAKE,
+             i=32, q2=FAKE, sb2=FAKE, sg2=FAKE, y=FAKE, dt=1, ldy=64, ids=FAKE, p=FAKE, ws=FAKE, bytes=BIG)
+    a.update(k)
+    return L.jetq_moe_nvfp4(a["x"], a["m"], a["h"], a["ldx"], a["router"], a["ldr"], a["e"], a["topk"], a["renorm"],
+                            a["q13"], a["sb13"], a["sg13"], a["i"], a["q2"], a["sb2"], a["sg2"], a["y"], a["dt"],
+                            a["ldy"], a["ids"], a["p"], a["ws"], ctypes.c_size_t(a["bytes"]), None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(m=-1), INVALID), (dict(h=0), INVALID), (dict(i=0), INVALID), (dict(e=0), INVALID), (dict(topk=0), INVALID),
+    (dict(renorm=2), INVALID), (dict(dt=2), INVALID), (dict(x=None), INVALID), (dict(router=None), INVALID),
+    (dict(q13=None), INVALID), (dict(sb13=None), INVALID), (dict(sg13=None), INVALID), (dict(q2=None), INVALID),
+    (dict(sb2=None), INVALID), (dict(sg2=None), INVALID), (dict(y=None), INVALID), (dict(ws=None), INVALID),
+    (dict(bytes=64), INVALID),
+    (dict(m=17), SHAPE), (dict(e=257), SHAPE), (dict(topk=9), SHAPE), (dict(e=64, topk=17), SHAPE),
+    (dict(h=48, ldx=48, ldr=48, ldy=48), SHAPE), (dict(i=48), SHAPE), (dict(ldx=56), SHAPE), (dict(ldr=56), SHAPE),
+    (dict(ldy=63), SHAPE), (dict(i=1 << 21), SHAPE),
+    (dict(x=P(4104)), ALIGN), (dict(ldx=68), ALIGN), (dict(router=P(4104)), ALIGN), (dict(ldr=68), ALIGN),
+    (dict(q13=P(4104)), ALIGN), (dict(q2=P(4104)), ALIGN), (dict(sb13=P(4097)), ALIGN), (dict(sb2=P(4097)), ALIGN),
+    (dict(sg13=P(4098)), ALIGN), (dict(sg2=P(4098)), ALIGN), (dict(y=P(4097)), ALIGN), (dict(y=P(4098), dt=0), ALIGN),
+    (dict(ids=P(4100)), ALIGN), (dict(p=P(4098)), ALIGN), (dict(ws=P(4104)), ALIGN),
+])
+def test_moe_refuses(L, change, status):
+    assert _moe(L, **change) == status
+
+
+def test_moe_of_no_tokens(L):
+    assert _moe(L, m=0, x=None, y=None, ids=None, p=None, ws=None, bytes=0) == OK
+
+
+def test_moe_workspaces(L):
+    size = L.jetq_moe_nvfp4_workspace_bytes
+    assert size(0, 8, 32, 2) == size(17, 8, 32, 2) == size(4, 257, 32, 2) == size(4, 8, 32, 17) == 0
+    # logits, and three BF16 numbers an activation
+    assert size(16, 128, 768, 8) >= 16 * 128 * 4 + 16 * 8 * 768 * 6
+
+
+def test_moe_helper_checks_its_tensors():
+    import rollout_x128_act_gb300 as jq
+
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        jq.moe_nvfp4(x, x, {}, {}, 2)
