@@ -11,12 +11,14 @@
 // again by the backward pass, which needs N and S first), launches for short ones.
 //
 // Work is split along the tokens, not the sequences, whose lengths run from
-// one to millions: a warp takes a window of 128 tokens (four a lane, loaded
-// together) and walks the sequences that cross it.  The part of sequence s in
-// window w is piece w + s of the partial sums: along the staircase of windows
-// and sequences each step raises one of the two, so no two pieces share an index
-// and none needs a counter or an atomic.  A second kernel joins each sequence's
-// pieces in binary64 (few values) in a fixed order: results are repeatable.
+// one to millions: a warp takes windows of 128 tokens (four a lane, loaded a
+// window ahead) and walks the sequences that cross them.  The part of sequence
+// s in window w is piece w + s of the partial sums: along the staircase of
+// windows and sequences each step raises one of the two, so no two pieces share
+// an index and none needs a counter or an atomic.  A second kernel joins each
+// sequence's pieces in a fixed order, with compensated FP32 sums (binary64 is
+// slow here: the join took 25 to 49 us with it): results are repeatable.  Up to
+// 4096 tokens one CTA does both.
 //
 // Which side of the clip's border a token is on decides whether its gradient
 // is there at all, so logr keeps the rounding error of its subtraction and is
@@ -42,14 +44,15 @@ struct PolicyParams {
     int64_t n, windows;
     int nseg;
     bool adv_token, by_seg;
+    int chunk; // consecutive windows a warp
     int mean;
     float scale, kl;
-    float low, high, dual;             // 1 - low, 1 + high, the bound or infinity
+    float low, high, dual;              // 1 - low, 1 + high, the bound or infinity
     float2 log_low, log_high, log_dual; // their logarithms, in two floats
     struct Piece *pieces;
-    double *part;     // [join CTAs][5]
-    unsigned *ticket; // of the join's CTAs
-    int segs_cta;     // sequences a CTA of the join
+    struct Totals *part; // [join CTAs]
+    unsigned *ticket;    // of the join's CTAs
+    int segs_cta;        // sequences a CTA of the join
     float *out, *save;
     const float *dloss;
     float *dnll;
@@ -57,9 +60,15 @@ struct PolicyParams {
 
 // Sums over the counted tokens of a sequence in a window.
 struct alignas(16) Piece {
-    float count, clipped; // clipped: of a segment's ratio the tokens with A < 0
-    float a, b, c, kl;    // a: L, or the positive A; b: the negative A; a segment's logr is c + c_rest
+    int count, clipped; // clipped: of a segment's ratio the tokens with A < 0
+    float a, b, c, kl;  // a: L, or the positive A; b: the negative A; a segment's logr is c + c_rest
     float c_rest, unused;
+};
+
+// Sums over sequences: surrogate and KL term (with their rests), numbers of clipped tokens, tokens, sequences.
+struct alignas(16) Totals {
+    float l, l_rest, kl, kl_rest;
+    unsigned long long clipped, tokens, segs;
 };
 
 __device__ __forceinline__ bool above(float d, float e, float2 t)
@@ -135,32 +144,48 @@ __device__ __forceinline__ int first_segment(const int64_t *seg, int nseg, int64
     return lo;
 }
 
-// The sequences that cross tokens [t0, t1), in turn: fn(sequence, first token, last token + 1, its advantage).
-template <class F>
-__device__ __forceinline__ void walk(const PolicyParams &p, int64_t t0, int64_t t1, int lane, F fn)
-{
-    if (!p.seg) {
-        fn(0, t0, t1, p.adv_token ? 0.0f : __ldg(p.adv));
-        return;
+// The sequences that cross a warp's windows, in turn.
+struct Walker {
+    int s, base; // the sequence, the first of the 32 that the lanes hold (-1: none yet)
+    int64_t begin, end;
+    float adv;
+    float2 save;
+    __device__ __forceinline__ void start(const PolicyParams &p, int64_t t0, int lane)
+    {
+        s = p.seg ? first_segment(p.seg, p.nseg, t0, lane) : 0;
+        base = -1;
     }
-    int s = first_segment(p.seg, p.nseg, t0, lane);
-    while (s < p.nseg) {
-        const int mine = min(s + lane, p.nseg - 1); // 32 sequences' offsets in one load
-        const int64_t begin = __ldg(p.seg + mine), end = __ldg(p.seg + mine + 1);
-        const float adv = p.adv_token ? 0.0f : __ldg(p.adv + mine);
-        const int many = min(32, p.nseg - s);
-        for (int i = 0; i < many; ++i) {
+    // fn(sequence, first token, last token + 1, advantage, saved pair) for tokens [t0, t1); windows follow one another
+    template <bool SAVED, class F>
+    __device__ __forceinline__ void window(const PolicyParams &p, int64_t t0, int64_t t1, int lane, F fn)
+    {
+        while (s < p.nseg) {
+            if (base < 0 || s - base >= 32) { // 32 sequences' values in one load
+                base = s;
+                const int mine = min(s + lane, p.nseg - 1);
+                begin = p.seg ? __ldg(p.seg + mine) : 0;
+                end = p.seg ? __ldg(p.seg + mine + 1) : p.n;
+                adv = p.adv_token ? 0.0f : __ldg(p.adv + mine);
+                if (SAVED)
+                    save = __ldcg(reinterpret_cast<const float2 *>(p.save) + mine);
+            }
+            const int i = s - base;
             const int64_t b = __shfl_sync(0xFFFFFFFFu, begin, i), e = __shfl_sync(0xFFFFFFFFu, end, i);
             const float A = __shfl_sync(0xFFFFFFFFu, adv, i);
+            float2 sv = make_float2(0.0f, 0.0f);
+            if (SAVED)
+                sv = make_float2(__shfl_sync(0xFFFFFFFFu, save.x, i), __shfl_sync(0xFFFFFFFFu, save.y, i));
             if (b >= t1)
                 return;
             const int64_t from = b > t0 ? b : t0, to = e < t1 ? e : t1;
             if (from < to)
-                fn(s + i, from, to, A);
+                fn(s, from, to, A, sv);
+            if (e > t1)
+                return;
+            ++s;
         }
-        s += many;
     }
-}
+};
 
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -172,11 +197,10 @@ __device__ __forceinline__ float warp_sum(float v)
 
 // What a lane loads of its tokens t0 + lane + 32 k.
 struct Tokens {
-    float d[kSlots], e[kSlots], dref[kSlots], A[kSlots];
+    float x[kSlots], y[kSlots], z[kSlots], A[kSlots];
     bool on[kSlots];
     __device__ __forceinline__ void load(const PolicyParams &p, int64_t t0, int lane)
     {
-        float x[kSlots], y[kSlots], z[kSlots];
 #pragma unroll
         for (int k = 0; k < kSlots; ++k) {
             const int64_t t = t0 + lane + 32 * k;
@@ -193,326 +217,459 @@ struct Tokens {
                     on[k] = __ldg(p.mask + t) != 0;
             }
         }
-#pragma unroll
-        for (int k = 0; k < kSlots; ++k) {
-            two_diff(y[k], x[k], d[k], e[k]);
-            dref[k] = p.ref ? x[k] - z[k] : 0.0f;
-        }
     }
 };
 
-template <bool BY_SEG>
-__global__ void __launch_bounds__(32 * kWarps) k_policy_pieces(const PolicyParams p)
+// exp of d + e
+__device__ __forceinline__ float ratio_of(float d, float e)
 {
-    ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), t0 = w * kWindow;
-    if (blockIdx.x == 0 && threadIdx.x == 0)
-        *p.ticket = 0;
-    if (t0 >= p.n)
-        return;
-    Tokens tk;
-    tk.load(p, t0, lane);
-    float r[kSlots], kl[kSlots];
-#pragma unroll
-    for (int k = 0; k < kSlots; ++k) {
-        r[k] = 0.0f;
-        if (!BY_SEG) {
-            r[k] = expf(tk.d[k]);
-            if (tk.e[k] != 0.0f)
-                r[k] = fmaf(r[k], tk.e[k], r[k]);
-        }
-        kl[k] = p.ref ? kl_term(tk.dref[k]) : 0.0f;
-    }
-    const int64_t t1 = min(t0 + kWindow, p.n);
-    walk(p, t0, t1, lane, [&](int s, int64_t from, int64_t to, float A_seg) {
-        const int lo = (int)(from - t0) - lane, hi = (int)(to - t0) - lane;
-        int count = 0, clipped = 0;
-        float a = 0.0f, b = 0.0f, c = 0.0f, rest = 0.0f, q = 0.0f;
+    const float r = expf(d);
+    return e != 0.0f ? fmaf(r, e, r) : r;
+}
+
+// A warp's windows: the sums of each piece.
+template <bool BY_SEG>
+__device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t w0, int64_t w1, int lane)
+{
+    Tokens tk, next;
+    next.load(p, w0 * kWindow, lane);
+    Walker walk;
+    walk.start(p, w0 * kWindow, lane);
+    for (int64_t w = w0; w < w1; ++w) {
+        tk = next;
+        if (w + 1 < w1)
+            next.load(p, (w + 1) * kWindow, lane);
+        float d[kSlots], e[kSlots], r[kSlots], kl[kSlots];
 #pragma unroll
         for (int k = 0; k < kSlots; ++k) {
-            const bool in = tk.on[k] && 32 * k >= lo && 32 * k < hi;
-            const float A = p.adv_token ? tk.A[k] : A_seg;
-            bool side;
-            if (BY_SEG) {
-                side = A < 0.0f;
-                a += in && !side ? A : 0.0f;
-                b += in && side ? A : 0.0f;
-                if (in) {
-                    add_to(c, rest, tk.d[k]);
-                    rest += tk.e[k];
-                }
-            } else {
-                float bound;
-                side = clip(p, A, tk.d[k], tk.e[k], bound);
-                a += in ? -A * (side ? bound : r[k]) : 0.0f;
-            }
-            q += in ? kl[k] : 0.0f;
-            count += __popc(__ballot_sync(0xFFFFFFFFu, in));
-            clipped += __popc(__ballot_sync(0xFFFFFFFFu, in && side));
+            two_diff(tk.y[k], tk.x[k], d[k], e[k]);
+            r[k] = BY_SEG ? 0.0f : ratio_of(d[k], e[k]);
+            kl[k] = p.ref ? kl_term(tk.x[k] - tk.z[k]) : 0.0f;
         }
-        a = warp_sum(a);
-        if (p.ref)
-            q = warp_sum(q);
-        if (BY_SEG) {
-            b = warp_sum(b);
+        const int64_t t0 = w * kWindow, t1 = min(t0 + kWindow, p.n);
+        walk.window<false>(p, t0, t1, lane, [&](int s, int64_t from, int64_t to, float A_seg, float2) {
+            const int lo = (int)(from - t0) - lane, hi = (int)(to - t0) - lane;
+            int count = 0, clipped = 0;
+            float a = 0.0f, b = 0.0f, c = 0.0f, rest = 0.0f, q = 0.0f;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                const float c2 = __shfl_xor_sync(0xFFFFFFFFu, c, o), r2 = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
-                add_to(c, rest, c2);
-                rest += r2;
+            for (int k = 0; k < kSlots; ++k) {
+                const bool in = tk.on[k] && 32 * k >= lo && 32 * k < hi;
+                const float A = p.adv_token ? tk.A[k] : A_seg;
+                bool side;
+                if (BY_SEG) {
+                    side = A < 0.0f;
+                    a += in && !side ? A : 0.0f;
+                    b += in && side ? A : 0.0f;
+                    if (in) {
+                        add_to(c, rest, d[k]);
+                        rest += e[k];
+                    }
+                } else {
+                    float bound;
+                    side = clip(p, A, d[k], e[k], bound);
+                    a += in ? -A * (side ? bound : r[k]) : 0.0f;
+                }
+                q += in ? kl[k] : 0.0f;
+                count += __popc(__ballot_sync(0xFFFFFFFFu, in));
+                clipped += __popc(__ballot_sync(0xFFFFFFFFu, in && side));
             }
-        }
-        if (lane == 0) {
-            float4 *out = reinterpret_cast<float4 *>(p.pieces + (w + s));
-            out[0] = make_float4((float)count, (float)clipped, a, b);
-            out[1] = make_float4(c, q, rest, 0.0f);
-        }
-    });
+            a = warp_sum(a);
+            if (p.ref)
+                q = warp_sum(q);
+            if (BY_SEG) {
+                b = warp_sum(b);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    const float c2 = __shfl_xor_sync(0xFFFFFFFFu, c, o), r2 = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+                    add_to(c, rest, c2);
+                    rest += r2;
+                }
+            }
+            if (lane == 0) {
+                float4 *out = reinterpret_cast<float4 *>(p.pieces + (w + s));
+                out[0] = make_float4(__int_as_float(count), __int_as_float(clipped), a, b);
+                out[1] = make_float4(c, q, rest, 0.0f);
+            }
+        });
+    }
+}
+
+// Value of a sum and its rest; an infinite one has none.
+__device__ __forceinline__ float whole(float s, float rest)
+{
+    return fabsf(s) < INFINITY ? s + rest : s;
 }
 
 struct SegSums {
-    double count, clipped, a, b, c, kl;
-    __device__ __forceinline__ void clear() { count = clipped = a = b = c = kl = 0.0; }
+    unsigned long long count, clipped;
+    float a, a_rest, b, b_rest, c, c_rest, kl, kl_rest;
+    __device__ __forceinline__ void clear()
+    {
+        count = clipped = 0;
+        a = a_rest = b = b_rest = c = c_rest = kl = kl_rest = 0.0f;
+    }
     __device__ __forceinline__ void add(const Piece *piece, bool by_seg)
     {
         const float4 u = __ldcg(reinterpret_cast<const float4 *>(piece));
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece) + 1);
-        count += u.x;
-        clipped += u.y;
-        a += u.z;
-        kl += v.y;
+        count += (unsigned)__float_as_int(u.x);
+        clipped += (unsigned)__float_as_int(u.y);
+        add_to(a, a_rest, u.z);
+        add_to(kl, kl_rest, v.y);
         if (by_seg) {
-            b += u.w;
-            c += (double)v.x + (fabsf(v.x) < INFINITY ? (double)v.z : 0.0);
+            add_to(b, b_rest, u.w);
+            add_to(c, c_rest, v.x);
+            c_rest += v.z;
         }
     }
-    template <class S>
-    __device__ __forceinline__ void all(S sum)
+    __device__ __forceinline__ void add(const SegSums &o, bool by_seg)
     {
-        count = sum(count);
-        clipped = sum(clipped);
-        a = sum(a);
-        b = sum(b);
-        c = sum(c);
-        kl = sum(kl);
+        count += o.count;
+        clipped += o.clipped;
+        add_to(a, a_rest, o.a);
+        a_rest += o.a_rest;
+        add_to(kl, kl_rest, o.kl);
+        kl_rest += o.kl_rest;
+        if (by_seg) {
+            add_to(b, b_rest, o.b);
+            b_rest += o.b_rest;
+            add_to(c, c_rest, o.c);
+            c_rest += o.c_rest;
+        }
+    }
+    __device__ __forceinline__ void add_lane(int o, bool by_seg) // of lane ^ o
+    {
+        SegSums x;
+        x.count = __shfl_xor_sync(0xFFFFFFFFu, count, o);
+        x.clipped = __shfl_xor_sync(0xFFFFFFFFu, clipped, o);
+        x.a = __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        x.a_rest = __shfl_xor_sync(0xFFFFFFFFu, a_rest, o);
+        x.kl = __shfl_xor_sync(0xFFFFFFFFu, kl, o);
+        x.kl_rest = __shfl_xor_sync(0xFFFFFFFFu, kl_rest, o);
+        if (by_seg) {
+            x.b = __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            x.b_rest = __shfl_xor_sync(0xFFFFFFFFu, b_rest, o);
+            x.c = __shfl_xor_sync(0xFFFFFFFFu, c, o);
+            x.c_rest = __shfl_xor_sync(0xFFFFFFFFu, c_rest, o);
+        }
+        add(x, by_seg);
     }
 };
 
-constexpr int kJoinThreads = 256, kLanesSeg = 4, kLong = 256; // a sequence's lanes; pieces from which the CTA takes it
-
-// Sums of each sequence's pieces; their share of the loss; the last CTA to finish adds the CTAs' shares.
-__global__ void __launch_bounds__(kJoinThreads) k_policy_join(const PolicyParams p)
+__device__ __forceinline__ void add_totals(Totals &t, const Totals &o)
 {
-    __shared__ double red[kJoinThreads / 32][6];
-    __shared__ int longs[kJoinThreads / kLanesSeg], num_longs;
-    __shared__ bool last;
-    ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = threadIdx.x % kLanesSeg;
-    if (threadIdx.x == 0)
-        num_longs = 0;
+    add_to(t.l, t.l_rest, o.l);
+    t.l_rest += o.l_rest;
+    add_to(t.kl, t.kl_rest, o.kl);
+    t.kl_rest += o.kl_rest;
+    t.clipped += o.clipped;
+    t.tokens += o.tokens;
+    t.segs += o.segs;
+}
+
+// Sum over the first `lanes` (a power of two) lanes of a warp.
+__device__ __forceinline__ void warp_totals(Totals &t, int lanes)
+{
+    for (int o = lanes / 2; o; o >>= 1) {
+        Totals x;
+        x.l = __shfl_xor_sync(0xFFFFFFFFu, t.l, o);
+        x.l_rest = __shfl_xor_sync(0xFFFFFFFFu, t.l_rest, o);
+        x.kl = __shfl_xor_sync(0xFFFFFFFFu, t.kl, o);
+        x.kl_rest = __shfl_xor_sync(0xFFFFFFFFu, t.kl_rest, o);
+        x.clipped = __shfl_xor_sync(0xFFFFFFFFu, t.clipped, o);
+        x.tokens = __shfl_xor_sync(0xFFFFFFFFu, t.tokens, o);
+        x.segs = __shfl_xor_sync(0xFFFFFFFFu, t.segs, o);
+        add_totals(t, x);
+    }
+}
+
+// A sequence's saved pair and its share of the totals.
+__device__ __forceinline__ void finish(const PolicyParams &p, int s, const SegSums &x, Totals &tot)
+{
+    const float a = whole(x.a, x.a_rest), n = (float)x.count;
+    float l = a, l_rest = 0.0f, g = 0.0f;
+    unsigned long long clipped = x.clipped;
+    if (fabsf(x.a) < INFINITY) {
+        l = x.a;
+        l_rest = x.a_rest;
+    }
+    if (p.by_seg && x.count) {
+        const float b = whole(x.b, x.b_rest), c = whole(x.c, x.c_rest);
+        // the mean in two floats: it is compared with the borders
+        const float mean = __fdiv_rn(c, n);
+        float rest = 0.0f;
+        if (fabsf(c) < INFINITY) {
+            const float lost = __fadd_rn(__fsub_rn(x.c, c), x.c_rest);
+            rest = __fdiv_rn(__fadd_rn(fmaf(-mean, n, c), lost), n);
+        }
+        const bool hi = above(mean, rest, p.log_high), lo = below(mean, rest, p.log_low);
+        const bool du = above(mean, rest, p.log_dual);
+        const float ratio = ratio_of(mean, rest);
+        // a sum without a token of its sign stays out: 0 * infinity is no number
+        const float pos = a != 0.0f ? -a * (hi ? p.high : ratio) : 0.0f;
+        const float neg = b != 0.0f ? -b * (lo ? p.low : du ? p.dual : ratio) : 0.0f;
+        const float live = (hi ? 0.0f : a) + (lo || du ? 0.0f : b);
+        l = pos;
+        l_rest = 0.0f;
+        add_to(l, l_rest, neg);
+        clipped = (hi ? x.count - x.clipped : 0ull) + (lo || du ? x.clipped : 0ull);
+        g = live != 0.0f ? __fdiv_rn(live * ratio, n) : 0.0f;
+    }
+    reinterpret_cast<float2 *>(p.save)[s] = make_float2(n, g);
+    if (x.count) {
+        Totals t = {l, l_rest, x.kl, x.kl_rest, clipped, x.count, 1ull};
+        if (p.mean == JETQ_POLICY_MEAN_SEGMENTS) {
+            t.l = __fdiv_rn(whole(l, l_rest), n);
+            t.kl = __fdiv_rn(whole(x.kl, x.kl_rest), n);
+            t.l_rest = t.kl_rest = 0.0f;
+        }
+        add_totals(tot, t);
+    }
+}
+
+__device__ __forceinline__ void write_out(const PolicyParams &p, const Totals &t)
+{
+    float f = p.scale;
+    if (p.mean != JETQ_POLICY_SUM) {
+        const unsigned long long by = p.mean == JETQ_POLICY_MEAN_SEGMENTS ? t.segs : t.tokens;
+        f = by ? __fdiv_rn(f, (float)by) : 0.0f;
+    }
+    const float l = f * whole(t.l, t.l_rest), kl = f * whole(t.kl, t.kl_rest);
+    p.out[0] = p.ref ? fmaf(p.kl, kl, l) : l;
+    p.out[1] = l;
+    p.out[2] = kl;
+    p.out[3] = (float)t.clipped;
+    p.out[4] = (float)t.tokens;
+    p.out[5] = (float)t.segs;
+}
+
+constexpr int kLanesSeg = 4, kLong = 256; // a sequence's lanes; pieces above which the CTA takes it
+
+template <int THREADS>
+struct JoinShared {
+    SegSums seg[THREADS / 32];
+    Totals tot[THREADS / 32];
+    int longs[THREADS / kLanesSeg], num_longs;
+    bool last;
+};
+
+// The CTA's sum of `t`, in all lanes of warp 0.
+template <int THREADS>
+__device__ __forceinline__ void cta_totals(Totals &t, JoinShared<THREADS> &sh)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kWarpsCta = THREADS / 32;
+    warp_totals(t, 32);
+    if (lane == 0)
+        sh.tot[warp] = t;
     __syncthreads();
-    double tot[5] = {0.0, 0.0, 0.0, 0.0, 0.0}; // surrogate, kl, clipped, tokens, sequences
-    auto range = [&](int s, int64_t &w0, int64_t &w1) { // windows of sequence s
+    if (warp == 0) {
+        t = lane < kWarpsCta ? sh.tot[lane] : Totals{};
+        warp_totals(t, 32);
+    }
+}
+
+// Sequences [first, end) by a CTA: their saved pairs, and the totals in warp 0.
+template <int THREADS>
+__device__ __forceinline__ Totals join_segments(const PolicyParams &p, int64_t first, int64_t end,
+                                                JoinShared<THREADS> &sh)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = threadIdx.x % kLanesSeg;
+    Totals tot = {};
+    auto range = [&](int64_t s, int64_t &w0, int64_t &w1) { // windows of sequence s
         int64_t b = p.seg ? __ldg(p.seg + s) : 0, e = p.seg ? __ldg(p.seg + s + 1) : p.n;
         b = b < 0 ? 0 : b;
         e = e > p.n ? p.n : e;
         w0 = b / kWindow;
         w1 = e > b ? (e - 1) / kWindow + 1 : w0;
     };
-    auto finish = [&](int s, const SegSums &x) {
-        double surrogate = x.a, clipped = x.clipped;
-        float g = 0.0f;
-        if (p.by_seg && x.count > 0.0) {
-            const double mean = x.c / x.count;
-            const float2 l = p.log_low, h = p.log_high, u = p.log_dual;
-            const bool hi = mean > (double)h.x + h.y, lo = mean < (double)l.x + l.y, du = mean > (double)u.x + u.y;
-            const double ratio = exp(mean);
-            // a sum without a token of its sign stays out: 0 * infinity is no number
-            const double pos = x.a != 0.0 ? -x.a * (hi ? (double)p.high : ratio) : 0.0;
-            const double neg = x.b != 0.0 ? -x.b * (lo ? (double)p.low : du ? (double)p.dual : ratio) : 0.0;
-            const double live = (hi ? 0.0 : x.a) + (lo || du ? 0.0 : x.b);
-            surrogate = pos + neg;
-            clipped = (hi ? x.count - x.clipped : 0.0) + (lo || du ? x.clipped : 0.0);
-            g = live != 0.0 ? (float)(live * ratio / x.count) : 0.0f;
-        }
-        reinterpret_cast<float2 *>(p.save)[s] = make_float2((float)x.count, g);
-        if (x.count > 0.0) {
-            const double f = p.mean == JETQ_POLICY_MEAN_SEGMENTS ? 1.0 / x.count : 1.0;
-            tot[0] += f * surrogate;
-            tot[1] += f * x.kl;
-            tot[2] += clipped;
-            tot[3] += x.count;
-            tot[4] += 1.0;
-        }
-    };
-    const int64_t first = (int64_t)blockIdx.x * p.segs_cta;
-    const int mine = threadIdx.x / kLanesSeg;
-    {
-        const int64_t s = first + mine;
-        const bool have = mine < p.segs_cta && s < p.nseg;
+    for (int64_t s0 = first; s0 < end; s0 += THREADS / kLanesSeg) {
+        if (threadIdx.x == 0)
+            sh.num_longs = 0;
+        __syncthreads();
+        const int64_t s = s0 + threadIdx.x / kLanesSeg;
         int64_t w0 = 0, w1 = 0;
-        if (have)
-            range((int)s, w0, w1);
+        if (s < end)
+            range(s, w0, w1);
         const bool is_long = w1 - w0 > kLong;
         if (is_long && sub == 0)
-            longs[atomicAdd(&num_longs, 1)] = (int)s;
+            sh.longs[atomicAdd(&sh.num_longs, 1)] = (int)s;
         SegSums x;
         x.clear();
-        if (!is_long)
+        if (!is_long) {
+#pragma unroll 2
             for (int64_t w = w0 + sub; w < w1; w += kLanesSeg)
                 x.add(p.pieces + (w + s), p.by_seg);
-        x.all([&](double v) {
+        }
 #pragma unroll
-            for (int o = kLanesSeg / 2; o; o >>= 1)
-                v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            return v;
-        });
-        if (have && !is_long && sub == 0)
-            finish((int)s, x);
-    }
-    __syncthreads();
-    const int many = num_longs;
-    // in the order of the sequences, whatever the order in which they were listed
-    int after = -1;
-    for (int i = 0; i < many; ++i) {
-        int s = 0x7FFFFFFF;
-        for (int j = 0; j < many; ++j)
-            if (longs[j] > after)
-                s = min(s, longs[j]);
-        after = s;
-        int64_t w0, w1;
-        range(s, w0, w1);
-        SegSums x;
-        x.clear();
+        for (int o = kLanesSeg / 2; o; o >>= 1)
+            x.add_lane(o, p.by_seg);
+        if (s < end && !is_long && sub == 0)
+            finish(p, (int)s, x, tot);
+        __syncthreads();
+        const int many = sh.num_longs;
+        // in the order of the sequences, whatever the order in which they were listed
+        int after = -1;
+        for (int i = 0; i < many; ++i) {
+            int which = 0x7FFFFFFF;
+            for (int j = 0; j < many; ++j)
+                if (sh.longs[j] > after)
+                    which = min(which, sh.longs[j]);
+            after = which;
+            range(which, w0, w1);
+            x.clear();
 #pragma unroll 4
-        for (int64_t w = w0 + threadIdx.x; w < w1; w += kJoinThreads)
-            x.add(p.pieces + (w + s), p.by_seg);
-        auto warp_all = [&](double v) {
+            for (int64_t w = w0 + threadIdx.x; w < w1; w += THREADS)
+                x.add(p.pieces + (w + which), p.by_seg);
 #pragma unroll
             for (int o = 16; o; o >>= 1)
-                v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            return v;
-        };
-        x.all(warp_all);
-        if (lane == 0) {
-            const double v[6] = {x.count, x.clipped, x.a, x.b, x.c, x.kl};
-            for (int k = 0; k < 6; ++k)
-                red[warp][k] = v[k];
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            double v[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
-            for (int g = 0; g < kJoinThreads / 32; ++g)
-                for (int k = 0; k < 6; ++k)
-                    v[k] += red[g][k];
-            finish(s, SegSums{v[0], v[1], v[2], v[3], v[4], v[5]});
+                x.add_lane(o, p.by_seg);
+            if (lane == 0)
+                sh.seg[warp] = x;
+            __syncthreads();
+            if (warp == 0) {
+                if (lane < THREADS / 32)
+                    x = sh.seg[lane];
+                else
+                    x.clear();
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    x.add_lane(o, p.by_seg);
+                if (lane == 0)
+                    finish(p, which, x, tot);
+            }
+            __syncthreads();
         }
         __syncthreads();
     }
-    // the CTA's share, then all of them
-    auto cta_sum = [&](double (&v)[5]) { // to thread 0
-        for (int k = 0; k < 5; ++k) {
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
-            if (lane == 0)
-                red[warp][k] = v[k];
-        }
-        __syncthreads();
-        if (threadIdx.x == 0)
-            for (int k = 0; k < 5; ++k) {
-                v[k] = 0.0;
-                for (int g = 0; g < kJoinThreads / 32; ++g)
-                    v[k] += red[g][k];
-            }
-    };
-    cta_sum(tot);
+    cta_totals<THREADS>(tot, sh);
+    return tot;
+}
+
+constexpr int kSmallThreads = 1024, kJoinThreads = 256;
+constexpr int kSmallSegs = 4096; // sequences (most of them empty) that one CTA joins
+
+template <bool BY_SEG>
+__global__ void __launch_bounds__(32 * kWarps, 3) k_policy_pieces(const PolicyParams p)
+{
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int64_t w = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.chunk;
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *p.ticket = 0;
+    if (w < p.windows)
+        sum_pieces<BY_SEG>(p, w, min(w + p.chunk, p.windows), threadIdx.x & 31);
+}
+
+// The last CTA to finish adds the CTAs' totals.
+__global__ void __launch_bounds__(kJoinThreads) k_policy_join(const PolicyParams p)
+{
+    __shared__ JoinShared<kJoinThreads> sh;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int64_t first = (int64_t)blockIdx.x * p.segs_cta;
+    Totals t = join_segments<kJoinThreads>(p, first, min(first + p.segs_cta, (int64_t)p.nseg), sh);
     if (gridDim.x > 1) {
         if (threadIdx.x == 0) {
-            for (int k = 0; k < 5; ++k)
-                p.part[(int64_t)blockIdx.x * 5 + k] = tot[k];
+            p.part[blockIdx.x] = t;
             __threadfence();
-            last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+            sh.last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
         }
         __syncthreads();
-        if (!last)
+        if (!sh.last)
             return;
         __threadfence();
-        for (int k = 0; k < 5; ++k)
-            tot[k] = 0.0;
-        for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads)
-            for (int k = 0; k < 5; ++k)
-                tot[k] += __ldcg(p.part + (int64_t)i * 5 + k);
-        cta_sum(tot);
-    }
-    if (threadIdx.x == 0) {
-        double f = p.scale;
-        if (p.mean != JETQ_POLICY_SUM) {
-            const double by = p.mean == JETQ_POLICY_MEAN_SEGMENTS ? tot[4] : tot[3];
-            f = by > 0.0 ? f / by : 0.0;
+        t = Totals{};
+        for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads) {
+            Totals o;
+            const float4 f = __ldcg(reinterpret_cast<const float4 *>(p.part + i));
+            const ulonglong2 u = __ldcg(reinterpret_cast<const ulonglong2 *>(p.part + i) + 1);
+            o.l = f.x;
+            o.l_rest = f.y;
+            o.kl = f.z;
+            o.kl_rest = f.w;
+            o.clipped = u.x;
+            o.tokens = u.y;
+            o.segs = __ldcg(&p.part[i].segs);
+            add_totals(t, o);
         }
-        p.out[0] = (float)(f * (tot[0] + (p.ref ? (double)p.kl * tot[1] : 0.0)));
-        p.out[1] = (float)(f * tot[0]);
-        p.out[2] = (float)(f * tot[1]);
-        p.out[3] = (float)tot[2];
-        p.out[4] = (float)tot[3];
-        p.out[5] = (float)tot[4];
+        cta_totals<kJoinThreads>(t, sh);
     }
+    if (threadIdx.x == 0)
+        write_out(p, t);
+}
+
+// Both steps by one CTA, a window a warp.
+template <bool BY_SEG>
+__global__ void __launch_bounds__(kSmallThreads) k_policy_small(const PolicyParams p)
+{
+    __shared__ JoinShared<kSmallThreads> sh;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int64_t w = threadIdx.x >> 5;
+    if (w < p.windows)
+        sum_pieces<BY_SEG>(p, w, w + 1, threadIdx.x & 31);
+    __syncthreads(); // the pieces are there for the whole CTA
+    const Totals t = join_segments<kSmallThreads>(p, 0, p.nseg, sh);
+    if (threadIdx.x == 0)
+        write_out(p, t);
 }
 
 template <bool BY_SEG>
-__global__ void __launch_bounds__(32 * kWarps) k_policy_bwd(const PolicyParams p)
+__global__ void __launch_bounds__(32 * kWarps, 3) k_policy_bwd(const PolicyParams p)
 {
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kWindow;
-    if (t0 >= p.n)
+    const int64_t w0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.chunk;
+    if (w0 >= p.windows)
         return;
-    Tokens tk;
-    tk.load(p, t0, lane);
+    const int64_t w1 = min(w0 + p.chunk, p.windows);
+    Tokens tk, next;
+    next.load(p, w0 * kWindow, lane);
     float scale = p.scale;
     if (p.mean == JETQ_POLICY_MEAN_TOKENS)
-        scale = __fdiv_rn(scale, __ldg(p.out + 4));
+        scale = __fdiv_rn(scale, __ldcg(p.out + 4));
     else if (p.mean == JETQ_POLICY_MEAN_SEGMENTS)
-        scale = __fdiv_rn(scale, __ldg(p.out + 5));
+        scale = __fdiv_rn(scale, __ldcg(p.out + 5));
     if (p.dloss)
         scale *= __ldg(p.dloss);
-    float g[kSlots];
+    Walker walk;
+    walk.start(p, w0 * kWindow, lane);
+    for (int64_t w = w0; w < w1; ++w) {
+        tk = next;
+        if (w + 1 < w1)
+            next.load(p, (w + 1) * kWindow, lane);
+        float d[kSlots], e[kSlots], r[kSlots], kl[kSlots], g[kSlots];
 #pragma unroll
-    for (int k = 0; k < kSlots; ++k)
-        g[k] = 0.0f;
-    const int64_t t1 = min(t0 + kWindow, p.n);
-    walk(p, t0, t1, lane, [&](int s, int64_t from, int64_t to, float A_seg) {
-        const int lo = (int)(from - t0) - lane, hi = (int)(to - t0) - lane;
-        const float2 seg = __ldg(reinterpret_cast<const float2 *>(p.save) + s);
-        const float f = p.mean == JETQ_POLICY_MEAN_SEGMENTS ? __fdiv_rn(scale, seg.x) : scale;
+        for (int k = 0; k < kSlots; ++k) {
+            two_diff(tk.y[k], tk.x[k], d[k], e[k]);
+            r[k] = BY_SEG ? 0.0f : ratio_of(d[k], e[k]);
+            kl[k] = p.ref ? p.kl * expm1f(tk.x[k] - tk.z[k]) : 0.0f;
+            g[k] = 0.0f;
+        }
+        const int64_t t0 = w * kWindow, t1 = min(t0 + kWindow, p.n);
+        walk.window<true>(p, t0, t1, lane, [&](int, int64_t from, int64_t to, float A_seg, float2 seg) {
+            const int lo = (int)(from - t0) - lane, hi = (int)(to - t0) - lane;
+            const float f = p.mean == JETQ_POLICY_MEAN_SEGMENTS ? __fdiv_rn(scale, seg.x) : scale;
 #pragma unroll
-        for (int k = 0; k < kSlots; ++k)
-            if (tk.on[k] && 32 * k >= lo && 32 * k < hi) {
-                float v = seg.y;
-                if (!BY_SEG) {
-                    const float A = p.adv_token ? tk.A[k] : A_seg;
-                    float bound;
-                    v = 0.0f;
-                    if (!clip(p, A, tk.d[k], tk.e[k], bound)) {
-                        const float r = expf(tk.d[k]);
-                        v = A * (tk.e[k] != 0.0f ? fmaf(r, tk.e[k], r) : r);
+            for (int k = 0; k < kSlots; ++k)
+                if (tk.on[k] && 32 * k >= lo && 32 * k < hi) {
+                    float v = seg.y;
+                    if (!BY_SEG) {
+                        const float A = p.adv_token ? tk.A[k] : A_seg;
+                        float bound;
+                        v = clip(p, A, d[k], e[k], bound) ? 0.0f : A * r[k];
                     }
+                    g[k] = f * (v + kl[k]);
                 }
-                if (p.ref)
-                    v = fmaf(p.kl, expm1f(tk.dref[k]), v);
-                g[k] = f * v;
-            }
-    });
+        });
 #pragma unroll
-    for (int k = 0; k < kSlots; ++k) {
-        const int64_t t = t0 + lane + 32 * k;
-        if (t < p.n)
-            p.dnll[t] = g[k];
+        for (int k = 0; k < kSlots; ++k) {
+            const int64_t t = t0 + lane + 32 * k;
+            if (t < p.n)
+                p.dnll[t] = g[k];
+        }
     }
 }
 
@@ -520,6 +677,8 @@ int64_t ceil_div(int64_t a, int64_t b)
 {
     return (a + b - 1) / b;
 }
+
+constexpr int kWarpsSm = 24; // warps an SM that share the windows: what its registers hold
 
 float2 two_floats(double v)
 {
@@ -541,6 +700,8 @@ PolicyParams params_of(const PolicyArgs &a)
     p.nseg = a.seg ? a.nseg : 1;
     p.adv_token = a.adv_per_token != 0;
     p.by_seg = a.level == JETQ_POLICY_SEGMENT;
+    const int64_t warps = (int64_t)sm_count() * kWarpsSm;
+    p.chunk = (int)ceil_div(p.windows, warps);
     p.mean = a.mean;
     p.scale = a.scale;
     p.kl = a.kl;
@@ -570,7 +731,7 @@ size_t policy_loss_workspace(int64_t n, int64_t nseg)
 {
     const int64_t windows = ceil_div(n, kWindow);
     return 16 + (size_t)(windows + nseg) * sizeof(Piece) +
-           (size_t)ceil_div(nseg, segs_a_cta(windows, nseg)) * 5 * sizeof(double);
+           (size_t)ceil_div(nseg, segs_a_cta(windows, nseg)) * sizeof(Totals);
 }
 
 cudaError_t launch_policy_fwd(const PolicyArgs &a, cudaStream_t st)
@@ -579,9 +740,12 @@ cudaError_t launch_policy_fwd(const PolicyArgs &a, cudaStream_t st)
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     p.ticket = reinterpret_cast<unsigned *>(ws);
     p.pieces = reinterpret_cast<Piece *>(ws + 16);
-    p.part = reinterpret_cast<double *>(ws + 16 + (size_t)(p.windows + p.nseg) * sizeof(Piece));
+    p.part = reinterpret_cast<Totals *>(ws + 16 + (size_t)(p.windows + p.nseg) * sizeof(Piece));
+    if (p.windows <= kSmallThreads / 32 && p.nseg <= kSmallSegs)
+        return p.by_seg ? launch_pdl(k_policy_small<true>, dim3(1), dim3(kSmallThreads), 0, st, p)
+                        : launch_pdl(k_policy_small<false>, dim3(1), dim3(kSmallThreads), 0, st, p);
     p.segs_cta = segs_a_cta(p.windows, p.nseg);
-    const dim3 grid((unsigned)ceil_div(p.windows, kWarps)), block(32 * kWarps);
+    const dim3 grid((unsigned)ceil_div(p.windows, (int64_t)kWarps * p.chunk)), block(32 * kWarps);
     const cudaError_t e = p.by_seg ? launch_pdl(k_policy_pieces<true>, grid, block, 0, st, p)
                                    : launch_pdl(k_policy_pieces<false>, grid, block, 0, st, p);
     if (e != cudaSuccess)
@@ -592,7 +756,7 @@ cudaError_t launch_policy_fwd(const PolicyArgs &a, cudaStream_t st)
 cudaError_t launch_policy_bwd(const PolicyArgs &a, cudaStream_t st)
 {
     const PolicyParams p = params_of(a);
-    const dim3 grid((unsigned)ceil_div(p.windows, kWarps)), block(32 * kWarps);
+    const dim3 grid((unsigned)ceil_div(p.windows, (int64_t)kWarps * p.chunk)), block(32 * kWarps);
     return p.by_seg ? launch_pdl(k_policy_bwd<true>, grid, block, 0, st, p)
                     : launch_pdl(k_policy_bwd<false>, grid, block, 0, st, p);
 }
