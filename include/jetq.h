@@ -592,7 +592,7 @@ JETQ_API jetq_status jetq_gemv_nvfp4(const uint8_t *qw, const uint8_t *sbw, cons
  *   router, ldr        BF16 [num_experts x h], row stride ldr (multiple of 8)
  *   q13, sb13, sg13    experts' gate and up weights as jetq_quant_nvfp4 writes them with a tensor scope:
  *                      codes [num_experts x 2 inter x h/2] (16-byte aligned), each expert's gate rows
- *                      before its up rows, block scales [num_experts x 2 inter x h/16] (2-byte aligned),
+ *                      before its up rows, block scales [num_experts x 2 inter x h/16] (16-byte aligned),
  *                      float [num_experts]
  *   q2, sb2, sg2       down weights: [num_experts x h x inter/2], [num_experts x h x inter/16], [num_experts]
  *   y, ldy             F32 or BF16 [m x h], any stride ldy >= h, element-aligned
@@ -600,7 +600,7 @@ JETQ_API jetq_status jetq_gemv_nvfp4(const uint8_t *qw, const uint8_t *sbw, cons
  *   workspace          device memory, 16-byte aligned, at least
  *                      jetq_moe_nvfp4_workspace_bytes(m, num_experts, inter, topk) bytes; calls that share
  *                      one must not overlap on the GPU
- * Limits: 1 <= num_experts <= 256, 1 <= topk <= min(16, num_experts); h and inter multiples of 32, up to 2^20.
+ * Limits: 1 <= num_experts <= 256, 1 <= topk <= min(16, num_experts); h and inter multiples of 32, up to 16384.
  * m == 0 is a no-op.  Bitwise repeatable.  Three launches.
  */
 JETQ_API size_t jetq_moe_nvfp4_workspace_bytes(int64_t m, int64_t num_experts, int64_t inter, int64_t topk);

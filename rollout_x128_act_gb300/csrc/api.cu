@@ -165,7 +165,7 @@ jetq_status jetq_check_device_error(void *stream)
     if (gemm_read_and_clear_error(st, &word) != cudaSuccess || gemm_mx_read_and_clear_error(st, &word) != cudaSuccess ||
         gemm_decode_read_and_clear_error(st, &word) != cudaSuccess || quant_read_and_clear_error(st, &word) != cudaSuccess ||
         gemm_nvfp4_read_and_clear_error(st, &word) != cudaSuccess || linear_ce_read_and_clear_error(st, &word) != cudaSuccess ||
-        norm_read_and_clear_error(st, &word) != cudaSuccess)
+        norm_read_and_clear_error(st, &word) != cudaSuccess || moe_read_and_clear_error(st, &word) != cudaSuccess)
         return JETQ_ERR_CUDA;
     return word ? JETQ_ERR_TIMEOUT : JETQ_OK;
 }
@@ -1056,7 +1056,7 @@ jetq_status jetq_policy_loss_bwd(const float *nll, const float *nll_old, const f
 
 size_t jetq_moe_nvfp4_workspace_bytes(int64_t m, int64_t num_experts, int64_t inter, int64_t topk)
 {
-    if (m <= 0 || m > 16 || num_experts <= 0 || num_experts > 256 || inter <= 0 || inter > (1 << 20) || topk <= 0 ||
+    if (m <= 0 || m > 16 || num_experts <= 0 || num_experts > 256 || inter <= 0 || inter > 16384 || topk <= 0 ||
         topk > 16)
         return 0;
     return moe_nvfp4_workspace(m, num_experts, inter, topk);
@@ -1072,7 +1072,7 @@ jetq_status jetq_moe_nvfp4(const uint16_t *x, int64_t m, int64_t h, int64_t ldx,
     JQ_REQUIRE(renorm == 0 || renorm == 1, JETQ_ERR_INVALID_ARG);
     JQ_REQUIRE(y_dtype == JETQ_OUT_F32 || y_dtype == JETQ_OUT_BF16, JETQ_ERR_INVALID_ARG);
     JQ_REQUIRE(m <= 16 && num_experts <= 256 && topk <= 16 && topk <= num_experts && h % 32 == 0 && inter % 32 == 0 &&
-                   h <= (1 << 20) && inter <= (1 << 20) && ldx >= h && ldr >= h && ldy >= h,
+                   h <= 16384 && inter <= 16384 && ldx >= h && ldr >= h && ldy >= h,
                JETQ_ERR_UNSUPPORTED_SHAPE);
     JQ_REQUIRE(ldx <= ((int64_t)1 << 36) && ldr <= ((int64_t)1 << 36) && ldy <= ((int64_t)1 << 36),
                JETQ_ERR_UNSUPPORTED_SHAPE);
@@ -1083,8 +1083,7 @@ jetq_status jetq_moe_nvfp4(const uint16_t *x, int64_t m, int64_t h, int64_t ldx,
                JETQ_ERR_INVALID_ARG);
     JQ_REQUIRE(workspace_bytes >= moe_nvfp4_workspace(m, num_experts, inter, topk), JETQ_ERR_INVALID_ARG);
     JQ_REQUIRE(aligned16(x) && ldx % 8 == 0 && aligned16(router) && ldr % 8 == 0 && aligned16(q13) && aligned16(q2) &&
-                   ((reinterpret_cast<uintptr_t>(sb13) | reinterpret_cast<uintptr_t>(sb2)) & 1u) == 0 &&
-                   aligned4(sg13) && aligned4(sg2) && aligned16(workspace) &&
+                   aligned16(sb13) && aligned16(sb2) && aligned4(sg13) && aligned4(sg2) && aligned16(workspace) &&
                    (reinterpret_cast<uintptr_t>(y) & (y_dtype == JETQ_OUT_F32 ? 3u : 1u)) == 0 &&
                    (reinterpret_cast<uintptr_t>(ids) & 7u) == 0 && aligned4(weights),
                JETQ_ERR_MISALIGNED);

@@ -281,6 +281,7 @@ struct MoeNvfp4Args {
 };
 size_t moe_nvfp4_workspace(int64_t m, int64_t experts, int64_t inter, int64_t topk);
 cudaError_t launch_moe_nvfp4(const MoeNvfp4Args &a, cudaStream_t st);
+cudaError_t moe_read_and_clear_error(cudaStream_t st, unsigned *out);
 
 // Layer norm / RMS norm of rows [n x c], forward (out = y; mean and rstd
 // written) and backward (out = dx; dw, db).

@@ -7,25 +7,32 @@
 //
 // Floor: the chosen experts' weights from HBM (9/16 byte each).  Three kernels:
 //   1. router logits, a CTA an expert;
-//   2. gate and up: a unit is 16 rows of gate and the same 16 of up of one
-//      chosen expert, for all tokens that chose it; eight warps share K, the
-//      next unit's weights are in flight while one is reduced;
-//   3. down: a CTA owns 16 rows of y and runs through all chosen experts, its
-//      warps sharing (expert, K) steps, so that y is summed in the CTA's
-//      registers and written once, without atomics.
+//   2. gate and up: a unit is 8 rows of gate and the same 8 of up of one chosen
+//      expert, for all tokens that chose it.  Both are contiguous in memory: a
+//      producer thread keeps a ring of bulk copies into shared memory ahead of
+//      two or four groups of warps, which take a unit each and share its K;
+//   3. down: a CTA owns 16 rows of y and runs through all chosen experts in the
+//      same way, its 16 warps sharing (expert, K) steps, so that y is summed in
+//      the CTA's registers and written once, without atomics.
+// With loads issued by the threads themselves and K shared by eight warps (a
+// unit's 16 rows of each kind reduced before the next), sixteen tokens of 128
+// experts, 2048/768, took 91 us for the second kernel and 65 for the third.
 // Kernels 2 and 3 each choose the experts from the logits themselves: it takes
 // a warp half a microsecond a token, less than one more kernel, and kernel 3
-// does it, and loads its first weights, while kernel 2 is still running
-// (kernel 2 lets it start once the logits are there).
+// does it, and starts its copies, before kernel 2 is through (kernel 2 lets it
+// start once the logits are there).
 //
 // Both products run on mma.m16n8k16 (weight rows as M, tokens as N), decoded
-// in registers as in the few-token product.  In the down product the
-// activations are FP32 values p * sg * a: each goes in as two BF16 numbers (16
-// bits; a BF16 y rounds to 8) or, for an FP32 y, three (24 bits), in columns of
-// their own that are added at the end, so nothing is rounded between the two
-// products beyond that.
+// in registers as in the few-token product.  In the first, rows 0 to 7 of the M
+// axis are gate and 8 to 15 up, so that a lane holds both of an activation's
+// factors.  In the second the activations are FP32 values p * sg * a: each goes
+// in as two BF16 numbers (16 bits; a BF16 y rounds to 8) or, for an FP32 y,
+// three (24 bits), in columns of their own that are added at the end, so nothing
+// is rounded between the two products beyond that.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "jetq_internal.h"
 #include "nvfp4_mma.cuh"
@@ -33,10 +40,20 @@
 
 namespace jetq {
 
+__device__ unsigned g_moe_error;
+
 namespace {
 
+constexpr unsigned kErrTimeout = 1u;
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+
 constexpr int kMaxTokens = 16, kMaxExperts = 256, kMaxTop = 16;
-constexpr int kRows = 16, kStep = 128; // rows a unit, columns a warp step
+constexpr int kStep = 128;             // columns a warp step
+constexpr int kConsumers = 16;         // warps that compute; one more copies
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kMaxStages = 24;
+constexpr int kRingBytes = 192 * 1024;
+constexpr int64_t kPrefetchBytes = 32 << 20; // down weights that kernel 2 brings into L2 for kernel 3
 
 struct MoeParams {
     const uint16_t *x, *router;
@@ -52,9 +69,11 @@ struct MoeParams {
     void *y;
     int64_t ldy;
     int out_bf16;
+    int stages;      // of the kernel's ring
+    unsigned long long limit_ns;
 };
 
-constexpr int kRouterThreads = 128;
+constexpr int kRouterThreads = 256;
 
 // Logits of one expert, eight tokens at a time; the CTA's threads share K.
 __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const MoeParams p)
@@ -71,18 +90,20 @@ __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const MoeParams p
             acc[i] = make_float2(0.0f, 0.0f);
         for (int k = 8 * threadIdx.x; k < p.h; k += 8 * kRouterThreads) { // h and the rows are whole vectors
             const uint4 a = __ldg(reinterpret_cast<const uint4 *>(w + k));
-            const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+            uint4 b[8]; // all in flight; past the last token its row again
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (t0 + i < p.m) {
-                    const uint4 b = __ldg(reinterpret_cast<const uint4 *>(p.x + (t0 + i) * p.ldx + k));
-                    const uint32_t v[4] = {b.x, b.y, b.z, b.w};
+                b[i] = __ldg(reinterpret_cast<const uint4 *>(p.x + min(t0 + i, p.m - 1) * p.ldx + k));
+            const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i] = __ffma2_rn(
-                            make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)),
-                            make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u)), acc[i]);
-                }
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t v[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i] = __ffma2_rn(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)),
+                                        make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u)),
+                                        acc[i]);
+            }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -217,38 +238,56 @@ __device__ __forceinline__ int nth_bit(unsigned mask, int n)
     return __ffs(mask) - 1;
 }
 
-// Codes and scales of two rows (g and g + 8 of 16) of a warp step.
-struct Codes {
-    uint4 a, b;
-    uint32_t fa, fb;
-    __device__ __forceinline__ void clear()
+// acc += two weight rows (32 codes and 2 scales of a lane each) x a column's 32 values: pairs (0, 4), (1, 5),
+// (2, 6), (3, 7), as the weights come.
+struct Decoded {
+    uint32_t a[4][4], b[4][4];
+    __device__ __forceinline__ void decode(const uint4 &wa, const uint4 &wb, uint32_t fa, uint32_t fb)
     {
-        a = b = make_uint4(0, 0, 0, 0);
-        fa = fb = 0;
+        uint32_t sa[2], sb[2];
+        decode_scales(fa, sa);
+        decode_scales(fb, sb);
+        const uint32_t ua[4] = {wa.x, wa.y, wa.z, wa.w}, ub[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            decode8(ua[j], sa[j >> 1], a[j]);
+            decode8(ub[j], sb[j >> 1], b[j]);
+        }
     }
-    // q, sb: row g's; K columns a row; the rows are 8 apart
-    __device__ __forceinline__ void load(const uint8_t *q, const uint8_t *sb, int K, int step)
+    __device__ __forceinline__ void multiply(float (&acc)[4], const uint4 (&x)[4]) const
     {
-        a = __ldcs(reinterpret_cast<const uint4 *>(q + step * 64)); // each weight is read once
-        b = __ldcs(reinterpret_cast<const uint4 *>(q + (int64_t)4 * K + step * 64));
-        fa = __ldg(reinterpret_cast<const uint16_t *>(sb + step * 8));
-        fb = __ldg(reinterpret_cast<const uint16_t *>(sb + K / 2 + step * 8));
-    }
-    // the pairs that the MMA takes of eight values j of each row
-    __device__ __forceinline__ void decode(int j, const uint32_t (&sa)[2], const uint32_t (&sb)[2], uint32_t (&pa)[4],
-                                           uint32_t (&pb)[4]) const
-    {
-        decode8(j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : a.w, sa[j >> 1], pa);
-        decode8(j == 0 ? b.x : j == 1 ? b.y : j == 2 ? b.z : b.w, sb[j >> 1], pb);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            mma_16816(acc, a[j][0], b[j][0], a[j][1], b[j][1], __byte_perm(x[j].x, x[j].z, 0x5410),
+                      __byte_perm(x[j].x, x[j].z, 0x7632));
+            mma_16816(acc, a[j][2], b[j][2], a[j][3], b[j][3], __byte_perm(x[j].y, x[j].w, 0x5410),
+                      __byte_perm(x[j].y, x[j].w, 0x7632));
+        }
     }
 };
 
-// acc += rows x a column (a lane's eight values x): pairs (0, 4), (1, 5), (2, 6), (3, 7), as the weights come
-__device__ __forceinline__ void multiply(float (&acc)[4], const uint32_t (&pa)[4], const uint32_t (&pb)[4],
-                                         const uint4 &x)
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
 {
-    mma_16816(acc, pa[0], pb[0], pa[1], pb[1], __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632));
-    mma_16816(acc, pa[2], pb[2], pa[3], pb[3], __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds16(uint32_t addr)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void prefetch_l2(const uint8_t *src, int64_t bytes)
+{
+    for (int64_t at = 0; at < bytes; at += 16384)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src + at),
+                     "r"((uint32_t)(bytes - at < 16384 ? bytes - at : 16384))
+                     : "memory");
 }
 
 // a as the sum of BF16 numbers, rounded to nearest each.
@@ -263,18 +302,82 @@ __device__ __forceinline__ void split(float a, __nv_bfloat16 (&out)[PARTS])
     }
 }
 
-constexpr int kGateWarps = 8, kGateUnroll = 2;
+// The ring: `stages` buffers, each filled by the producer thread's bulk copies
+// (full) and given back by the warps that read it (empty).
+struct Ring {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int abort_word;
+};
 
-// MT: tokens of an expert in eights; PARTS: BF16 numbers an activation is stored as
-template <int MT, int PARTS>
-__global__ void __launch_bounds__(32 * kGateWarps, 2) k_moe_gate_up(const MoeParams p)
+__device__ __forceinline__ void init_ring(Ring &ring, int stages, int readers)
 {
+    if (threadIdx.x == 0) {
+        ring.abort_word = 0;
+        for (int s = 0; s < stages; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&ring.full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ring.empty[s]), readers);
+        }
+        ptx::fence_barrier_init();
+    }
+    // the caller's next __syncthreads makes them visible
+}
+
+// The producer thread: buffer `i % stages` gets item i, for each of `items`; copy(i, buffer, barrier) issues `bytes`.
+template <class F>
+__device__ __forceinline__ void produce(Ring &ring, int stages, int items, uint32_t bytes,
+                                        unsigned long long limit_ns, F copy)
+{
+    volatile int *abort_flag = &ring.abort_word;
+    int s = 0, i = 0;
+    uint32_t ph = 0;
+    for (; i < items; ++i) {
+        if (!ptx::mbar_wait(ptx::smem_addr(&ring.empty[s]), ph ^ 1u, abort_flag, &g_moe_error, kErrTimeout, limit_ns))
+            break;
+        const uint32_t bar = ptx::smem_addr(&ring.full[s]);
+        ptx::mbar_arrive_expect_tx(bar, bytes);
+        copy(i, s, bar);
+        if (++s == stages) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+    // no copy may be in flight when the CTA ends
+    for (int q = 0; q < stages && q < i; ++q)
+        ptx::mbar_wait(ptx::smem_addr(&ring.full[q]), (uint32_t)((i - 1 - q) / stages) & 1u, abort_flag, &g_moe_error,
+                       kErrTimeout, limit_ns, false);
+}
+
+// A reader's wait for item i.  After a timeout the warps still run through
+// their items and meet their barriers, on whatever the buffers hold.
+__device__ __forceinline__ void wait_full(Ring &ring, int stages, int i, unsigned long long limit_ns)
+{
+    ptx::mbar_wait(ptx::smem_addr(&ring.full[i % stages]), (uint32_t)(i / stages) & 1u, &ring.abort_word, &g_moe_error,
+                   kErrTimeout, limit_ns);
+}
+
+__device__ __forceinline__ void give_back(Ring &ring, int stages, int i, int lane)
+{
+    __syncwarp();
+    if (lane == 0)
+        ptx::mbar_arrive(ptx::smem_addr(&ring.empty[i % stages]));
+}
+
+constexpr int kUnitRows = 8; // of gate and of up
+
+// KS: warps that share a unit's K.  PARTS: BF16 numbers an activation is stored as.
+template <int KS, int PARTS>
+__global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
+{
+    constexpr int kGroups = kConsumers / KS;
+    extern __shared__ uint8_t smem_raw[];
     __shared__ Routes r;
-    __shared__ float red[kGateWarps][2 * kRows][8 * MT + 1];
-    __shared__ int list[kMaxTokens]; // the unit's tokens
+    __shared__ Ring ring;
+    __shared__ float red[2][kConsumers][2 * kUnitRows][9];
+    uint8_t *buffers = ptx::align_smem<128>(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    init_ring(ring, p.stages, KS);
     ptx::grid_dep_wait();
     ptx::grid_dep_launch(); // after the wait: the next kernel may read the logits at once
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     choose(p, r);
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < p.m * p.topk; i += blockDim.x) {
@@ -283,258 +386,274 @@ __global__ void __launch_bounds__(32 * kGateWarps, 2) k_moe_gate_up(const MoePar
             if (p.weights)
                 p.weights[i] = r.p[i / p.topk][i % p.topk];
         }
-    const int blocks = p.inter / kRows, units = r.slots * blocks;
-    const int steps = (p.h + kStep - 1) / kStep;
-    const int s0 = steps * warp / kGateWarps, s1 = steps * (warp + 1) / kGateWarps;
-    const int left = p.h - 32 * t; // columns from this lane's first one on
+    const int blocks = p.inter / kUnitRows, units = r.slots * blocks;
+    const int items = units > (int)blockIdx.x ? (units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    // a buffer: gate codes, up codes (4 h bytes each), gate scales, up scales (h / 2 each)
+    const uint32_t codes = 4u * p.h, scales = (uint32_t)p.h / 2, bytes = 2 * (codes + scales);
 
-    struct Batch {
-        Codes gate[kGateUnroll], up[kGateUnroll];
-    };
-    auto load = [&](int unit, int s, Batch &b) {
-#pragma unroll
-        for (int u = 0; u < kGateUnroll; ++u) {
-            b.gate[u].clear();
-            b.up[u].clear();
-        }
-        if (unit >= units)
-            return;
-        const int64_t row = (int64_t)r.expert[unit / blocks] * 2 * p.inter + unit % blocks * kRows + g;
-        const uint8_t *q = p.q13 + row * (p.h / 2) + 16 * t, *sb = p.sb13 + row * (p.h / 16) + 2 * t;
-        const int64_t up_q = (int64_t)p.inter * (p.h / 2), up_sb = (int64_t)p.inter * (p.h / 16);
-#pragma unroll
-        for (int u = 0; u < kGateUnroll; ++u)
-            if (s + u < s1 && (s + u) * kStep < left) {
-                b.gate[u].load(q, sb, p.h, s + u);
-                b.up[u].load(q + up_q, sb + up_sb, p.h, s + u);
+    if (warp == kConsumers) {
+        if (lane == 0) {
+            produce(ring, p.stages, items, bytes, p.limit_ns, [&](int i, int s, uint32_t bar) {
+                const int unit = (int)blockIdx.x + i * (int)gridDim.x;
+                const int64_t row =
+                    (int64_t)r.expert[unit / blocks] * 2 * p.inter + (int64_t)(unit % blocks) * kUnitRows;
+                const uint32_t dst = ptx::smem_addr(buffers) + (uint32_t)s * bytes;
+                const uint8_t *q = p.q13 + row * (p.h / 2), *sb = p.sb13 + row * (p.h / 16);
+                ptx::bulk_load(dst, q, codes, bar);
+                ptx::bulk_load(dst + codes, q + (int64_t)p.inter * (p.h / 2), codes, bar);
+                ptx::bulk_load(dst + 2 * codes, sb, scales, bar);
+                ptx::bulk_load(dst + 2 * codes + scales, sb + (int64_t)p.inter * (p.h / 16), scales, bar);
+            });
+        } else if (lane == 1) { // the down weights of few experts into L2, a share a CTA
+            const int64_t q = (int64_t)p.h * (p.inter / 2), sb = (int64_t)p.h * (p.inter / 16);
+            if (r.slots * (q + sb) <= kPrefetchBytes) {
+                const int64_t share = ((q + (int64_t)gridDim.x - 1) / gridDim.x + 15) / 16 * 16;
+                const int64_t a = min(q, share * blockIdx.x), b = min(q, a + share);
+                for (int i = 0; i < r.slots; ++i)
+                    prefetch_l2(p.q2 + r.expert[i] * q + a, b - a);
+                if ((int)blockIdx.x < r.slots)
+                    prefetch_l2(p.sb2 + r.expert[blockIdx.x] * sb, sb);
             }
-    };
-    Batch now, next;
-    load(blockIdx.x, s0, now);
-    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int e = r.expert[unit / blocks];
+        }
+        __syncwarp();
+        return;
+    }
+
+    const int group = warp / KS, kw = warp % KS;
+    const int steps = (p.h + kStep - 1) / kStep;
+    const int s0 = steps * kw / KS, s1 = steps * (kw + 1) / KS;
+    const int left = p.h - 32 * t; // columns from this lane's first one on
+    int buf = 0;
+    for (int i = group; i < items; i += kGroups) {
+        const int unit = (int)blockIdx.x + i * (int)gridDim.x;
+        const int e = r.expert[unit / blocks], row0 = unit % blocks * kUnitRows;
         const unsigned tokens = r.tokens[e];
         const int many = __popc(tokens);
-        const uint16_t *xr[MT]; // this lane's columns' rows of x
-        bool have[MT], on[MT];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            on[i] = 8 * i < many;
-            have[i] = 8 * i + g < many;
-            const int tok = have[i] ? nth_bit(tokens, 8 * i + g) : 0;
-            xr[i] = p.x + tok * p.ldx + 32 * t;
-            if (warp == 0 && t == 0 && have[i])
-                list[8 * i + g] = tok;
-        }
-        float ga[MT][4], ua[MT][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                ga[i][j] = ua[i][j] = 0.0f;
-        for (int s = s0; s < s1; s += kGateUnroll) {
-            if (s + kGateUnroll < s1)
-                load(unit, s + kGateUnroll, next);
-            else
-                load(unit + gridDim.x, s0, next);
-#pragma unroll
-            for (int u = 0; u < kGateUnroll; ++u) {
-                if (s + u >= s1)
-                    break;
-                uint32_t sga[2], sgb[2], sua[2], sub[2];
-                decode_scales(now.gate[u].fa, sga);
-                decode_scales(now.gate[u].fb, sgb);
-                decode_scales(now.up[u].fa, sua);
-                decode_scales(now.up[u].fb, sub);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    if (!on[i]) // few experts have more than eight tokens: those decode twice
-                        break;
-                    uint4 x[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[j] = have[i] && (s + u) * kStep < left
-                                   ? __ldg(reinterpret_cast<const uint4 *>(xr[i] + (s + u) * kStep + 8 * j))
-                                   : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t pa[4], pb[4];
-                        now.gate[u].decode(j, sga, sgb, pa, pb);
-                        multiply(ga[i], pa, pb, x[j]);
-                        now.up[u].decode(j, sua, sub, pa, pb);
-                        multiply(ua[i], pa, pb, x[j]);
-                    }
-                }
-            }
-            now = next;
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            if (!on[i])
-                break;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = g + (j >> 1) * 8, col = 8 * i + 2 * t + (j & 1);
-                red[warp][row][col] = ga[i][j];
-                red[warp][kRows + row][col] = ua[i][j];
-            }
-        }
-        __syncthreads();
         const float scale = __ldg(p.sg13 + e) * 65536.0f, out = __ldg(p.sg2 + e);
-        for (int i = threadIdx.x; i < kRows * many; i += 32 * kGateWarps) {
-            const int row = i % kRows, n = i / kRows, tok = list[n];
-            float gate = 0.0f, up = 0.0f;
+        const uint32_t at = ptx::smem_addr(buffers) + (uint32_t)(i % p.stages) * bytes;
+        const uint32_t row_q = at + (uint32_t)(g * (p.h / 2) + 16 * t);
+        const uint32_t row_s = at + 2 * codes + (uint32_t)(g * (p.h / 16) + 2 * t);
+        for (int n0 = 0; n0 < many; n0 += 8) { // eight tokens at a time; few experts have more
+            const bool have = n0 + g < many;
+            const uint16_t *xr = p.x + (have ? nth_bit(tokens, n0 + g) : 0) * p.ldx + 32 * t;
+            auto column = [&](int s, uint4 (&x)[4]) {
 #pragma unroll
-            for (int w = 0; w < kGateWarps; ++w) {
-                gate += red[w][row][n];
-                up += red[w][kRows + row][n];
+                for (int j = 0; j < 4; ++j)
+                    x[j] = have && s * kStep < left ? __ldg(reinterpret_cast<const uint4 *>(xr + s * kStep) + j)
+                                                    : make_uint4(0, 0, 0, 0);
+            };
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}; // gate, gate, up, up of row g, tokens 2t and 2t + 1
+            uint4 x[4], next[4];
+            if (s0 < s1)
+                column(s0, x);
+            if (n0 == 0)
+                wait_full(ring, p.stages, i, p.limit_ns);
+            for (int s = s0; s < s1; ++s) {
+                if (s + 1 < s1)
+                    column(s + 1, next);
+                uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                uint32_t fa = 0, fb = 0;
+                if (s * kStep < left) {
+                    a = lds128(row_q + 64u * s);
+                    b = lds128(row_q + codes + 64u * s);
+                    fa = lds16(row_s + 8u * s);
+                    fb = lds16(row_s + scales + 8u * s);
+                }
+                Decoded w;
+                w.decode(a, b, fa, fb);
+                w.multiply(acc, x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[j] = next[j];
             }
-            gate *= scale;
-            up *= scale;
-            const int j = r.choice[e][tok];
-            const float a = __fdiv_rn(gate, 1.0f + expf(-gate)) * up * (r.p[tok][j] * out);
-            __nv_bfloat16 part[PARTS];
-            split<PARTS>(a, part);
-            __nv_bfloat16 *at =
-                p.act + (int64_t)(tok * p.topk + j) * PARTS * p.inter + unit % blocks * kRows + row;
+            if (n0 + 8 >= many)
+                give_back(ring, p.stages, i, lane);
+            float(&mine)[2 * kUnitRows][9] = red[buf][warp];
+            mine[g][2 * t] = acc[0];
+            mine[g][2 * t + 1] = acc[1];
+            mine[kUnitRows + g][2 * t] = acc[2];
+            mine[kUnitRows + g][2 * t + 1] = acc[3];
+            ptx::named_bar_sync(1 + group, 32 * KS);
+            for (int k = kw * 32 + lane; k < kUnitRows * min(8, many - n0); k += 32 * KS) {
+                const int row = k % kUnitRows, n = k / kUnitRows, tok = nth_bit(tokens, n0 + n);
+                float gate = 0.0f, up = 0.0f;
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k)
-                at[(int64_t)k * p.inter] = part[k];
+                for (int w = 0; w < KS; ++w) {
+                    gate += red[buf][group * KS + w][row][n];
+                    up += red[buf][group * KS + w][kUnitRows + row][n];
+                }
+                gate *= scale;
+                up *= scale;
+                const int j = r.choice[e][tok];
+                const float a = __fdiv_rn(gate, 1.0f + expf(-gate)) * up * (r.p[tok][j] * out);
+                __nv_bfloat16 part[PARTS];
+                split<PARTS>(a, part);
+                __nv_bfloat16 *to = p.act + (int64_t)(tok * p.topk + j) * PARTS * p.inter + row0 + row;
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q)
+                    to[(int64_t)q * p.inter] = part[q];
+            }
+            buf ^= 1; // the other half: the next barrier tells that this one has been read
         }
-        __syncthreads();
     }
 }
 
-constexpr int kDownUnroll = 2;
+constexpr int kDownRows = 16;
 
 // NT: tiles of eight columns; a token has COLS columns (PARTS of them in use).
-template <int NT, int COLS, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 1 : 2) k_moe_down(const MoeParams p)
+template <int NT, int COLS>
+__global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
 {
     constexpr int kParts = COLS == 4 ? 3 : 2, kTok = 8 / COLS; // tokens a tile
+    extern __shared__ uint8_t smem_raw[];
     __shared__ Routes r;
-    __shared__ float red[kWarps][kRows][kTok * NT + 1];
+    __shared__ Ring ring;
+    __shared__ float red[kConsumers][kDownRows][kTok * NT + 1];
+    uint8_t *buffers = ptx::align_smem<128>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    init_ring(ring, p.stages, kConsumers);
     choose(p, r); // from the logits, which were there before this kernel could start
-    const int steps = (p.inter + kStep - 1) / kStep;
-    const int total = r.slots * steps; // (slot, K step) pairs
-    const int i0 = (int)((int64_t)total * warp / kWarps), i1 = (int)((int64_t)total * (warp + 1) / kWarps);
-    const int64_t row0 = (int64_t)blockIdx.x * kRows;
-    const int left = p.inter - 32 * t;
-
-    struct Batch {
-        Codes c[kDownUnroll];
-    };
-    struct Cursor { // a (slot, K step) pair
-        int slot, s;
-        __device__ __forceinline__ void advance(int steps)
-        {
-            if (++s == steps) {
-                s = 0;
-                ++slot;
-            }
-        }
-    };
-    Cursor ahead = {i0 / steps, i0 % steps}, here = ahead;
-    auto load = [&](int i, Batch &b) {
+    const int64_t row0 = (int64_t)blockIdx.x * kDownRows;
+    // a buffer: 16 rows' codes (8 inter bytes), their scales (inter)
+    const uint32_t codes = 8u * p.inter, scales = (uint32_t)p.inter, bytes = codes + scales;
+    if (warp == kConsumers) {
+        if (lane == 0)
+            produce(ring, p.stages, r.slots, bytes, p.limit_ns, [&](int i, int s, uint32_t bar) {
+                const int64_t row = (int64_t)r.expert[i] * p.h + row0;
+                const uint32_t dst = ptx::smem_addr(buffers) + (uint32_t)s * bytes;
+                ptx::bulk_load(dst, p.q2 + row * (p.inter / 2), codes, bar);
+                ptx::bulk_load(dst + codes, p.sb2 + row * (p.inter / 16), scales, bar);
+            });
+    } else {
+        const int steps = (p.inter + kStep - 1) / kStep;
+        const int left = p.inter - 32 * t;
+        float acc[NT][4];
 #pragma unroll
-        for (int u = 0; u < kDownUnroll; ++u) {
-            b.c[u].clear();
-            if (i + u < i1) {
-                const int slot = ahead.slot, s = ahead.s;
-                ahead.advance(steps);
-                if (s * kStep < left) {
-                    const int64_t row = (int64_t)r.expert[slot] * p.h + row0 + g;
-                    b.c[u].load(p.q2 + row * (p.inter / 2) + 16 * t, p.sb2 + row * (p.inter / 16) + 2 * t, p.inter, s);
-                }
-            }
-        }
-    };
-    float acc[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[i][j] = 0.0f;
-    Batch now, next;
-    load(i0, now);
-    ptx::grid_dep_wait(); // the activations
-    ptx::grid_dep_launch();
-    for (int i = i0; i < i1; i += kDownUnroll) {
-        load(i + kDownUnroll, next);
-#pragma unroll
-        for (int u = 0; u < kDownUnroll; ++u) {
-            if (i + u >= i1)
-                break;
-            const int s = here.s, e = r.expert[here.slot];
-            here.advance(steps);
-            const unsigned tokens = r.tokens[e];
-            uint32_t sa[2], sb[2], pa[4][4], pb[4][4];
-            decode_scales(now.c[u].fa, sa);
-            decode_scales(now.c[u].fb, sb);
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                now.c[u].decode(j, sa, sb, pa[j], pb[j]);
+                acc[i][j] = 0.0f;
+        ptx::grid_dep_wait(); // the activations
+        ptx::grid_dep_launch();
+        int first = warp; // this warp's first step of the slot: (slot, step) pairs go to the warps in turn
+        for (int i = 0; i < r.slots; ++i) {
+            const int e = r.expert[i];
+            const unsigned tokens = r.tokens[e];
+            const uint32_t at = ptx::smem_addr(buffers) + (uint32_t)(i % p.stages) * bytes;
+            bool waited = false;
+            int s = first;
+            for (; s < steps; s += kConsumers) {
+                auto column = [&](int n, uint4 (&x)[4]) { // tile n's values of this lane
+                    const int tok = n * kTok + g / COLS, part = g % COLS;
+                    const bool have = part < kParts && (tokens >> tok & 1u) && s * kStep < left;
+                    const __nv_bfloat16 *from = p.act;
+                    if (have)
+                        from += ((int64_t)(tok * p.topk + r.choice[e][tok]) * kParts + part) * p.inter + s * kStep +
+                                32 * t;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if ((tokens >> (n * kTok) & ((1u << kTok) - 1u)) == 0) // no token of this tile takes the expert
-                    continue;
-                const int tok = n * kTok + g / COLS, part = g % COLS;
-                const bool have = part < kParts && (tokens >> tok & 1u) && s * kStep < left;
-                const __nv_bfloat16 *at = p.act;
-                if (have)
-                    at += ((int64_t)(tok * p.topk + r.choice[e][tok]) * kParts + part) * p.inter + s * kStep + 32 * t;
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = have ? __ldcg(reinterpret_cast<const uint4 *>(from) + j) : make_uint4(0, 0, 0, 0);
+                };
+                auto on = [&](int n) { return (tokens >> (n * kTok) & ((1u << kTok) - 1u)) != 0; };
                 uint4 x[4];
+                int tile = 0; // the first one with a token that takes the expert
+                while (tile < NT - 1 && !on(tile))
+                    ++tile;
+                column(tile, x);
+                if (!waited)
+                    wait_full(ring, p.stages, i, p.limit_ns);
+                waited = true;
+                uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                uint32_t fa = 0, fb = 0;
+                if (s * kStep < left) {
+                    const uint32_t q = at + (uint32_t)(g * (p.inter / 2) + 16 * t + 64 * s);
+                    const uint32_t sb = at + codes + (uint32_t)(g * (p.inter / 16) + 2 * t + 8 * s);
+                    a = lds128(q);
+                    b = lds128(q + 4u * p.inter);
+                    fa = lds16(sb);
+                    fb = lds16(sb + (uint32_t)p.inter / 2);
+                }
+                Decoded w;
+                w.decode(a, b, fa, fb);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[j] = have ? __ldcg(reinterpret_cast<const uint4 *>(at) + j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    multiply(acc[n], pa[j], pb[j], x[j]);
+                for (int n = 0; n < NT; ++n) {
+                    if (n < tile || !on(n))
+                        continue;
+                    if (n > tile)
+                        column(n, x);
+                    w.multiply(acc[n], x);
+                }
             }
+            first = s - steps;
+            if (!waited) // a warp without a step waits too: it must not give a buffer back twice in one round
+                wait_full(ring, p.stages, i, p.limit_ns);
+            give_back(ring, p.stages, i, lane);
         }
-        now = next;
+        // the parts of a token's sum lie in neighbouring columns
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float v = acc[n][2 * half] + acc[n][2 * half + 1];
+                if (COLS == 4)
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                if (COLS == 2 || (t & 1) == 0)
+                    red[warp][g + 8 * half][n * kTok + (COLS == 2 ? t : t >> 1)] = v;
+            }
     }
-    // the parts of a token's sum lie in neighbouring columns
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v = acc[n][2 * half] + acc[n][2 * half + 1];
-            if (COLS == 4)
-                v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-            if (COLS == 2 || (t & 1) == 0)
-                red[warp][g + 8 * half][n * kTok + (COLS == 2 ? t : t >> 1)] = v;
-        }
     __syncthreads();
-    for (int i = threadIdx.x; i < kRows * p.m; i += 32 * kWarps) {
-        const int row = i % kRows, tok = i / kRows;
+    if (warp == kConsumers)
+        return;
+    for (int i = threadIdx.x; i < kDownRows * p.m; i += 32 * kConsumers) {
+        const int row = i % kDownRows, tok = i / kDownRows;
         float a = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
+        for (int w = 0; w < kConsumers; ++w)
             a += red[w][row][tok];
         a *= 65536.0f; // of the decoding
-        const int64_t at = tok * p.ldy + row0 + row;
+        const int64_t to = tok * p.ldy + row0 + row;
         if (p.out_bf16)
-            static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(a);
+            static_cast<__nv_bfloat16 *>(p.y)[to] = __float2bfloat16_rn(a);
         else
-            static_cast<float *>(p.y)[at] = a;
+            static_cast<float *>(p.y)[to] = a;
     }
 }
 
-template <int COLS, int kWarps>
-cudaError_t run_down(const MoeParams &p, cudaStream_t st)
+// One launch with a ring of as many buffers as there is room for (`items` at most).
+template <class K>
+cudaError_t run_ring(K kern, std::atomic<unsigned long long> &configured, int64_t grid, int64_t buffer, int64_t items,
+                     MoeParams p, cudaStream_t st)
 {
-    const dim3 grid((unsigned)(p.h / kRows)), block(32 * kWarps);
-    constexpr int kTok = 8 / COLS;
-    if (p.m <= kTok)
-        return launch_pdl(k_moe_down<1, COLS, kWarps>, grid, block, 0, st, p);
-    if (p.m <= 2 * kTok)
-        return launch_pdl(k_moe_down<2, COLS, kWarps>, grid, block, 0, st, p);
-    if constexpr (COLS == 4)
-        if (p.m > 4 * kTok)
-            return launch_pdl(k_moe_down<8, COLS, kWarps>, grid, block, 0, st, p);
-    return launch_pdl(k_moe_down<4, COLS, kWarps>, grid, block, 0, st, p);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !(configured.load(std::memory_order_relaxed) >> dev & 1u)) {
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 128)) !=
+            cudaSuccess)
+            return e;
+        if (dev < 64)
+            configured.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    int64_t stages = kRingBytes / buffer;
+    stages = stages < kMaxStages ? stages : kMaxStages;
+    p.stages = (int)(stages < items ? stages : items);
+    return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), (size_t)(p.stages * buffer + 128), st, p);
+}
+
+template <int KS, int PARTS>
+cudaError_t run_gate_up(const MoeParams &p, int64_t units, cudaStream_t st)
+{
+    static std::atomic<unsigned long long> configured{0};
+    const int64_t grid = units < sm_count() ? units : sm_count();
+    return run_ring(k_moe_gate_up<KS, PARTS>, configured, grid, 9 * (int64_t)p.h, (units + grid - 1) / grid, p, st);
+}
+
+template <int NT, int COLS>
+cudaError_t run_down(const MoeParams &p, int64_t slots, cudaStream_t st)
+{
+    static std::atomic<unsigned long long> configured{0};
+    return run_ring(k_moe_down<NT, COLS>, configured, p.h / kDownRows, 9 * (int64_t)p.inter, slots, p, st);
 }
 
 size_t logits_bytes(int64_t m, int64_t experts)
@@ -575,24 +694,47 @@ cudaError_t launch_moe_nvfp4(const MoeNvfp4Args &a, cudaStream_t st)
     p.y = a.y;
     p.ldy = a.ldy;
     p.out_bf16 = a.out_dtype == JETQ_OUT_BF16;
+    p.limit_ns = kWaitLimitNs;
     cudaError_t e = launch_pdl(k_moe_router, dim3((unsigned)a.experts), dim3(kRouterThreads), 0, st, p);
     if (e != cudaSuccess)
         return e;
-    // as many CTAs as run at a time, or units at most
-    const int64_t used = a.m * a.topk < a.experts ? a.m * a.topk : a.experts, units = used * (a.inter / kRows);
-    const int64_t cap = 2 * (int64_t)sm_count();
-    const dim3 grid((unsigned)(units < cap ? units : cap)), block(32 * kGateWarps);
+    // slots at most
+    const int64_t slots = a.m * a.topk < a.experts ? a.m * a.topk : a.experts, units = slots * (a.inter / kUnitRows);
+    // Warps that share a unit: eight where a CTA has few units, so that all of
+    // them run at a time; four (half the reductions) where it has many.
+    const bool few = units <= 8 * (int64_t)sm_count();
     if (p.out_bf16)
-        e = a.m <= 8 ? launch_pdl(k_moe_gate_up<1, 2>, grid, block, 0, st, p)
-                     : launch_pdl(k_moe_gate_up<2, 2>, grid, block, 0, st, p);
+        e = few ? run_gate_up<8, 2>(p, units, st) : run_gate_up<4, 2>(p, units, st);
     else
-        e = a.m <= 8 ? launch_pdl(k_moe_gate_up<1, 3>, grid, block, 0, st, p)
-                     : launch_pdl(k_moe_gate_up<2, 3>, grid, block, 0, st, p);
+        e = few ? run_gate_up<8, 3>(p, units, st) : run_gate_up<4, 3>(p, units, st);
     if (e != cudaSuccess)
         return e;
-    if (a.h / kRows <= sm_count())
-        return p.out_bf16 ? run_down<2, 16>(p, st) : run_down<4, 16>(p, st);
-    return p.out_bf16 ? run_down<2, 8>(p, st) : run_down<4, 8>(p, st);
+    if (p.out_bf16)
+        return a.m <= 4   ? run_down<1, 2>(p, slots, st)
+               : a.m <= 8 ? run_down<2, 2>(p, slots, st)
+                          : run_down<4, 2>(p, slots, st);
+    return a.m <= 2   ? run_down<1, 4>(p, slots, st)
+           : a.m <= 4 ? run_down<2, 4>(p, slots, st)
+           : a.m <= 8 ? run_down<4, 4>(p, slots, st)
+                      : run_down<8, 4>(p, slots, st);
+}
+
+cudaError_t moe_read_and_clear_error(cudaStream_t st, unsigned *out)
+{
+    unsigned v = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_moe_error, sizeof v, 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess)
+        return e;
+    *out |= v;
+    if (v) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbolAsync(g_moe_error, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
+        if (e == cudaSuccess)
+            e = cudaStreamSynchronize(st);
+    }
+    return e;
 }
 
 } // namespace jetq

@@ -169,9 +169,9 @@ def _moe(L, **k):
     (dict(bytes=64), INVALID),
     (dict(m=17), SHAPE), (dict(e=257), SHAPE), (dict(topk=9), SHAPE), (dict(e=64, topk=17), SHAPE),
     (dict(h=48, ldx=48, ldr=48, ldy=48), SHAPE), (dict(i=48), SHAPE), (dict(ldx=56), SHAPE), (dict(ldr=56), SHAPE),
-    (dict(ldy=63), SHAPE), (dict(i=1 << 21), SHAPE),
+    (dict(ldy=63), SHAPE), (dict(i=16416), SHAPE), (dict(h=16416, ldx=16416, ldr=16416, ldy=16416), SHAPE),
     (dict(x=P(4104)), ALIGN), (dict(ldx=68), ALIGN), (dict(router=P(4104)), ALIGN), (dict(ldr=68), ALIGN),
-    (dict(q13=P(4104)), ALIGN), (dict(q2=P(4104)), ALIGN), (dict(sb13=P(4097)), ALIGN), (dict(sb2=P(4097)), ALIGN),
+    (dict(q13=P(4104)), ALIGN), (dict(q2=P(4104)), ALIGN), (dict(sb13=P(4104)), ALIGN), (dict(sb2=P(4104)), ALIGN),
     (dict(sg13=P(4098)), ALIGN), (dict(sg2=P(4098)), ALIGN), (dict(y=P(4097)), ALIGN), (dict(y=P(4098), dt=0), ALIGN),
     (dict(ids=P(4100)), ALIGN), (dict(p=P(4098)), ALIGN), (dict(ws=P(4104)), ALIGN),
 ])
