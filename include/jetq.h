@@ -585,8 +585,9 @@ JETQ_API jetq_status jetq_gemv_nvfp4(const uint8_t *qw, const uint8_t *sbw, cons
  *   p[i, j]  = exp(l of choice j) / sum of exp(l) over the chosen (renorm = 1) or over all experts (renorm = 0)
  *   a        = silu(gate x) * (up x), silu(z) = z / (1 + exp(-z))
  *   y[i]     = sum_j p[i, j] * down a       (gate, up, down and a of expert chosen[i, j])
- * Products of weights and x are exact, sums FP32; a enters the second product
- * with 16 bits (y BF16) or 24 (y F32); y is rounded once.
+ * Products of weights and x are exact (values of x below 2^-30 of their token's
+ * largest are rounded to steps of 2^-39 of it), sums FP32; a enters the second
+ * product with 16 bits (y BF16) or 24 (y F32); y is rounded once.
  *
  *   x, m, h, ldx       BF16 [m x h], row stride ldx (multiple of 8), 0 <= m <= 16
  *   router, ldr        BF16 [num_experts x h], row stride ldr (multiple of 8)
@@ -598,12 +599,12 @@ JETQ_API jetq_status jetq_gemv_nvfp4(const uint8_t *qw, const uint8_t *sbw, cons
  *   y, ldy             F32 or BF16 [m x h], any stride ldy >= h, element-aligned
  *   ids, weights       int64 and float [m x topk], the choices and p; each nullable
  *   workspace          device memory, 16-byte aligned, at least
- *                      jetq_moe_nvfp4_workspace_bytes(m, num_experts, inter, topk) bytes; calls that share
- *                      one must not overlap on the GPU
+ *                      jetq_moe_nvfp4_workspace_bytes(m, num_experts, h, inter, topk) bytes; calls that
+ *                      share one must not overlap on the GPU
  * Limits: 1 <= num_experts <= 256, 1 <= topk <= min(16, num_experts); h and inter multiples of 32, up to 16384.
  * m == 0 is a no-op.  Bitwise repeatable.  Three launches.
  */
-JETQ_API size_t jetq_moe_nvfp4_workspace_bytes(int64_t m, int64_t num_experts, int64_t inter, int64_t topk);
+JETQ_API size_t jetq_moe_nvfp4_workspace_bytes(int64_t m, int64_t num_experts, int64_t h, int64_t inter, int64_t topk);
 JETQ_API jetq_status jetq_moe_nvfp4(const uint16_t *x, int64_t m, int64_t h, int64_t ldx, const uint16_t *router,
                                     int64_t ldr, int64_t num_experts, int64_t topk, int renorm, const uint8_t *q13,
                                     const uint8_t *sb13, const float *sg13, int64_t inter, const uint8_t *q2,

@@ -98,7 +98,7 @@ def lib() -> ctypes.CDLL:
             "jetq_linear_distill_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64, I32]),
             "jetq_linear_distill_bwd": (I32, [P, I64, I64, I64, P, I64, I64, P, I64, P, I64, I64, I32, F32, P, P, P, P,
                                               I64, P, I32, I64, I32, P, ctypes.c_size_t, P]),
-            "jetq_moe_nvfp4_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64]),
+            "jetq_moe_nvfp4_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64, I64]),
             "jetq_moe_nvfp4": (I32, [P, I64, I64, I64, P, I64, I64, I64, I32, P, P, P, I64, P, P, P, P, I32, I64, P, P,
                                      P, ctypes.c_size_t, P]),
             "jetq_policy_loss_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
@@ -324,8 +324,8 @@ def jetq_gemv_nvfp4(qw, sbw, sgw, x, y, stream=None):
                                  _out_dtype(y), y.stride(0), _s(stream)), "jetq_gemv_nvfp4")
 
 
-def jetq_moe_nvfp4_workspace_bytes(m: int, num_experts: int, inter: int, topk: int) -> int:
-    return int(lib().jetq_moe_nvfp4_workspace_bytes(m, num_experts, inter, topk))
+def jetq_moe_nvfp4_workspace_bytes(m: int, num_experts: int, h: int, inter: int, topk: int) -> int:
+    return int(lib().jetq_moe_nvfp4_workspace_bytes(m, num_experts, h, inter, topk))
 
 
 def jetq_moe_nvfp4(x, router, topk, renorm, q13, sb13, sg13, q2, sb2, sg2, y, ids, weights, ws, stream=None):
@@ -718,7 +718,7 @@ def moe_nvfp4(x, router, w13, w2, topk, renorm=True, out_dtype=torch.bfloat16, w
     y = torch.empty((m, h), dtype=out_dtype, device=x.device)
     ids = torch.empty((m, topk), dtype=torch.int64, device=x.device)
     p = torch.empty((m, topk), dtype=torch.float32, device=x.device)
-    need = jetq_moe_nvfp4_workspace_bytes(m, e, i, topk)
+    need = jetq_moe_nvfp4_workspace_bytes(m, e, h, i, topk)
     if workspace is None or _bytes(workspace) < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     jetq_moe_nvfp4(_row_stride(x), _row_stride(router), topk, renorm, q13, sb13, sg13, q2, sb2, sg2, y, ids, p,

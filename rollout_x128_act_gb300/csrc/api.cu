@@ -1054,12 +1054,12 @@ jetq_status jetq_policy_loss_bwd(const float *nll, const float *nll_old, const f
     return from_cuda(launch_policy_bwd(g, static_cast<cudaStream_t>(stream)));
 }
 
-size_t jetq_moe_nvfp4_workspace_bytes(int64_t m, int64_t num_experts, int64_t inter, int64_t topk)
+size_t jetq_moe_nvfp4_workspace_bytes(int64_t m, int64_t num_experts, int64_t h, int64_t inter, int64_t topk)
 {
-    if (m <= 0 || m > 16 || num_experts <= 0 || num_experts > 256 || inter <= 0 || inter > 16384 || topk <= 0 ||
-        topk > 16)
+    if (m <= 0 || m > 16 || num_experts <= 0 || num_experts > 256 || h <= 0 || h > 16384 || inter <= 0 ||
+        inter > 16384 || topk <= 0 || topk > 16)
         return 0;
-    return moe_nvfp4_workspace(m, num_experts, inter, topk);
+    return moe_nvfp4_workspace(m, num_experts, h, inter, topk);
 }
 
 jetq_status jetq_moe_nvfp4(const uint16_t *x, int64_t m, int64_t h, int64_t ldx, const uint16_t *router, int64_t ldr,
@@ -1081,7 +1081,7 @@ jetq_status jetq_moe_nvfp4(const uint16_t *x, int64_t m, int64_t h, int64_t ldx,
     JQ_REQUIRE(x != nullptr && router != nullptr && q13 != nullptr && sb13 != nullptr && sg13 != nullptr &&
                    q2 != nullptr && sb2 != nullptr && sg2 != nullptr && y != nullptr && workspace != nullptr,
                JETQ_ERR_INVALID_ARG);
-    JQ_REQUIRE(workspace_bytes >= moe_nvfp4_workspace(m, num_experts, inter, topk), JETQ_ERR_INVALID_ARG);
+    JQ_REQUIRE(workspace_bytes >= moe_nvfp4_workspace(m, num_experts, h, inter, topk), JETQ_ERR_INVALID_ARG);
     JQ_REQUIRE(aligned16(x) && ldx % 8 == 0 && aligned16(router) && ldr % 8 == 0 && aligned16(q13) && aligned16(q2) &&
                    aligned16(sb13) && aligned16(sb2) && aligned4(sg13) && aligned4(sg2) && aligned16(workspace) &&
                    (reinterpret_cast<uintptr_t>(y) & (y_dtype == JETQ_OUT_F32 ? 3u : 1u)) == 0 &&

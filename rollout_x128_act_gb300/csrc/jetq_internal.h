@@ -279,7 +279,7 @@ struct MoeNvfp4Args {
     float *weights; // nullable
     void *ws;
 };
-size_t moe_nvfp4_workspace(int64_t m, int64_t experts, int64_t inter, int64_t topk);
+size_t moe_nvfp4_workspace(int64_t m, int64_t experts, int64_t h, int64_t inter, int64_t topk);
 cudaError_t launch_moe_nvfp4(const MoeNvfp4Args &a, cudaStream_t st);
 cudaError_t moe_read_and_clear_error(cudaStream_t st, unsigned *out);
 

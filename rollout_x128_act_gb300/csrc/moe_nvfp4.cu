@@ -30,6 +30,7 @@
 // three (24 bits), in columns of their own that are added at the end, so nothing
 // is rounded between the two products beyond that.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -63,6 +64,8 @@ struct MoeParams {
     const uint8_t *q13, *sb13, *q2, *sb2;
     const float *sg13, *sg2;
     float *logits;        // [m][experts]
+    __half *x16;          // [m][h]: x times a power of two, and its inverse [m]
+    float *unscale;
     __nv_bfloat16 *act;   // [m * topk][parts][inter]
     int64_t *ids;
     float *weights;
@@ -75,12 +78,59 @@ struct MoeParams {
 
 constexpr int kRouterThreads = 256;
 
-// Logits of one expert, eight tokens at a time; the CTA's threads share K.
+// A token's x as FP16 for the first product: times the power of two that puts
+// its largest value in [2^14, 2^15), which is exact for all values down to 2^-30
+// of the largest (below, rounded to steps of 2^-39 of it).
+__device__ __forceinline__ void scale_token(const MoeParams &p, int tok, float *red)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint16_t *x = p.x + tok * p.ldx;
+    float m = 0.0f;
+    for (int k = 8 * threadIdx.x; k < p.h; k += 8 * kRouterThreads) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + k));
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) // NaN too becomes infinity
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (lane == 0)
+        red[warp] = m;
+    __syncthreads();
+    for (int g = 0; g < kRouterThreads / 32; ++g)
+        m = fmaxf(m, red[g]);
+    // 2^(14 - exponent of m), at most 2^114; 1 for no largest number
+    const int e = m > 0.0f && m < INFINITY ? (int)(__float_as_uint(m) >> 23) - 127 : 14;
+    const int up = min(14 - e, 114);
+    const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+    if (threadIdx.x == 0)
+        p.unscale[tok] = __uint_as_float((uint32_t)(127 - up) << 23);
+    for (int k = 8 * threadIdx.x; k < p.h; k += 8 * kRouterThreads) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + k));
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(u[i] << 16) * f, __uint_as_float(u[i] & 0xffff0000u) * f);
+            v[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p.x16 + (int64_t)tok * p.h + k) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// Logits of one expert, eight tokens at a time; the CTA's threads share K.  The
+// CTAs past the experts scale a token each.
 __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const MoeParams p)
 {
     __shared__ float red[kRouterThreads / 32][8];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
+    if ((int)blockIdx.x >= p.experts) {
+        scale_token(p, (int)blockIdx.x - p.experts, &red[0][0]);
+        return;
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint16_t *w = p.router + (int64_t)blockIdx.x * p.ldr;
     for (int t0 = 0; t0 < p.m; t0 += 8) {
@@ -135,6 +185,7 @@ struct Routes {
     unsigned tokens[kMaxExperts];           // bit i: token i takes the expert
     uint8_t choice[kMaxExperts][kMaxTokens]; // which of the token's choices the expert is
     short expert[kMaxExperts];              // of a slot
+    uint8_t list[kMaxExperts][kMaxTokens];  // a slot's tokens, in rising order
     int slots;
 };
 
@@ -228,14 +279,21 @@ __device__ __forceinline__ void choose(const MoeParams &p, Routes &r)
             r.slots = n;
     }
     __syncthreads();
+    for (int i = threadIdx.x; i < r.slots; i += blockDim.x) {
+        unsigned left = r.tokens[r.expert[i]];
+        for (int n = 0; left; ++n, left &= left - 1u)
+            r.list[i][n] = (uint8_t)(__ffs(left) - 1);
+    }
+    __syncthreads();
 }
 
-// The n-th set bit of a mask that has it.
-__device__ __forceinline__ int nth_bit(unsigned mask, int n)
+__device__ __forceinline__ void mma_16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
 {
-    while (n-- > 0)
-        mask &= mask - 1u;
-    return __ffs(mask) - 1;
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // acc += two weight rows (32 codes and 2 scales of a lane each) x a column's 32 values: pairs (0, 4), (1, 5),
@@ -262,6 +320,41 @@ struct Decoded {
                       __byte_perm(x[j].x, x[j].z, 0x7632));
             mma_16816(acc, a[j][2], b[j][2], a[j][3], b[j][3], __byte_perm(x[j].y, x[j].w, 0x5410),
                       __byte_perm(x[j].y, x[j].w, 0x7632));
+        }
+    }
+};
+
+// The same with FP16 columns: an E2M1 pair is one conversion, times the block scale exact in FP16 (6 significant
+// bits, 2^-10 to 2688), and the pairs are those of neighbours.
+struct DecodedHalf {
+    uint32_t a[4][4], b[4][4];
+    static __device__ __forceinline__ void decode(const uint4 &w, uint32_t scales, uint32_t (&out)[4][4])
+    {
+        uint32_t s2;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)scales));
+        const uint32_t s[2] = {__byte_perm(s2, 0, 0x1010), __byte_perm(s2, 0, 0x3232)};
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t v[4];
+            asm("{.reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4; cvt.rn.f16x2.e2m1x2 %0, a; "
+                "cvt.rn.f16x2.e2m1x2 %1, b; cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d;}"
+                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                : "r"(u[j]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 q = __hmul2(*reinterpret_cast<const __half2 *>(&v[i]),
+                                          *reinterpret_cast<const __half2 *>(&s[j >> 1]));
+                out[j][i] = *reinterpret_cast<const uint32_t *>(&q);
+            }
+        }
+    }
+    __device__ __forceinline__ void multiply(float (&acc)[4], const uint4 (&x)[4]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            mma_16816_f16(acc, a[j][0], b[j][0], a[j][1], b[j][1], x[j].x, x[j].y);
+            mma_16816_f16(acc, a[j][2], b[j][2], a[j][3], b[j][3], x[j].z, x[j].w);
         }
     }
 };
@@ -347,19 +440,32 @@ __device__ __forceinline__ void produce(Ring &ring, int stages, int items, uint3
                        kErrTimeout, limit_ns, false);
 }
 
-// A reader's wait for item i.  After a timeout the warps still run through
-// their items and meet their barriers, on whatever the buffers hold.
-__device__ __forceinline__ void wait_full(Ring &ring, int stages, int i, unsigned long long limit_ns)
+// A reader's place in the ring.
+struct Place {
+    int s;
+    uint32_t ph;
+    __device__ __forceinline__ void forward(int items, int stages)
+    {
+        s += items;
+        while (s >= stages) {
+            s -= stages;
+            ph ^= 1u;
+        }
+    }
+};
+
+// After a timeout the warps still run through their items and meet their
+// barriers, on whatever the buffers hold.
+__device__ __forceinline__ void wait_full(Ring &ring, Place at, unsigned long long limit_ns)
 {
-    ptx::mbar_wait(ptx::smem_addr(&ring.full[i % stages]), (uint32_t)(i / stages) & 1u, &ring.abort_word, &g_moe_error,
-                   kErrTimeout, limit_ns);
+    ptx::mbar_wait(ptx::smem_addr(&ring.full[at.s]), at.ph, &ring.abort_word, &g_moe_error, kErrTimeout, limit_ns);
 }
 
-__device__ __forceinline__ void give_back(Ring &ring, int stages, int i, int lane)
+__device__ __forceinline__ void give_back(Ring &ring, Place at, int lane)
 {
     __syncwarp();
     if (lane == 0)
-        ptx::mbar_arrive(ptx::smem_addr(&ring.empty[i % stages]));
+        ptx::mbar_arrive(ptx::smem_addr(&ring.empty[at.s]));
 }
 
 constexpr int kUnitRows = 8; // of gate and of up
@@ -423,23 +529,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
     const int steps = (p.h + kStep - 1) / kStep;
     const int s0 = steps * kw / KS, s1 = steps * (kw + 1) / KS;
     const int left = p.h - 32 * t; // columns from this lane's first one on
+    const int jump = kGroups * (int)gridDim.x, jump_slots = jump / blocks, jump_blocks = jump - jump_slots * blocks;
+    int unit = (int)blockIdx.x + group * (int)gridDim.x, slot = unit / blocks, block = unit - slot * blocks;
     int buf = 0;
-    for (int i = group; i < items; i += kGroups) {
-        const int unit = (int)blockIdx.x + i * (int)gridDim.x;
-        const int e = r.expert[unit / blocks], row0 = unit % blocks * kUnitRows;
-        const unsigned tokens = r.tokens[e];
-        const int many = __popc(tokens);
-        const float scale = __ldg(p.sg13 + e) * 65536.0f, out = __ldg(p.sg2 + e);
-        const uint32_t at = ptx::smem_addr(buffers) + (uint32_t)(i % p.stages) * bytes;
-        const uint32_t row_q = at + (uint32_t)(g * (p.h / 2) + 16 * t);
-        const uint32_t row_s = at + 2 * codes + (uint32_t)(g * (p.h / 16) + 2 * t);
+    Place at = {0, 0};
+    at.forward(group, p.stages);
+    for (; unit < units; unit += jump, at.forward(kGroups, p.stages)) {
+        const int e = r.expert[slot], row0 = block * kUnitRows;
+        const int many = __popc(r.tokens[e]);
+        const uint8_t *list = r.list[slot];
+        const float scale = __ldg(p.sg13 + e), out = __ldg(p.sg2 + e);
+        const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.s * bytes;
+        const uint32_t row_q = from + (uint32_t)(g * (p.h / 2) + 16 * t);
+        const uint32_t row_s = from + 2 * codes + (uint32_t)(g * (p.h / 16) + 2 * t);
         for (int n0 = 0; n0 < many; n0 += 8) { // eight tokens at a time; few experts have more
             const bool have = n0 + g < many;
-            const uint16_t *xr = p.x + (have ? nth_bit(tokens, n0 + g) : 0) * p.ldx + 32 * t;
+            const __half *xr = p.x16 + (have ? (int64_t)list[n0 + g] * p.h : 0) + 32 * t;
             auto column = [&](int s, uint4 (&x)[4]) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    x[j] = have && s * kStep < left ? __ldg(reinterpret_cast<const uint4 *>(xr + s * kStep) + j)
+                    x[j] = have && s * kStep < left ? __ldcg(reinterpret_cast<const uint4 *>(xr + s * kStep) + j)
                                                     : make_uint4(0, 0, 0, 0);
             };
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}; // gate, gate, up, up of row g, tokens 2t and 2t + 1
@@ -447,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
             if (s0 < s1)
                 column(s0, x);
             if (n0 == 0)
-                wait_full(ring, p.stages, i, p.limit_ns);
+                wait_full(ring, at, p.limit_ns);
+#pragma unroll 2
             for (int s = s0; s < s1; ++s) {
                 if (s + 1 < s1)
                     column(s + 1, next);
@@ -459,15 +569,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
                     fa = lds16(row_s + 8u * s);
                     fb = lds16(row_s + scales + 8u * s);
                 }
-                Decoded w;
-                w.decode(a, b, fa, fb);
+                DecodedHalf w;
+                DecodedHalf::decode(a, fa, w.a);
+                DecodedHalf::decode(b, fb, w.b);
                 w.multiply(acc, x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     x[j] = next[j];
             }
             if (n0 + 8 >= many)
-                give_back(ring, p.stages, i, lane);
+                give_back(ring, at, lane);
             float(&mine)[2 * kUnitRows][9] = red[buf][warp];
             mine[g][2 * t] = acc[0];
             mine[g][2 * t + 1] = acc[1];
@@ -475,15 +586,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
             mine[kUnitRows + g][2 * t + 1] = acc[3];
             ptx::named_bar_sync(1 + group, 32 * KS);
             for (int k = kw * 32 + lane; k < kUnitRows * min(8, many - n0); k += 32 * KS) {
-                const int row = k % kUnitRows, n = k / kUnitRows, tok = nth_bit(tokens, n0 + n);
+                const int row = k % kUnitRows, n = k / kUnitRows, tok = list[n0 + n];
                 float gate = 0.0f, up = 0.0f;
 #pragma unroll
                 for (int w = 0; w < KS; ++w) {
                     gate += red[buf][group * KS + w][row][n];
                     up += red[buf][group * KS + w][kUnitRows + row][n];
                 }
-                gate *= scale;
-                up *= scale;
+                const float f = __ldcg(p.unscale + tok) * scale;
+                gate *= f;
+                up *= f;
                 const int j = r.choice[e][tok];
                 const float a = __fdiv_rn(gate, 1.0f + expf(-gate)) * up * (r.p[tok][j] * out);
                 __nv_bfloat16 part[PARTS];
@@ -494,6 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
                     to[(int64_t)q * p.inter] = part[q];
             }
             buf ^= 1; // the other half: the next barrier tells that this one has been read
+        }
+        slot += jump_slots;
+        block += jump_blocks;
+        if (block >= blocks) {
+            block -= blocks;
+            ++slot;
         }
     }
 }
@@ -511,8 +629,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
     __shared__ float red[kConsumers][kDownRows][kTok * NT + 1];
     uint8_t *buffers = ptx::align_smem<128>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    init_ring(ring, p.stages, kConsumers);
     choose(p, r); // from the logits, which were there before this kernel could start
+    const int steps = (p.inter + kStep - 1) / kStep;
+    // Warps that share a slot's K, a power of two: what leaves the fewest steps to the busiest warp.
+    int share = 1;
+    for (int k = 1, best = 0x7FFFFFFF; k <= kConsumers; k *= 2) {
+        const int cost = (r.slots + kConsumers / k - 1) / (kConsumers / k) * ((steps + k - 1) / k);
+        if (cost < best) {
+            best = cost;
+            share = k;
+        }
+    }
+    init_ring(ring, p.stages, share);
+    __syncthreads();
     const int64_t row0 = (int64_t)blockIdx.x * kDownRows;
     // a buffer: 16 rows' codes (8 inter bytes), their scales (inter)
     const uint32_t codes = 8u * p.inter, scales = (uint32_t)p.inter, bytes = codes + scales;
@@ -525,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
                 ptx::bulk_load(dst + codes, p.sb2 + row * (p.inter / 16), scales, bar);
             });
     } else {
-        const int steps = (p.inter + kStep - 1) / kStep;
+        const int groups = kConsumers / share, group = warp / share, kw = warp % share;
         const int left = p.inter - 32 * t;
         float acc[NT][4];
 #pragma unroll
@@ -535,39 +664,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
                 acc[i][j] = 0.0f;
         ptx::grid_dep_wait(); // the activations
         ptx::grid_dep_launch();
-        int first = warp; // this warp's first step of the slot: (slot, step) pairs go to the warps in turn
-        for (int i = 0; i < r.slots; ++i) {
+        Place at = {0, 0};
+        at.forward(group, p.stages);
+        for (int i = group; i < r.slots; i += groups, at.forward(groups, p.stages)) {
             const int e = r.expert[i];
             const unsigned tokens = r.tokens[e];
-            const uint32_t at = ptx::smem_addr(buffers) + (uint32_t)(i % p.stages) * bytes;
-            bool waited = false;
-            int s = first;
-            for (; s < steps; s += kConsumers) {
-                auto column = [&](int n, uint4 (&x)[4]) { // tile n's values of this lane
-                    const int tok = n * kTok + g / COLS, part = g % COLS;
-                    const bool have = part < kParts && (tokens >> tok & 1u) && s * kStep < left;
-                    const __nv_bfloat16 *from = p.act;
-                    if (have)
-                        from += ((int64_t)(tok * p.topk + r.choice[e][tok]) * kParts + part) * p.inter + s * kStep +
-                                32 * t;
+            const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.s * bytes;
+            auto column = [&](int n, int s, uint4 (&x)[4]) { // tile n's values of this lane
+                const int tok = n * kTok + g / COLS, part = g % COLS;
+                const bool have = part < kParts && (tokens >> tok & 1u) && s * kStep < left;
+                const __nv_bfloat16 *act = p.act;
+                if (have)
+                    act += ((int64_t)(tok * p.topk + r.choice[e][tok]) * kParts + part) * p.inter + s * kStep + 32 * t;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[j] = have ? __ldcg(reinterpret_cast<const uint4 *>(from) + j) : make_uint4(0, 0, 0, 0);
-                };
-                auto on = [&](int n) { return (tokens >> (n * kTok) & ((1u << kTok) - 1u)) != 0; };
-                uint4 x[4];
-                int tile = 0; // the first one with a token that takes the expert
-                while (tile < NT - 1 && !on(tile))
-                    ++tile;
-                column(tile, x);
-                if (!waited)
-                    wait_full(ring, p.stages, i, p.limit_ns);
-                waited = true;
+                for (int j = 0; j < 4; ++j)
+                    x[j] = have ? __ldcg(reinterpret_cast<const uint4 *>(act) + j) : make_uint4(0, 0, 0, 0);
+            };
+            auto on = [&](int n) { return (tokens >> (n * kTok) & ((1u << kTok) - 1u)) != 0; };
+            int tile = 0; // the first one with a token that takes the expert
+            while (tile < NT - 1 && !on(tile))
+                ++tile;
+            uint4 x[4], next[4];
+            if (NT == 1 && kw < steps)
+                column(tile, kw, x);
+            wait_full(ring, at, p.limit_ns);
+            for (int s = kw; s < steps; s += share) {
+                if (NT > 1) // more tiles take the registers of values a step ahead
+                    column(tile, s, x);
+                else if (s + share < steps)
+                    column(tile, s + share, next);
                 uint4 a = make_uint4(0, 0, 0, 0), b = a;
                 uint32_t fa = 0, fb = 0;
                 if (s * kStep < left) {
-                    const uint32_t q = at + (uint32_t)(g * (p.inter / 2) + 16 * t + 64 * s);
-                    const uint32_t sb = at + codes + (uint32_t)(g * (p.inter / 16) + 2 * t + 8 * s);
+                    const uint32_t q = from + (uint32_t)(g * (p.inter / 2) + 16 * t + 64 * s);
+                    const uint32_t sb = from + codes + (uint32_t)(g * (p.inter / 16) + 2 * t + 8 * s);
                     a = lds128(q);
                     b = lds128(q + 4u * p.inter);
                     fa = lds16(sb);
@@ -580,14 +710,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
                     if (n < tile || !on(n))
                         continue;
                     if (n > tile)
-                        column(n, x);
+                        column(n, s, x);
                     w.multiply(acc[n], x);
                 }
+                if (NT == 1)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = next[j];
             }
-            first = s - steps;
-            if (!waited) // a warp without a step waits too: it must not give a buffer back twice in one round
-                wait_full(ring, p.stages, i, p.limit_ns);
-            give_back(ring, p.stages, i, lane);
+            give_back(ring, at, lane);
         }
         // the parts of a token's sum lie in neighbouring columns
 #pragma unroll
@@ -656,16 +787,20 @@ cudaError_t run_down(const MoeParams &p, int64_t slots, cudaStream_t st)
     return run_ring(k_moe_down<NT, COLS>, configured, p.h / kDownRows, 9 * (int64_t)p.inter, slots, p, st);
 }
 
+// The workspace: logits, the tokens' inverse scales, x in FP16, the activations.
 size_t logits_bytes(int64_t m, int64_t experts)
 {
     return ((size_t)m * (size_t)experts * 4 + 15) / 16 * 16;
 }
 
+constexpr size_t kUnscaleBytes = kMaxTokens * sizeof(float);
+
 } // namespace
 
-size_t moe_nvfp4_workspace(int64_t m, int64_t experts, int64_t inter, int64_t topk)
+size_t moe_nvfp4_workspace(int64_t m, int64_t experts, int64_t h, int64_t inter, int64_t topk)
 {
-    return logits_bytes(m, experts) + (size_t)m * (size_t)topk * 3 * (size_t)inter * 2;
+    return logits_bytes(m, experts) + kUnscaleBytes + (size_t)m * (size_t)h * 2 +
+           (size_t)m * (size_t)topk * 3 * (size_t)inter * 2;
 }
 
 cudaError_t launch_moe_nvfp4(const MoeNvfp4Args &a, cudaStream_t st)
@@ -688,14 +823,17 @@ cudaError_t launch_moe_nvfp4(const MoeNvfp4Args &a, cudaStream_t st)
     p.sb2 = a.sb2;
     p.sg2 = a.sg2;
     p.logits = static_cast<float *>(a.ws);
-    p.act = reinterpret_cast<__nv_bfloat16 *>(static_cast<uint8_t *>(a.ws) + logits_bytes(a.m, a.experts));
+    uint8_t *at = static_cast<uint8_t *>(a.ws) + logits_bytes(a.m, a.experts);
+    p.unscale = reinterpret_cast<float *>(at);
+    p.x16 = reinterpret_cast<__half *>(at + kUnscaleBytes);
+    p.act = reinterpret_cast<__nv_bfloat16 *>(at + kUnscaleBytes + (size_t)a.m * (size_t)a.h * 2);
     p.ids = a.ids;
     p.weights = a.weights;
     p.y = a.y;
     p.ldy = a.ldy;
     p.out_bf16 = a.out_dtype == JETQ_OUT_BF16;
     p.limit_ns = kWaitLimitNs;
-    cudaError_t e = launch_pdl(k_moe_router, dim3((unsigned)a.experts), dim3(kRouterThreads), 0, st, p);
+    cudaError_t e = launch_pdl(k_moe_router, dim3((unsigned)(a.experts + a.m)), dim3(kRouterThreads), 0, st, p);
     if (e != cudaSuccess)
         return e;
     // slots at most

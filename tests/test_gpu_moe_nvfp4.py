@@ -156,7 +156,7 @@ def test_no_tokens_strided_rows_and_absent_outputs():
     wide_r = torch.full((10, 144), float("nan"), dtype=torch.bfloat16, device=DEV)
     wide_r[:, :128] = router
     out = torch.full((6, 131), 7.0, dtype=torch.bfloat16, device=DEV)
-    ws = torch.full((jq.jetq_moe_nvfp4_workspace_bytes(6, 10, 64, 2),), 255, dtype=torch.uint8, device=DEV)
+    ws = torch.full((jq.jetq_moe_nvfp4_workspace_bytes(6, 10, 128, 64, 2),), 255, dtype=torch.uint8, device=DEV)
     jq.jetq_moe_nvfp4(wide_x[:, 8:136], wide_r[:, :128], 2, True, w13["q"], w13["sb"], w13["sg"], w2["q"], w2["sb"],
                       w2["sg"], out[:, 1:129], None, None, ws)
     assert torch.equal(out[:, 1:129], y)
@@ -189,7 +189,7 @@ def test_repeatable_captured_and_on_another_stream():
 def test_layers_that_share_a_workspace():
     """Calls in stream order on one workspace, different choices each."""
     x, router, w13, w2 = _layer(16, 48, 512, 160, 12)
-    ws = torch.empty(jq.jetq_moe_nvfp4_workspace_bytes(16, 48, 160, 8), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(jq.jetq_moe_nvfp4_workspace_bytes(16, 48, 512, 160, 8), dtype=torch.uint8, device=DEV)
     rows = [x[:k].flip(0) if k % 2 else x[-k:] for k in (16, 1, 7, 12, 3, 16)]
     alone = [jq.moe_nvfp4(r, router, w13, w2, 8) for r in rows]
     for _ in range(10):

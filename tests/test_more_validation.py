@@ -185,9 +185,9 @@ def test_moe_of_no_tokens(L):
 
 def test_moe_workspaces(L):
     size = L.jetq_moe_nvfp4_workspace_bytes
-    assert size(0, 8, 32, 2) == size(17, 8, 32, 2) == size(4, 257, 32, 2) == size(4, 8, 32, 17) == 0
-    # logits, and three BF16 numbers an activation
-    assert size(16, 128, 768, 8) >= 16 * 128 * 4 + 16 * 8 * 768 * 6
+    assert size(0, 8, 64, 32, 2) == size(17, 8, 64, 32, 2) == size(4, 257, 64, 32, 2) == size(4, 8, 64, 32, 17) == 0
+    # logits, x in 16 bits, three 16-bit numbers an activation
+    assert size(16, 128, 2048, 768, 8) >= 16 * 128 * 4 + 16 * 2048 * 2 + 16 * 8 * 768 * 6
 
 
 def test_moe_helper_checks_its_tensors():
