@@ -13,6 +13,7 @@ matching ``jetq_*`` function.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -324,6 +325,7 @@ def jetq_gemv_nvfp4(qw, sbw, sgw, x, y, stream=None):
                                  _out_dtype(y), y.stride(0), _s(stream)), "jetq_gemv_nvfp4")
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
 def jetq_moe_nvfp4_workspace_bytes(m: int, num_experts: int, h: int, inter: int, topk: int) -> int:
     return int(lib().jetq_moe_nvfp4_workspace_bytes(m, num_experts, h, inter, topk))
 
@@ -402,6 +404,7 @@ def jetq_linear_distill_bwd(x, w, ids, teacher, renorm, scale, lse, logp, dloss,
                                          _p(ws), _bytes(ws), _s(stream)), "jetq_linear_distill_bwd")
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
 def jetq_policy_loss_workspace_bytes(n: int, nseg: int = 1) -> int:
     return int(lib().jetq_policy_loss_workspace_bytes(n, nseg))
 
@@ -440,13 +443,14 @@ def _want(t, name, dtype, shape=None, rows=False):
         raise ValueError(f"{name}: rows of consecutive elements are wanted, got strides {t.stride()}")
 
 
-def _one_device(x, **tensors):
+def _one_device(x, *tensors):
     """All tensors (None passes) on x's device, which is the current one: the launch goes to its stream."""
-    if x.get_device() != torch._C._cuda_getDevice():
+    at = x.get_device()
+    if at != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on {x.device}: make it the current device for the call")
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != x.get_device():
-            raise ValueError(f"{name}: on {t.device}, the other tensors on {x.device}")
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"tensors on {x.device} and {t.device}: one device is wanted")
 
 
 # ------------------------------------------------------------------ allocating helpers
@@ -714,7 +718,7 @@ def moe_nvfp4(x, router, w13, w2, topk, renorm=True, out_dtype=torch.bfloat16, w
     _want(sg2, "w2['sg']", torch.float32, (e,))
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out_dtype: {out_dtype} is neither BF16 nor FP32")
-    _one_device(x, router=router, q13=q13, sb13=sb13, sg13=sg13, q2=q2, sb2=sb2, sg2=sg2, workspace=workspace)
+    _one_device(x, router, q13, sb13, sg13, q2, sb2, sg2, workspace)
     y = torch.empty((m, h), dtype=out_dtype, device=x.device)
     ids = torch.empty((m, topk), dtype=torch.int64, device=x.device)
     p = torch.empty((m, topk), dtype=torch.float32, device=x.device)
@@ -851,7 +855,7 @@ def _check_distill(x, w, ids, teacher):
         raise ValueError(f"ids: {n} rows of 1 to 256 entries are wanted, got shape {tuple(ids.shape)}")
     if x.shape[1] != w.shape[1]:
         raise ValueError(f"x and w: widths {x.shape[1]} and {w.shape[1]}")
-    _one_device(x, w=w, ids=ids, teacher=teacher)
+    _one_device(x, w, ids, teacher)
 
 
 def _row_stride(t):
@@ -897,7 +901,7 @@ def linear_distill_bwd(x, w, ids, teacher, lse, logp, dloss, scale=1.0, renorm=T
             raise ValueError("accumulate needs a dw to add into")
         dw = torch.empty((v, c), dtype=dw_dtype, device=x.device)
     _want(dw, "dw", (torch.float32, torch.bfloat16), (v, c), rows=True)
-    _one_device(x, lse=lse, logp=logp, dloss=dloss, dw=dw, workspace=workspace)
+    _one_device(x, lse, logp, dloss, dw, workspace)
     dx = torch.empty((n, c), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = torch.empty(jetq_linear_distill_bwd_workspace_bytes(n, v, c, k), dtype=torch.uint8,
@@ -909,33 +913,33 @@ def linear_distill_bwd(x, w, ids, teacher, lse, logp, dloss, scale=1.0, renorm=T
 
 def _policy_args(nll, nll_old, adv, seg_offsets, nll_ref, mask, workspace=None, out=None, seg=None, dloss=None):
     """Checks of the policy loss's tensors -> the number of sequences."""
-    _want(nll, "nll", torch.float32)
-    n = nll.shape[0] if nll.dim() == 1 else -1
-    if n < 0:
-        raise ValueError(f"nll: one axis is wanted, got shape {tuple(nll.shape)}")
-    _want(nll_old, "nll_old", torch.float32, (n,))
+    f32, shape = torch.float32, nll.shape
+    _want(nll, "nll", f32)
+    if len(shape) != 1:
+        raise ValueError(f"nll: one axis is wanted, got shape {tuple(shape)}")
+    _want(nll_old, "nll_old", f32, shape)
     nseg = 1
     if seg_offsets is not None:
         _want(seg_offsets, "seg_offsets", torch.int64)
         nseg = seg_offsets.numel() - 1
         if seg_offsets.dim() != 1 or nseg < 1:
             raise ValueError(f"seg_offsets: at least two on one axis, got shape {tuple(seg_offsets.shape)}")
-    _want(adv, "adv", torch.float32)
-    if adv.shape != (n,) and adv.shape != (nseg,):
-        raise ValueError(f"adv: one for each of {n} tokens or of {nseg} sequences, got shape {tuple(adv.shape)}")
+    _want(adv, "adv", f32)
+    if adv.shape != shape and adv.shape != (nseg,):
+        raise ValueError(f"adv: one for each of {shape[0]} tokens or of {nseg} sequences, got shape "
+                         f"{tuple(adv.shape)}")
     if nll_ref is not None:
-        _want(nll_ref, "nll_ref", torch.float32, (n,))
+        _want(nll_ref, "nll_ref", f32, shape)
     if mask is not None:
-        _want(mask, "mask", (torch.bool, torch.uint8), (n,))
+        _want(mask, "mask", (torch.bool, torch.uint8), shape)
     if out is not None:
-        _want(out, "out", torch.float32, (6,))
-        _want(seg, "seg", torch.float32, (nseg, 2))
+        _want(out, "out", f32, (6,))
+        _want(seg, "seg", f32, (nseg, 2))
     if dloss is not None:
-        _want(dloss, "dloss", torch.float32)
+        _want(dloss, "dloss", f32)
         if dloss.numel() != 1:
             raise ValueError(f"dloss: one value is wanted, got shape {tuple(dloss.shape)}")
-    _one_device(nll, nll_old=nll_old, adv=adv, seg_offsets=seg_offsets, nll_ref=nll_ref, mask=mask, out=out, seg=seg,
-                dloss=dloss, workspace=workspace)
+    _one_device(nll, nll_old, adv, seg_offsets, nll_ref, mask, out, seg, dloss, workspace)
     return nseg
 
 

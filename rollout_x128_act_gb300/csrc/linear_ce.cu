@@ -88,6 +88,7 @@ struct HeadParams {
     int box_a, stages;                 // FEW: rows of A's box, ring stages of box_a rows of A and B's rows
     float k2;                          // scale * log2(e): exponents in base 2
     const int64_t *target;
+    bool wait_x;                       // kStatsSkip: x comes from the kernel before
     const uint4 *skip;                 // kStatsSkip: a bit a column, [M][kParts * nt] of 128 columns each
     int fold;                          // kStats: 64-blocks of K summed inside the tensor core, see the epilogue
     int64_t V, col0;                   // whole vocabulary; first vocabulary row of this piece
@@ -206,7 +207,10 @@ __global__ void __launch_bounds__(HeadCfg<CG, MODE, FEW>::kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
+    // kStatsSkip: what the product reads was there before the kernel that marks the columns, which let this one
+    // start after its own wait; unless that kernel also copies x, only the epilogue needs its result
+    if (MODE != kStatsSkip || warp >= 4 || p.wait_x)
+        ptx::grid_dep_wait();
     if constexpr (C::kRegSplit) {
         if (warp < 4)
             ptx::setmaxnreg_dec<C::kRegProducer>();
@@ -1023,7 +1027,8 @@ StatsShape stats_shape(int64_t n, int64_t v)
 
 // The statistics of the logits, a.x in the rows that the product reads.
 template <int MODE>
-cudaError_t run_stats(const LinearCeArgs &a, const StatsShape &shape, float2 *part, const uint4 *skip, cudaStream_t st)
+cudaError_t run_stats(const LinearCeArgs &a, const StatsShape &shape, float2 *part, const uint4 *skip, bool wait_x,
+                      cudaStream_t st)
 {
     HeadParams p = {};
     const int cg = shape.cg;
@@ -1044,6 +1049,7 @@ cudaError_t run_stats(const LinearCeArgs &a, const StatsShape &shape, float2 *pa
     p.k2 = a.scale * kLog2e;
     p.target = a.target;
     p.skip = skip;
+    p.wait_x = wait_x;
     // The error of a loss grows with the steps of a partial tile.  Pairs: 8 blocks (1.2e-7 in the 2-norm over
     // 4096 tokens, an FP32 matrix product has 6.7e-7; 4096 x 131072 x 4096 took 2.65 ms with 8, 2.97 with 4 and
     // 4.03 with 2, whose hand-overs between the CTAs stall the tensor core).  Single CTAs: 4 (1e-7; 2 us less than
@@ -1069,7 +1075,7 @@ cudaError_t launch_linear_ce_fwd(LinearCeArgs a, cudaStream_t st)
         return e;
     const StatsShape shape = stats_shape(a.n, a.v);
     float2 *part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + fwd_lines(a.n, a.c));
-    if ((e = run_stats<kStats>(a, shape, part, nullptr, st)) != cudaSuccess)
+    if ((e = run_stats<kStats>(a, shape, part, nullptr, true, st)) != cudaSuccess)
         return e;
     const int parts = kParts * shape.nt;
     int rx = 1, ry = 1;
@@ -1106,7 +1112,7 @@ cudaError_t launch_linear_distill_fwd(LinearCeArgs a, const DistillArgs &t, cuda
         a.x = copy;
         a.ldx = lines_ld(a.c);
     }
-    if ((e = run_stats<kStatsSkip>(a, shape, part, skip, st)) != cudaSuccess)
+    if ((e = run_stats<kStatsSkip>(a, shape, part, skip, copy != nullptr, st)) != cudaSuccess)
         return e;
     return launch_distill_join(a, t, part, parts, dots, st);
 }

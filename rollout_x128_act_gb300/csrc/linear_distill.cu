@@ -60,20 +60,78 @@ struct RowsParams {
 };
 
 // A CTA a row: its marks, its copy of x, and the products of x with the listed
-// rows of w, four a warp at a time (x is unpacked once for them).
+// rows of w, N a warp at a time (x is unpacked once for them).  Few rows take
+// N = 1 and several CTAs a row (blockIdx.y), with more loads in flight for each
+// product: a single token's 32 entries 17 us by one CTA with N = 4.
+template <int N>
 __global__ void __launch_bounds__(32 * kRowWarps) k_distill_rows(const RowsParams p)
 {
     constexpr int kChunk = 1024;             // marks' 128-column parts at a time
     __shared__ uint32_t marks[kChunk * 4];
     __shared__ int64_t ids[kMaxListed];
-    ptx::grid_dep_launch();
+    // The launch after the wait: the product may start on x and w, whose writers are through.
     ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int j = threadIdx.x; j < p.k; j += blockDim.x) {
         const int64_t id = __ldg(p.ids + row * p.ldi + j);
         ids[j] = id >= 0 && id < p.v ? id : -1;
     }
+    __syncthreads();
+    const uint16_t *x = p.x + row * p.ldx;
+    for (int j0 = N * (warp + kRowWarps * (int)blockIdx.y); j0 < p.k; j0 += N * kRowWarps * (int)gridDim.y) {
+        const uint16_t *w[N];
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t id = j0 + i < p.k ? ids[j0 + i] : -1;
+            any |= id >= 0;
+            w[i] = p.w + (id >= 0 ? id : 0) * p.ldw; // row 0 is there: its product is not used
+        }
+        float2 acc[N][4];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][e] = make_float2(0.0f, 0.0f);
+        if (any) {
+#pragma unroll(N == 1 ? 8 : 2)
+            for (int64_t k = 8 * lane; k < p.c; k += 256) { // c and the rows are whole vectors
+                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + k));
+                uint4 b[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    b[i] = __ldg(reinterpret_cast<const uint4 *>(w[i] + k));
+                const float2 f[4] = {unpack2(a.x), unpack2(a.y), unpack2(a.z), unpack2(a.w)};
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const uint32_t u[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][e] = __ffma2_rn(f[e], unpack2(u[e]), acc[i][e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float s = acc[i][0].x, c = 0.0f;
+            two_sum(s, c, acc[i][0].y);
+#pragma unroll
+            for (int e = 1; e < 4; ++e) {
+                two_sum(s, c, acc[i][e].x);
+                two_sum(s, c, acc[i][e].y);
+            }
+            warp_two_sum(s, c);
+            if (lane == 0 && j0 + i < p.k)
+                p.dots[row * p.k + j0 + i] = make_float2(s, c);
+        }
+    }
+    if (blockIdx.y > 0)
+        return;
+    if (p.copy)
+        for (int64_t k = 8 * threadIdx.x; k < p.c; k += 8 * blockDim.x)
+            *reinterpret_cast<uint4 *>(p.copy + row * p.ldc + k) = __ldg(reinterpret_cast<const uint4 *>(x + k));
     for (int q0 = 0; q0 < p.parts; q0 += kChunk) {
         const int many = min(kChunk, p.parts - q0);
         for (int i = threadIdx.x; i < many * 4; i += blockDim.x)
@@ -92,56 +150,6 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_distill_rows(const RowsParam
         for (int i = threadIdx.x; i < many; i += blockDim.x)
             p.skip[row * p.parts + q0 + i] = reinterpret_cast<const uint4 *>(marks)[i];
         __syncthreads();
-    }
-    const uint16_t *x = p.x + row * p.ldx;
-    if (p.copy)
-        for (int64_t k = 8 * threadIdx.x; k < p.c; k += 8 * blockDim.x)
-            *reinterpret_cast<uint4 *>(p.copy + row * p.ldc + k) = __ldg(reinterpret_cast<const uint4 *>(x + k));
-    for (int j0 = 4 * warp; j0 < p.k; j0 += 4 * kRowWarps) {
-        const uint16_t *w[4];
-        bool any = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t id = j0 + i < p.k ? ids[j0 + i] : -1;
-            any |= id >= 0;
-            w[i] = p.w + (id >= 0 ? id : 0) * p.ldw; // row 0 is there: its product is not used
-        }
-        float2 acc[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[i][e] = make_float2(0.0f, 0.0f);
-        if (any)
-#pragma unroll 2
-            for (int64_t k = 8 * lane; k < p.c; k += 256) { // c and the rows are whole vectors
-                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + k));
-                uint4 b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    b[i] = __ldg(reinterpret_cast<const uint4 *>(w[i] + k));
-                const float2 f[4] = {unpack2(a.x), unpack2(a.y), unpack2(a.z), unpack2(a.w)};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t u[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][e] = __ffma2_rn(f[e], unpack2(u[e]), acc[i][e]);
-                }
-            }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float s = acc[i][0].x, c = 0.0f;
-            two_sum(s, c, acc[i][0].y);
-#pragma unroll
-            for (int e = 1; e < 4; ++e) {
-                two_sum(s, c, acc[i][e].x);
-                two_sum(s, c, acc[i][e].y);
-            }
-            warp_two_sum(s, c);
-            if (lane == 0 && j0 + i < p.k)
-                p.dots[row * p.k + j0 + i] = make_float2(s, c);
-        }
     }
 }
 
@@ -220,42 +228,45 @@ struct Teacher {
 };
 
 // Joins a row's pairs, the exact terms of its listed columns and the teacher:
-// loss, lse and the listed log-probabilities.  Eight rows a CTA, a warp each
-// once the pairs are joined.  Sums of the pairs: threadIdx % 8 walks rows
-// (contiguous in part).
+// loss, lse and the listed log-probabilities.  `cta_rows` rows a CTA (eight, or
+// one where there are few), a warp each once the pairs are joined.  Sums of the
+// pairs: threadIdx % cta_rows walks rows (contiguous in part).
 __global__ void __launch_bounds__(256)
-    k_distill_join(const float2 *part, int parts, const float2 *dots, const int64_t *ids, int64_t ldi,
+    k_distill_join(int cta_rows, const float2 *part, int parts, const float2 *dots, const int64_t *ids, int64_t ldi,
                    const float *teacher, int64_t ldt, int k, int renorm, int64_t n, int64_t v, float scale, float k2,
                    float *loss, float *lse, float *logp)
 {
-    __shared__ float2 red[32][9];
+    __shared__ float2 red[256];
     __shared__ int64_t list[8][kMaxListed];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int64_t row0 = (int64_t)blockIdx.x * 8;
+    const int64_t row0 = (int64_t)blockIdx.x * cta_rows;
+    const int along = 256 / cta_rows; // threads along a row's pairs
     {
-        const int rx = threadIdx.x & 7, ry = threadIdx.x >> 3;
+        const int rx = threadIdx.x % cta_rows, ry = threadIdx.x / cta_rows;
         const int64_t row = row0 + rx;
         float2 a = make_float2(-INFINITY, 0.0f);
         if (row < n)
-            for (int q = ry; q < parts; q += 128) { // four loads in flight
+            for (int q = ry; q < parts; q += 4 * along) { // four loads in flight
                 float2 b[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    b[i] = q + 32 * i < parts ? __ldg(part + (int64_t)(q + 32 * i) * n + row)
-                                              : make_float2(-INFINITY, 0.0f);
+                    b[i] = q + along * i < parts ? __ldg(part + (int64_t)(q + along * i) * n + row)
+                                                 : make_float2(-INFINITY, 0.0f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     join_pair(a, b[i]);
             }
-        red[ry][rx] = a;
+        red[rx * along + ry] = a;
     }
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = row0 + warp;
-    if (row >= n)
+    if (warp >= cta_rows || row >= n)
         return;
-    float2 a = red[lane][warp];
+    float2 a = red[warp * along + lane];
+    for (int i = lane + 32; i < along; i += 32)
+        join_pair(a, red[warp * along + i]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const float2 b = make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, o), __shfl_xor_sync(0xFFFFFFFFu, a.y, o));
@@ -424,6 +435,8 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+constexpr int kFewRows = 64; // rows that take several CTAs each
+
 int64_t ceil_div(int64_t a, int64_t b)
 {
     return (a + b - 1) / b;
@@ -435,15 +448,19 @@ cudaError_t launch_distill_rows(const LinearCeArgs &a, const DistillArgs &t, uin
                                 int parts, uint4 *skip, float2 *dots, cudaStream_t st)
 {
     RowsParams p = {a.x, a.w, a.c, a.ldx, a.ldw, a.v, t.ids, t.ldi, t.k, bn, parts, copy, ldc, skip, dots};
-    return launch_pdl(k_distill_rows, dim3((unsigned)a.n), dim3(32 * kRowWarps), 0, st, p);
+    const dim3 block(32 * kRowWarps);
+    if (a.n > kFewRows)
+        return launch_pdl(k_distill_rows<4>, dim3((unsigned)a.n), block, 0, st, p);
+    return launch_pdl(k_distill_rows<1>, dim3((unsigned)a.n, (unsigned)ceil_div(t.k, kRowWarps)), block, 0, st, p);
 }
 
 cudaError_t launch_distill_join(const LinearCeArgs &a, const DistillArgs &t, const float2 *part, int parts,
                                 const float2 *dots, cudaStream_t st)
 {
-    return launch_pdl(k_distill_join, dim3((unsigned)ceil_div(a.n, 8)), dim3(256), 0, st, part, parts, dots, t.ids,
-                      t.ldi, t.teacher, t.ldt, t.k, t.renorm, a.n, a.v, a.scale, a.scale * kLog2e, a.loss, a.lse,
-                      t.logp);
+    const int rows = a.n > kFewRows ? 8 : 1;
+    return launch_pdl(k_distill_join, dim3((unsigned)ceil_div(a.n, rows)), dim3(256), 0, st, rows, part, parts, dots,
+                      t.ids, t.ldi, t.teacher, t.ldt, t.k, t.renorm, a.n, a.v, a.scale, a.scale * kLog2e, a.loss,
+                      a.lse, t.logp);
 }
 
 cudaError_t launch_distill_start(const LinearCeArgs &a, const DistillArgs &t, uint16_t *copy, int64_t ldc,

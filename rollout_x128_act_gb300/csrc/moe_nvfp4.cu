@@ -211,24 +211,27 @@ __device__ __forceinline__ void choose(const MoeParams &p, Routes &r)
         r.tokens[e] = 0;
     __syncthreads();
     for (int t = warp; t < p.m; t += warps) {
-        unsigned key[kMaxExperts / 32];
+        unsigned key[kMaxExperts / 32], best = 0;
+        int at = 0;
         float all = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kMaxExperts / 32; ++i) {
-            const int e = 32 * i + lane;
-            key[i] = e < p.experts ? order_key(__ldcg(p.logits + (int64_t)t * p.experts + e)) : 0u;
-        }
-        unsigned mine = 0, top = 0;
-        int id = 0;
-        for (int j = 0; j < p.topk; ++j) {
-            unsigned best = 0;
-            int at = 0;
+        auto local_best = [&]() {
+            best = 0;
 #pragma unroll
             for (int i = 0; i < kMaxExperts / 32; ++i)
                 if (key[i] > best) { // the first of equals
                     best = key[i];
                     at = 32 * i + lane;
                 }
+        };
+#pragma unroll
+        for (int i = 0; i < kMaxExperts / 32; ++i) {
+            const int e = 32 * i + lane;
+            key[i] = e < p.experts ? order_key(__ldcg(p.logits + (int64_t)t * p.experts + e)) : 0u;
+        }
+        local_best();
+        unsigned mine = 0, top = 0;
+        int id = 0;
+        for (int j = 0; j < p.topk; ++j) {
             const unsigned m = __reduce_max_sync(0xFFFFFFFFu, best);
             const int w = (int)__reduce_min_sync(0xFFFFFFFFu, best == m ? (unsigned)at : 0xFFFFu);
             if (j == 0) {
@@ -242,10 +245,13 @@ __device__ __forceinline__ void choose(const MoeParams &p, Routes &r)
                         all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
                 }
             }
+            if (lane == w % 32) { // the lane that held it looks for its next
 #pragma unroll
-            for (int i = 0; i < kMaxExperts / 32; ++i)
-                if (32 * i + lane == w)
-                    key[i] = 0;
+                for (int i = 0; i < kMaxExperts / 32; ++i)
+                    if (32 * i + lane == w)
+                        key[i] = 0;
+                local_best();
+            }
             if (lane == j) {
                 mine = m;
                 id = w;
@@ -534,6 +540,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
     int buf = 0;
     Place at = {0, 0};
     at.forward(group, p.stages);
+    // eight of a unit's tokens at a time (few experts have more); the values of x are loaded a step ahead
+    struct Columns {
+        const __half *row; // of this lane's token
+        bool have;
+    };
+    auto columns = [&](int slot, int n0) {
+        const int many = __popc(r.tokens[r.expert[slot]]);
+        Columns c;
+        c.have = n0 + g < many;
+        c.row = p.x16 + (c.have ? (int64_t)r.list[slot][n0 + g] * p.h : 0) + 32 * t;
+        return c;
+    };
+    auto load = [&](const Columns &c, int s, uint4 (&x)[4]) {
+        const bool in = c.have && s * kStep < left;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[j] = in ? reinterpret_cast<const uint4 *>(c.row + s * kStep)[j] : make_uint4(0, 0, 0, 0);
+    };
+    uint4 x[4], next[4];
+    if (unit < units && s0 < s1)
+        load(columns(slot, 0), s0, x);
     for (; unit < units; unit += jump, at.forward(kGroups, p.stages)) {
         const int e = r.expert[slot], row0 = block * kUnitRows;
         const int many = __popc(r.tokens[e]);
@@ -542,25 +569,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
         const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.s * bytes;
         const uint32_t row_q = from + (uint32_t)(g * (p.h / 2) + 16 * t);
         const uint32_t row_s = from + 2 * codes + (uint32_t)(g * (p.h / 16) + 2 * t);
-        for (int n0 = 0; n0 < many; n0 += 8) { // eight tokens at a time; few experts have more
-            const bool have = n0 + g < many;
-            const __half *xr = p.x16 + (have ? (int64_t)list[n0 + g] * p.h : 0) + 32 * t;
-            auto column = [&](int s, uint4 (&x)[4]) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[j] = have && s * kStep < left ? __ldcg(reinterpret_cast<const uint4 *>(xr + s * kStep) + j)
-                                                    : make_uint4(0, 0, 0, 0);
-            };
+        slot += jump_slots; // the next unit's
+        block += jump_blocks;
+        if (block >= blocks) {
+            block -= blocks;
+            ++slot;
+        }
+        wait_full(ring, at, p.limit_ns);
+        for (int n0 = 0; n0 < many; n0 += 8) {
+            const bool last = n0 + 8 >= many;
+            const Columns here = {p.x16 + (n0 + g < many ? (int64_t)list[n0 + g] * p.h : 0) + 32 * t, n0 + g < many};
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}; // gate, gate, up, up of row g, tokens 2t and 2t + 1
-            uint4 x[4], next[4];
-            if (s0 < s1)
-                column(s0, x);
-            if (n0 == 0)
-                wait_full(ring, at, p.limit_ns);
 #pragma unroll 2
             for (int s = s0; s < s1; ++s) {
                 if (s + 1 < s1)
-                    column(s + 1, next);
+                    load(here, s + 1, next);
+                else if (!last)
+                    load({p.x16 + (n0 + 8 + g < many ? (int64_t)list[n0 + 8 + g] * p.h : 0) + 32 * t, n0 + 8 + g < many}, s0, next);
+                else if (unit + jump < units)
+                    load(columns(slot, 0), s0, next);
                 uint4 a = make_uint4(0, 0, 0, 0), b = a;
                 uint32_t fa = 0, fb = 0;
                 if (s * kStep < left) {
@@ -577,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
                 for (int j = 0; j < 4; ++j)
                     x[j] = next[j];
             }
-            if (n0 + 8 >= many)
+            if (last)
                 give_back(ring, at, lane);
             float(&mine)[2 * kUnitRows][9] = red[buf][warp];
             mine[g][2 * t] = acc[0];
@@ -585,7 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
             mine[kUnitRows + g][2 * t] = acc[2];
             mine[kUnitRows + g][2 * t + 1] = acc[3];
             ptx::named_bar_sync(1 + group, 32 * KS);
-            for (int k = kw * 32 + lane; k < kUnitRows * min(8, many - n0); k += 32 * KS) {
+            // the few sums are done by another warp each time
+            for (int k = ((kw + unit) % KS) * 32 + lane; k < kUnitRows * min(8, many - n0); k += 32 * KS) {
                 const int row = k % kUnitRows, n = k / kUnitRows, tok = list[n0 + n];
                 float gate = 0.0f, up = 0.0f;
 #pragma unroll
@@ -593,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
                     gate += red[buf][group * KS + w][row][n];
                     up += red[buf][group * KS + w][kUnitRows + row][n];
                 }
-                const float f = __ldcg(p.unscale + tok) * scale;
+                const float f = p.unscale[tok] * scale;
                 gate *= f;
                 up *= f;
                 const int j = r.choice[e][tok];
@@ -607,26 +635,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
             }
             buf ^= 1; // the other half: the next barrier tells that this one has been read
         }
-        slot += jump_slots;
-        block += jump_blocks;
-        if (block >= blocks) {
-            block -= blocks;
-            ++slot;
-        }
     }
 }
 
 constexpr int kDownRows = 16;
 
-// NT: tiles of eight columns; a token has COLS columns (PARTS of them in use).
-template <int NT, int COLS>
+// COLS: columns of a token (its activations' parts, and for three of them an
+// empty one).  A slot's tokens, 8 / COLS at a time, take the eight columns of a
+// tile; its sums are added to the warp's sums of the tokens in shared memory.
+template <int COLS>
 __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
 {
-    constexpr int kParts = COLS == 4 ? 3 : 2, kTok = 8 / COLS; // tokens a tile
+    constexpr int kParts = COLS == 4 ? 3 : 2, kTok = 8 / COLS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Routes r;
     __shared__ Ring ring;
-    __shared__ float red[kConsumers][kDownRows][kTok * NT + 1];
+    __shared__ float red[kConsumers][kDownRows][kMaxTokens + 1];
     uint8_t *buffers = ptx::align_smem<128>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     choose(p, r); // from the logits, which were there before this kernel could start
@@ -656,81 +680,83 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
     } else {
         const int groups = kConsumers / share, group = warp / share, kw = warp % share;
         const int left = p.inter - 32 * t;
-        float acc[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int i = lane; i < kDownRows * p.m; i += 32)
+            red[warp][i % kDownRows][i / kDownRows] = 0.0f;
+        __syncwarp();
+        // activations of tile n0 of a slot, loaded a step ahead
+        struct Columns {
+            const __nv_bfloat16 *row; // this lane's token's part
+            bool have;
+        };
+        auto columns = [&](int slot, int n0) {
+            const int e = r.expert[slot], n = n0 + g / COLS, part = g % COLS;
+            Columns c = {p.act + 32 * t, n < __popc(r.tokens[e]) && part < kParts};
+            if (c.have) {
+                const int tok = r.list[slot][n];
+                c.row += ((int64_t)(tok * p.topk + r.choice[e][tok]) * kParts + part) * p.inter;
+            }
+            return c;
+        };
+        auto load = [&](const Columns &c, int s, uint4 (&x)[4]) {
+            const bool in = c.have && s * kStep < left;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                acc[i][j] = 0.0f;
+                x[j] = in ? __ldcg(reinterpret_cast<const uint4 *>(c.row + s * kStep) + j) : make_uint4(0, 0, 0, 0);
+        };
         ptx::grid_dep_wait(); // the activations
         ptx::grid_dep_launch();
+        uint4 x[4], next[4];
+        if (group < r.slots && kw < steps)
+            load(columns(group, 0), kw, x);
         Place at = {0, 0};
         at.forward(group, p.stages);
         for (int i = group; i < r.slots; i += groups, at.forward(groups, p.stages)) {
-            const int e = r.expert[i];
-            const unsigned tokens = r.tokens[e];
+            const int many = __popc(r.tokens[r.expert[i]]);
             const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.s * bytes;
-            auto column = [&](int n, int s, uint4 (&x)[4]) { // tile n's values of this lane
-                const int tok = n * kTok + g / COLS, part = g % COLS;
-                const bool have = part < kParts && (tokens >> tok & 1u) && s * kStep < left;
-                const __nv_bfloat16 *act = p.act;
-                if (have)
-                    act += ((int64_t)(tok * p.topk + r.choice[e][tok]) * kParts + part) * p.inter + s * kStep + 32 * t;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[j] = have ? __ldcg(reinterpret_cast<const uint4 *>(act) + j) : make_uint4(0, 0, 0, 0);
-            };
-            auto on = [&](int n) { return (tokens >> (n * kTok) & ((1u << kTok) - 1u)) != 0; };
-            int tile = 0; // the first one with a token that takes the expert
-            while (tile < NT - 1 && !on(tile))
-                ++tile;
-            uint4 x[4], next[4];
-            if (NT == 1 && kw < steps)
-                column(tile, kw, x);
+            const uint32_t row_q = from + (uint32_t)(g * (p.inter / 2) + 16 * t);
+            const uint32_t row_s = from + codes + (uint32_t)(g * (p.inter / 16) + 2 * t);
             wait_full(ring, at, p.limit_ns);
-            for (int s = kw; s < steps; s += share) {
-                if (NT > 1) // more tiles take the registers of values a step ahead
-                    column(tile, s, x);
-                else if (s + share < steps)
-                    column(tile, s + share, next);
-                uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                uint32_t fa = 0, fb = 0;
-                if (s * kStep < left) {
-                    const uint32_t q = from + (uint32_t)(g * (p.inter / 2) + 16 * t + 64 * s);
-                    const uint32_t sb = from + codes + (uint32_t)(g * (p.inter / 16) + 2 * t + 8 * s);
-                    a = lds128(q);
-                    b = lds128(q + 4u * p.inter);
-                    fa = lds16(sb);
-                    fb = lds16(sb + (uint32_t)p.inter / 2);
-                }
-                Decoded w;
-                w.decode(a, b, fa, fb);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (n < tile || !on(n))
-                        continue;
-                    if (n > tile)
-                        column(n, s, x);
-                    w.multiply(acc[n], x);
-                }
-                if (NT == 1)
+            for (int n0 = 0; n0 < many; n0 += kTok) {
+                const bool last = n0 + kTok >= many;
+                const Columns here = columns(i, n0);
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int s = kw; s < steps; s += share) {
+                    if (s + share < steps)
+                        load(here, s + share, next);
+                    else if (!last)
+                        load(columns(i, n0 + kTok), kw, next);
+                    else if (i + groups < r.slots)
+                        load(columns(i + groups, 0), kw, next);
+                    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                    uint32_t fa = 0, fb = 0;
+                    if (s * kStep < left) {
+                        a = lds128(row_q + 64u * s);
+                        b = lds128(row_q + 4u * p.inter + 64u * s);
+                        fa = lds16(row_s + 8u * s);
+                        fb = lds16(row_s + (uint32_t)p.inter / 2 + 8u * s);
+                    }
+                    Decoded w;
+                    w.decode(a, b, fa, fb);
+                    w.multiply(acc, x);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         x[j] = next[j];
+                }
+                // the parts of a token's sum lie in neighbouring columns
+                float v = acc[0] + acc[1], u = acc[2] + acc[3];
+                if (COLS == 4) {
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                    u += __shfl_xor_sync(0xFFFFFFFFu, u, 1);
+                }
+                const int n = n0 + (COLS == 2 ? t : t >> 1);
+                if (n < many && (COLS == 2 || (t & 1) == 0)) {
+                    const int tok = r.list[i][n];
+                    red[warp][g][tok] += v;
+                    red[warp][g + 8][tok] += u;
+                }
             }
             give_back(ring, at, lane);
         }
-        // the parts of a token's sum lie in neighbouring columns
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float v = acc[n][2 * half] + acc[n][2 * half + 1];
-                if (COLS == 4)
-                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-                if (COLS == 2 || (t & 1) == 0)
-                    red[warp][g + 8 * half][n * kTok + (COLS == 2 ? t : t >> 1)] = v;
-            }
     }
     __syncthreads();
     if (warp == kConsumers)
@@ -780,11 +806,11 @@ cudaError_t run_gate_up(const MoeParams &p, int64_t units, cudaStream_t st)
     return run_ring(k_moe_gate_up<KS, PARTS>, configured, grid, 9 * (int64_t)p.h, (units + grid - 1) / grid, p, st);
 }
 
-template <int NT, int COLS>
+template <int COLS>
 cudaError_t run_down(const MoeParams &p, int64_t slots, cudaStream_t st)
 {
     static std::atomic<unsigned long long> configured{0};
-    return run_ring(k_moe_down<NT, COLS>, configured, p.h / kDownRows, 9 * (int64_t)p.inter, slots, p, st);
+    return run_ring(k_moe_down<COLS>, configured, p.h / kDownRows, 9 * (int64_t)p.inter, slots, p, st);
 }
 
 // The workspace: logits, the tokens' inverse scales, x in FP16, the activations.
@@ -847,14 +873,7 @@ cudaError_t launch_moe_nvfp4(const MoeNvfp4Args &a, cudaStream_t st)
         e = few ? run_gate_up<8, 3>(p, units, st) : run_gate_up<4, 3>(p, units, st);
     if (e != cudaSuccess)
         return e;
-    if (p.out_bf16)
-        return a.m <= 4   ? run_down<1, 2>(p, slots, st)
-               : a.m <= 8 ? run_down<2, 2>(p, slots, st)
-                          : run_down<4, 2>(p, slots, st);
-    return a.m <= 2   ? run_down<1, 4>(p, slots, st)
-           : a.m <= 4 ? run_down<2, 4>(p, slots, st)
-           : a.m <= 8 ? run_down<4, 4>(p, slots, st)
-                      : run_down<8, 4>(p, slots, st);
+    return p.out_bf16 ? run_down<2>(p, slots, st) : run_down<4>(p, slots, st);
 }
 
 cudaError_t moe_read_and_clear_error(cudaStream_t st, unsigned *out)

@@ -11,14 +11,15 @@
 // again by the backward pass, which needs N and S first), launches for short ones.
 //
 // Work is split along the tokens, not the sequences, whose lengths run from
-// one to millions: a warp takes windows of 128 tokens (four a lane, loaded a
-// window ahead) and walks the sequences that cross them.  The part of sequence
-// s in window w is piece w + s of the partial sums: along the staircase of
-// windows and sequences each step raises one of the two, so no two pieces share
-// an index and none needs a counter or an atomic.  A second kernel joins each
-// sequence's pieces in a fixed order, with compensated FP32 sums (binary64 is
-// slow here: the join took 25 to 49 us with it): results are repeatable.  Up to
-// 4096 tokens one CTA does both.
+// one to millions: a warp takes a chunk of consecutive windows of 128 tokens
+// (four a lane, loaded a window ahead) and walks the sequences that cross it.
+// The part of sequence s in chunk c is piece c + s of the partial sums: along
+// the staircase of chunks and sequences each step raises one of the two, so no
+// two pieces share an index and none needs a counter or an atomic.  A lane sums
+// its own tokens of a piece, and the lanes are added where the piece ends.  A
+// second kernel joins each sequence's pieces in a fixed order, with compensated
+// FP32 sums (binary64 is slow here: the join took 25 to 49 us with it): results
+// are repeatable.  Up to 4096 tokens one CTA does both.
 //
 // Which side of the clip's border a token is on decides whether its gradient
 // is there at all, so logr keeps the rounding error of its subtraction and is
@@ -58,7 +59,7 @@ struct PolicyParams {
     float *dnll;
 };
 
-// Sums over the counted tokens of a sequence in a window.
+// Sums over the counted tokens of a sequence in a chunk.
 struct alignas(16) Piece {
     int count, clipped; // clipped: of a segment's ratio the tokens with A < 0
     float a, b, c, kl;  // a: L, or the positive A; b: the negative A; a segment's logr is c + c_rest
@@ -97,11 +98,15 @@ __device__ __forceinline__ void add_to(float &s, float &c, float b)
     s = t;
 }
 
-// exp(d) - 1 - d: below 1/2 by its Taylor series (the next term is 1e-8 of the sum).
+// exp(d) - 1 - d: up to |d| = 1 by its Taylor series (the next term is below 2^-26 of the sum).
 __device__ __forceinline__ float kl_term(float d)
 {
-    if (fabsf(d) < 0.5f) {
-        float s = 1.0f / 40320.0f;
+    if (fabsf(d) < 1.0f) {
+        float s = 1.0f / 479001600.0f;
+        s = fmaf(s, d, 1.0f / 39916800.0f);
+        s = fmaf(s, d, 1.0f / 3628800.0f);
+        s = fmaf(s, d, 1.0f / 362880.0f);
+        s = fmaf(s, d, 1.0f / 40320.0f);
         s = fmaf(s, d, 1.0f / 5040.0f);
         s = fmaf(s, d, 1.0f / 720.0f);
         s = fmaf(s, d, 1.0f / 120.0f);
@@ -110,6 +115,12 @@ __device__ __forceinline__ float kl_term(float d)
         return d * d * fmaf(s, d, 0.5f);
     }
     return expm1f(d) - d;
+}
+
+// exp(d) - 1, from the term above where the two are near.
+__device__ __forceinline__ float kl_slope(float d)
+{
+    return fabsf(d) < 1.0f ? d + kl_term(d) : expm1f(d);
 }
 
 // The ratio's bound for advantage A where it is clipped.
@@ -155,9 +166,10 @@ struct Walker {
         s = p.seg ? first_segment(p.seg, p.nseg, t0, lane) : 0;
         base = -1;
     }
-    // fn(sequence, first token, last token + 1, advantage, saved pair) for tokens [t0, t1); windows follow one another
+    // fn(sequence, first token, last token + 1, advantage, saved pair, whether the sequence's part of the chunk ends
+    // here) for tokens [t0, t1), the last ones of the chunk or not; windows follow one another
     template <bool SAVED, class F>
-    __device__ __forceinline__ void window(const PolicyParams &p, int64_t t0, int64_t t1, int lane, F fn)
+    __device__ __forceinline__ void window(const PolicyParams &p, int64_t t0, int64_t t1, bool last, int lane, F fn)
     {
         while (s < p.nseg) {
             if (base < 0 || s - base >= 32) { // 32 sequences' values in one load
@@ -179,7 +191,7 @@ struct Walker {
                 return;
             const int64_t from = b > t0 ? b : t0, to = e < t1 ? e : t1;
             if (from < to)
-                fn(s, from, to, A, sv);
+                fn(s, from, to, A, sv, last || e <= t1);
             if (e > t1)
                 return;
             ++s;
@@ -201,21 +213,33 @@ struct Tokens {
     bool on[kSlots];
     __device__ __forceinline__ void load(const PolicyParams &p, int64_t t0, int lane)
     {
+        const int64_t at = t0 + lane;
+        const int left = (int)min(p.n - t0, (int64_t)kWindow) - lane; // slot k is a token: 32 k < left
+        const float *px = p.nll + at, *py = p.old + at;
 #pragma unroll
         for (int k = 0; k < kSlots; ++k) {
-            const int64_t t = t0 + lane + 32 * k;
-            on[k] = t < p.n;
-            x[k] = y[k] = z[k] = A[k] = 0.0f;
-            if (on[k]) {
-                x[k] = __ldg(p.nll + t);
-                y[k] = __ldg(p.old + t);
-                if (p.ref)
-                    z[k] = __ldg(p.ref + t);
-                if (p.adv_token)
-                    A[k] = __ldg(p.adv + t);
-                if (p.mask)
-                    on[k] = __ldg(p.mask + t) != 0;
-            }
+            on[k] = 32 * k < left;
+            x[k] = on[k] ? __ldg(px + 32 * k) : 0.0f;
+            y[k] = on[k] ? __ldg(py + 32 * k) : 0.0f;
+            z[k] = A[k] = 0.0f;
+        }
+        if (p.ref) {
+            const float *pz = p.ref + at;
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k)
+                z[k] = on[k] ? __ldg(pz + 32 * k) : 0.0f;
+        }
+        if (p.adv_token) {
+            const float *pa = p.adv + at;
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k)
+                A[k] = on[k] ? __ldg(pa + 32 * k) : 0.0f;
+        }
+        if (p.mask) {
+            const uint8_t *pm = p.mask + at;
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k)
+                on[k] = on[k] && __ldg(pm + 32 * k) != 0;
         }
     }
 };
@@ -227,14 +251,18 @@ __device__ __forceinline__ float ratio_of(float d, float e)
     return e != 0.0f ? fmaf(r, e, r) : r;
 }
 
-// A warp's windows: the sums of each piece.
+// A chunk's sums of each piece.
 template <bool BY_SEG>
-__device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t w0, int64_t w1, int lane)
+__device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t chunk, int lane)
 {
+    const int64_t w0 = chunk * p.chunk, w1 = min(w0 + p.chunk, p.windows);
     Tokens tk, next;
     next.load(p, w0 * kWindow, lane);
     Walker walk;
     walk.start(p, w0 * kWindow, lane);
+    // this lane's sums of the piece
+    int count = 0, clipped = 0;
+    float a = 0.0f, b = 0.0f, c = 0.0f, rest = 0.0f, q = 0.0f;
     for (int64_t w = w0; w < w1; ++w) {
         tk = next;
         if (w + 1 < w1)
@@ -247,10 +275,9 @@ __device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t w0, in
             kl[k] = p.ref ? kl_term(tk.x[k] - tk.z[k]) : 0.0f;
         }
         const int64_t t0 = w * kWindow, t1 = min(t0 + kWindow, p.n);
-        walk.window<false>(p, t0, t1, lane, [&](int s, int64_t from, int64_t to, float A_seg, float2) {
+        walk.window<false>(p, t0, t1, w + 1 == w1, lane,
+                           [&](int s, int64_t from, int64_t to, float A_seg, float2, bool ends) {
             const int lo = (int)(from - t0) - lane, hi = (int)(to - t0) - lane;
-            int count = 0, clipped = 0;
-            float a = 0.0f, b = 0.0f, c = 0.0f, rest = 0.0f, q = 0.0f;
 #pragma unroll
             for (int k = 0; k < kSlots; ++k) {
                 const bool in = tk.on[k] && 32 * k >= lo && 32 * k < hi;
@@ -270,9 +297,13 @@ __device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t w0, in
                     a += in ? -A * (side ? bound : r[k]) : 0.0f;
                 }
                 q += in ? kl[k] : 0.0f;
-                count += __popc(__ballot_sync(0xFFFFFFFFu, in));
-                clipped += __popc(__ballot_sync(0xFFFFFFFFu, in && side));
+                count += in;
+                clipped += in && side;
             }
+            if (!ends)
+                return;
+            count = __reduce_add_sync(0xFFFFFFFFu, count);
+            clipped = __reduce_add_sync(0xFFFFFFFFu, clipped);
             a = warp_sum(a);
             if (p.ref)
                 q = warp_sum(q);
@@ -286,10 +317,12 @@ __device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t w0, in
                 }
             }
             if (lane == 0) {
-                float4 *out = reinterpret_cast<float4 *>(p.pieces + (w + s));
+                float4 *out = reinterpret_cast<float4 *>(p.pieces + (chunk + s));
                 out[0] = make_float4(__int_as_float(count), __int_as_float(clipped), a, b);
                 out[1] = make_float4(c, q, rest, 0.0f);
             }
+            count = clipped = 0;
+            a = b = c = rest = q = 0.0f;
         });
     }
 }
@@ -443,7 +476,7 @@ __device__ __forceinline__ void write_out(const PolicyParams &p, const Totals &t
     p.out[5] = (float)t.segs;
 }
 
-constexpr int kLanesSeg = 4, kLong = 256; // a sequence's lanes; pieces above which the CTA takes it
+constexpr int kLanesSeg = 4, kLong = 64; // a sequence's lanes; pieces above which the CTA takes it
 
 template <int THREADS>
 struct JoinShared {
@@ -476,12 +509,13 @@ __device__ __forceinline__ Totals join_segments(const PolicyParams &p, int64_t f
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = threadIdx.x % kLanesSeg;
     Totals tot = {};
-    auto range = [&](int64_t s, int64_t &w0, int64_t &w1) { // windows of sequence s
+    const int64_t span = (int64_t)p.chunk * kWindow;
+    auto range = [&](int64_t s, int64_t &w0, int64_t &w1) { // chunks of sequence s
         int64_t b = p.seg ? __ldg(p.seg + s) : 0, e = p.seg ? __ldg(p.seg + s + 1) : p.n;
         b = b < 0 ? 0 : b;
         e = e > p.n ? p.n : e;
-        w0 = b / kWindow;
-        w1 = e > b ? (e - 1) / kWindow + 1 : w0;
+        w0 = b / span;
+        w1 = e > b ? (e - 1) / span + 1 : w0;
     };
     for (int64_t s0 = first; s0 < end; s0 += THREADS / kLanesSeg) {
         if (threadIdx.x == 0)
@@ -554,11 +588,11 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_policy_pieces(const PolicyPa
 {
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int64_t w = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.chunk;
+    const int64_t chunk = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (blockIdx.x == 0 && threadIdx.x == 0)
         *p.ticket = 0;
-    if (w < p.windows)
-        sum_pieces<BY_SEG>(p, w, min(w + p.chunk, p.windows), threadIdx.x & 31);
+    if (chunk * p.chunk < p.windows)
+        sum_pieces<BY_SEG>(p, chunk, threadIdx.x & 31);
 }
 
 // The last CTA to finish adds the CTAs' totals.
@@ -606,9 +640,8 @@ __global__ void __launch_bounds__(kSmallThreads) k_policy_small(const PolicyPara
     __shared__ JoinShared<kSmallThreads> sh;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int64_t w = threadIdx.x >> 5;
-    if (w < p.windows)
-        sum_pieces<BY_SEG>(p, w, w + 1, threadIdx.x & 31);
+    if ((threadIdx.x >> 5) < p.windows) // chunks of one window
+        sum_pieces<BY_SEG>(p, threadIdx.x >> 5, threadIdx.x & 31);
     __syncthreads(); // the pieces are there for the whole CTA
     const Totals t = join_segments<kSmallThreads>(p, 0, p.nseg, sh);
     if (threadIdx.x == 0)
@@ -645,11 +678,11 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_policy_bwd(const PolicyParam
         for (int k = 0; k < kSlots; ++k) {
             two_diff(tk.y[k], tk.x[k], d[k], e[k]);
             r[k] = BY_SEG ? 0.0f : ratio_of(d[k], e[k]);
-            kl[k] = p.ref ? p.kl * expm1f(tk.x[k] - tk.z[k]) : 0.0f;
+            kl[k] = p.ref ? p.kl * kl_slope(tk.x[k] - tk.z[k]) : 0.0f;
             g[k] = 0.0f;
         }
         const int64_t t0 = w * kWindow, t1 = min(t0 + kWindow, p.n);
-        walk.window<true>(p, t0, t1, lane, [&](int, int64_t from, int64_t to, float A_seg, float2 seg) {
+        walk.window<true>(p, t0, t1, false, lane, [&](int, int64_t from, int64_t to, float A_seg, float2 seg, bool) {
             const int lo = (int)(from - t0) - lane, hi = (int)(to - t0) - lane;
             const float f = p.mean == JETQ_POLICY_MEAN_SEGMENTS ? __fdiv_rn(scale, seg.x) : scale;
 #pragma unroll
@@ -664,12 +697,12 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_policy_bwd(const PolicyParam
                     g[k] = f * (v + kl[k]);
                 }
         });
+        float *out = p.dnll + t0 + lane;
+        const int left = (int)(t1 - t0) - lane;
 #pragma unroll
-        for (int k = 0; k < kSlots; ++k) {
-            const int64_t t = t0 + lane + 32 * k;
-            if (t < p.n)
-                p.dnll[t] = g[k];
-        }
+        for (int k = 0; k < kSlots; ++k)
+            if (32 * k < left)
+                out[32 * k] = g[k];
     }
 }
 
@@ -678,6 +711,7 @@ int64_t ceil_div(int64_t a, int64_t b)
     return (a + b - 1) / b;
 }
 
+constexpr int kMaxChunk = 32; // a lane's FP32 sums are of 128 tokens at most
 constexpr int kWarpsSm = 24; // warps an SM that share the windows: what its registers hold
 
 float2 two_floats(double v)
@@ -701,7 +735,8 @@ PolicyParams params_of(const PolicyArgs &a)
     p.adv_token = a.adv_per_token != 0;
     p.by_seg = a.level == JETQ_POLICY_SEGMENT;
     const int64_t warps = (int64_t)sm_count() * kWarpsSm;
-    p.chunk = (int)ceil_div(p.windows, warps);
+    const int64_t chunk = ceil_div(p.windows, warps);
+    p.chunk = (int)(chunk < kMaxChunk ? chunk : kMaxChunk);
     p.mean = a.mean;
     p.scale = a.scale;
     p.kl = a.kl;
@@ -718,20 +753,20 @@ PolicyParams params_of(const PolicyArgs &a)
     return p;
 }
 
-// Sequences a CTA of the join: about 512 pieces, in as many CTAs as that makes.
-int segs_a_cta(int64_t windows, int64_t nseg)
+// Sequences a CTA of the join: about 128 pieces, in as many CTAs as that makes.
+int segs_a_cta(int64_t chunks, int64_t nseg)
 {
-    const int64_t most = kJoinThreads / kLanesSeg, s = 512 * nseg / (windows + nseg);
+    const int64_t most = kJoinThreads / kLanesSeg, s = 128 * nseg / (chunks + nseg);
     return (int)(s < 1 ? 1 : s > most ? most : s);
 }
 
 } // namespace
 
+// Enough for chunks of one window, whatever the device: a chunk's size only takes pieces away.
 size_t policy_loss_workspace(int64_t n, int64_t nseg)
 {
     const int64_t windows = ceil_div(n, kWindow);
-    return 16 + (size_t)(windows + nseg) * sizeof(Piece) +
-           (size_t)ceil_div(nseg, segs_a_cta(windows, nseg)) * sizeof(Totals);
+    return 16 + (size_t)(windows + nseg) * sizeof(Piece) + (size_t)nseg * sizeof(Totals);
 }
 
 cudaError_t launch_policy_fwd(const PolicyArgs &a, cudaStream_t st)
@@ -740,11 +775,12 @@ cudaError_t launch_policy_fwd(const PolicyArgs &a, cudaStream_t st)
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     p.ticket = reinterpret_cast<unsigned *>(ws);
     p.pieces = reinterpret_cast<Piece *>(ws + 16);
-    p.part = reinterpret_cast<Totals *>(ws + 16 + (size_t)(p.windows + p.nseg) * sizeof(Piece));
-    if (p.windows <= kSmallThreads / 32 && p.nseg <= kSmallSegs)
+    const int64_t chunks = ceil_div(p.windows, p.chunk);
+    p.part = reinterpret_cast<Totals *>(ws + 16 + (size_t)(chunks + p.nseg) * sizeof(Piece));
+    if (p.windows <= kSmallThreads / 32 && p.chunk == 1 && p.nseg <= kSmallSegs)
         return p.by_seg ? launch_pdl(k_policy_small<true>, dim3(1), dim3(kSmallThreads), 0, st, p)
                         : launch_pdl(k_policy_small<false>, dim3(1), dim3(kSmallThreads), 0, st, p);
-    p.segs_cta = segs_a_cta(p.windows, p.nseg);
+    p.segs_cta = segs_a_cta(chunks, p.nseg);
     const dim3 grid((unsigned)ceil_div(p.windows, (int64_t)kWarps * p.chunk)), block(32 * kWarps);
     const cudaError_t e = p.by_seg ? launch_pdl(k_policy_pieces<true>, grid, block, 0, st, p)
                                    : launch_pdl(k_policy_pieces<false>, grid, block, 0, st, p);

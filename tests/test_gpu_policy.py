@@ -2,7 +2,7 @@
 
 Tolerances.  A token's ratio is expf (2 ulp) of a difference whose rounding error is kept, times the advantage:
 4 roundings of 2^-24 and the 2 ulp; expm1 of the reference term the same, of a difference rounded to 2^-24 of
-itself.  Sums of at most 128 tokens are FP32 (9 roundings), the rest binary64.  Weights add 3 roundings.  All of
+itself.  Sums of at most 128 tokens are FP32 (9 roundings), the rest compensated.  Weights add 3 roundings.  All of
 it is below 2^-20 of the terms' magnitudes.  Counts are whole numbers.
 """
 import itertools
@@ -81,7 +81,7 @@ def dev(a):
 
 
 def check(nll, old, adv, off=None, ref=None, mask=None, low=0.2, high=0.2, dual=0.0, kl=0.0, by_seg=False,
-          mean="tokens", scale=1.0, per_token=None, dloss=None):
+          mean="tokens", scale=1.0, per_token=None, dloss=None, tol=TOL):
     n = nll.size
     whole = np.array([0, n], dtype=np.int64) if off is None else off
     if per_token is None:
@@ -97,8 +97,8 @@ def check(nll, old, adv, off=None, ref=None, mask=None, low=0.2, high=0.2, dual=
     got, dgot = out.double().cpu().numpy(), dnll.double().cpu().numpy()
     factor = 1.0 if dloss is None else float(dloss[0])
     assert np.array_equal(got[3:], want[3:])
-    assert np.all(np.abs(got[:3] - want[:3]) <= TOL * sums + 1e-37)
-    assert np.all(np.abs(dgot - factor * dwant) <= TOL * abs(factor) * size + 1e-37)
+    assert np.all(np.abs(got[:3] - want[:3]) <= tol * sums + 1e-37)
+    assert np.all(np.abs(dgot - factor * dwant) <= tol * abs(factor) * size + 1e-37)
     return out, seg, dnll, args, kw
 
 
@@ -140,6 +140,16 @@ def test_many_sequences_in_many_blocks():
     rng, old, nll, ref, adv = data(n, nseg, 5)
     check(nll, old, adv, offsets(n, nseg, rng), ref, rng.random(n) < 0.5, 0.2, 0.2, 0.0, 0.01, False, "segs")
     check(nll, old, adv, offsets(n, nseg, rng), ref, rng.random(n) < 0.5, 0.003, 0.004, 0.0, 0.01, True, "segs")
+
+
+@pytest.mark.parametrize("nseg", [1, 25, 3000])
+@pytest.mark.parametrize("by_seg", [False, True])
+def test_chunks_of_several_windows(by_seg, nseg):
+    """More windows than warps run at a time: a lane sums 3 windows (12 more roundings than a single one's 9)."""
+    n = 1300003
+    rng, old, nll, ref, adv = data(n, n if nseg == 25 else nseg, 40 + nseg)
+    check(nll, old, adv, offsets(n, nseg, rng, 5000, 700), ref, rng.random(n) < 0.9, 0.003, 0.004, 0.0, 0.02, by_seg,
+          "segs", tol=2 * TOL)
 
 
 @pytest.mark.parametrize("by_seg", [False, True])
