@@ -332,9 +332,10 @@ def jetq_moe_nvfp4_workspace_bytes(m: int, num_experts: int, h: int, inter: int,
 
 def jetq_moe_nvfp4(x, router, topk, renorm, q13, sb13, sg13, q2, sb2, sg2, y, ids, weights, ws, stream=None):
     m, h = x.shape
-    _check(lib().jetq_moe_nvfp4(_p(x), m, h, x.stride(0), _p(router), router.stride(0), router.shape[0], topk,
-                                1 if renorm else 0, _p(q13), _p(sb13), _p(sg13), q13.shape[1] // 2, _p(q2), _p(sb2),
-                                _p(sg2), _p(y), _out_dtype(y), y.stride(0), _p(ids), _p(weights), _p(ws), _bytes(ws),
+    _check(lib().jetq_moe_nvfp4(x.data_ptr(), m, h, x.stride(0), router.data_ptr(), router.stride(0), router.shape[0],
+                                topk, 1 if renorm else 0, q13.data_ptr(), sb13.data_ptr(), sg13.data_ptr(),
+                                q13.shape[1] // 2, q2.data_ptr(), sb2.data_ptr(), sg2.data_ptr(), y.data_ptr(),
+                                _out_dtype(y), y.stride(0), _p(ids), _p(weights), ws.data_ptr(), _bytes(ws),
                                 _s(stream)), "jetq_moe_nvfp4")
 
 
@@ -411,18 +412,18 @@ def jetq_policy_loss_workspace_bytes(n: int, nseg: int = 1) -> int:
 
 def jetq_policy_loss_fwd(nll, nll_old, nll_ref, adv, adv_per_token, mask, seg_offsets, nseg, level, mean, scale,
                          clip_low, clip_high, clip_dual, kl, out, seg, ws, stream=None):
-    _check(lib().jetq_policy_loss_fwd(_p(nll), _p(nll_old), _p(nll_ref), _p(adv), int(adv_per_token), _p(mask),
-                                      nll.numel(), _p(seg_offsets), nseg, level, mean, scale, clip_low, clip_high,
-                                      clip_dual, kl, _p(out), _p(seg), _p(ws), _bytes(ws), _s(stream)),
-           "jetq_policy_loss_fwd")
+    _check(lib().jetq_policy_loss_fwd(nll.data_ptr(), nll_old.data_ptr(), _p(nll_ref), adv.data_ptr(), adv_per_token,
+                                      _p(mask), nll.numel(), _p(seg_offsets), nseg, level, mean, scale, clip_low,
+                                      clip_high, clip_dual, kl, out.data_ptr(), seg.data_ptr(), ws.data_ptr(),
+                                      _bytes(ws), _s(stream)), "jetq_policy_loss_fwd")
 
 
 def jetq_policy_loss_bwd(nll, nll_old, nll_ref, adv, adv_per_token, mask, seg_offsets, nseg, level, mean, scale,
                          clip_low, clip_high, clip_dual, kl, out, seg, dloss, dnll, stream=None):
-    _check(lib().jetq_policy_loss_bwd(_p(nll), _p(nll_old), _p(nll_ref), _p(adv), int(adv_per_token), _p(mask),
-                                      nll.numel(), _p(seg_offsets), nseg, level, mean, scale, clip_low, clip_high,
-                                      clip_dual, kl, _p(out), _p(seg), _p(dloss), _p(dnll), _s(stream)),
-           "jetq_policy_loss_bwd")
+    _check(lib().jetq_policy_loss_bwd(nll.data_ptr(), nll_old.data_ptr(), _p(nll_ref), adv.data_ptr(), adv_per_token,
+                                      _p(mask), nll.numel(), _p(seg_offsets), nseg, level, mean, scale, clip_low,
+                                      clip_high, clip_dual, kl, out.data_ptr(), seg.data_ptr(), _p(dloss),
+                                      dnll.data_ptr(), _s(stream)), "jetq_policy_loss_bwd")
 
 
 # ------------------------------------------------------------------ argument checks of the tensor helpers

@@ -66,7 +66,7 @@ struct MoeParams {
     float *logits;        // [m][experts]
     __half *x16;          // [m][h]: x times a power of two, and its inverse [m]
     float *unscale;
-    __nv_bfloat16 *act;   // [m * topk][parts][inter]
+    __nv_bfloat16 *act;   // [m * topk][parts][inter], eights in the order 0 4 1 5 2 6 3 7: the weights' pairs
     int64_t *ids;
     float *weights;
     void *y;
@@ -302,8 +302,8 @@ __device__ __forceinline__ void mma_16816_f16(float (&c)[4], uint32_t a0, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// acc += two weight rows (32 codes and 2 scales of a lane each) x a column's 32 values: pairs (0, 4), (1, 5),
-// (2, 6), (3, 7), as the weights come.
+// acc += two weight rows (32 codes and 2 scales of a lane each) x a column's 32 values, which come in the order of
+// the decoded pairs (0, 4), (1, 5), (2, 6), (3, 7).
 struct Decoded {
     uint32_t a[4][4], b[4][4];
     __device__ __forceinline__ void decode(const uint4 &wa, const uint4 &wb, uint32_t fa, uint32_t fb)
@@ -322,10 +322,8 @@ struct Decoded {
     {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            mma_16816(acc, a[j][0], b[j][0], a[j][1], b[j][1], __byte_perm(x[j].x, x[j].z, 0x5410),
-                      __byte_perm(x[j].x, x[j].z, 0x7632));
-            mma_16816(acc, a[j][2], b[j][2], a[j][3], b[j][3], __byte_perm(x[j].y, x[j].w, 0x5410),
-                      __byte_perm(x[j].y, x[j].w, 0x7632));
+            mma_16816(acc, a[j][0], b[j][0], a[j][1], b[j][1], x[j].x, x[j].y);
+            mma_16816(acc, a[j][2], b[j][2], a[j][3], b[j][3], x[j].z, x[j].w);
         }
     }
 };
@@ -628,7 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
                 const float a = __fdiv_rn(gate, 1.0f + expf(-gate)) * up * (r.p[tok][j] * out);
                 __nv_bfloat16 part[PARTS];
                 split<PARTS>(a, part);
-                __nv_bfloat16 *to = p.act + (int64_t)(tok * p.topk + j) * PARTS * p.inter + row0 + row;
+                static_assert(kUnitRows == 8, "an eight of activations");
+                __nv_bfloat16 *to = p.act + (int64_t)(tok * p.topk + j) * PARTS * p.inter + row0 +
+                                    (row < 4 ? 2 * row : 2 * row - 7);
 #pragma unroll
                 for (int q = 0; q < PARTS; ++q)
                     to[(int64_t)q * p.inter] = part[q];
@@ -720,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
                 const bool last = n0 + kTok >= many;
                 const Columns here = columns(i, n0);
                 float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
                 for (int s = kw; s < steps; s += share) {
                     if (s + share < steps)
                         load(here, s + share, next);
