@@ -17,10 +17,8 @@
 // With loads issued by the threads themselves and K shared by eight warps (a
 // unit's 16 rows of each kind reduced before the next), sixteen tokens of 128
 // experts, 2048/768, took 91 us for the second kernel and 65 for the third.
-// Kernels 2 and 3 each choose the experts from the logits themselves: it takes
-// a warp half a microsecond a token, less than one more kernel, and kernel 3
-// does it, and starts its copies, before kernel 2 is through (kernel 2 lets it
-// start once the logits are there).
+// Each CTA of kernel 2 chooses the experts from the logits itself (3 to 4 us, in
+// place of another kernel), and the first one leaves its choices to kernel 3.
 //
 // Both products run on mma.m16n8k16 (weight rows as M, tokens as N), decoded
 // in registers as in the few-token product.  In the first, rows 0 to 7 of the M
@@ -66,6 +64,7 @@ struct MoeParams {
     float *logits;        // [m][experts]
     __half *x16;          // [m][h]: x times a power of two, and its inverse [m]
     float *unscale;
+    struct Routes *routes; // kernel 2's choices, for kernel 3
     __nv_bfloat16 *act;   // [m * topk][parts][inter], eights in the order 0 4 1 5 2 6 3 7: the weights' pairs
     int64_t *ids;
     float *weights;
@@ -120,20 +119,23 @@ __device__ __forceinline__ void scale_token(const MoeParams &p, int tok, float *
     }
 }
 
-// Logits of one expert, eight tokens at a time; the CTA's threads share K.  The
-// CTAs past the experts scale a token each.
+// Logits of one expert for eight tokens (blockIdx.y); the CTA's threads share K.
+// The CTAs past the experts scale a token each.
 __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const MoeParams p)
 {
     __shared__ float red[kRouterThreads / 32][8];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     if ((int)blockIdx.x >= p.experts) {
-        scale_token(p, (int)blockIdx.x - p.experts, &red[0][0]);
+        const int tok = (int)blockIdx.x - p.experts + 8 * (int)blockIdx.y;
+        if (tok < p.m)
+            scale_token(p, tok, &red[0][0]);
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint16_t *w = p.router + (int64_t)blockIdx.x * p.ldr;
-    for (int t0 = 0; t0 < p.m; t0 += 8) {
+    const int t0 = 8 * (int)blockIdx.y;
+    {
         float2 acc[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -166,20 +168,19 @@ __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const MoeParams p
                     red[warp][i] = s;
             }
         __syncthreads();
-        if (threadIdx.x < 8 && t0 + threadIdx.x < p.m) {
+        if (threadIdx.x < 8 && t0 + (int)threadIdx.x < p.m) {
             float s = 0.0f;
 #pragma unroll
             for (int g = 0; g < kRouterThreads / 32; ++g)
                 s += red[g][threadIdx.x];
             p.logits[(int64_t)(t0 + threadIdx.x) * p.experts + blockIdx.x] = s;
         }
-        __syncthreads();
     }
 }
 
 // Which experts the tokens take.  Slots number the experts that some token
 // takes, in rising order.
-struct Routes {
+struct alignas(16) Routes {
     int id[kMaxTokens][kMaxTop];
     float p[kMaxTokens][kMaxTop];
     unsigned tokens[kMaxExperts];           // bit i: token i takes the expert
@@ -302,66 +303,40 @@ __device__ __forceinline__ void mma_16816_f16(float (&c)[4], uint32_t a0, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// acc += two weight rows (32 codes and 2 scales of a lane each) x a column's 32 values, which come in the order of
-// the decoded pairs (0, 4), (1, 5), (2, 6), (3, 7).
-struct Decoded {
-    uint32_t a[4][4], b[4][4];
-    __device__ __forceinline__ void decode(const uint4 &wa, const uint4 &wb, uint32_t fa, uint32_t fb)
-    {
-        uint32_t sa[2], sb[2];
-        decode_scales(fa, sa);
-        decode_scales(fb, sb);
-        const uint32_t ua[4] = {wa.x, wa.y, wa.z, wa.w}, ub[4] = {wb.x, wb.y, wb.z, wb.w};
+// A lane's 32 codes of a weight row with their two scales, as the pairs that the MMA takes.  FP16: pairs of
+// neighbours; an E2M1 pair is one conversion, times the block scale exact in FP16 (6 significant bits, 2^-10 to 2688).
+__device__ __forceinline__ void decode_half(const uint4 &w, uint32_t scales, uint32_t (&out)[4][4])
+{
+    uint32_t s2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)scales));
+    const uint32_t s[2] = {__byte_perm(s2, 0, 0x1010), __byte_perm(s2, 0, 0x3232)};
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            decode8(ua[j], sa[j >> 1], a[j]);
-            decode8(ub[j], sb[j >> 1], b[j]);
+    for (int j = 0; j < 4; ++j) {
+        uint32_t v[4];
+        asm("{.reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4; cvt.rn.f16x2.e2m1x2 %0, a; "
+            "cvt.rn.f16x2.e2m1x2 %1, b; cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d;}"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+            : "r"(u[j]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 q = __hmul2(*reinterpret_cast<const __half2 *>(&v[i]),
+                                      *reinterpret_cast<const __half2 *>(&s[j >> 1]));
+            out[j][i] = *reinterpret_cast<const uint32_t *>(&q);
         }
     }
-    __device__ __forceinline__ void multiply(float (&acc)[4], const uint4 (&x)[4]) const
-    {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            mma_16816(acc, a[j][0], b[j][0], a[j][1], b[j][1], x[j].x, x[j].y);
-            mma_16816(acc, a[j][2], b[j][2], a[j][3], b[j][3], x[j].z, x[j].w);
-        }
-    }
-};
+}
 
-// The same with FP16 columns: an E2M1 pair is one conversion, times the block scale exact in FP16 (6 significant
-// bits, 2^-10 to 2688), and the pairs are those of neighbours.
-struct DecodedHalf {
-    uint32_t a[4][4], b[4][4];
-    static __device__ __forceinline__ void decode(const uint4 &w, uint32_t scales, uint32_t (&out)[4][4])
-    {
-        uint32_t s2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)scales));
-        const uint32_t s[2] = {__byte_perm(s2, 0, 0x1010), __byte_perm(s2, 0, 0x3232)};
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// BF16: pairs (0, 4), (1, 5), (2, 6), (3, 7) of each eight, times 2^-16.
+__device__ __forceinline__ void decode_bf16(const uint4 &w, uint32_t scales, uint32_t (&out)[4][4])
+{
+    uint32_t s[2];
+    decode_scales(scales, s);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t v[4];
-            asm("{.reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4; cvt.rn.f16x2.e2m1x2 %0, a; "
-                "cvt.rn.f16x2.e2m1x2 %1, b; cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d;}"
-                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                : "r"(u[j]));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2 q = __hmul2(*reinterpret_cast<const __half2 *>(&v[i]),
-                                          *reinterpret_cast<const __half2 *>(&s[j >> 1]));
-                out[j][i] = *reinterpret_cast<const uint32_t *>(&q);
-            }
-        }
-    }
-    __device__ __forceinline__ void multiply(float (&acc)[4], const uint4 (&x)[4]) const
-    {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            mma_16816_f16(acc, a[j][0], b[j][0], a[j][1], b[j][1], x[j].x, x[j].y);
-            mma_16816_f16(acc, a[j][2], b[j][2], a[j][3], b[j][3], x[j].z, x[j].w);
-        }
-    }
-};
+    for (int j = 0; j < 4; ++j)
+        decode8(u[j], s[j >> 1], out[j]);
+}
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr)
 {
@@ -379,12 +354,12 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ void prefetch_l2(const uint8_t *src, int64_t bytes)
+// A byte range into L2, line by line, shared by `lanes` threads.  (Not by bulk prefetches: nothing tells when those
+// are through, and a CTA without work ends at once.)
+__device__ __forceinline__ void prefetch_l2(const uint8_t *src, int64_t bytes, int lane, int lanes)
 {
-    for (int64_t at = 0; at < bytes; at += 16384)
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src + at),
-                     "r"((uint32_t)(bytes - at < 16384 ? bytes - at : 16384))
-                     : "memory");
+    for (int64_t at = 128 * lane; at < bytes; at += 128 * lanes)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(src + at));
 }
 
 // a as the sum of BF16 numbers, rounded to nearest each.
@@ -463,6 +438,7 @@ struct Place {
 __device__ __forceinline__ void wait_full(Ring &ring, Place at, unsigned long long limit_ns)
 {
     ptx::mbar_wait(ptx::smem_addr(&ring.full[at.s]), at.ph, &ring.abort_word, &g_moe_error, kErrTimeout, limit_ns);
+    __syncwarp(); // the lanes go on to a warp's instructions
 }
 
 __device__ __forceinline__ void give_back(Ring &ring, Place at, int lane)
@@ -487,15 +463,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     init_ring(ring, p.stages, KS);
     ptx::grid_dep_wait();
-    ptx::grid_dep_launch(); // after the wait: the next kernel may read the logits at once
+    ptx::grid_dep_launch();
     choose(p, r);
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < (int)(sizeof(Routes) / 16); i += blockDim.x)
+            reinterpret_cast<uint4 *>(p.routes)[i] = reinterpret_cast<const uint4 *>(&r)[i];
         for (int i = threadIdx.x; i < p.m * p.topk; i += blockDim.x) {
             if (p.ids)
                 p.ids[i] = r.id[i / p.topk][i % p.topk];
             if (p.weights)
                 p.weights[i] = r.p[i / p.topk][i % p.topk];
         }
+    }
     const int blocks = p.inter / kUnitRows, units = r.slots * blocks;
     const int items = units > (int)blockIdx.x ? (units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     // a buffer: gate codes, up codes (4 h bytes each), gate scales, up scales (h / 2 each)
@@ -514,15 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
                 ptx::bulk_load(dst + 2 * codes, sb, scales, bar);
                 ptx::bulk_load(dst + 2 * codes + scales, sb + (int64_t)p.inter * (p.h / 16), scales, bar);
             });
-        } else if (lane == 1) { // the down weights of few experts into L2, a share a CTA
+        } else { // the down weights of few experts into L2, a share a CTA
             const int64_t q = (int64_t)p.h * (p.inter / 2), sb = (int64_t)p.h * (p.inter / 16);
             if (r.slots * (q + sb) <= kPrefetchBytes) {
-                const int64_t share = ((q + (int64_t)gridDim.x - 1) / gridDim.x + 15) / 16 * 16;
+                const int64_t share = ((q + (int64_t)gridDim.x - 1) / gridDim.x + 127) / 128 * 128;
                 const int64_t a = min(q, share * blockIdx.x), b = min(q, a + share);
                 for (int i = 0; i < r.slots; ++i)
-                    prefetch_l2(p.q2 + r.expert[i] * q + a, b - a);
+                    prefetch_l2(p.q2 + r.expert[i] * q + a, b - a, lane - 1, 31);
                 if ((int)blockIdx.x < r.slots)
-                    prefetch_l2(p.sb2 + r.expert[blockIdx.x] * sb, sb);
+                    prefetch_l2(p.sb2 + r.expert[blockIdx.x] * sb, sb, lane - 1, 31);
             }
         }
         __syncwarp();
@@ -544,64 +523,63 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
         bool have;
     };
     auto columns = [&](int slot, int n0) {
-        const int many = __popc(r.tokens[r.expert[slot]]);
-        Columns c;
-        c.have = n0 + g < many;
-        c.row = p.x16 + (c.have ? (int64_t)r.list[slot][n0 + g] * p.h : 0) + 32 * t;
-        return c;
+        const bool have = n0 + g < __popc(r.tokens[r.expert[slot]]);
+        return Columns{p.x16 + (have ? (int64_t)r.list[slot][n0 + g] * p.h : 0) + 32 * t, have};
     };
-    auto load = [&](const Columns &c, int s, uint4 (&x)[4]) {
-        const bool in = c.have && s * kStep < left;
+    // null: zeros (from a line of zeros in memory they took twice as long as everything else)
+    auto source = [&](const Columns &c, int s) { return c.have && s * kStep < left ? c.row + s * kStep : nullptr; };
+    auto load = [&](const __half *from, uint4 (&x)[4]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            x[j] = in ? reinterpret_cast<const uint4 *>(c.row + s * kStep)[j] : make_uint4(0, 0, 0, 0);
+            x[j] = from ? reinterpret_cast<const uint4 *>(from)[j] : make_uint4(0, 0, 0, 0);
     };
     uint4 x[4], next[4];
-    if (unit < units && s0 < s1)
-        load(columns(slot, 0), s0, x);
+    Columns here = unit < units ? columns(slot, 0) : Columns{nullptr, false};
+    load(source(here, s0), x);
     for (; unit < units; unit += jump, at.forward(kGroups, p.stages)) {
-        const int e = r.expert[slot], row0 = block * kUnitRows;
+        const int e = r.expert[slot], row0 = block * kUnitRows, this_slot = slot;
         const int many = __popc(r.tokens[e]);
         const uint8_t *list = r.list[slot];
         const float scale = __ldg(p.sg13 + e), out = __ldg(p.sg2 + e);
         const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.s * bytes;
-        const uint32_t row_q = from + (uint32_t)(g * (p.h / 2) + 16 * t);
-        const uint32_t row_s = from + 2 * codes + (uint32_t)(g * (p.h / 16) + 2 * t);
+        const uint32_t row_q = from + (uint32_t)(g * (p.h / 2));
+        const uint32_t row_s = from + 2 * codes + (uint32_t)(g * (p.h / 16));
         slot += jump_slots; // the next unit's
         block += jump_blocks;
         if (block >= blocks) {
             block -= blocks;
             ++slot;
         }
-        wait_full(ring, at, p.limit_ns);
         for (int n0 = 0; n0 < many; n0 += 8) {
             const bool last = n0 + 8 >= many;
-            const Columns here = {p.x16 + (n0 + g < many ? (int64_t)list[n0 + g] * p.h : 0) + 32 * t, n0 + g < many};
+            Columns then = {nullptr, false};
+            if (!last)
+                then = columns(this_slot, n0 + 8);
+            else if (unit + jump < units)
+                then = columns(slot, 0);
+            if (n0 == 0)
+                wait_full(ring, at, p.limit_ns);
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}; // gate, gate, up, up of row g, tokens 2t and 2t + 1
 #pragma unroll 2
             for (int s = s0; s < s1; ++s) {
-                if (s + 1 < s1)
-                    load(here, s + 1, next);
-                else if (!last)
-                    load({p.x16 + (n0 + 8 + g < many ? (int64_t)list[n0 + 8 + g] * p.h : 0) + 32 * t, n0 + 8 + g < many}, s0, next);
-                else if (unit + jump < units)
-                    load(columns(slot, 0), s0, next);
-                uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                uint32_t fa = 0, fb = 0;
-                if (s * kStep < left) {
-                    a = lds128(row_q + 64u * s);
-                    b = lds128(row_q + codes + 64u * s);
-                    fa = lds16(row_s + 8u * s);
-                    fb = lds16(row_s + scales + 8u * s);
+                load(s + 1 < s1 ? source(here, s + 1) : source(then, s0), next);
+                // this lane's 32 columns of the rows; lanes past their end multiply zeros by their start
+                const uint32_t k = s * kStep < left ? (uint32_t)(s * (kStep / 32) + t) : 0u;
+                uint32_t wa[4][4], wb[4][4];
+                decode_half(lds128(row_q + 16u * k), lds16(row_s + 2u * k), wa);
+                decode_half(lds128(row_q + codes + 16u * k), lds16(row_s + scales + 2u * k), wb);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    mma_16816_f16(acc, wa[j][0], wb[j][0], wa[j][1], wb[j][1], x[j].x, x[j].y);
+                    mma_16816_f16(acc, wa[j][2], wb[j][2], wa[j][3], wb[j][3], x[j].z, x[j].w);
                 }
-                DecodedHalf w;
-                DecodedHalf::decode(a, fa, w.a);
-                DecodedHalf::decode(b, fb, w.b);
-                w.multiply(acc, x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     x[j] = next[j];
             }
+            if (s0 >= s1)
+                load(source(then, s0), x);
+            here = then;
             if (last)
                 give_back(ring, at, lane);
             float(&mine)[2 * kUnitRows][9] = red[buf][warp];
@@ -653,7 +631,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
     __shared__ float red[kConsumers][kDownRows][kMaxTokens + 1];
     uint8_t *buffers = ptx::align_smem<128>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    choose(p, r); // from the logits, which were there before this kernel could start
+    ptx::grid_dep_wait(); // the choices and the activations
+    ptx::grid_dep_launch();
+    for (int i = threadIdx.x; i < (int)(sizeof(Routes) / 16); i += blockDim.x)
+        reinterpret_cast<uint4 *>(&r)[i] = __ldcg(reinterpret_cast<const uint4 *>(p.routes) + i);
+    __syncthreads();
     const int steps = (p.inter + kStep - 1) / kStep;
     // Warps that share a slot's K, a power of two: what leaves the fewest steps to the busiest warp.
     int share = 1;
@@ -697,52 +679,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
             }
             return c;
         };
-        auto load = [&](const Columns &c, int s, uint4 (&x)[4]) {
-            const bool in = c.have && s * kStep < left;
+        auto source = [&](const Columns &c, int s) { return c.have && s * kStep < left ? c.row + s * kStep : nullptr; };
+        auto load = [&](const __nv_bfloat16 *from, uint4 (&x)[4]) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                x[j] = in ? __ldcg(reinterpret_cast<const uint4 *>(c.row + s * kStep) + j) : make_uint4(0, 0, 0, 0);
+                x[j] = from ? __ldcg(reinterpret_cast<const uint4 *>(from) + j) : make_uint4(0, 0, 0, 0);
         };
-        ptx::grid_dep_wait(); // the activations
-        ptx::grid_dep_launch();
         uint4 x[4], next[4];
-        if (group < r.slots && kw < steps)
-            load(columns(group, 0), kw, x);
+        Columns here = group < r.slots ? columns(group, 0) : Columns{nullptr, false};
+        load(source(here, kw), x);
         Place at = {0, 0};
         at.forward(group, p.stages);
         for (int i = group; i < r.slots; i += groups, at.forward(groups, p.stages)) {
             const int many = __popc(r.tokens[r.expert[i]]);
             const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.s * bytes;
-            const uint32_t row_q = from + (uint32_t)(g * (p.inter / 2) + 16 * t);
-            const uint32_t row_s = from + codes + (uint32_t)(g * (p.inter / 16) + 2 * t);
-            wait_full(ring, at, p.limit_ns);
+            const uint32_t row_q = from + (uint32_t)(g * (p.inter / 2));
+            const uint32_t row_s = from + codes + (uint32_t)(g * (p.inter / 16));
             for (int n0 = 0; n0 < many; n0 += kTok) {
                 const bool last = n0 + kTok >= many;
-                const Columns here = columns(i, n0);
+                Columns then = {nullptr, false};
+                if (!last)
+                    then = columns(i, n0 + kTok);
+                else if (i + groups < r.slots)
+                    then = columns(i + groups, 0);
+                if (n0 == 0)
+                    wait_full(ring, at, p.limit_ns);
                 float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 2
                 for (int s = kw; s < steps; s += share) {
-                    if (s + share < steps)
-                        load(here, s + share, next);
-                    else if (!last)
-                        load(columns(i, n0 + kTok), kw, next);
-                    else if (i + groups < r.slots)
-                        load(columns(i + groups, 0), kw, next);
-                    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                    uint32_t fa = 0, fb = 0;
-                    if (s * kStep < left) {
-                        a = lds128(row_q + 64u * s);
-                        b = lds128(row_q + 4u * p.inter + 64u * s);
-                        fa = lds16(row_s + 8u * s);
-                        fb = lds16(row_s + (uint32_t)p.inter / 2 + 8u * s);
+                    load(s + share < steps ? source(here, s + share) : source(then, kw), next);
+                    // this lane's 32 columns of the rows; lanes past their end multiply zeros by their start
+                    const uint32_t k = s * kStep < left ? (uint32_t)(s * (kStep / 32) + t) : 0u;
+                    uint32_t wa[4][4], wb[4][4];
+                    decode_bf16(lds128(row_q + 16u * k), lds16(row_s + 2u * k), wa);
+                    decode_bf16(lds128(row_q + 4u * p.inter + 16u * k), lds16(row_s + (uint32_t)p.inter / 2 + 2u * k),
+                                wb);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        mma_16816(acc, wa[j][0], wb[j][0], wa[j][1], wb[j][1], x[j].x, x[j].y);
+                        mma_16816(acc, wa[j][2], wb[j][2], wa[j][3], wb[j][3], x[j].z, x[j].w);
                     }
-                    Decoded w;
-                    w.decode(a, b, fa, fb);
-                    w.multiply(acc, x);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         x[j] = next[j];
                 }
+                here = then; // warps without a step have none of any slot
                 // the parts of a token's sum lie in neighbouring columns
                 float v = acc[0] + acc[1], u = acc[2] + acc[3];
                 if (COLS == 4) {
@@ -814,19 +795,19 @@ cudaError_t run_down(const MoeParams &p, int64_t slots, cudaStream_t st)
     return run_ring(k_moe_down<COLS>, configured, p.h / kDownRows, 9 * (int64_t)p.inter, slots, p, st);
 }
 
-// The workspace: logits, the tokens' inverse scales, x in FP16, the activations.
+// The workspace: logits, the tokens' inverse scales, the choices, x in FP16, the activations.
 size_t logits_bytes(int64_t m, int64_t experts)
 {
     return ((size_t)m * (size_t)experts * 4 + 15) / 16 * 16;
 }
 
-constexpr size_t kUnscaleBytes = kMaxTokens * sizeof(float);
+constexpr size_t kFixedBytes = kMaxTokens * sizeof(float) + sizeof(Routes);
 
 } // namespace
 
 size_t moe_nvfp4_workspace(int64_t m, int64_t experts, int64_t h, int64_t inter, int64_t topk)
 {
-    return logits_bytes(m, experts) + kUnscaleBytes + (size_t)m * (size_t)h * 2 +
+    return logits_bytes(m, experts) + kFixedBytes + (size_t)m * (size_t)h * 2 +
            (size_t)m * (size_t)topk * 3 * (size_t)inter * 2;
 }
 
@@ -852,15 +833,16 @@ cudaError_t launch_moe_nvfp4(const MoeNvfp4Args &a, cudaStream_t st)
     p.logits = static_cast<float *>(a.ws);
     uint8_t *at = static_cast<uint8_t *>(a.ws) + logits_bytes(a.m, a.experts);
     p.unscale = reinterpret_cast<float *>(at);
-    p.x16 = reinterpret_cast<__half *>(at + kUnscaleBytes);
-    p.act = reinterpret_cast<__nv_bfloat16 *>(at + kUnscaleBytes + (size_t)a.m * (size_t)a.h * 2);
+    p.routes = reinterpret_cast<Routes *>(at + kMaxTokens * sizeof(float));
+    p.x16 = reinterpret_cast<__half *>(at + kFixedBytes);
+    p.act = reinterpret_cast<__nv_bfloat16 *>(at + kFixedBytes + (size_t)a.m * (size_t)a.h * 2);
     p.ids = a.ids;
     p.weights = a.weights;
     p.y = a.y;
     p.ldy = a.ldy;
     p.out_bf16 = a.out_dtype == JETQ_OUT_BF16;
     p.limit_ns = kWaitLimitNs;
-    cudaError_t e = launch_pdl(k_moe_router, dim3((unsigned)(a.experts + a.m)), dim3(kRouterThreads), 0, st, p);
+    cudaError_t e = launch_pdl(k_moe_router, dim3((unsigned)(a.experts + (a.m < 8 ? a.m : 8)), (unsigned)((a.m + 7) / 8)), dim3(kRouterThreads), 0, st, p);
     if (e != cudaSuccess)
         return e;
     // slots at most
