@@ -29,7 +29,10 @@ namespace jetq {
 namespace {
 
 constexpr int kMaxListed = 256; // entries a row
-constexpr int kRowWarps = 8;
+__host__ __device__ constexpr int row_warps(int n) // of a CTA of k_distill_rows<n>
+{
+    return n == 1 ? 8 : 4;
+}
 
 __device__ __forceinline__ float2 unpack2(uint32_t u)
 {
@@ -59,13 +62,15 @@ struct RowsParams {
     float2 *dots;  // [n][k]
 };
 
-// A CTA a row: its marks, its copy of x, and the products of x with the listed
-// rows of w, N a warp at a time (x is unpacked once for them).  Few rows take
-// N = 1 and several CTAs a row (blockIdx.y), with more loads in flight for each
-// product: a single token's 32 entries 17 us by one CTA with N = 4.
+// A row's CTAs (blockIdx.y): the last one writes its marks and its copy of x,
+// the others the products of x with the listed rows of w, N a warp at a time (x
+// is unpacked once for them).  Few rows take N = 1 and several CTAs for the
+// products, with more loads in flight for each: a single token's 32 entries took
+// 17 us by one CTA with N = 4.
 template <int N>
-__global__ void __launch_bounds__(32 * kRowWarps) k_distill_rows(const RowsParams p)
+__global__ void __launch_bounds__(32 * row_warps(N), N == 1 ? 2 : 6) k_distill_rows(const RowsParams p)
 {
+    constexpr int kRowWarps = row_warps(N);
     constexpr int kChunk = 1024;             // marks' 128-column parts at a time
     __shared__ uint32_t marks[kChunk * 4];
     __shared__ int64_t ids[kMaxListed];
@@ -80,7 +85,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_distill_rows(const RowsParam
     }
     __syncthreads();
     const uint16_t *x = p.x + row * p.ldx;
-    for (int j0 = N * (warp + kRowWarps * (int)blockIdx.y); j0 < p.k; j0 += N * kRowWarps * (int)gridDim.y) {
+    const int shares = (int)gridDim.y - 1;
+    for (int j0 = N * (warp + kRowWarps * (int)blockIdx.y); (int)blockIdx.y < shares && j0 < p.k;
+         j0 += N * kRowWarps * shares) {
         const uint16_t *w[N];
         bool any = false;
 #pragma unroll
@@ -127,7 +134,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_distill_rows(const RowsParam
                 p.dots[row * p.k + j0 + i] = make_float2(s, c);
         }
     }
-    if (blockIdx.y > 0)
+    if ((int)blockIdx.y < shares)
         return;
     if (p.copy)
         for (int64_t k = 8 * threadIdx.x; k < p.c; k += 8 * blockDim.x)
@@ -448,10 +455,10 @@ cudaError_t launch_distill_rows(const LinearCeArgs &a, const DistillArgs &t, uin
                                 int parts, uint4 *skip, float2 *dots, cudaStream_t st)
 {
     RowsParams p = {a.x, a.w, a.c, a.ldx, a.ldw, a.v, t.ids, t.ldi, t.k, bn, parts, copy, ldc, skip, dots};
-    const dim3 block(32 * kRowWarps);
     if (a.n > kFewRows)
-        return launch_pdl(k_distill_rows<4>, dim3((unsigned)a.n), block, 0, st, p);
-    return launch_pdl(k_distill_rows<1>, dim3((unsigned)a.n, (unsigned)ceil_div(t.k, kRowWarps)), block, 0, st, p);
+        return launch_pdl(k_distill_rows<4>, dim3((unsigned)a.n, 2), dim3(32 * row_warps(4)), 0, st, p);
+    const dim3 grid((unsigned)a.n, (unsigned)ceil_div(t.k, row_warps(1)) + 1);
+    return launch_pdl(k_distill_rows<1>, grid, dim3(32 * row_warps(1)), 0, st, p);
 }
 
 cudaError_t launch_distill_join(const LinearCeArgs &a, const DistillArgs &t, const float2 *part, int parts,
