@@ -89,7 +89,7 @@ __device__ __forceinline__ void scale_token(const MoeParams &p, int tok, float *
         const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x + k));
         const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) // NaN too becomes infinity
+        for (int e = 0; e < 4; ++e) // passes over NaN, which stays one in FP16
             m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
     }
 #pragma unroll
