@@ -62,8 +62,8 @@ struct PolicyParams {
 // Sums over the counted tokens of a sequence in a chunk.
 struct alignas(16) Piece {
     int count, clipped; // clipped: of a segment's ratio the tokens with A < 0
-    float a, b, c, kl;  // a: L, or the positive A; b: the negative A; a segment's logr is c + c_rest
-    float c_rest, unused;
+    float a, b, c, kl;  // c + c_rest: L, or of a segment's ratio logr; then with an advantage a token
+    float c_rest, unused; // a: the positive A, b: the negative A
 };
 
 // Sums over sequences: surrogate and KL term (with their rests), numbers of clipped tokens, tokens, sequences.
@@ -283,10 +283,14 @@ __device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t chunk,
                 const bool in = tk.on[k] && 32 * k >= lo && 32 * k < hi;
                 const float A = p.adv_token ? tk.A[k] : A_seg;
                 bool side;
+                // compensated: a policy that is still its sampling policy adds the same -A at each token of a
+                // sequence, whose roundings do not average out
                 if (BY_SEG) {
                     side = A < 0.0f;
-                    a += in && !side ? A : 0.0f;
-                    b += in && side ? A : 0.0f;
+                    if (p.adv_token) {
+                        a += in && !side ? A : 0.0f;
+                        b += in && side ? A : 0.0f;
+                    }
                     if (in) {
                         add_to(c, rest, d[k]);
                         rest += e[k];
@@ -294,7 +298,8 @@ __device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t chunk,
                 } else {
                     float bound;
                     side = clip(p, A, d[k], e[k], bound);
-                    a += in ? -A * (side ? bound : r[k]) : 0.0f;
+                    if (in)
+                        add_to(c, rest, -A * (side ? bound : r[k]));
                 }
                 q += in ? kl[k] : 0.0f;
                 count += in;
@@ -304,17 +309,17 @@ __device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t chunk,
                 return;
             count = __reduce_add_sync(0xFFFFFFFFu, count);
             clipped = __reduce_add_sync(0xFFFFFFFFu, clipped);
-            a = warp_sum(a);
             if (p.ref)
                 q = warp_sum(q);
-            if (BY_SEG) {
+            if (BY_SEG && p.adv_token) {
+                a = warp_sum(a);
                 b = warp_sum(b);
+            }
 #pragma unroll
-                for (int o = 16; o; o >>= 1) {
-                    const float c2 = __shfl_xor_sync(0xFFFFFFFFu, c, o), r2 = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
-                    add_to(c, rest, c2);
-                    rest += r2;
-                }
+            for (int o = 16; o; o >>= 1) {
+                const float c2 = __shfl_xor_sync(0xFFFFFFFFu, c, o), r2 = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+                add_to(c, rest, c2);
+                rest += r2;
             }
             if (lane == 0) {
                 float4 *out = reinterpret_cast<float4 *>(p.pieces + (chunk + s));
@@ -347,27 +352,27 @@ struct SegSums {
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece) + 1);
         count += (unsigned)__float_as_int(u.x);
         clipped += (unsigned)__float_as_int(u.y);
-        add_to(a, a_rest, u.z);
+        add_to(c, c_rest, v.x);
+        c_rest += v.z;
         add_to(kl, kl_rest, v.y);
         if (by_seg) {
+            add_to(a, a_rest, u.z);
             add_to(b, b_rest, u.w);
-            add_to(c, c_rest, v.x);
-            c_rest += v.z;
         }
     }
     __device__ __forceinline__ void add(const SegSums &o, bool by_seg)
     {
         count += o.count;
         clipped += o.clipped;
-        add_to(a, a_rest, o.a);
-        a_rest += o.a_rest;
+        add_to(c, c_rest, o.c);
+        c_rest += o.c_rest;
         add_to(kl, kl_rest, o.kl);
         kl_rest += o.kl_rest;
         if (by_seg) {
+            add_to(a, a_rest, o.a);
+            a_rest += o.a_rest;
             add_to(b, b_rest, o.b);
             b_rest += o.b_rest;
-            add_to(c, c_rest, o.c);
-            c_rest += o.c_rest;
         }
     }
     __device__ __forceinline__ void add_lane(int o, bool by_seg) // of lane ^ o
@@ -375,15 +380,15 @@ struct SegSums {
         SegSums x;
         x.count = __shfl_xor_sync(0xFFFFFFFFu, count, o);
         x.clipped = __shfl_xor_sync(0xFFFFFFFFu, clipped, o);
-        x.a = __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        x.a_rest = __shfl_xor_sync(0xFFFFFFFFu, a_rest, o);
+        x.c = __shfl_xor_sync(0xFFFFFFFFu, c, o);
+        x.c_rest = __shfl_xor_sync(0xFFFFFFFFu, c_rest, o);
         x.kl = __shfl_xor_sync(0xFFFFFFFFu, kl, o);
         x.kl_rest = __shfl_xor_sync(0xFFFFFFFFu, kl_rest, o);
         if (by_seg) {
+            x.a = __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            x.a_rest = __shfl_xor_sync(0xFFFFFFFFu, a_rest, o);
             x.b = __shfl_xor_sync(0xFFFFFFFFu, b, o);
             x.b_rest = __shfl_xor_sync(0xFFFFFFFFu, b_rest, o);
-            x.c = __shfl_xor_sync(0xFFFFFFFFu, c, o);
-            x.c_rest = __shfl_xor_sync(0xFFFFFFFFu, c_rest, o);
         }
         add(x, by_seg);
     }
@@ -419,15 +424,17 @@ __device__ __forceinline__ void warp_totals(Totals &t, int lanes)
 // A sequence's saved pair and its share of the totals.
 __device__ __forceinline__ void finish(const PolicyParams &p, int s, const SegSums &x, Totals &tot)
 {
-    const float a = whole(x.a, x.a_rest), n = (float)x.count;
-    float l = a, l_rest = 0.0f, g = 0.0f;
+    const float n = (float)x.count;
+    float l = x.c, l_rest = fabsf(x.c) < INFINITY ? x.c_rest : 0.0f, g = 0.0f;
     unsigned long long clipped = x.clipped;
-    if (fabsf(x.a) < INFINITY) {
-        l = x.a;
-        l_rest = x.a_rest;
-    }
     if (p.by_seg && x.count) {
-        const float b = whole(x.b, x.b_rest), c = whole(x.c, x.c_rest);
+        float a = whole(x.a, x.a_rest), b = whole(x.b, x.b_rest);
+        if (!p.adv_token) { // one advantage: no sum
+            const float A = __ldg(p.adv + s);
+            a = A < 0.0f ? 0.0f : A * n;
+            b = A < 0.0f ? A * n : 0.0f;
+        }
+        const float c = whole(x.c, x.c_rest);
         // the mean in two floats: it is compared with the borders
         const float mean = __fdiv_rn(c, n);
         float rest = 0.0f;

@@ -153,6 +153,16 @@ def test_chunks_of_several_windows(by_seg, nseg):
 
 
 @pytest.mark.parametrize("by_seg", [False, True])
+def test_a_policy_that_is_still_its_sampling_policy(by_seg):
+    """Ratios of 1: each token of a sequence adds the same -A, and the advantages of the sequences nearly cancel.
+    The sums are compensated: 4 roundings of 2^-24 of the mean magnitude, however long a sequence is."""
+    n, nseg = 1200000, 6
+    rng, old, nll, _, adv = data(n, nseg, 50)
+    adv = np.float32([0.1, -0.1, 0.3, -0.3, 0.7, -0.7])
+    check(old, old, adv, (np.arange(nseg + 1) * (n // nseg)).astype(np.int64), by_seg=by_seg, tol=4 * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("by_seg", [False, True])
 def test_what_is_not_counted_may_hold_anything(by_seg):
     n, nseg = 1000, 7
     rng, old, nll, ref, adv = data(n, n, 8)
