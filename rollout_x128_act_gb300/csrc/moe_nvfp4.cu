@@ -14,11 +14,15 @@
 //   3. down: a CTA owns 16 rows of y and runs through all chosen experts in the
 //      same way, its 16 warps sharing (expert, K) steps, so that y is summed in
 //      the CTA's registers and written once, without atomics.
-// With loads issued by the threads themselves and K shared by eight warps (a
-// unit's 16 rows of each kind reduced before the next), sixteen tokens of 128
-// experts, 2048/768, took 91 us for the second kernel and 65 for the third.
 // Each CTA of kernel 2 chooses the experts from the logits itself (3 to 4 us, in
 // place of another kernel), and the first one leaves its choices to kernel 3.
+// Measured in a graph, 128 experts of which 8 are taken, 2048/768: one token 23 us
+// (HBM 3.2; the launches, the choice and the kernels' first copies are most of
+// it), sixteen tokens (82 experts) 90 us: router 5, choice 4, gate and up 35, down
+// 36, HBM 32; the last two use half of the issue slots, most of them to decode.
+// Loads issued by the threads themselves, with K shared by eight warps: 145 us.
+// Rows copied one by one to a pitch without bank conflicts: 147 us (a bulk copy
+// costs about 50 ns, whatever its size).
 //
 // Both products run on mma.m16n8k16 (weight rows as M, tokens as N), decoded
 // in registers as in the few-token product.  In the first, rows 0 to 7 of the M

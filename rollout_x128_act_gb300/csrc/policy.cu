@@ -7,8 +7,12 @@
 //   loss = sum over counted tokens of w (L + kl_coef * kl),   w = scale / N, scale / (S n_s) or scale
 //   dnll = w (A r [not clipped] + kl_coef * (exp(d) - 1))
 //
-// Bound: HBM for long batches (17 to 21 bytes a token, read by the forward and
-// again by the backward pass, which needs N and S first), launches for short ones.
+// Floor: HBM for long batches (17 to 21 bytes a token, read by the forward and
+// again by the backward pass, which needs N and S first), launches for short
+// ones.  Both directions in a graph: 4194304 tokens in 8192 sequences 45 us
+// (issue slots 70% used: some 120 instructions a token and direction; HBM would
+// take 10), 1000003 tokens in 24 sequences 31 us (the latencies of three kernels;
+// 10 us of it the join), 524288 in 512 21 us, 1531 in 8 15 us.
 //
 // Work is split along the tokens, not the sequences, whose lengths run from
 // one to millions: a warp takes a chunk of consecutive windows of 128 tokens
