@@ -423,15 +423,17 @@ __device__ __forceinline__ void produce(Ring &ring, int stages, int items, uint3
                        kErrTimeout, limit_ns, false);
 }
 
-// A reader's place in the ring.
+// A reader's place in the ring.  Every warp waits for every item in turn and gives
+// its buffer back, its group's own items after reading them: a wait knows the
+// phase of a barrier by its parity only, so a reader that skipped items could
+// take an older phase for its own, or be passed by two.
 struct Place {
     int s;
     uint32_t ph;
-    __device__ __forceinline__ void forward(int items, int stages)
+    __device__ __forceinline__ void forward(int stages)
     {
-        s += items;
-        while (s >= stages) {
-            s -= stages;
+        if (++s == stages) {
+            s = 0;
             ph ^= 1u;
         }
     }
@@ -452,6 +454,17 @@ __device__ __forceinline__ void give_back(Ring &ring, Place at, int lane)
         ptx::mbar_arrive(ptx::smem_addr(&ring.empty[at.s]));
 }
 
+// Passes over `items` that other groups read.
+__device__ __forceinline__ void pass_over(Ring &ring, Place &at, int items, int stages, int lane,
+                                          unsigned long long limit_ns)
+{
+    for (int i = 0; i < items; ++i) {
+        wait_full(ring, at, limit_ns);
+        give_back(ring, at, lane);
+        at.forward(stages);
+    }
+}
+
 constexpr int kUnitRows = 8; // of gate and of up
 
 // KS: warps that share a unit's K.  PARTS: BF16 numbers an activation is stored as.
@@ -465,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
     __shared__ float red[2][kConsumers][2 * kUnitRows][9];
     uint8_t *buffers = ptx::align_smem<128>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    init_ring(ring, p.stages, KS);
+    init_ring(ring, p.stages, kConsumers);
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     choose(p, r);
@@ -520,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
     int unit = (int)blockIdx.x + group * (int)gridDim.x, slot = unit / blocks, block = unit - slot * blocks;
     int buf = 0;
     Place at = {0, 0};
-    at.forward(group, p.stages);
+    int item = 0; // where the ring is
     // eight of a unit's tokens at a time (few experts have more); the values of x are loaded a step ahead
     struct Columns {
         const __half *row; // of this lane's token
@@ -540,7 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
     uint4 x[4], next[4];
     Columns here = unit < units ? columns(slot, 0) : Columns{nullptr, false};
     load(source(here, s0), x);
-    for (; unit < units; unit += jump, at.forward(kGroups, p.stages)) {
+    for (int mine = group; unit < units; unit += jump, mine += kGroups) {
+        pass_over(ring, at, mine - item, p.stages, lane, p.limit_ns);
+        item = mine + 1;
         const int e = r.expert[slot], row0 = block * kUnitRows, this_slot = slot;
         const int many = __popc(r.tokens[e]);
         const uint8_t *list = r.list[slot];
@@ -584,13 +599,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
             if (s0 >= s1)
                 load(source(then, s0), x);
             here = then;
-            if (last)
+            if (last) {
                 give_back(ring, at, lane);
-            float(&mine)[2 * kUnitRows][9] = red[buf][warp];
-            mine[g][2 * t] = acc[0];
-            mine[g][2 * t + 1] = acc[1];
-            mine[kUnitRows + g][2 * t] = acc[2];
-            mine[kUnitRows + g][2 * t + 1] = acc[3];
+                at.forward(p.stages);
+            }
+            float(&sums)[2 * kUnitRows][9] = red[buf][warp];
+            sums[g][2 * t] = acc[0];
+            sums[g][2 * t + 1] = acc[1];
+            sums[kUnitRows + g][2 * t] = acc[2];
+            sums[kUnitRows + g][2 * t + 1] = acc[3];
             ptx::named_bar_sync(1 + group, 32 * KS);
             // the few sums are done by another warp each time
             for (int k = ((kw + unit) % KS) * 32 + lane; k < kUnitRows * min(8, many - n0); k += 32 * KS) {
@@ -618,6 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
             buf ^= 1; // the other half: the next barrier tells that this one has been read
         }
     }
+    pass_over(ring, at, items - item, p.stages, lane, p.limit_ns);
 }
 
 constexpr int kDownRows = 16;
@@ -650,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
             share = k;
         }
     }
-    init_ring(ring, p.stages, share);
+    init_ring(ring, p.stages, kConsumers);
     __syncthreads();
     const int64_t row0 = (int64_t)blockIdx.x * kDownRows;
     // a buffer: 16 rows' codes (8 inter bytes), their scales (inter)
@@ -693,8 +711,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
         Columns here = group < r.slots ? columns(group, 0) : Columns{nullptr, false};
         load(source(here, kw), x);
         Place at = {0, 0};
-        at.forward(group, p.stages);
-        for (int i = group; i < r.slots; i += groups, at.forward(groups, p.stages)) {
+        int item = 0; // where the ring is
+        for (int i = group; i < r.slots; i += groups) {
+            pass_over(ring, at, i - item, p.stages, lane, p.limit_ns);
+            item = i + 1;
             const int many = __popc(r.tokens[r.expert[i]]);
             const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.s * bytes;
             const uint32_t row_q = from + (uint32_t)(g * (p.inter / 2));
@@ -742,7 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
                 }
             }
             give_back(ring, at, lane);
+            at.forward(p.stages);
         }
+        pass_over(ring, at, r.slots - item, p.stages, lane, p.limit_ns);
     }
     __syncthreads();
     if (warp == kConsumers)

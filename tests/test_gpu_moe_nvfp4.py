@@ -196,3 +196,43 @@ def test_layers_that_share_a_workspace():
         shared = [jq.moe_nvfp4(r, router, w13, w2, 8, workspace=ws) for r in rows]
         for a, b in zip(alone, shared):
             assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize("m,e,h,i,topk", [(2, 2, 16384, 64, 1), (1, 2, 64, 16384, 2), (16, 3, 16384, 32, 2)])
+def test_the_widest_layers(m, e, h, i, topk):
+    """Rows of 16384 values: one buffer in the ring, given back before it is filled again."""
+    x, router, w13, w2 = _layer(m, e, h, i, 13)
+    for out_dtype in (torch.bfloat16, torch.float32):
+        y, ids, p = jq.moe_nvfp4(x, router, w13, w2, topk, True, out_dtype)
+        assert jq.jetq_check_device_error() == jq.OK
+        _check(x, router, w13, w2, topk, True, out_dtype, y, ids, p)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e30])
+def test_tokens_of_any_magnitude(size):
+    """x times 2^k gives gate and up times 2^k: both products see the same FP16 values, whatever k is (up is scaled
+    back by a power of two; gate is kept at the size where silu is not linear by its weights' scale)."""
+    x, router, w13, w2 = _layer(3, 6, 128, 64, 14)
+    k = 2.0 ** round(torch.tensor(size).log2().item())
+    w13s = dict(w13, sg=w13["sg"] / k)
+    a = jq.moe_nvfp4(x, router, w13, w2, 6, out_dtype=torch.float32)
+    b = jq.moe_nvfp4((x.float() * k).to(torch.bfloat16), (router.float() / k).to(torch.bfloat16), w13s, w2, 6,
+                     out_dtype=torch.float32)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with a workspace of its own."""
+    x, router, w13, w2 = _layer(16, 40, 512, 160, 15)
+    want = [jq.moe_nvfp4(x[:9], router, w13, w2, 5), jq.moe_nvfp4(x, router, w13, w2, 7)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(30):
+        got[0].append(jq.moe_nvfp4(x[:9], router, w13, w2, 5, stream=streams[0]))
+        got[1].append(jq.moe_nvfp4(x, router, w13, w2, 7, stream=streams[1]))
+    torch.cuda.synchronize()
+    for runs, w in zip(got, want):
+        for r in runs:
+            assert all(torch.equal(a, b) for a, b in zip(r, w))

@@ -125,7 +125,7 @@ def test_lengths_of_one_sequence(n, by_seg):
 
 @pytest.mark.parametrize("lengths", [
     [1] * 700, [0, 0, 5, 0, 0, 0, 123, 0, 1, 0], [128] * 9, [127, 129, 0, 128, 1], [40000, 1, 0, 50000],
-    [3] * 300 + [70000] + [0] * 200 + [2] * 400, [33000] * 5])
+    [3] * 300 + [70000] + [0] * 200 + [2] * 400, [33000] * 5, [0] * 5000 + [700] + [0] * 5000, [1] * 2000 + [0] * 4000])
 @pytest.mark.parametrize("by_seg,mean", [(False, "segs"), (True, "tokens")])
 def test_ragged_sequences(lengths, by_seg, mean):
     """Sequences of one token, empty ones, ends on a window's border, some that a whole block has to join."""
