@@ -10,16 +10,16 @@
 //   2. gate and up: a unit is 8 rows of gate and the same 8 of up of one chosen
 //      expert, for all tokens that chose it.  Both are contiguous in memory: a
 //      producer thread keeps a ring of bulk copies into shared memory ahead of
-//      two or four groups of warps, which take a unit each and share its K;
+//      one to four groups of warps, which take a unit each and share its K;
 //   3. down: a CTA owns 16 rows of y and runs through all chosen experts in the
 //      same way, its 16 warps sharing (expert, K) steps, so that y is summed in
 //      the CTA's registers and written once, without atomics.
 // Each CTA of kernel 2 chooses the experts from the logits itself (3 to 4 us, in
 // place of another kernel), and the first one leaves its choices to kernel 3.
-// Measured in a graph, 128 experts of which 8 are taken, 2048/768: one token 23 us
+// Measured in a graph, 128 experts of which 8 are taken, 2048/768: one token 23 to 25 us
 // (HBM 3.2; the launches, the choice and the kernels' first copies are most of
-// it), sixteen tokens (82 experts) 90 us: router 5, choice 4, gate and up 35, down
-// 36, HBM 32; the last two use half of the issue slots, most of them to decode.
+// it), sixteen tokens (82 experts) 92 us: router 5, choice 4, gate and up 36, down
+// 37, HBM 32; the last two use half of the issue slots, most of them to decode.
 // Loads issued by the threads themselves, with K shared by eight warps: 145 us.
 // Rows copied one by one to a pitch without bank conflicts: 147 us (a bulk copy
 // costs about 50 ns, whatever its size).
@@ -54,7 +54,7 @@ constexpr int kMaxTokens = 16, kMaxExperts = 256, kMaxTop = 16;
 constexpr int kStep = 128;             // columns a warp step
 constexpr int kConsumers = 16;         // warps that compute; one more copies
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kMaxStages = 24;
+constexpr int kMaxStages = 28;         // buffers of a ring
 constexpr int kRingBytes = 192 * 1024;
 constexpr int64_t kPrefetchBytes = 32 << 20; // down weights that kernel 2 brings into L2 for kernel 3
 
@@ -75,7 +75,8 @@ struct MoeParams {
     void *y;
     int64_t ldy;
     int out_bf16;
-    int stages;      // of the kernel's ring
+    int depth;       // of the kernel's ring: buffers a group (gate and up)
+    int buffers;     // in all
     unsigned long long limit_ns;
 };
 
@@ -378,18 +379,22 @@ __device__ __forceinline__ void split(float a, __nv_bfloat16 (&out)[PARTS])
     }
 }
 
-// The ring: `stages` buffers, each filled by the producer thread's bulk copies
-// (full) and given back by the warps that read it (empty).
+// The ring: `groups` times `depth` buffers, each filled by the producer thread's
+// bulk copies (full) and given back by the warps that read it (empty).  Item i
+// is group i % groups' own and goes through that group's buffers in turn, so that
+// the same warps follow every phase of a barrier: a wait knows a phase by its
+// parity only, and a reader that skipped items of others in a common ring could
+// take an older phase for its own.
 struct Ring {
     uint64_t full[kMaxStages], empty[kMaxStages];
     int abort_word;
 };
 
-__device__ __forceinline__ void init_ring(Ring &ring, int stages, int readers)
+__device__ __forceinline__ void init_ring(Ring &ring, int buffers, int readers)
 {
     if (threadIdx.x == 0) {
         ring.abort_word = 0;
-        for (int s = 0; s < stages; ++s) {
+        for (int s = 0; s < buffers; ++s) {
             ptx::mbar_init(ptx::smem_addr(&ring.full[s]), 1);
             ptx::mbar_init(ptx::smem_addr(&ring.empty[s]), readers);
         }
@@ -398,42 +403,47 @@ __device__ __forceinline__ void init_ring(Ring &ring, int stages, int readers)
     // the caller's next __syncthreads makes them visible
 }
 
-// The producer thread: buffer `i % stages` gets item i, for each of `items`; copy(i, buffer, barrier) issues `bytes`.
+// The producer thread: copy(i, buffer, barrier) issues the `bytes` of item i, for each of `items`.
 template <class F>
-__device__ __forceinline__ void produce(Ring &ring, int stages, int items, uint32_t bytes,
+__device__ __forceinline__ void produce(Ring &ring, int groups, int depth, int items, uint32_t bytes,
                                         unsigned long long limit_ns, F copy)
 {
     volatile int *abort_flag = &ring.abort_word;
-    int s = 0, i = 0;
+    int i = 0, g = 0, c = 0; // the item's group and place in its buffers
     uint32_t ph = 0;
     for (; i < items; ++i) {
+        const int s = g * depth + c;
         if (!ptx::mbar_wait(ptx::smem_addr(&ring.empty[s]), ph ^ 1u, abort_flag, &g_moe_error, kErrTimeout, limit_ns))
             break;
         const uint32_t bar = ptx::smem_addr(&ring.full[s]);
         ptx::mbar_arrive_expect_tx(bar, bytes);
         copy(i, s, bar);
-        if (++s == stages) {
-            s = 0;
-            ph ^= 1u;
+        if (++g == groups) {
+            g = 0;
+            if (++c == depth) {
+                c = 0;
+                ph ^= 1u;
+            }
         }
     }
-    // no copy may be in flight when the CTA ends
-    for (int q = 0; q < stages && q < i; ++q)
-        ptx::mbar_wait(ptx::smem_addr(&ring.full[q]), (uint32_t)((i - 1 - q) / stages) & 1u, abort_flag, &g_moe_error,
-                       kErrTimeout, limit_ns, false);
+    // no copy may be in flight when the CTA ends: the last one of each buffer
+    for (g = 0; g < groups && g < i; ++g) {
+        const int mine = (i - 1 - g) / groups + 1; // the group's items
+        for (c = 0; c < depth && c < mine; ++c)
+            ptx::mbar_wait(ptx::smem_addr(&ring.full[g * depth + c]), (uint32_t)((mine - 1 - c) / depth) & 1u,
+                           abort_flag, &g_moe_error, kErrTimeout, limit_ns, false);
+    }
 }
 
-// A reader's place in the ring.  Every warp waits for every item in turn and gives
-// its buffer back, its group's own items after reading them: a wait knows the
-// phase of a barrier by its parity only, so a reader that skipped items could
-// take an older phase for its own, or be passed by two.
+// A reader's place in its group's buffers, the first of which is `first`.
 struct Place {
-    int s;
+    int first, c;
     uint32_t ph;
-    __device__ __forceinline__ void forward(int stages)
+    __device__ __forceinline__ int buffer() const { return first + c; }
+    __device__ __forceinline__ void forward(int depth)
     {
-        if (++s == stages) {
-            s = 0;
+        if (++c == depth) {
+            c = 0;
             ph ^= 1u;
         }
     }
@@ -443,7 +453,8 @@ struct Place {
 // barriers, on whatever the buffers hold.
 __device__ __forceinline__ void wait_full(Ring &ring, Place at, unsigned long long limit_ns)
 {
-    ptx::mbar_wait(ptx::smem_addr(&ring.full[at.s]), at.ph, &ring.abort_word, &g_moe_error, kErrTimeout, limit_ns);
+    ptx::mbar_wait(ptx::smem_addr(&ring.full[at.buffer()]), at.ph, &ring.abort_word, &g_moe_error, kErrTimeout,
+                   limit_ns);
     __syncwarp(); // the lanes go on to a warp's instructions
 }
 
@@ -451,18 +462,7 @@ __device__ __forceinline__ void give_back(Ring &ring, Place at, int lane)
 {
     __syncwarp();
     if (lane == 0)
-        ptx::mbar_arrive(ptx::smem_addr(&ring.empty[at.s]));
-}
-
-// Passes over `items` that other groups read.
-__device__ __forceinline__ void pass_over(Ring &ring, Place &at, int items, int stages, int lane,
-                                          unsigned long long limit_ns)
-{
-    for (int i = 0; i < items; ++i) {
-        wait_full(ring, at, limit_ns);
-        give_back(ring, at, lane);
-        at.forward(stages);
-    }
+        ptx::mbar_arrive(ptx::smem_addr(&ring.empty[at.buffer()]));
 }
 
 constexpr int kUnitRows = 8; // of gate and of up
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
     __shared__ float red[2][kConsumers][2 * kUnitRows][9];
     uint8_t *buffers = ptx::align_smem<128>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    init_ring(ring, p.stages, kConsumers);
+    init_ring(ring, kGroups * p.depth, KS);
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     choose(p, r);
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
 
     if (warp == kConsumers) {
         if (lane == 0) {
-            produce(ring, p.stages, items, bytes, p.limit_ns, [&](int i, int s, uint32_t bar) {
+            produce(ring, kGroups, p.depth, items, bytes, p.limit_ns, [&](int i, int s, uint32_t bar) {
                 const int unit = (int)blockIdx.x + i * (int)gridDim.x;
                 const int64_t row =
                     (int64_t)r.expert[unit / blocks] * 2 * p.inter + (int64_t)(unit % blocks) * kUnitRows;
@@ -532,8 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
     const int jump = kGroups * (int)gridDim.x, jump_slots = jump / blocks, jump_blocks = jump - jump_slots * blocks;
     int unit = (int)blockIdx.x + group * (int)gridDim.x, slot = unit / blocks, block = unit - slot * blocks;
     int buf = 0;
-    Place at = {0, 0};
-    int item = 0; // where the ring is
+    Place at = {group * p.depth, 0, 0};
     // eight of a unit's tokens at a time (few experts have more); the values of x are loaded a step ahead
     struct Columns {
         const __half *row; // of this lane's token
@@ -553,14 +552,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
     uint4 x[4], next[4];
     Columns here = unit < units ? columns(slot, 0) : Columns{nullptr, false};
     load(source(here, s0), x);
-    for (int mine = group; unit < units; unit += jump, mine += kGroups) {
-        pass_over(ring, at, mine - item, p.stages, lane, p.limit_ns);
-        item = mine + 1;
+    for (; unit < units; unit += jump, at.forward(p.depth)) {
         const int e = r.expert[slot], row0 = block * kUnitRows, this_slot = slot;
         const int many = __popc(r.tokens[e]);
         const uint8_t *list = r.list[slot];
         const float scale = __ldg(p.sg13 + e), out = __ldg(p.sg2 + e);
-        const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.s * bytes;
+        const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.buffer() * bytes;
         const uint32_t row_q = from + (uint32_t)(g * (p.h / 2));
         const uint32_t row_s = from + 2 * codes + (uint32_t)(g * (p.h / 16));
         slot += jump_slots; // the next unit's
@@ -599,10 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
             if (s0 >= s1)
                 load(source(then, s0), x);
             here = then;
-            if (last) {
+            if (last)
                 give_back(ring, at, lane);
-                at.forward(p.stages);
-            }
             float(&sums)[2 * kUnitRows][9] = red[buf][warp];
             sums[g][2 * t] = acc[0];
             sums[g][2 * t + 1] = acc[1];
@@ -635,7 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
             buf ^= 1; // the other half: the next barrier tells that this one has been read
         }
     }
-    pass_over(ring, at, items - item, p.stages, lane, p.limit_ns);
 }
 
 constexpr int kDownRows = 16;
@@ -659,23 +653,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
         reinterpret_cast<uint4 *>(&r)[i] = __ldcg(reinterpret_cast<const uint4 *>(p.routes) + i);
     __syncthreads();
     const int steps = (p.inter + kStep - 1) / kStep;
-    // Warps that share a slot's K, a power of two: what leaves the fewest steps to the busiest warp.
-    int share = 1;
-    for (int k = 1, best = 0x7FFFFFFF; k <= kConsumers; k *= 2) {
-        const int cost = (r.slots + kConsumers / k - 1) / (kConsumers / k) * ((steps + k - 1) / k);
-        if (cost < best) {
+    // Warps that share a slot's K, a power of two: what leaves the fewest steps to the busiest warp, where the ring
+    // has two buffers for each group that has a slot, or one for every slot.
+    int share = kConsumers, depth = p.buffers;
+    for (int k = kConsumers, best = 0x7FFFFFFF; k >= 1; k /= 2) {
+        const int groups = kConsumers / k, used = min(groups, r.slots);
+        const int cost = (r.slots + groups - 1) / groups * ((steps + k - 1) / k);
+        if ((used == 1 || 2 * used <= p.buffers || (used == r.slots && used <= p.buffers)) && cost <= best) {
             best = cost;
             share = k;
+            depth = p.buffers / used;
         }
     }
-    init_ring(ring, p.stages, kConsumers);
+    init_ring(ring, p.buffers, share);
     __syncthreads();
     const int64_t row0 = (int64_t)blockIdx.x * kDownRows;
     // a buffer: 16 rows' codes (8 inter bytes), their scales (inter)
     const uint32_t codes = 8u * p.inter, scales = (uint32_t)p.inter, bytes = codes + scales;
     if (warp == kConsumers) {
         if (lane == 0)
-            produce(ring, p.stages, r.slots, bytes, p.limit_ns, [&](int i, int s, uint32_t bar) {
+            produce(ring, kConsumers / share, depth, r.slots, bytes, p.limit_ns, [&](int i, int s, uint32_t bar) {
                 const int64_t row = (int64_t)r.expert[i] * p.h + row0;
                 const uint32_t dst = ptx::smem_addr(buffers) + (uint32_t)s * bytes;
                 ptx::bulk_load(dst, p.q2 + row * (p.inter / 2), codes, bar);
@@ -710,13 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
         uint4 x[4], next[4];
         Columns here = group < r.slots ? columns(group, 0) : Columns{nullptr, false};
         load(source(here, kw), x);
-        Place at = {0, 0};
-        int item = 0; // where the ring is
-        for (int i = group; i < r.slots; i += groups) {
-            pass_over(ring, at, i - item, p.stages, lane, p.limit_ns);
-            item = i + 1;
+        Place at = {group * depth, 0, 0};
+        for (int i = group; i < r.slots; i += groups, at.forward(depth)) {
             const int many = __popc(r.tokens[r.expert[i]]);
-            const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.s * bytes;
+            const uint32_t from = ptx::smem_addr(buffers) + (uint32_t)at.buffer() * bytes;
             const uint32_t row_q = from + (uint32_t)(g * (p.inter / 2));
             const uint32_t row_s = from + codes + (uint32_t)(g * (p.inter / 16));
             for (int n0 = 0; n0 < many; n0 += kTok) {
@@ -762,9 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
                 }
             }
             give_back(ring, at, lane);
-            at.forward(p.stages);
         }
-        pass_over(ring, at, r.slots - item, p.stages, lane, p.limit_ns);
     }
     __syncthreads();
     if (warp == kConsumers)
@@ -784,10 +776,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(const MoeParams p)
     }
 }
 
-// One launch with a ring of as many buffers as there is room for (`items` at most).
+// Buffers that the ring has room for.
+int64_t ring_room(int64_t buffer)
+{
+    const int64_t room = kRingBytes / buffer;
+    return room < kMaxStages ? room : kMaxStages;
+}
+
 template <class K>
-cudaError_t run_ring(K kern, std::atomic<unsigned long long> &configured, int64_t grid, int64_t buffer, int64_t items,
-                     MoeParams p, cudaStream_t st)
+cudaError_t run_ring(K kern, std::atomic<unsigned long long> &configured, int64_t grid, int64_t buffer, MoeParams p,
+                     cudaStream_t st)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -800,25 +798,41 @@ cudaError_t run_ring(K kern, std::atomic<unsigned long long> &configured, int64_
         if (dev < 64)
             configured.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    int64_t stages = kRingBytes / buffer;
-    stages = stages < kMaxStages ? stages : kMaxStages;
-    p.stages = (int)(stages < items ? stages : items);
-    return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), (size_t)(p.stages * buffer + 128), st, p);
+    return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), (size_t)(p.buffers * buffer + 128), st, p);
 }
 
 template <int KS, int PARTS>
-cudaError_t run_gate_up(const MoeParams &p, int64_t units, cudaStream_t st)
+cudaError_t run_gate_up(MoeParams p, int64_t units, cudaStream_t st)
 {
     static std::atomic<unsigned long long> configured{0};
-    const int64_t grid = units < sm_count() ? units : sm_count();
-    return run_ring(k_moe_gate_up<KS, PARTS>, configured, grid, 9 * (int64_t)p.h, (units + grid - 1) / grid, p, st);
+    constexpr int kGroups = kConsumers / KS;
+    const int64_t grid = units < sm_count() ? units : sm_count(), buffer = 9 * (int64_t)p.h;
+    const int64_t room = ring_room(buffer) / kGroups, items = (units + grid - 1) / grid; // a group's; a CTA's at most
+    const int64_t most = (items + kGroups - 1) / kGroups;
+    p.depth = (int)(room < most ? room : most);
+    p.buffers = p.depth * kGroups;
+    return run_ring(k_moe_gate_up<KS, PARTS>, configured, grid, buffer, p, st);
+}
+
+// Warps that share a unit: eight where a CTA has few units, so that all of
+// them run at a time; four (half the reductions) where it has many; more where
+// the ring has no room for two buffers a group.
+template <int PARTS>
+cudaError_t run_gate_up(const MoeParams &p, int64_t units, cudaStream_t st)
+{
+    const int64_t room = ring_room(9 * (int64_t)p.h);
+    if (units > 8 * (int64_t)sm_count() && room >= 8)
+        return run_gate_up<4, PARTS>(p, units, st);
+    return room >= 4 ? run_gate_up<8, PARTS>(p, units, st) : run_gate_up<16, PARTS>(p, units, st);
 }
 
 template <int COLS>
-cudaError_t run_down(const MoeParams &p, int64_t slots, cudaStream_t st)
+cudaError_t run_down(MoeParams p, int64_t slots, cudaStream_t st)
 {
     static std::atomic<unsigned long long> configured{0};
-    return run_ring(k_moe_down<COLS>, configured, p.h / kDownRows, 9 * (int64_t)p.inter, slots, p, st);
+    const int64_t buffer = 9 * (int64_t)p.inter, room = ring_room(buffer);
+    p.buffers = (int)(room < slots ? room : slots);
+    return run_ring(k_moe_down<COLS>, configured, p.h / kDownRows, buffer, p, st);
 }
 
 // The workspace: logits, the tokens' inverse scales, the choices, x in FP16, the activations.
@@ -873,13 +887,7 @@ cudaError_t launch_moe_nvfp4(const MoeNvfp4Args &a, cudaStream_t st)
         return e;
     // slots at most
     const int64_t slots = a.m * a.topk < a.experts ? a.m * a.topk : a.experts, units = slots * (a.inter / kUnitRows);
-    // Warps that share a unit: eight where a CTA has few units, so that all of
-    // them run at a time; four (half the reductions) where it has many.
-    const bool few = units <= 8 * (int64_t)sm_count();
-    if (p.out_bf16)
-        e = few ? run_gate_up<8, 2>(p, units, st) : run_gate_up<4, 2>(p, units, st);
-    else
-        e = few ? run_gate_up<8, 3>(p, units, st) : run_gate_up<4, 3>(p, units, st);
+    e = p.out_bf16 ? run_gate_up<2>(p, units, st) : run_gate_up<3>(p, units, st);
     if (e != cudaSuccess)
         return e;
     return p.out_bf16 ? run_down<2>(p, slots, st) : run_down<4>(p, slots, st);

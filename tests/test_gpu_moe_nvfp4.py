@@ -198,9 +198,12 @@ def test_layers_that_share_a_workspace():
             assert all(torch.equal(s, t) for s, t in zip(a, b))
 
 
-@pytest.mark.parametrize("m,e,h,i,topk", [(2, 2, 16384, 64, 1), (1, 2, 64, 16384, 2), (16, 3, 16384, 32, 2)])
-def test_the_widest_layers(m, e, h, i, topk):
-    """Rows of 16384 values: one buffer in the ring, given back before it is filled again."""
+@pytest.mark.parametrize("m,e,h,i,topk", [
+    (2, 2, 16384, 64, 1), (1, 2, 64, 16384, 2), (16, 3, 16384, 32, 2), (5, 4, 8192, 96, 2), (9, 6, 128, 8192, 3),
+    (16, 40, 4096, 256, 8), (7, 9, 96, 4096, 4)])
+def test_wide_layers(m, e, h, i, topk):
+    """Rows of up to 16384 values: rings of one to five buffers, each given back before it is filled again, shared by
+    all warps, two groups or eight."""
     x, router, w13, w2 = _layer(m, e, h, i, 13)
     for out_dtype in (torch.bfloat16, torch.float32):
         y, ids, p = jq.moe_nvfp4(x, router, w13, w2, topk, True, out_dtype)
