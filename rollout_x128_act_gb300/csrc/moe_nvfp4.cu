@@ -117,7 +117,8 @@ __device__ __forceinline__ void scale_token(const MoeParams &p, int tok, float *
         uint32_t v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __half2 h = __floats2half2_rn(__uint_as_float(u[i] << 16) * f, __uint_as_float(u[i] & 0xffff0000u) * f);
+            const __half2 h =
+                __floats2half2_rn(__uint_as_float(u[i] << 16) * f, __uint_as_float(u[i] & 0xffff0000u) * f);
             v[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
         *reinterpret_cast<uint4 *>(p.x16 + (int64_t)tok * p.h + k) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -882,7 +883,8 @@ cudaError_t launch_moe_nvfp4(const MoeNvfp4Args &a, cudaStream_t st)
     p.ldy = a.ldy;
     p.out_bf16 = a.out_dtype == JETQ_OUT_BF16;
     p.limit_ns = kWaitLimitNs;
-    cudaError_t e = launch_pdl(k_moe_router, dim3((unsigned)(a.experts + (a.m < 8 ? a.m : 8)), (unsigned)((a.m + 7) / 8)), dim3(kRouterThreads), 0, st, p);
+    const dim3 router((unsigned)(a.experts + (a.m < 8 ? a.m : 8)), (unsigned)((a.m + 7) / 8));
+    cudaError_t e = launch_pdl(k_moe_router, router, dim3(kRouterThreads), 0, st, p);
     if (e != cudaSuccess)
         return e;
     // slots at most
