@@ -49,6 +49,7 @@ struct PolicyParams {
     int64_t n, windows;
     int nseg;
     bool adv_token, by_seg;
+    bool adv_sums; // both: sums of the advantages of either sign
     int chunk; // consecutive windows a warp
     int mean;
     float scale, kl;
@@ -66,8 +67,9 @@ struct PolicyParams {
 // Sums over the counted tokens of a sequence in a chunk.
 struct alignas(16) Piece {
     int count, clipped; // clipped: of a segment's ratio the tokens with A < 0
-    float a, b, c, kl;  // c + c_rest: L, or of a segment's ratio logr; then with an advantage a token
-    float c_rest, unused; // a: the positive A, b: the negative A
+    float c, c_rest;    // c + c_rest: L, or of a segment's ratio logr
+    float kl, unused[3];
+    float a, a_rest, b, b_rest; // of a segment's ratio with an advantage a token: the positive A, the negative A
 };
 
 // Sums over sequences: surrogate and KL term (with their rests), numbers of clipped tokens, tokens, sequences.
@@ -211,6 +213,17 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// s + c of all lanes, compensated.
+__device__ __forceinline__ void warp_sum(float &s, float &c)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float s2 = __shfl_xor_sync(0xFFFFFFFFu, s, o), c2 = __shfl_xor_sync(0xFFFFFFFFu, c, o);
+        add_to(s, c, s2);
+        c += c2;
+    }
+}
+
 // What a lane loads of its tokens t0 + lane + 32 k.
 struct Tokens {
     float x[kSlots], y[kSlots], z[kSlots], A[kSlots];
@@ -266,7 +279,7 @@ __device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t chunk,
     walk.start(p, w0 * kWindow, lane);
     // this lane's sums of the piece
     int count = 0, clipped = 0;
-    float a = 0.0f, b = 0.0f, c = 0.0f, rest = 0.0f, q = 0.0f;
+    float a = 0.0f, a_rest = 0.0f, b = 0.0f, b_rest = 0.0f, c = 0.0f, rest = 0.0f, q = 0.0f;
     for (int64_t w = w0; w < w1; ++w) {
         tk = next;
         if (w + 1 < w1)
@@ -288,12 +301,16 @@ __device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t chunk,
                 const float A = p.adv_token ? tk.A[k] : A_seg;
                 bool side;
                 // compensated: a policy that is still its sampling policy adds the same -A at each token of a
-                // sequence, whose roundings do not average out
+                // sequence, whose roundings do not average out; and A of either sign nearly cancel
                 if (BY_SEG) {
                     side = A < 0.0f;
-                    if (p.adv_token) {
-                        a += in && !side ? A : 0.0f;
-                        b += in && side ? A : 0.0f;
+                    if (p.adv_token && in) {
+                        float sum = side ? b : a, lost = side ? b_rest : a_rest;
+                        add_to(sum, lost, A);
+                        a = side ? a : sum;
+                        a_rest = side ? a_rest : lost;
+                        b = side ? sum : b;
+                        b_rest = side ? lost : b_rest;
                     }
                     if (in) {
                         add_to(c, rest, d[k]);
@@ -315,23 +332,20 @@ __device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t chunk,
             clipped = __reduce_add_sync(0xFFFFFFFFu, clipped);
             if (p.ref)
                 q = warp_sum(q);
+            warp_sum(c, rest);
             if (BY_SEG && p.adv_token) {
-                a = warp_sum(a);
-                b = warp_sum(b);
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                const float c2 = __shfl_xor_sync(0xFFFFFFFFu, c, o), r2 = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
-                add_to(c, rest, c2);
-                rest += r2;
+                warp_sum(a, a_rest);
+                warp_sum(b, b_rest);
             }
             if (lane == 0) {
                 float4 *out = reinterpret_cast<float4 *>(p.pieces + (chunk + s));
-                out[0] = make_float4(__int_as_float(count), __int_as_float(clipped), a, b);
-                out[1] = make_float4(c, q, rest, 0.0f);
+                out[0] = make_float4(__int_as_float(count), __int_as_float(clipped), c, rest);
+                p.pieces[chunk + s].kl = q;
+                if (BY_SEG && p.adv_token)
+                    out[2] = make_float4(a, a_rest, b, b_rest);
             }
             count = clipped = 0;
-            a = b = c = rest = q = 0.0f;
+            a = a_rest = b = b_rest = c = rest = q = 0.0f;
         });
     }
 }
@@ -350,21 +364,23 @@ struct SegSums {
         count = clipped = 0;
         a = a_rest = b = b_rest = c = c_rest = kl = kl_rest = 0.0f;
     }
-    __device__ __forceinline__ void add(const Piece *piece, bool by_seg)
+    __device__ __forceinline__ void add(const Piece *piece, bool adv_sums)
     {
         const float4 u = __ldcg(reinterpret_cast<const float4 *>(piece));
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece) + 1);
         count += (unsigned)__float_as_int(u.x);
         clipped += (unsigned)__float_as_int(u.y);
-        add_to(c, c_rest, v.x);
-        c_rest += v.z;
-        add_to(kl, kl_rest, v.y);
-        if (by_seg) {
-            add_to(a, a_rest, u.z);
-            add_to(b, b_rest, u.w);
+        add_to(c, c_rest, u.z);
+        c_rest += u.w;
+        add_to(kl, kl_rest, __ldcg(&piece->kl));
+        if (adv_sums) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece) + 2);
+            add_to(a, a_rest, v.x);
+            a_rest += v.y;
+            add_to(b, b_rest, v.z);
+            b_rest += v.w;
         }
     }
-    __device__ __forceinline__ void add(const SegSums &o, bool by_seg)
+    __device__ __forceinline__ void add(const SegSums &o, bool adv_sums)
     {
         count += o.count;
         clipped += o.clipped;
@@ -372,14 +388,14 @@ struct SegSums {
         c_rest += o.c_rest;
         add_to(kl, kl_rest, o.kl);
         kl_rest += o.kl_rest;
-        if (by_seg) {
+        if (adv_sums) {
             add_to(a, a_rest, o.a);
             a_rest += o.a_rest;
             add_to(b, b_rest, o.b);
             b_rest += o.b_rest;
         }
     }
-    __device__ __forceinline__ void add_lane(int o, bool by_seg) // of lane ^ o
+    __device__ __forceinline__ void add_lane(int o, bool adv_sums) // of lane ^ o
     {
         SegSums x;
         x.count = __shfl_xor_sync(0xFFFFFFFFu, count, o);
@@ -388,13 +404,13 @@ struct SegSums {
         x.c_rest = __shfl_xor_sync(0xFFFFFFFFu, c_rest, o);
         x.kl = __shfl_xor_sync(0xFFFFFFFFu, kl, o);
         x.kl_rest = __shfl_xor_sync(0xFFFFFFFFu, kl_rest, o);
-        if (by_seg) {
+        if (adv_sums) {
             x.a = __shfl_xor_sync(0xFFFFFFFFu, a, o);
             x.a_rest = __shfl_xor_sync(0xFFFFFFFFu, a_rest, o);
             x.b = __shfl_xor_sync(0xFFFFFFFFu, b, o);
             x.b_rest = __shfl_xor_sync(0xFFFFFFFFu, b_rest, o);
         }
-        add(x, by_seg);
+        add(x, adv_sums);
     }
 };
 
@@ -425,6 +441,17 @@ __device__ __forceinline__ void warp_totals(Totals &t, int lanes)
     }
 }
 
+// s + c -= (a + a_rest) f
+__device__ __forceinline__ void sub_product(float &s, float &c, float a, float a_rest, float f)
+{
+    if (a == 0.0f) // a sum without a token of its sign stays out: 0 * infinity is no number
+        return;
+    const float v = __fmul_rn(-a, f);
+    add_to(s, c, v);
+    if (fabsf(v) < INFINITY)
+        c += fmaf(-a, f, -v) - a_rest * f;
+}
+
 // A sequence's saved pair and its share of the totals.
 __device__ __forceinline__ void finish(const PolicyParams &p, int s, const SegSums &x, Totals &tot)
 {
@@ -432,11 +459,14 @@ __device__ __forceinline__ void finish(const PolicyParams &p, int s, const SegSu
     float l = x.c, l_rest = fabsf(x.c) < INFINITY ? x.c_rest : 0.0f, g = 0.0f;
     unsigned long long clipped = x.clipped;
     if (p.by_seg && x.count) {
-        float a = whole(x.a, x.a_rest), b = whole(x.b, x.b_rest);
+        float a = x.a, a_rest = fabsf(x.a) < INFINITY ? x.a_rest : 0.0f;
+        float b = x.b, b_rest = fabsf(x.b) < INFINITY ? x.b_rest : 0.0f;
         if (!p.adv_token) { // one advantage: no sum
-            const float A = __ldg(p.adv + s);
-            a = A < 0.0f ? 0.0f : A * n;
-            b = A < 0.0f ? A * n : 0.0f;
+            const float A = __ldg(p.adv + s), An = A * n, rest = fabsf(An) < INFINITY ? fmaf(A, n, -An) : 0.0f;
+            a = A < 0.0f ? 0.0f : An;
+            a_rest = A < 0.0f ? 0.0f : rest;
+            b = A < 0.0f ? An : 0.0f;
+            b_rest = A < 0.0f ? rest : 0.0f;
         }
         const float c = whole(x.c, x.c_rest);
         // the mean in two floats: it is compared with the borders
@@ -449,13 +479,20 @@ __device__ __forceinline__ void finish(const PolicyParams &p, int s, const SegSu
         const bool hi = above(mean, rest, p.log_high), lo = below(mean, rest, p.log_low);
         const bool du = above(mean, rest, p.log_dual);
         const float ratio = ratio_of(mean, rest);
-        // a sum without a token of its sign stays out: 0 * infinity is no number
-        const float pos = a != 0.0f ? -a * (hi ? p.high : ratio) : 0.0f;
-        const float neg = b != 0.0f ? -b * (lo ? p.low : du ? p.dual : ratio) : 0.0f;
-        const float live = (hi ? 0.0f : a) + (lo || du ? 0.0f : b);
-        l = pos;
-        l_rest = 0.0f;
-        add_to(l, l_rest, neg);
+        // What the ratio multiplies, rounded after the two signs have met: their sums grow with n, their
+        // difference with its root (each sum rounded first, gradients of 2 million tokens were off by 1e-5).
+        float live = hi ? 0.0f : a, live_rest = hi ? 0.0f : a_rest;
+        if (!lo && !du) {
+            add_to(live, live_rest, b);
+            live_rest += b_rest;
+        }
+        live = whole(live, live_rest);
+        l = l_rest = 0.0f;
+        sub_product(l, l_rest, live, 0.0f, ratio);
+        if (hi)
+            sub_product(l, l_rest, a, a_rest, p.high);
+        if (lo || du)
+            sub_product(l, l_rest, b, b_rest, lo ? p.low : p.dual);
         clipped = (hi ? x.count - x.clipped : 0ull) + (lo || du ? x.clipped : 0ull);
         g = live != 0.0f ? __fdiv_rn(live * ratio, n) : 0.0f;
     }
@@ -544,11 +581,11 @@ __device__ __forceinline__ Totals join_segments(const PolicyParams &p, int64_t f
         if (!is_long) {
 #pragma unroll 2
             for (int64_t w = w0 + sub; w < w1; w += kLanesSeg)
-                x.add(p.pieces + (w + s), p.by_seg);
+                x.add(p.pieces + (w + s), p.adv_sums);
         }
 #pragma unroll
         for (int o = kLanesSeg / 2; o; o >>= 1)
-            x.add_lane(o, p.by_seg);
+            x.add_lane(o, p.adv_sums);
         if (s < end && !is_long && sub == 0)
             finish(p, (int)s, x, tot);
         __syncthreads();
@@ -565,10 +602,10 @@ __device__ __forceinline__ Totals join_segments(const PolicyParams &p, int64_t f
             x.clear();
 #pragma unroll 4
             for (int64_t w = w0 + threadIdx.x; w < w1; w += THREADS)
-                x.add(p.pieces + (w + which), p.by_seg);
+                x.add(p.pieces + (w + which), p.adv_sums);
 #pragma unroll
             for (int o = 16; o; o >>= 1)
-                x.add_lane(o, p.by_seg);
+                x.add_lane(o, p.adv_sums);
             if (lane == 0)
                 sh.seg[warp] = x;
             __syncthreads();
@@ -579,7 +616,7 @@ __device__ __forceinline__ Totals join_segments(const PolicyParams &p, int64_t f
                     x.clear();
 #pragma unroll
                 for (int o = 16; o; o >>= 1)
-                    x.add_lane(o, p.by_seg);
+                    x.add_lane(o, p.adv_sums);
                 if (lane == 0)
                     finish(p, which, x, tot);
             }
@@ -745,6 +782,7 @@ PolicyParams params_of(const PolicyArgs &a)
     p.nseg = a.seg ? a.nseg : 1;
     p.adv_token = a.adv_per_token != 0;
     p.by_seg = a.level == JETQ_POLICY_SEGMENT;
+    p.adv_sums = p.by_seg && p.adv_token;
     const int64_t warps = (int64_t)sm_count() * kWarpsSm;
     const int64_t chunk = ceil_div(p.windows, warps);
     p.chunk = (int)(chunk < kMaxChunk ? chunk : kMaxChunk);

@@ -1,0 +1,54 @@
+"""The policy loss where FP32 loses most: sums of advantages that nearly cancel, ratios beyond FP32's range, advantages
+of zero, the longest chunks.  Against the definition in binary64."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import rollout_x128_act_gb300 as jq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+@pytest.mark.parametrize("lengths,clip", [([500000], 0.2), ([2000001], 0.2), ([700001, 3, 600000, 1], 0.2)])
+@pytest.mark.parametrize("n_tail", [0, 999])
+def test_advantages_that_nearly_cancel(lengths, clip, n_tail):
+    """One ratio a sequence, an advantage a token, nothing clipped: gradient and loss are r times the sum of A, which
+    is some sqrt(n) where the sums of either sign are n / 2.5.
+
+    Bound, relative to the result itself: 2 ulp of expf and 2^-24 of the mean for r (its sums are compensated), and
+    roundings of the sum, its product with r, the division by n and the weight (2^-22 + 6 U, taken as 12 U).  The
+    compensated sum of A adds m^2 U^2 of the sum of |A|, m at most 128 + 64 steps one after another."""
+    rng = np.random.default_rng(sum(lengths))
+    n = sum(lengths) + n_tail
+    old = rng.exponential(1.0, n).astype(np.float32)
+    nll = (old + 0.15 * rng.standard_normal(n)).astype(np.float32)
+    adv = rng.standard_normal(n).astype(np.float32)
+    off = np.concatenate(([0], np.cumsum(lengths))).astype(np.int64)
+    args = dev(nll), dev(old), dev(adv)
+    kw = dict(seg_offsets=dev(off), clip_low=clip, clip_high=clip, level=jq.POLICY_SEGMENT, mean=jq.POLICY_SUM,
+              adv_per_token=True)
+    out, seg = jq.policy_loss(*args, **kw)
+    dnll = jq.policy_loss_bwd(*args, out, seg, **kw).cpu().numpy()
+    loss, slack = 0.0, 0.0
+    logr = old.astype(np.float64) - nll.astype(np.float64)
+    for a, b in zip(off[:-1], off[1:]):
+        mean = math.fsum(logr[a:b]) / (b - a)
+        assert math.log(1 - clip) < mean < math.log(1 + clip)
+        r, total, size = math.exp(mean), math.fsum(adv[a:b].tolist()), math.fsum(np.abs(adv[a:b]).tolist())
+        lost = 192.0 ** 2 * U * U * size
+        got = dnll[a:b].astype(np.float64)
+        assert np.all(got == got[0])
+        want = r * total / (b - a)
+        assert abs(got[0] - want) <= 12 * U * abs(want) + r * lost / (b - a)
+        loss -= r * total
+        slack += r * (12 * U * abs(total) + lost)
+    assert np.all(dnll[off[-1]:] == 0)
+    assert abs(float(out[0]) - loss) <= slack + U * abs(loss)
