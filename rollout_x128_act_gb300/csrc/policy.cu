@@ -261,11 +261,11 @@ struct Tokens {
     }
 };
 
-// exp of d + e
+// exp of d + e; an infinite one has no rest (infinity * e + infinity is no number for a negative e)
 __device__ __forceinline__ float ratio_of(float d, float e)
 {
     const float r = expf(d);
-    return e != 0.0f ? fmaf(r, e, r) : r;
+    return e != 0.0f && r < INFINITY ? fmaf(r, e, r) : r;
 }
 
 // A chunk's sums of each piece.

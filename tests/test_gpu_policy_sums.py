@@ -52,3 +52,30 @@ def test_advantages_that_nearly_cancel(lengths, clip, n_tail):
         slack += r * (12 * U * abs(total) + lost)
     assert np.all(dnll[off[-1]:] == 0)
     assert abs(float(out[0]) - loss) <= slack + U * abs(loss)
+
+
+@pytest.mark.parametrize("by_seg", [False, True])
+@pytest.mark.parametrize("length", [1, 3])
+def test_ratios_that_overflow_with_a_rest(by_seg, length):
+    """Differences of nll above 88.7 that are no FP32 numbers, rests of either sign: the ratio is infinite, and so are
+    loss and gradient where nothing bounds it."""
+    rng = np.random.default_rng(length)
+    nll = rng.uniform(0.1, 0.9, 60).astype(np.float32)
+    old = rng.uniform(95.0, 140.0, 60).astype(np.float32)
+    diff = old - nll  # FP32
+    rest = (old.astype(np.float64) - nll.astype(np.float64)) - diff.astype(np.float64)
+    assert (rest < 0).any() and (rest > 0).any()
+    off = np.arange(0, 61, length, dtype=np.int64)
+    for A, kw in ((-1.0, dict()), (-1.0, dict(clip_dual=3.0)), (1.0, dict())):
+        kw = dict(kw, level=jq.POLICY_SEGMENT if by_seg else jq.POLICY_TOKEN, mean=jq.POLICY_SUM, seg_offsets=dev(off),
+                  adv_per_token=True)
+        args = dev(nll), dev(old), torch.full((60,), A, device=DEV)
+        out, seg = jq.policy_loss(*args, **kw)
+        dnll = jq.policy_loss_bwd(*args, out, seg, **kw)
+        if A < 0 and "clip_dual" not in kw:
+            assert float(out[0]) == math.inf and float(out[3]) == 0
+            assert bool((dnll == -math.inf).all())
+        else:
+            bound = 3.0 if A < 0 else -float(np.float32(1.2))
+            assert abs(float(out[0]) - 60 * bound) <= 60 * abs(bound) * 2 * U
+            assert float(out[3]) == 60 and bool((dnll == 0).all())
