@@ -787,7 +787,8 @@ JETQ_API jetq_status jetq_linear_distill_bwd(const uint16_t *x, int64_t n, int64
  *   clip_low, clip_high        in [0, 1] and [0, 1e6];  clip_dual: 0 (none) or at least 1
  *   scale, kl                  finite
  *   out                        float [6]: loss, sum of weight * L, sum of weight * kl, number of clipped tokens
- *                              (those whose L has no gradient), N, S (rounded to FP32)
+ *                              (those whose A r the bound changes: with A = 0 none, unless r is infinite and
+ *                              the bound stands in for 0 * infinity), N, S (rounded to FP32)
  *   seg                        float [2 nseg] (2 without seg_offsets), 8-byte aligned, for the backward pass
  *   workspace                  device memory, 16-byte aligned, at least
  *                              jetq_policy_loss_workspace_bytes(n, nseg) bytes (nseg = 1 without

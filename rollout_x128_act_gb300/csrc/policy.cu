@@ -66,7 +66,8 @@ struct PolicyParams {
 
 // Sums over the counted tokens of a sequence in a chunk.
 struct alignas(16) Piece {
-    int count, clipped; // clipped: of a segment's ratio the tokens with A < 0
+    // clipped: of a segment's ratio with an advantage a token those with A < 0, and 2^16 times those with A = 0
+    int count, clipped;
     float c, c_rest;    // c + c_rest: L, or of a segment's ratio logr
     float kl, unused[3];
     float a, a_rest, b, b_rest; // of a segment's ratio with an advantage a token: the positive A, the negative A
@@ -129,7 +130,8 @@ __device__ __forceinline__ float kl_slope(float d)
     return fabsf(d) < 1.0f ? d + kl_term(d) : expm1f(d);
 }
 
-// The ratio's bound for advantage A where it is clipped.
+// The bound of the ratio, and whether the ratio is beyond it, for advantage A.  With A = 0 the bound changes nothing,
+// so such a token is not counted as clipped, unless the ratio is infinite: the bound stands in for 0 * infinity.
 __device__ __forceinline__ bool clip(const PolicyParams &p, float A, float d, float e, float &bound)
 {
     if (A < 0.0f) {
@@ -324,7 +326,10 @@ __device__ __forceinline__ void sum_pieces(const PolicyParams &p, int64_t chunk,
                 }
                 q += in ? kl[k] : 0.0f;
                 count += in;
-                clipped += in && side;
+                if (BY_SEG) // 4096 tokens a piece at most
+                    clipped += in && p.adv_token ? side ? 1 : A == 0.0f ? 1 << 16 : 0 : 0;
+                else
+                    clipped += in && side && (A != 0.0f || !(r[k] < INFINITY));
             }
             if (!ends)
                 return;
@@ -357,23 +362,25 @@ __device__ __forceinline__ float whole(float s, float rest)
 }
 
 struct SegSums {
-    unsigned long long count, clipped;
+    unsigned long long count, clipped, zero; // zero: with sums of the advantages, the tokens with A = 0
     float a, a_rest, b, b_rest, c, c_rest, kl, kl_rest;
     __device__ __forceinline__ void clear()
     {
-        count = clipped = 0;
+        count = clipped = zero = 0;
         a = a_rest = b = b_rest = c = c_rest = kl = kl_rest = 0.0f;
     }
     __device__ __forceinline__ void add(const Piece *piece, bool adv_sums)
     {
         const float4 u = __ldcg(reinterpret_cast<const float4 *>(piece));
+        const unsigned two = (unsigned)__float_as_int(u.y);
         count += (unsigned)__float_as_int(u.x);
-        clipped += (unsigned)__float_as_int(u.y);
+        clipped += adv_sums ? two & 0xFFFFu : two;
         add_to(c, c_rest, u.z);
         c_rest += u.w;
         add_to(kl, kl_rest, __ldcg(&piece->kl));
         if (adv_sums) {
             const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece) + 2);
+            zero += two >> 16;
             add_to(a, a_rest, v.x);
             a_rest += v.y;
             add_to(b, b_rest, v.z);
@@ -389,6 +396,7 @@ struct SegSums {
         add_to(kl, kl_rest, o.kl);
         kl_rest += o.kl_rest;
         if (adv_sums) {
+            zero += o.zero;
             add_to(a, a_rest, o.a);
             a_rest += o.a_rest;
             add_to(b, b_rest, o.b);
@@ -405,6 +413,7 @@ struct SegSums {
         x.kl = __shfl_xor_sync(0xFFFFFFFFu, kl, o);
         x.kl_rest = __shfl_xor_sync(0xFFFFFFFFu, kl_rest, o);
         if (adv_sums) {
+            x.zero = __shfl_xor_sync(0xFFFFFFFFu, zero, o);
             x.a = __shfl_xor_sync(0xFFFFFFFFu, a, o);
             x.a_rest = __shfl_xor_sync(0xFFFFFFFFu, a_rest, o);
             x.b = __shfl_xor_sync(0xFFFFFFFFu, b, o);
@@ -460,6 +469,7 @@ __device__ __forceinline__ void finish(const PolicyParams &p, int s, const SegSu
     unsigned long long clipped = x.clipped;
     if (p.by_seg && x.count) {
         float a = x.a, a_rest = fabsf(x.a) < INFINITY ? x.a_rest : 0.0f;
+        unsigned long long neg = x.clipped, zero = x.zero;
         float b = x.b, b_rest = fabsf(x.b) < INFINITY ? x.b_rest : 0.0f;
         if (!p.adv_token) { // one advantage: no sum
             const float A = __ldg(p.adv + s), An = A * n, rest = fabsf(An) < INFINITY ? fmaf(A, n, -An) : 0.0f;
@@ -467,6 +477,8 @@ __device__ __forceinline__ void finish(const PolicyParams &p, int s, const SegSu
             a_rest = A < 0.0f ? 0.0f : rest;
             b = A < 0.0f ? An : 0.0f;
             b_rest = A < 0.0f ? rest : 0.0f;
+            neg = A < 0.0f ? x.count : 0ull;
+            zero = A == 0.0f ? x.count : 0ull;
         }
         const float c = whole(x.c, x.c_rest);
         // the mean in two floats: it is compared with the borders
@@ -493,7 +505,7 @@ __device__ __forceinline__ void finish(const PolicyParams &p, int s, const SegSu
             sub_product(l, l_rest, a, a_rest, p.high);
         if (lo || du)
             sub_product(l, l_rest, b, b_rest, lo ? p.low : p.dual);
-        clipped = (hi ? x.count - x.clipped : 0ull) + (lo || du ? x.clipped : 0ull);
+        clipped = (hi ? x.count - neg - (ratio < INFINITY ? zero : 0ull) : 0ull) + (lo || du ? neg : 0ull);
         g = live != 0.0f ? __fdiv_rn(live * ratio, n) : 0.0f;
     }
     reinterpret_cast<float2 *>(p.save)[s] = make_float2(n, g);

@@ -79,3 +79,47 @@ def test_ratios_that_overflow_with_a_rest(by_seg, length):
             bound = 3.0 if A < 0 else -float(np.float32(1.2))
             assert abs(float(out[0]) - 60 * bound) <= 60 * abs(bound) * 2 * U
             assert float(out[3]) == 60 and bool((dnll == 0).all())
+
+
+@pytest.mark.parametrize("per_token", [False, True])
+@pytest.mark.parametrize("by_seg", [False, True])
+def test_advantages_of_zero_are_not_clipped(by_seg, per_token):
+    """Answers that all earn the same: nothing to bound, whatever the ratio.  A clipped token is one whose A * r the
+    bound changes."""
+    rng = np.random.default_rng(3)
+    nseg, length = 60, 5
+    n = nseg * length
+    adv_seg = np.float32(rng.choice([0.0, -0.0, 0.0, 1.5, -0.7], nseg))
+    adv = np.float32(rng.choice([0.0, -0.0, 0.0, 1.5, -0.7], n)) if per_token else adv_seg
+    jump = np.repeat(rng.choice([-0.9, 0.0, 0.9, 2.0], nseg), length) if by_seg else rng.choice([-0.9, 0.0, 0.9, 2.0], n)
+    old = rng.exponential(1.0, n).astype(np.float32)
+    nll = (old - jump + 0.01 * rng.standard_normal(n)).astype(np.float32)
+    mask = rng.random(n) < 0.8
+    off = (np.arange(nseg + 1) * length).astype(np.int64)
+    A = (adv if per_token else np.repeat(adv_seg, length)).astype(np.float64)
+    logr = old.astype(np.float64) - nll.astype(np.float64)
+    if by_seg:
+        for a, b in zip(off[:-1], off[1:]):
+            if mask[a:b].any():
+                logr[a:b] = logr[a:b][mask[a:b]].mean()
+    r = np.exp(logr)
+    low, high, dual = 1 - float(np.float32(0.2)), 1 + float(np.float32(0.2)), 3.0
+    for use_dual in (False, True):
+        bounded = np.minimum(r * A, np.clip(r, low, high) * A)
+        if use_dual:
+            bounded = np.where(A < 0, np.maximum(bounded, dual * A), bounded)
+        changed = (bounded != r * A) & mask
+        assert changed.any() and not (changed & (A == 0)).any()
+        kw = dict(seg_offsets=dev(off), mask=dev(mask), clip_dual=dual if use_dual else 0.0, mean=jq.POLICY_MEAN_TOKENS,
+                  level=jq.POLICY_SEGMENT if by_seg else jq.POLICY_TOKEN, adv_per_token=per_token)
+        args = dev(nll), dev(old), dev(adv)
+        out, seg = jq.policy_loss(*args, **kw)
+        assert float(out[3]) == changed.sum()
+        dnll = jq.policy_loss_bwd(*args, out, seg, **kw).cpu().numpy()
+        if not by_seg:
+            assert np.all(dnll[(A == 0) & mask] == 0)
+    if not per_token:
+        zero = torch.zeros(nseg, device=DEV)
+        out, seg = jq.policy_loss(args[0], args[1], zero, **kw)
+        assert bool((out[:4] == 0).all())
+        assert bool((jq.policy_loss_bwd(args[0], args[1], zero, out, seg, **kw) == 0).all())
