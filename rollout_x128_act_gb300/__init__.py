@@ -444,6 +444,16 @@ def _want(t, name, dtype, shape=None, rows=False):
         raise ValueError(f"{name}: rows of consecutive elements are wanted, got strides {t.stride()}")
 
 
+def _check_workspace(workspace, x):
+    """A caller's workspace (None passes): consecutive bytes on x's device, all of them the kernels' to write."""
+    if workspace is None:
+        return
+    if not isinstance(workspace, torch.Tensor) or workspace.device != x.device:
+        raise ValueError(f"workspace: a tensor on {x.device} is wanted")
+    if not workspace.is_contiguous():
+        raise ValueError(f"workspace: consecutive elements are wanted, got strides {workspace.stride()}")
+
+
 def _one_device(x, *tensors):
     """All tensors (None passes) on x's device, which is the current one: the launch goes to its stream."""
     at = x.get_device()
@@ -615,6 +625,7 @@ def fprop(qx, sx, qw, sw, out_dtype=torch.float32, path=PATH_AUTO, recipe=RECIPE
     SMs get a workspace (the caller's, if large enough, else a fresh one)."""
     n, c = qx.shape
     d = qw.shape[0]
+    _check_workspace(workspace, qx)
     y = torch.empty((n, d), dtype=out_dtype, device=qx.device)
     wsb = jetq_decode_workspace_bytes(n, d, c) if recipe == RECIPE_BLOCK128 and path != PATH_TRAIN else 0
     if wsb:
@@ -719,7 +730,8 @@ def moe_nvfp4(x, router, w13, w2, topk, renorm=True, out_dtype=torch.bfloat16, w
     _want(sg2, "w2['sg']", torch.float32, (e,))
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out_dtype: {out_dtype} is neither BF16 nor FP32")
-    _one_device(x, router, q13, sb13, sg13, q2, sb2, sg2, workspace)
+    _one_device(x, router, q13, sb13, sg13, q2, sb2, sg2)
+    _check_workspace(workspace, x)
     y = torch.empty((m, h), dtype=out_dtype, device=x.device)
     ids = torch.empty((m, topk), dtype=torch.int64, device=x.device)
     p = torch.empty((m, topk), dtype=torch.float32, device=x.device)
@@ -787,6 +799,7 @@ def norm_bwd(dy, x, w, mean, rstd, kind=NORM_LAYER, bias=False, workspace=None, 
     _want(rstd, "rstd", torch.float32, (n,))
     if kind == NORM_LAYER:
         _want(mean, "mean", torch.float32, (n,))
+    _check_workspace(workspace, x)
     dy, x = _aligned_rows(dy), _aligned_rows(x)
     dx = _norm_rows(x, n, c)
     dw = torch.empty(c, dtype=torch.float32, device=x.device)
@@ -813,6 +826,7 @@ def linear_ce(x, w, target, scale=1.0, workspace=None, stream=None):
         with torch.cuda.stream(stream):
             return linear_ce(x, w, target, scale, workspace)
     _check_head(x, w, target)
+    _check_workspace(workspace, x)
     (n, c), v = x.shape, w.shape[0]
     loss = torch.empty(n, dtype=torch.float32, device=x.device)
     lse = torch.empty(n, dtype=torch.float32, device=x.device)
@@ -831,6 +845,7 @@ def linear_ce_bwd(x, w, target, lse, dloss, scale=1.0, dw_dtype=torch.float32, d
         with torch.cuda.stream(stream):
             return linear_ce_bwd(x, w, target, lse, dloss, scale, dw_dtype, dw, accumulate, workspace)
     _check_head(x, w, target)
+    _check_workspace(workspace, x)
     (n, c), v = x.shape, w.shape[0]
     _want(lse, "lse", torch.float32, (n,))
     _want(dloss, "dloss", torch.float32, (n,))
@@ -872,6 +887,7 @@ def linear_distill(x, w, ids, teacher, scale=1.0, renorm=True, workspace=None, s
         with torch.cuda.stream(stream):
             return linear_distill(x, w, ids, teacher, scale, renorm, workspace)
     _check_distill(x, w, ids, teacher)
+    _check_workspace(workspace, x)
     (n, c), v, k = x.shape, w.shape[0], ids.shape[1]
     loss = torch.empty(n, dtype=torch.float32, device=x.device)
     lse = torch.empty(n, dtype=torch.float32, device=x.device)
@@ -893,6 +909,7 @@ def linear_distill_bwd(x, w, ids, teacher, lse, logp, dloss, scale=1.0, renorm=T
             return linear_distill_bwd(x, w, ids, teacher, lse, logp, dloss, scale, renorm, dw_dtype, dw, accumulate,
                                       workspace)
     _check_distill(x, w, ids, teacher)
+    _check_workspace(workspace, x)
     (n, c), v, k = x.shape, w.shape[0], ids.shape[1]
     _want(lse, "lse", torch.float32, (n,))
     _want(logp, "logp", torch.float32, (n, k))
@@ -902,7 +919,7 @@ def linear_distill_bwd(x, w, ids, teacher, lse, logp, dloss, scale=1.0, renorm=T
             raise ValueError("accumulate needs a dw to add into")
         dw = torch.empty((v, c), dtype=dw_dtype, device=x.device)
     _want(dw, "dw", (torch.float32, torch.bfloat16), (v, c), rows=True)
-    _one_device(x, lse, logp, dloss, dw, workspace)
+    _one_device(x, lse, logp, dloss, dw)
     dx = torch.empty((n, c), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = torch.empty(jetq_linear_distill_bwd_workspace_bytes(n, v, c, k), dtype=torch.uint8,
@@ -940,7 +957,8 @@ def _policy_args(nll, nll_old, adv, seg_offsets, nll_ref, mask, workspace=None, 
         _want(dloss, "dloss", f32)
         if dloss.numel() != 1:
             raise ValueError(f"dloss: one value is wanted, got shape {tuple(dloss.shape)}")
-    _one_device(nll, nll_old, adv, seg_offsets, nll_ref, mask, out, seg, dloss, workspace)
+    _one_device(nll, nll_old, adv, seg_offsets, nll_ref, mask, out, seg, dloss)
+    _check_workspace(workspace, nll)
     return nseg
 
 
