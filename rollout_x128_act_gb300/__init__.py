@@ -694,17 +694,23 @@ def gemv_nvfp4(x, b, out_dtype=torch.float32, stream=None):
 
 
 def quant_nvfp4_experts(w, stream=None):
-    """NVFP4 copies of stacked expert weights, BF16 w [e x r x c], a tensor scope each:
+    """NVFP4 copies of stacked expert weights, BF16 w [e x r x c] (rows of consecutive elements), a tensor scope each:
     dict(q [e x r x c/2] u8, sb [e x r x c/16] u8, sg [e] f32), as moe_nvfp4 takes them."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return quant_nvfp4_experts(w)
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w: a tensor [experts x rows x columns] is wanted")
     e, r, c = w.shape
+    if e > 0:
+        _want(w[0], "an expert's weight", torch.bfloat16, rows=True)  # the others are laid out alike
+        _one_device(w)
     out = dict(q=torch.empty((e, r, c // 2), dtype=torch.uint8, device=w.device),
                sb=torch.empty((e, r, c // 16), dtype=torch.uint8, device=w.device),
                sg=torch.empty(e, dtype=torch.float32, device=w.device))
     for i in range(e):
-        jetq_quant_nvfp4(w[i], out["q"][i], out["sb"][i], out["sg"][i:i + 1], amax_bf16(w[i]))
+        one = _row_stride(w[i])
+        jetq_quant_nvfp4(one, out["q"][i], out["sb"][i], out["sg"][i:i + 1], amax_bf16(one))
     return out
 
 

@@ -80,3 +80,24 @@ def test_a_workspace_of_the_right_kind(cuda, call):
         CALLS[call](_t(1 << 20, 16, dtype=F32))
     with pytest.raises(Launched):
         CALLS[call](None)
+
+
+def test_experts_that_quant_nvfp4_experts_takes(cuda):
+    """BF16 [e x r x c] with consecutive elements along the last axis; experts and rows may lie apart."""
+    for w in (_t(3, 32, 64), _t(3, 32, 72)[:, :, :64], _t(6, 32, 64)[::2], _t(3, 64, 64)[:, ::2], _t(3, 1, 64),
+              _t(1, 32, 64).expand(3, 32, 64)):
+        with pytest.raises(Launched):
+            jq.quant_nvfp4_experts(w)
+
+
+@pytest.mark.parametrize("bad", ["FP32", "FP16", "two axes", "strided last axis", "transposed", "host",
+                                 "another device", "rows that overlap"])
+def test_experts_that_quant_nvfp4_experts_refuses(cuda, bad):
+    """Their bits would be read as those of a dense BF16 tensor."""
+    w = {"FP32": lambda: _t(3, 32, 64, dtype=F32), "FP16": lambda: _t(3, 32, 64, dtype=torch.float16),
+         "two axes": lambda: _t(32, 64), "strided last axis": lambda: _t(3, 32, 128)[:, :, ::2],
+         "transposed": lambda: _t(3, 64, 32).transpose(1, 2), "host": lambda: _t(3, 32, 64, device="cpu"),
+         "another device": lambda: _t(3, 32, 64, device="cuda:1"),
+         "rows that overlap": lambda: _t(3, 1, 64).expand(3, 32, 64)}[bad]()
+    with pytest.raises(ValueError):
+        jq.quant_nvfp4_experts(w)
