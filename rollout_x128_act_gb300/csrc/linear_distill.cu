@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(32 * row_warps(N), N == 1 ? 2 : 6) k_distill_r
 {
     constexpr int kRowWarps = row_warps(N);
     constexpr int kChunk = 1024;             // marks' 128-column parts at a time
-    __shared__ uint32_t marks[kChunk * 4];
+    __shared__ __align__(16) uint32_t marks[kChunk * 4]; // read 16 bytes at a time
     __shared__ int64_t ids[kMaxListed];
     // The launch after the wait: the product may start on x and w, whose writers are through.
     ptx::grid_dep_wait();
