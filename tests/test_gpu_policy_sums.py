@@ -123,3 +123,51 @@ def test_advantages_of_zero_are_not_clipped(by_seg, per_token):
         out, seg = jq.policy_loss(args[0], args[1], zero, **kw)
         assert bool((out[:4] == 0).all())
         assert bool((jq.policy_loss_bwd(args[0], args[1], zero, out, seg, **kw) == 0).all())
+
+
+@pytest.mark.parametrize("by_seg,per_token", [(False, False), (True, False), (True, True)])
+def test_the_longest_chunks(by_seg, per_token):
+    """More than 128 * 32 tokens for each of a GPU's 3648 warps (152 SMs): chunks of 32 windows, the most there are.
+
+    A lane then sums KL terms of 128 tokens in FP32, and five shuffles add the lanes: 133 roundings of the sum of the
+    terms' magnitudes, and the terms' own 2^-20.  Everything else is compensated (2^-20, as for short chunks)."""
+    lengths = [9000001, 0, 1, 6500000, 130]
+    n = sum(lengths) + 4097
+    g = torch.Generator(device=DEV).manual_seed(7)
+    old = torch.empty(n, device=DEV).exponential_(1.0, generator=g)
+    nll = old + 0.15 * torch.randn(n, generator=g, device=DEV)
+    ref = old + 0.3 * torch.randn(n, generator=g, device=DEV)
+    nseg = len(lengths)
+    off = torch.tensor([0] + lengths, device=DEV).cumsum(0)
+    adv = torch.randn(n if per_token else nseg, generator=g, device=DEV)
+    low, high, kl = (float(np.float32(v)) for v in (0.2, 0.28, 0.03))
+    kw = dict(seg_offsets=off, nll_ref=ref, clip_low=low, clip_high=high, kl=kl, mean=jq.POLICY_MEAN_TOKENS,
+              level=jq.POLICY_SEGMENT if by_seg else jq.POLICY_TOKEN, adv_per_token=per_token)
+    out, seg = jq.policy_loss(nll, old, adv, **kw)
+    dnll = jq.policy_loss_bwd(nll, old, adv, out, seg, **kw)
+    N = sum(lengths)
+    sums, sizes, clipped = np.zeros(2), np.zeros(2), 0
+    for s, (a, b) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        if a == b:
+            continue
+        A = adv[a:b].double() if per_token else adv[s].double().expand(b - a)
+        logr = old[a:b].double() - nll[a:b].double()
+        if by_seg:
+            logr = logr.mean().expand(b - a)
+        r, d = logr.exp(), nll[a:b].double() - ref[a:b].double()
+        m = torch.where(A >= 0, r.clamp(max=1 + high), r.clamp(min=1 - low))
+        live, k = m == r, torch.expm1(d) - d
+        slope = torch.where(live, A * r, torch.zeros_like(A))
+        size = slope.abs()
+        if by_seg:
+            slope, size = slope.mean().expand(b - a), size.mean().expand(b - a)
+        slope, size = slope + kl * torch.expm1(d), size + kl * (torch.expm1(d).abs() + d.abs() * d.exp())
+        assert bool(((dnll[a:b].double() * N - slope).abs() <= 2.0 ** -20 * size).all())
+        sums += [float((-A * m).sum()) / N, float(k.sum()) / N]
+        sizes += [float((A * m).abs().sum()) / N, float(k.sum()) / N]
+        clipped += int((~live).sum())
+    assert bool((dnll[off[-1]:] == 0).all())
+    tol = 2.0 ** -20 * sizes + np.array([0.0, 133 * U * sizes[1]])
+    assert abs(float(out[1]) - sums[0]) <= tol[0] and abs(float(out[2]) - sums[1]) <= tol[1]
+    assert abs(float(out[0]) - sums[0] - kl * sums[1]) <= tol[0] + kl * tol[1]
+    assert [float(v) for v in out[3:]] == [float(np.float32(clipped)), float(np.float32(N)), 4.0]
