@@ -16,13 +16,15 @@
 //      the CTA's registers and written once, without atomics.
 // Each CTA of kernel 2 chooses the experts from the logits itself (3 to 4 us, in
 // place of another kernel), and the first one leaves its choices to kernel 3.
-// Measured in a graph, 128 experts of which 8 are taken, 2048/768: one token 23 to 25 us
+// Measured in a graph, 128 experts of which 8 are taken, 2048/768: one token 23 us
 // (HBM 3.2; the launches, the choice and the kernels' first copies are most of
 // it), sixteen tokens (82 experts) 92 us: router 5, choice 4, gate and up 36, down
 // 37, HBM 32; the last two use half of the issue slots, most of them to decode.
 // Loads issued by the threads themselves, with K shared by eight warps: 145 us.
 // Rows copied one by one to a pitch without bank conflicts: 147 us (a bulk copy
-// costs about 50 ns, whatever its size).
+// costs about 50 ns, whatever its size).  The down weights of few experts
+// prefetched into L2 by kernel 2's idle lanes: one token 24.7 us for 22.7, two
+// 32.9 for 30.9, five 55 for 50; they take the bandwidth that gate and up need.
 //
 // Both products run on mma.m16n8k16 (weight rows as M, tokens as N), decoded
 // in registers as in the few-token product.  In the first, rows 0 to 7 of the M
@@ -56,7 +58,6 @@ constexpr int kConsumers = 16;         // warps that compute; one more copies
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kMaxStages = 28;         // buffers of a ring
 constexpr int kRingBytes = 192 * 1024;
-constexpr int64_t kPrefetchBytes = 32 << 20; // down weights that kernel 2 brings into L2 for kernel 3
 
 struct MoeParams {
     const uint16_t *x, *router;
@@ -360,14 +361,6 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr)
     return v;
 }
 
-// A byte range into L2, line by line, shared by `lanes` threads.  (Not by bulk prefetches: nothing tells when those
-// are through, and a CTA without work ends at once.)
-__device__ __forceinline__ void prefetch_l2(const uint8_t *src, int64_t bytes, int lane, int lanes)
-{
-    for (int64_t at = 128 * lane; at < bytes; at += 128 * lanes)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(src + at));
-}
-
 // a as the sum of BF16 numbers, rounded to nearest each.
 template <int PARTS>
 __device__ __forceinline__ void split(float a, __nv_bfloat16 (&out)[PARTS])
@@ -499,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
     const uint32_t codes = 4u * p.h, scales = (uint32_t)p.h / 2, bytes = 2 * (codes + scales);
 
     if (warp == kConsumers) {
-        if (lane == 0) {
+        if (lane == 0)
             produce(ring, kGroups, p.depth, items, bytes, p.limit_ns, [&](int i, int s, uint32_t bar) {
                 const int unit = (int)blockIdx.x + i * (int)gridDim.x;
                 const int64_t row =
@@ -511,17 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gate_up(const MoeParams p)
                 ptx::bulk_load(dst + 2 * codes, sb, scales, bar);
                 ptx::bulk_load(dst + 2 * codes + scales, sb + (int64_t)p.inter * (p.h / 16), scales, bar);
             });
-        } else { // the down weights of few experts into L2, a share a CTA
-            const int64_t q = (int64_t)p.h * (p.inter / 2), sb = (int64_t)p.h * (p.inter / 16);
-            if (r.slots * (q + sb) <= kPrefetchBytes) {
-                const int64_t share = ((q + (int64_t)gridDim.x - 1) / gridDim.x + 127) / 128 * 128;
-                const int64_t a = min(q, share * blockIdx.x), b = min(q, a + share);
-                for (int i = 0; i < r.slots; ++i)
-                    prefetch_l2(p.q2 + r.expert[i] * q + a, b - a, lane - 1, 31);
-                if ((int)blockIdx.x < r.slots)
-                    prefetch_l2(p.sb2 + r.expert[blockIdx.x] * sb, sb, lane - 1, 31);
-            }
-        }
         __syncwarp();
         return;
     }
