@@ -536,7 +536,10 @@ __device__ __forceinline__ void write_out(const PolicyParams &p, const Totals &t
     p.out[5] = (float)t.segs;
 }
 
-constexpr int kLanesSeg = 4, kLong = 64; // a sequence's lanes; pieces above which the CTA takes it
+// A sequence's lanes in the join; pieces above which the whole CTA takes it.  In a graph, both directions, bounds of
+// 16, 64 and 256 pieces: 1000003 tokens in 24 sequences 27, 29 and 41 us, 524288 in 512 25, 23 and 23, 4194304 in 1
+// 53 (256 without a bound).
+constexpr int kLanesSeg = 4, kLong = 64;
 
 template <int THREADS>
 struct JoinShared {
@@ -641,7 +644,10 @@ __device__ __forceinline__ Totals join_segments(const PolicyParams &p, int64_t f
 }
 
 constexpr int kSmallThreads = 1024, kJoinThreads = 256;
-constexpr int kSmallSegs = 4096; // sequences (most of them empty) that one CTA joins
+// Sequences that one CTA joins.  One launch in place of two, which is what a call costs: 1531 tokens in 8 sequences
+// 42 us both directions (45 with the two kernels; in a graph 14.5 and 12.5).  Its warps walk the sequences of their
+// windows alone: 4096 tokens in 500 sequences are done after 72 us (64), in 4000 after 232 (161).
+constexpr int kSmallSegs = 256;
 
 template <bool BY_SEG>
 __global__ void __launch_bounds__(32 * kWarps, 3) k_policy_pieces(const PolicyParams p)
