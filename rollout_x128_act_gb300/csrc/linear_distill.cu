@@ -449,7 +449,12 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-constexpr int kFewRows = 64; // rows that take several CTAs each
+// Rows that take several CTAs each for their products.  Forward in a graph, with and without: 64 rows x 32000 x 4096,
+// 32 entries 58 and 80 us; 384 rows 111 and 126; 384 x 50257 x 1032, 20 entries 74 and 75, 512 rows of it 87 and 84.
+constexpr int kFewRows = 384;
+// Rows that take a CTA each in the join (above: eight a CTA): 2048 x 32000 x 4096, 32 entries 379 us (384), 2048 x
+// 4097 x 128 37 (43); 8192 x 4097 x 128 107 (98), 8192 x 32000 x 256 240 (222).
+constexpr int kJoinRows = 2048;
 
 int64_t ceil_div(int64_t a, int64_t b)
 {
@@ -471,7 +476,7 @@ cudaError_t launch_distill_rows(const LinearCeArgs &a, const DistillArgs &t, uin
 cudaError_t launch_distill_join(const LinearCeArgs &a, const DistillArgs &t, const float2 *part, int parts,
                                 const float2 *dots, cudaStream_t st)
 {
-    const int rows = a.n > kFewRows ? 8 : 1;
+    const int rows = a.n > kJoinRows ? 8 : 1;
     return launch_pdl(k_distill_join, dim3((unsigned)ceil_div(a.n, rows)), dim3(256), 0, st, rows, part, parts, dots,
                       t.ids, t.ldi, t.teacher, t.ldt, t.k, t.renorm, a.n, a.v, a.scale, a.scale * kLog2e, a.loss,
                       a.lse, t.logp);
