@@ -750,7 +750,8 @@ JETQ_API jetq_status jetq_linear_distill_fwd(const uint16_t *x, int64_t n, int64
  * Its gradient, from the forward call's lse and logp:
  *   d[i, j] = (Q p[i, j] - q[i, j]) * dloss[i],  p = exp(z - lse), Q = the row's sum of q, q = 0 where not listed
  *   dx = scale * d w,   dw = scale * d^T x
- * d, dx, dw, dloss and workspace as for jetq_linear_ce_bwd; the listed entries of d come from logp and are rounded once.
+ * d, dx, dw, dloss and workspace as for jetq_linear_ce_bwd; the listed entries of d come from logp, and what their
+ * BF16 value leaves of them is added to dx in FP32 (dw takes d in BF16).
  */
 JETQ_API size_t jetq_linear_distill_bwd_workspace_bytes(int64_t n, int64_t v, int64_t c, int64_t k, int smallest);
 JETQ_API jetq_status jetq_linear_distill_bwd(const uint16_t *x, int64_t n, int64_t c, int64_t ldx,

@@ -348,7 +348,7 @@ cudaError_t launch_linear_distill_fwd(LinearCeArgs a, const DistillArgs &t, cuda
 
 // The distillation's own steps around the head's products (linear_distill.cu).
 struct GradRow;
-struct Listed { // an entry of d: its column (-1: none) and Q p - q
+struct Listed { // an entry of d: its column (-1: none, or listed before) and Q p - q
     int id;
     float d;
 };
@@ -360,6 +360,8 @@ cudaError_t launch_distill_start(const LinearCeArgs &a, const DistillArgs &t, ui
                                  GradRow *rows, Listed *listed, float *gmax, cudaStream_t st);
 cudaError_t launch_distill_patch(const LinearCeArgs &a, const DistillArgs &t, const Listed *listed, const float *gmax,
                                  uint16_t *d, int64_t ldd, int64_t col0, int64_t cols, cudaStream_t st);
+cudaError_t launch_distill_dx(const LinearCeArgs &a, const DistillArgs &t, const Listed *listed, const float *slab,
+                              int slabs, const float *gmax, cudaStream_t st);
 cudaError_t linear_ce_read_and_clear_error(cudaStream_t st, unsigned *out);
 
 // Clipped policy-gradient loss of packed sequences, forward (out, save

@@ -1203,6 +1203,8 @@ cudaError_t launch_linear_ce_bwd(LinearCeArgs a, const DistillArgs *t, cudaStrea
         if (e != cudaSuccess)
             return e;
     }
+    if (t)
+        return launch_distill_dx(a, *t, listed, slab, plan.splits, gmax, st);
     const int64_t blocks = ceil_div(a.n * (a.c / 4), 256), cap = (int64_t)sm_count() * 8;
     return launch_pdl(k_ce_dx, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, st, (const float *)slab,
                       plan.splits, a.n, a.c, (const float *)gmax, a.scale, a.dx, a.lddx);

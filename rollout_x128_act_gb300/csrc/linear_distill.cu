@@ -15,15 +15,26 @@
 // terms in (losses of 2048 tokens were off by 2e-5 in the 2-norm where an FP32
 // product gave the logits).  The backward product writes d = f Q p for every
 // column, and k_distill_patch replaces the listed entries, where the two terms
-// nearly cancel, by f (Q p - q) from the forward call's log-probabilities,
-// rounded once.
+// nearly cancel, by f (Q p - q) from the forward call's log-probabilities.
+//
+// d is BF16, the tensor cores' operand.  A confident token's d is a few large
+// listed entries, whose rounding (2^-8) shows in a gradient: 2.2e-3 to 2.5e-3 in
+// the 2-norm, where the rounding of BF16 results alone is 1.7e-3.  For dx, which
+// all gradients before the head are made of, what a listed entry's BF16 value
+// leaves of it, its rest, is added to the FP32 sums where the slabs are joined
+// (k_distill_dx): dx is then at 1.7e-3, as with two BF16 terms for all of d, for
+// 4% of the time at 777 tokens x 50257 x 1032 and 2% at 2048 x 131072 x 4096.  dw
+// takes d in BF16, as the cross entropy's does: a second term of d costs a third
+// of the pass, and rests added in that product's epilogue cost 5% where the
+// tokens list different columns but twice to five times the pass where many list
+// the same (one row of dw takes all of their rows of x, in each of its tiles).
 //
 // Bound by the head's products, but for k_distill_rows, which reads the listed
 // rows of w in the order of the tokens: 2048 tokens x 64 entries (half of them
 // listed) x 4096 take 130 us at 3.7 TB/s, a tenth of the forward pass over 131072
-// rows (1.30 to 1.35 ms in all; backward 3.7 to 3.9).  A single token's 32
-// entries are read under the product's first tiles (one token x 32000 x 4096
-// 55 us in a graph, 38.6 of it HBM's).
+// rows (1.31 to 1.35 ms for a few passes, 1.41 back to back at the power cap).  A
+// single token's 32 entries are read under the product's first tiles (one token x
+// 32000 x 4096 55 us in a graph, 38.6 of it HBM's).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -397,16 +408,21 @@ __global__ void __launch_bounds__(256)
         for (int j = lane; j < k; j += 32) {
             Listed e = {-1, 0.0f};
             if (has && mine[j] >= 0) {
-                // columns listed twice: their q is the sum, and both entries hold the same value
+                // a column listed twice: its q is the sum, in the first of its entries
+                bool first = true;
                 float here = 0.0f, other = 0.0f;
                 for (int i = 0; i < k; ++i) {
-                    here += mine[i] == mine[j] ? q[i] : 0.0f;
-                    other += mine[i] == mine[j] ? 0.0f : q[i];
+                    const bool same = mine[i] == mine[j];
+                    first &= !same || i >= j;
+                    here += same ? q[i] : 0.0f;
+                    other += same ? 0.0f : q[i];
                 }
-                // Q p - q; for a confident token as Q (p - 1) + the other q, which keeps its small value
-                const float lp = __ldg(logp + r * k + j);
-                e.id = (int)mine[j];
-                e.d = lp > -0.7f ? fmaf(Q, expm1f(lp), other) : fmaf(Q, expf(lp), -here);
+                if (first) {
+                    // Q p - q; for a confident token as Q (p - 1) + the other q, which keeps its small value
+                    const float lp = __ldg(logp + r * k + j);
+                    e.id = (int)mine[j];
+                    e.d = lp > -0.7f ? fmaf(Q, expm1f(lp), other) : fmaf(Q, expf(lp), -here);
+                }
             }
             listed[r * k + j] = e;
         }
@@ -429,6 +445,12 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// d at a listed entry, in FP32: d is scaled by the largest |dloss|, f = dloss / gmax.
+__device__ __forceinline__ float entry_of(float d, float dloss, float gmax)
+{
+    return d * (gmax > 0.0f ? __fdiv_rn(dloss, gmax) : 0.0f);
+}
+
 // d at the listed columns of a piece [col0, col0 + cols) of the vocabulary.
 __global__ void __launch_bounds__(256)
     k_distill_patch(const Listed *listed, int64_t total, int k, const float *dloss, const float *gmax,
@@ -444,9 +466,83 @@ __global__ void __launch_bounds__(256)
         if (e.x < 0 || rel < 0 || rel >= cols)
             continue;
         const int64_t r = i / k;
-        const float f = g > 0.0f ? __fdiv_rn(__ldg(dloss + r), g) : 0.0f;
-        d[r * ldd + rel] = __float2bfloat16_rn(__int_as_float(e.y) * f);
+        d[r * ldd + rel] = __float2bfloat16_rn(entry_of(__int_as_float(e.y), __ldg(dloss + r), g));
     }
+}
+
+// dx = BF16(scale * gmax * (sum of the slabs + sum over a row's listed entries of their rest times w's row)), eight
+// columns a thread.  The rests' rows of w are what it reads most of: 91 us at 2048 tokens x 64 entries (half of them
+// listed) x 4096, 53 without them.
+__global__ void __launch_bounds__(128)
+    k_distill_dx(const float *slab, int slabs, int64_t n, int64_t c, const float *gmax, float scale,
+                 const float *dloss, const Listed *listed, int k, const uint16_t *w, int64_t ldw, uint16_t *dx,
+                 int64_t lddx)
+{
+    __shared__ int64_t from[kMaxListed];
+    __shared__ float rest[kMaxListed];
+    __shared__ int num;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int64_t r = blockIdx.x, col = 8 * ((int64_t)blockIdx.y * 128 + threadIdx.x);
+    const float g = __ldg(gmax);
+    if (threadIdx.x < 32) { // the row's entries that leave a rest, in their order
+        const int lane = threadIdx.x;
+        int m = 0;
+        for (int j0 = 0; j0 < k; j0 += 32) {
+            const int j = j0 + lane;
+            int2 e = make_int2(-1, 0);
+            if (j < k)
+                e = __ldg(reinterpret_cast<const int2 *>(listed) + r * k + j);
+            float v = 0.0f;
+            if (e.x >= 0) {
+                const float d = entry_of(__int_as_float(e.y), __ldg(dloss + r), g);
+                const float hi = __bfloat162float(__float2bfloat16_rn(d));
+                v = fabsf(hi) < INFINITY ? d - hi : 0.0f;
+            }
+            const unsigned on = __ballot_sync(0xFFFFFFFFu, v != 0.0f);
+            if (v != 0.0f) {
+                const int at = m + __popc(on & ((1u << lane) - 1u));
+                from[at] = (int64_t)e.x * ldw;
+                rest[at] = v;
+            }
+            m += __popc(on);
+        }
+        if (lane == 0)
+            num = m;
+    }
+    __syncthreads();
+    if (col >= c)
+        return;
+    float2 a[4] = {};
+    const int m = num;
+    for (int e0 = 0; e0 < m; e0 += 8) {
+        uint4 b[8]; // in flight together
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            b[e] = e0 + e < m ? __ldg(reinterpret_cast<const uint4 *>(w + from[e0 + e] + col)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float f = e0 + e < m ? rest[e0 + e] : 0.0f;
+            const uint32_t u[4] = {b[e].x, b[e].y, b[e].z, b[e].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                a[i] = __ffma2_rn(make_float2(f, f), unpack2(u[i]), a[i]);
+        }
+    }
+    const float f = g * scale;
+    const float4 *s = reinterpret_cast<const float4 *>(slab + r * c + col);
+    float4 lo = s[0], hi = s[1];
+    for (int q = 1; q < slabs; ++q) {
+        const float4 p = s[q * n * c / 4], t = s[q * n * c / 4 + 1];
+        lo = make_float4(lo.x + p.x, lo.y + p.y, lo.z + p.z, lo.w + p.w);
+        hi = make_float4(hi.x + t.x, hi.y + t.y, hi.z + t.z, hi.w + t.w);
+    }
+    alignas(16) const __nv_bfloat162 o[4] = {
+        __floats2bfloat162_rn((lo.x + a[0].x) * f, (lo.y + a[0].y) * f),
+        __floats2bfloat162_rn((lo.z + a[1].x) * f, (lo.w + a[1].y) * f),
+        __floats2bfloat162_rn((hi.x + a[2].x) * f, (hi.y + a[2].y) * f),
+        __floats2bfloat162_rn((hi.z + a[3].x) * f, (hi.w + a[3].y) * f)};
+    *reinterpret_cast<uint4 *>(dx + r * lddx + col) = *reinterpret_cast<const uint4 *>(o);
 }
 
 // Rows that take several CTAs each for their products.  Forward in a graph, with and without: 64 rows x 32000 x 4096,
@@ -501,6 +597,13 @@ cudaError_t launch_distill_patch(const LinearCeArgs &a, const DistillArgs &t, co
     const int64_t total = a.n * t.k, blocks = ceil_div(total, 256), cap = (int64_t)sm_count() * 8;
     return launch_pdl(k_distill_patch, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, st, listed, total,
                       t.k, a.dloss, gmax, reinterpret_cast<__nv_bfloat16 *>(d), ldd, col0, cols);
+}
+
+cudaError_t launch_distill_dx(const LinearCeArgs &a, const DistillArgs &t, const Listed *listed, const float *slab,
+                              int slabs, const float *gmax, cudaStream_t st)
+{
+    return launch_pdl(k_distill_dx, dim3((unsigned)a.n, (unsigned)ceil_div(a.c, 1024)), dim3(128), 0, st, slab, slabs,
+                      a.n, a.c, gmax, a.scale, a.dloss, listed, t.k, a.w, a.ldw, a.dx, a.lddx);
 }
 
 } // namespace jetq
