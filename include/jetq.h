@@ -577,17 +577,18 @@ JETQ_API jetq_status jetq_gemv_nvfp4(const uint8_t *qw, const uint8_t *sbw, cons
                                      int64_t ldy, void *stream);
 
 /*
- * A whole mixture-of-experts layer for 1 to 16 tokens (rollout decode; larger
- * batches sort their tokens and use jetq_gemm_grouped), NVFP4 expert weights
- * and BF16 activations:
+ * A whole mixture-of-experts layer for 1 to 16 tokens (rollout decode), NVFP4
+ * expert weights and BF16 activations.  More tokens are refused: no entry point
+ * takes NVFP4 experts for them (those of jetq_gemm_grouped are FP8).
  *   l[i, e]  = sum_k x[i, k] * router[e, k]
  *   chosen   = the topk experts of largest l (the lower index first among equals, NaN before all numbers)
  *   p[i, j]  = exp(l of choice j) / sum of exp(l) over the chosen (renorm = 1) or over all experts (renorm = 0)
  *   a        = silu(gate x) * (up x), silu(z) = z / (1 + exp(-z))
  *   y[i]     = sum_j p[i, j] * down a       (gate, up, down and a of expert chosen[i, j])
  * Products of weights and x are exact (values of x below 2^-30 of their token's
- * largest are rounded to steps of 2^-39 of it), sums FP32; a enters the second
- * product with 16 bits (y BF16) or 24 (y F32); y is rounded once.
+ * largest are off by up to 2^-39 of it), sums FP32, those of l too (experts
+ * whose l are nearer than that may change places); a enters the second product
+ * with 16 bits (y BF16) or 24 (y F32); y is rounded once.
  *
  *   x, m, h, ldx       BF16 [m x h], row stride ldx (multiple of 8), 0 <= m <= 16
  *   router, ldr        BF16 [num_experts x h], row stride ldr (multiple of 8)

@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(256)
 
 // dx = BF16(scale * gmax * (sum of the slabs + sum over a row's listed entries of their rest times w's row)), eight
 // columns a thread.  The rests' rows of w are what it reads most of: 91 us at 2048 tokens x 64 entries (half of them
-// listed) x 4096, 53 without them.
+// listed) x 4096, 29 without them.
 __global__ void __launch_bounds__(128)
     k_distill_dx(const float *slab, int slabs, int64_t n, int64_t c, const float *gmax, float scale,
                  const float *dloss, const Listed *listed, int k, const uint16_t *w, int64_t ldw, uint16_t *dx,

@@ -7,12 +7,14 @@
 //   loss = sum over counted tokens of w (L + kl_coef * kl),   w = scale / N, scale / (S n_s) or scale
 //   dnll = w (A r [not clipped] + kl_coef * (exp(d) - 1))
 //
-// Floor: HBM for long batches (17 to 21 bytes a token, read by the forward and
-// again by the backward pass, which needs N and S first), launches for short
-// ones.  Both directions in a graph: 4194304 tokens in 8192 sequences 45 us
-// (issue slots 70% used: some 120 instructions a token and direction; HBM would
-// take 10), 1000003 tokens in 24 sequences 31 us (the latencies of three kernels;
-// 10 us of it the join), 524288 in 512 21 us, 1531 in 8 15 us.
+// Floor: HBM for long batches (8 to 17 bytes a token, read by the forward and
+// again by the backward pass, which needs N and S first and writes 4), launches
+// for short ones.  Both directions in a graph: 4194304 tokens in 8192 sequences
+// 47 us (issue slots 68% used: some 120 instructions a token and direction; HBM
+// would take 10), 1000003 tokens in 24 sequences 29 us (the latencies of three
+// kernels; 10 us of it the join), 524288 in 512 21 us, 1531 in 8 15 us.  An
+// advantage a token under one ratio a sequence costs 4 us of 51 at 4194304 tokens:
+// its two sums are compensated.
 //
 // Work is split along the tokens, not the sequences, whose lengths run from
 // one to millions: a warp takes a chunk of consecutive windows of 128 tokens
@@ -23,7 +25,7 @@
 // its own tokens of a piece, and the lanes are added where the piece ends.  A
 // second kernel joins each sequence's pieces in a fixed order, with compensated
 // FP32 sums (binary64 is slow here: the join took 25 to 49 us with it): results
-// are repeatable.  Up to 4096 tokens one CTA does both.
+// are repeatable.  Up to 4096 tokens in 256 sequences one CTA does both.
 //
 // Which side of the clip's border a token is on decides whether its gradient
 // is there at all, so logr keeps the rounding error of its subtraction and is
