@@ -23,11 +23,12 @@
 // all gradients before the head are made of, what a listed entry's BF16 value
 // leaves of it, its rest, is added to the FP32 sums where the slabs are joined
 // (k_distill_dx): dx is then at 1.7e-3, as with two BF16 terms for all of d, for
-// 4% of the time at 777 tokens x 50257 x 1032 and 2% at 2048 x 131072 x 4096.  dw
-// takes d in BF16, as the cross entropy's does: a second term of d costs a third
-// of the pass, and rests added in that product's epilogue cost 5% where the
-// tokens list different columns but twice to five times the pass where many list
-// the same (one row of dw takes all of their rows of x, in each of its tiles).
+// 2% of the time at 777 tokens x 50257 x 1032 (253 to 258 us) and at 2048 x 131072
+// x 4096, 7% at 8192 x 32000 x 512 with 64 entries (613 to 654).  dw takes d in
+// BF16, as the cross entropy's does: a second term of d costs a third of the pass,
+// and rests added in that product's epilogue cost 5% where the tokens list
+// different columns but twice to five times the pass where many list the same
+// (one row of dw takes all of their rows of x, in each of its tiles).
 //
 // Bound by the head's products, but for k_distill_rows, which reads the listed
 // rows of w in the order of the tokens: 2048 tokens x 64 entries (half of them
@@ -216,7 +217,8 @@ struct Teacher {
     float2 log2; // of the sum of exp(t - top) (renorm), else 0
     float inv;   // 1 / that sum
     bool none;   // renorm, and nothing to normalize: q = 0
-    __device__ __forceinline__ void load(const float *t, const int64_t *ids, int k, bool renorm, int lane)
+    template <class Id>
+    __device__ __forceinline__ void load(const float *t, const Id *ids, int k, bool renorm, int lane)
     {
         top = 0.0f;
         log2 = make_float2(0.0f, 0.0f);
@@ -362,20 +364,20 @@ __global__ void __launch_bounds__(256)
                     const float *lse, const float *logp, const float *dloss, GradRow *rows, Listed *listed,
                     StartWords *start)
 {
-    __shared__ int64_t list[8][kMaxListed];
+    __shared__ int list[8][kMaxListed]; // below 2^31, -1: none
     __shared__ float qs[8][kMaxListed];
     __shared__ float red[8];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t *mine = list[warp];
+    int *mine = list[warp];
     float *q = qs[warp];
     // the teacher's probabilities of a row and their sum; whether there is a loss
     auto read_row = [&](int64_t r, float &Q) {
         bool any = false;
         for (int j = lane; j < k; j += 32) {
             const int64_t id = __ldg(ids + r * ldi + j);
-            mine[j] = id >= 0 && id < v ? id : -1;
+            mine[j] = id >= 0 && id < v ? (int)id : -1;
             any |= mine[j] >= 0;
         }
         __syncwarp();
@@ -409,18 +411,24 @@ __global__ void __launch_bounds__(256)
             Listed e = {-1, 0.0f};
             if (has && mine[j] >= 0) {
                 // a column listed twice: its q is the sum, in the first of its entries
-                bool first = true;
+                const int own = mine[j];
+                int last = -1; // the last entry of the column before this one
                 float here = 0.0f, other = 0.0f;
-                for (int i = 0; i < k; ++i) {
-                    const bool same = mine[i] == mine[j];
-                    first &= !same || i >= j;
+                for (int i = 0; i < j; ++i) {
+                    const bool same = mine[i] == own;
+                    last = same ? i : last;
                     here += same ? q[i] : 0.0f;
                     other += same ? 0.0f : q[i];
                 }
-                if (first) {
+                for (int i = j; i < k; ++i) {
+                    const bool same = mine[i] == own;
+                    here += same ? q[i] : 0.0f;
+                    other += same ? 0.0f : q[i];
+                }
+                if (last < 0) {
                     // Q p - q; for a confident token as Q (p - 1) + the other q, which keeps its small value
                     const float lp = __ldg(logp + r * k + j);
-                    e.id = (int)mine[j];
+                    e.id = mine[j];
                     e.d = lp > -0.7f ? fmaf(Q, expm1f(lp), other) : fmaf(Q, expf(lp), -here);
                 }
             }
@@ -471,64 +479,90 @@ __global__ void __launch_bounds__(256)
 }
 
 // dx = BF16(scale * gmax * (sum of the slabs + sum over a row's listed entries of their rest times w's row)), eight
-// columns a thread.  The rests' rows of w are what it reads most of: 91 us at 2048 tokens x 64 entries (half of them
-// listed) x 4096, 29 without them.
-__global__ void __launch_bounds__(128)
+// columns a thread.  The rests' rows of w are what it reads most of: 96 us at 2048 tokens x 64 entries (half of them
+// listed) x 4096, 29 without them.  A warp along 256 columns, four that share the entries: 64 or 128 threads along
+// wider pieces took 0 to 30% longer than the whole pass does with 32 (64 rows x 256 entries x 4096: 280 and 340 us
+// for 261; 777 x 20 x 1032: 260 and 266 for 258).
+constexpr int kDxThreads = 128;
+
+__global__ void __launch_bounds__(kDxThreads)
     k_distill_dx(const float *slab, int slabs, int64_t n, int64_t c, const float *gmax, float scale,
                  const float *dloss, const Listed *listed, int k, const uint16_t *w, int64_t ldw, uint16_t *dx,
                  int64_t lddx)
 {
+    constexpr int kGroups = kDxThreads / 32, kTurns = kMaxListed / kDxThreads;
     __shared__ int64_t from[kMaxListed];
     __shared__ float rest[kMaxListed];
-    __shared__ int num;
+    __shared__ int many[kTurns * kGroups];
+    __shared__ float2 sums[kGroups][4][32];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int64_t r = blockIdx.x, col = 8 * ((int64_t)blockIdx.y * 128 + threadIdx.x);
-    const float g = __ldg(gmax);
-    if (threadIdx.x < 32) { // the row's entries that leave a rest, in their order
-        const int lane = threadIdx.x;
-        int m = 0;
-        for (int j0 = 0; j0 < k; j0 += 32) {
-            const int j = j0 + lane;
-            int2 e = make_int2(-1, 0);
-            if (j < k)
-                e = __ldg(reinterpret_cast<const int2 *>(listed) + r * k + j);
-            float v = 0.0f;
-            if (e.x >= 0) {
-                const float d = entry_of(__int_as_float(e.y), __ldg(dloss + r), g);
-                const float hi = __bfloat162float(__float2bfloat16_rn(d));
-                v = fabsf(hi) < INFINITY ? d - hi : 0.0f;
-            }
-            const unsigned on = __ballot_sync(0xFFFFFFFFu, v != 0.0f);
-            if (v != 0.0f) {
-                const int at = m + __popc(on & ((1u << lane) - 1u));
-                from[at] = (int64_t)e.x * ldw;
-                rest[at] = v;
-            }
-            m += __popc(on);
+    const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+    const int64_t r = blockIdx.x, col = 8 * ((int64_t)blockIdx.y * 32 + lane);
+    const float g = __ldg(gmax), loss = __ldg(dloss + r);
+    // the row's entries that leave a rest, in their order
+    float v[kTurns];
+    int id[kTurns];
+    unsigned on[kTurns];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int j = i * kDxThreads + (int)threadIdx.x;
+        int2 e = make_int2(-1, 0);
+        if (j < k)
+            e = __ldg(reinterpret_cast<const int2 *>(listed) + r * k + j);
+        id[i] = e.x;
+        v[i] = 0.0f;
+        if (e.x >= 0) {
+            const float d = entry_of(__int_as_float(e.y), loss, g);
+            const float hi = __bfloat162float(__float2bfloat16_rn(d));
+            v[i] = fabsf(hi) < INFINITY ? d - hi : 0.0f;
         }
+        on[i] = __ballot_sync(0xFFFFFFFFu, v[i] != 0.0f);
         if (lane == 0)
-            num = m;
+            many[i * kGroups + group] = __popc(on[i]);
     }
     __syncthreads();
-    if (col >= c)
-        return;
-    float2 a[4] = {};
-    const int m = num;
-    for (int e0 = 0; e0 < m; e0 += 8) {
-        uint4 b[8]; // in flight together
+    int m = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            b[e] = e0 + e < m ? __ldg(reinterpret_cast<const uint4 *>(w + from[e0 + e] + col)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float f = e0 + e < m ? rest[e0 + e] : 0.0f;
-            const uint32_t u[4] = {b[e].x, b[e].y, b[e].z, b[e].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a[i] = __ffma2_rn(make_float2(f, f), unpack2(u[i]), a[i]);
+    for (int q = 0; q < kTurns * kGroups; ++q) {
+        if (q % kGroups == group && v[q / kGroups] != 0.0f) {
+            const int at = m + __popc(on[q / kGroups] & ((1u << lane) - 1u));
+            from[at] = (int64_t)id[q / kGroups] * ldw;
+            rest[at] = v[q / kGroups];
         }
+        m += many[q];
     }
+    __syncthreads();
+    float2 a[4] = {};
+    if (col < c)
+        for (int e0 = group; e0 < m; e0 += 8 * kGroups) {
+            uint4 b[8]; // in flight together
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                b[i] = e0 + i * kGroups < m ? __ldg(reinterpret_cast<const uint4 *>(w + from[e0 + i * kGroups] + col))
+                                            : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = e0 + i * kGroups < m ? rest[e0 + i * kGroups] : 0.0f;
+                const uint32_t u[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    a[q] = __ffma2_rn(make_float2(f, f), unpack2(u[q]), a[q]);
+            }
+        }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        sums[group][q][lane] = a[q];
+    __syncthreads();
+    if (group > 0 || col >= c)
+        return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            a[q].x += sums[i][q][lane].x;
+            a[q].y += sums[i][q][lane].y;
+        }
     const float f = g * scale;
     const float4 *s = reinterpret_cast<const float4 *>(slab + r * c + col);
     float4 lo = s[0], hi = s[1];
@@ -602,8 +636,8 @@ cudaError_t launch_distill_patch(const LinearCeArgs &a, const DistillArgs &t, co
 cudaError_t launch_distill_dx(const LinearCeArgs &a, const DistillArgs &t, const Listed *listed, const float *slab,
                               int slabs, const float *gmax, cudaStream_t st)
 {
-    return launch_pdl(k_distill_dx, dim3((unsigned)a.n, (unsigned)ceil_div(a.c, 1024)), dim3(128), 0, st, slab, slabs,
-                      a.n, a.c, gmax, a.scale, a.dloss, listed, t.k, a.w, a.ldw, a.dx, a.lddx);
+    return launch_pdl(k_distill_dx, dim3((unsigned)a.n, (unsigned)ceil_div(a.c, 256)), dim3(kDxThreads), 0, st, slab,
+                      slabs, a.n, a.c, gmax, a.scale, a.dloss, listed, t.k, a.w, a.ldw, a.dx, a.lddx);
 }
 
 } // namespace jetq
